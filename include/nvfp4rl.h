@@ -14,10 +14,13 @@
  *     "AQNの仕組み" and "ゼロオーバーヘッド：レイヤー正規化への統合";
  *   - "TRACE: rollout-guided quantization-aware training" summary (sns.style),
  *     sections "TRACE の中心的なアイデア" and "仕組みの工学的な理解".
+ * Around them stand the operators between a model's logits and that correction: token log-probs
+ * with entropy and top alternatives, top-k distillation, and the gradients of both.
  *
  * Conventions shared by every entry point:
  *   - Memory: every pointer argument is DEVICE memory, allocated and owned by
- *     the caller, and must be 16-byte aligned. The library allocates nothing;
+ *     the caller, and must be 16-byte aligned (the logits operators ask for their elements'
+ *     alignment only). The library allocates nothing;
  *     it keeps only per-device cached attributes and kernel resources.
  *   - Streams: `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream). Calls are asynchronous on that stream; outputs are complete when
@@ -71,6 +74,9 @@ typedef enum nvfp4rl_status {
 
 /* Element types of quantizer inputs. */
 enum { NVFP4RL_BF16 = 0, NVFP4RL_F32 = 1 };
+
+/* How topk_distill reads a teacher's listed log-probs. */
+enum { NVFP4RL_DISTILL_NORMALIZED = 0, NVFP4RL_DISTILL_TAIL = 1 };
 
 /* Operations for nvfp4rl_workspace_bytes(). */
 enum {
@@ -231,6 +237,100 @@ NVFP4RL_API nvfp4rl_status nvfp4_quantize_cached(const void* x, int32_t dtype, i
 NVFP4RL_API nvfp4rl_status ais_mixing(const float* logp_rollout, const float* logp_train, const float* adv,
                                       int64_t n, float C, float delta, float gamma, float beta, float* w_out,
                                       double* stats, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The logits operators: token_logprobs, token_logprobs_backward, topk_distill,
+ * topk_distill_backward. They stand before and after ais_mixing, which takes the sampled tokens'
+ * log-probs under both policies (AIS summary, section 2.1 "混合係数"; section 2.2 "GRPO への統合");
+ * the pages have no recipe of their own for them, so it is stated here. Common to the four:
+ *   logits   [M][ld] bf16 bits or fp32 (dtype), columns [0, V) of each row, ld >= V: a vocabulary
+ *            inside padded rows (a linear's N is a multiple of 128) is taken as it lies, and columns
+ *            [V, ld) are neither read nor written. Aligned to an element (2 or 4 bytes); rows may start
+ *            anywhere. V <= 2^30, M <= 2^31 - 1, M * ld <= 2^48.
+ *   scale    z = scale * x (the inverse sampling temperature), in [2^-20, 2^20]; p = softmax(z) over
+ *            the row's V columns.
+ *   A logit at or below -2^100 (-inf, the type's lowest value) is MASKED: its p is 0. A row that
+ *   holds a NaN or a logit above 2^100 has NaN for every result. Other rows are not affected.
+ *   Per-row arrays are fp32 or int32, aligned to 4 bytes.
+ *   Sums run in fp32 (a few hundred terms per thread, then a tree), exponentials are ex2.approx of
+ *   scores in log2 units. No workspace, no atomics on floating values: equal inputs give equal bits.
+ * Errors: NVFP4RL_ERR_INVALID_ARG (bad dtype or mode, negative sizes, ld < V, k out of range, scale
+ *   out of range, NULL pointers), NVFP4RL_ERR_UNSUPPORTED_SHAPE (V, M, M * ld or k too large),
+ *   NVFP4RL_ERR_MISALIGNED, NVFP4RL_ERR_ALIAS. M == 0 is a no-op.
+ */
+
+/*
+ * token_logprobs -- log-probs of given tokens, each row's entropy, and its top alternatives.
+ *   logp[m] = z_t - lse[m] with t = tokens[m], lse[m] = ln sum_j exp(z_j),
+ *   entropy[m] = -sum_j p_j ln p_j,
+ *   top_ids[m][i], top_logp[m][i]: the columns of the k largest logits, largest first, equal logits
+ *   by the lower column, and their log-probs; masked columns are not listed: where fewer than k are
+ *   left the list ends in (-1, -inf).
+ * Arguments:
+ *   tokens   int32 [M], or NULL (logp must then be NULL). A row whose token is outside [0, V)
+ *            (padding) is not read: logp, entropy and lse 0, its list (-1, -inf).
+ *   k        alternatives per row, 0 .. min(V, 256); 0: top_ids and top_logp are not used.
+ *   logp, entropy, lse  out, fp32 [M], each may be NULL. top_ids int32 [M][k], top_logp fp32 [M][k].
+ * A row without an unmasked column: lse = logp = -inf, entropy 0. A NaN row lists (-1, NaN).
+ */
+NVFP4RL_API nvfp4rl_status token_logprobs(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
+                                          const int32_t* tokens, float scale, int32_t k, float* logp, float* entropy,
+                                          float* lse, int32_t* top_ids, float* top_logp, void* stream);
+
+/*
+ * token_logprobs_backward -- gradient of sum_m dlogp[m] logp[m] + dentropy[m] entropy[m] to the logits:
+ *   dlogits[m][j] = scale (dlogp (1[j = t] - p_j) - dentropy p_j (ln p_j + entropy)),
+ *   p_j = exp(z_j - lse), rounded once to dtype.
+ * Arguments as token_logprobs, and
+ *   lse, entropy  fp32 [M] as the forward call wrote them for these logits and this scale; entropy
+ *            may be NULL without dentropy.
+ *   dlogp, dentropy  fp32 [M]; one of them may be NULL (no such term). dlogp needs tokens.
+ *   dlogits  out, [M][ldd] of dtype, ldd >= V; columns [V, ldd) are left as they are. It may be the
+ *            logits themselves (the same pointer and ldd == ld: overwritten in place), and may
+ *            overlap nothing otherwise.
+ * Rows whose token is outside [0, V), whose dlogp and dentropy are both 0, or whose lse is -inf get
+ * zeros and are not read.
+ */
+NVFP4RL_API nvfp4rl_status token_logprobs_backward(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
+                                                   const int32_t* tokens, float scale, const float* lse,
+                                                   const float* entropy, const float* dlogp, const float* dentropy,
+                                                   void* dlogits, int64_t ldd, void* stream);
+
+/*
+ * topk_distill -- distillation from a teacher's top logits: per row the divergence of the student's p from
+ *   the teacher's q, known at k listed columns (e.g. top_ids and top_logp of token_logprobs on the teacher's logits).
+ *   Entries whose id is outside [0, V) are skipped (lists shorter than k end in -1). With l_i = teacher_logp:
+ *   NVFP4RL_DISTILL_NORMALIZED: q_i = exp(l_i) / sum_i exp(l_i) (raw logits do as well as log-probs);
+ *     loss = sum_i q_i (ln q_i - ln p_i).
+ *   NVFP4RL_DISTILL_TAIL: q_i = exp(l_i), and everything unlisted is one more outcome:
+ *     loss = sum_i q_i (ln q_i - ln p_i) + q_0 (ln q_0 - ln p_0),
+ *     q_0 = max(0, 1 - sum_i q_i), p_0 = the sum of p over the unlisted columns; the last term is left
+ *     out when p_0 = 0 (every unlisted column masked, or none).
+ *   Terms with q_i = 0 are 0. A listed column that is masked in the student gives +inf (q_i > 0).
+ *   A column listed twice counts with both entries' q, and once in p.
+ * Arguments:
+ *   ids      int32 [M][k], teacher_logp fp32 [M][k] (-inf: q_i = 0), k in [1, 256]; mode as above.
+ *   loss     out, fp32 [M]. lse, lse_tail  out, fp32 [M] or NULL: ln sum exp(z) over the row, and over its
+ *            unlisted columns (TAIL only), as topk_distill_backward takes them.
+ * A row without an entry (or, NORMALIZED, with every l_i = -inf) is not read: loss, lse and lse_tail 0.
+ * A NaN among a row's counted l_i gives a NaN loss.
+ */
+NVFP4RL_API nvfp4rl_status topk_distill(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld, float scale,
+                                        const int32_t* ids, const float* teacher_logp, int32_t k, int32_t mode,
+                                        float* loss, float* lse, float* lse_tail, void* stream);
+
+/*
+ * topk_distill_backward -- gradient of sum_m dloss[m] loss[m] to the logits, rounded once to dtype:
+ *   dlogits[m][j] = scale dloss (Q p_j - q_j) at listed columns (q_j the sum of their entries' q), and
+ *   scale dloss (Q - q_0 / p_0) p_j at the others, Q = sum_i q_i + q_0 (NORMALIZED: Q = 1, q_0 = 0).
+ * Arguments as topk_distill; lse, lse_tail as it wrote them (lse_tail is used by TAIL only, which needs it); dloss fp32 [M];
+ *   dlogits, ldd as token_logprobs_backward.
+ * Rows without an entry, with dloss 0, or with lse = -inf get zeros and are not read.
+ */
+NVFP4RL_API nvfp4rl_status topk_distill_backward(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
+                                                 float scale, const int32_t* ids, const float* teacher_logp, int32_t k,
+                                                 int32_t mode, const float* lse, const float* lse_tail,
+                                                 const float* dloss, void* dlogits, int64_t ldd, void* stream);
 
 /*
  * nvfp4_kv_append -- writes one token's keys and values per sequence into an NVFP4 KV cache (TRACE

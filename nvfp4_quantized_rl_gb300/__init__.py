@@ -9,7 +9,8 @@ library or a GPU is missing -- there is no CPU fallback.
 
 Functions carry the C names: nvfp4_amax, nvfp4_quantize, nvfp4_quantize_guided,
 nvfp4_quantize_record, nvfp4_quantize_cached, nvfp4_quantize_batch, nvfp4_kv_append,
-nvfp4_kv_decode_attention, ais_mixing, aqn_sigma, rmsnorm_aqn, rmsnorm_aqn_quantize, nvfp4_lora_linear,
+nvfp4_kv_decode_attention, ais_mixing, token_logprobs, token_logprobs_backward, topk_distill,
+topk_distill_backward, aqn_sigma, rmsnorm_aqn, rmsnorm_aqn_quantize, nvfp4_lora_linear,
 nvfp4_lora_linear_w4a4.
 """
 from __future__ import annotations
@@ -24,6 +25,7 @@ LIB_PATH = _build.LIB
 
 OK = 0
 BF16, F32 = 0, 1
+DISTILL_NORMALIZED, DISTILL_TAIL = 0, 1
 (OP_QUANTIZE, OP_LINEAR_W4A16, OP_LINEAR_W4A4, OP_QUANTIZE_BATCH, OP_RMSNORM_QUANTIZE, OP_AIS, OP_KV_ATTENTION,
  OP_LINEAR_W4A4_QUANTIZED) = (0, 1, 2, 3, 4, 5, 6, 7)
 
@@ -47,6 +49,10 @@ def _signatures():
         "nvfp4_kv_decode_attention": (c.c_int, [p, p, p, p, p, p, p, p, i64, i64, i64, i64, i64, c.c_float, p, p,
                                                  sz, p]),
         "ais_mixing": (c.c_int, [p, p, p, i64, c.c_float, c.c_float, c.c_float, c.c_float, p, p, p, sz, p]),
+        "token_logprobs": (c.c_int, [p, i32, i64, i64, i64, p, f32, i32, p, p, p, p, p, p]),
+        "token_logprobs_backward": (c.c_int, [p, i32, i64, i64, i64, p, f32, p, p, p, p, p, i64, p]),
+        "topk_distill": (c.c_int, [p, i32, i64, i64, i64, f32, p, p, i32, i32, p, p, p, p]),
+        "topk_distill_backward": (c.c_int, [p, i32, i64, i64, i64, f32, p, p, i32, i32, p, p, p, p, i64, p]),
         "nvfp4_quantize_batch": (c.c_int, [i32, p, p, p, i32, p, p, p, p, sz, p]),
         "aqn_sigma": (f64, [f64, f64, i64, i64]),
         "rmsnorm_aqn": (c.c_int, [p, i64, i64, p, p, f32, f32, p, p]),
@@ -260,6 +266,146 @@ def ais_mixing(logp_rollout, logp_train, adv, C: float, delta: float, gamma: flo
                           workspace.numel() * workspace.element_size(), _stream(logp_rollout, stream))
     _check(st, "ais_mixing")
     return stats, (w_out if weights else None)
+
+
+def _logit_rows(x, what="logits"):
+    """dtype code, M, V and row stride of a 2-D bf16 or fp32 CUDA tensor whose columns are contiguous."""
+    import torch
+    dt = BF16 if x.dtype == torch.bfloat16 else F32 if x.dtype == torch.float32 else None
+    if dt is None:
+        raise TypeError(f"{what} must be bf16 or fp32")
+    if x.dim() != 2:
+        raise ValueError(f"{what} must be 2-D")
+    M, V = x.shape
+    ld = max(x.stride(0), V) if M <= 1 else x.stride(0)
+    if (V > 1 and x.stride(1) != 1) or ld < V:
+        raise ValueError(f"{what}: the columns of a row must be contiguous, and rows must not overlap")
+    return dt, M, V, ld
+
+
+def _row_array(t, name, dtype, shape, device):
+    """Checks one per-row argument (None passes): contiguous, of this dtype and shape, on the logits' device."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+
+
+def _on_device(t):
+    """The library launches on the current device: make it the tensor's."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy: bool = True, logp=None, h=None,
+                   lse=None, top_ids=None, top_logp=None, stream=None):
+    """Log-probs of tokens (int32 [M]) under softmax(scale * logits) (bf16 or fp32 [M, V], rows may be strided),
+    each row's entropy and log-sum-exp, and its k largest logits -> (logp, entropy, lse fp32 [M], top_ids
+    int32 [M, k], top_logp fp32 [M, k]); None where tokens is None, entropy is False or k is 0. Rows whose
+    token is outside [0, V) are ignored (0, and ids -1)."""
+    import torch
+    _require_cuda(logits, tokens, logp, h, lse, top_ids, top_logp)
+    dt, M, V, ld = _logit_rows(logits)
+    dev, f32 = logits.device, torch.float32
+    if tokens is None and logp is not None:
+        raise ValueError("logp needs tokens")
+    logp = _empty((M,), f32, dev) if logp is None and tokens is not None else logp
+    h = _empty((M,), f32, dev) if h is None and entropy else h if entropy else None
+    lse = _empty((M,), f32, dev) if lse is None else lse
+    if k > 0:
+        top_ids = _empty((M, k), torch.int32, dev) if top_ids is None else top_ids
+        top_logp = _empty((M, k), f32, dev) if top_logp is None else top_logp
+    else:
+        top_ids = top_logp = None
+    _row_array(tokens, "tokens", torch.int32, (M,), dev)
+    _row_array(logp, "logp", f32, (M,), dev)
+    _row_array(h, "h", f32, (M,), dev)
+    _row_array(lse, "lse", f32, (M,), dev)
+    _row_array(top_ids, "top_ids", torch.int32, (M, k), dev)
+    _row_array(top_logp, "top_logp", f32, (M, k), dev)
+    with _on_device(logits):
+        st = lib().token_logprobs(_ptr(logits), dt, M, V, ld, _ptr(tokens), float(scale), k, _ptr(logp), _ptr(h),
+                                  _ptr(lse), _ptr(top_ids), _ptr(top_logp), _stream(logits, stream))
+    _check(st, "token_logprobs")
+    return logp, h, lse, top_ids, top_logp
+
+
+def _dlogits(logits, out, M, V):
+    """The gradient's tensor (made when None) and its row stride."""
+    if out is None:
+        out = _empty((M, V), logits.dtype, logits.device)
+    if out.dtype != logits.dtype or tuple(out.shape) != (M, V) or out.device != logits.device:
+        raise ValueError("out must have the logits' dtype, shape and device")
+    return out, _logit_rows(out, "out")[3]
+
+
+def token_logprobs_backward(logits, tokens, lse, dlogp, scale: float = 1.0, entropy=None, dentropy=None, out=None,
+                            stream=None):
+    """Gradient of sum(dlogp * logp) + sum(dentropy * entropy) to the logits, lse and entropy as token_logprobs
+    gave them -> out [M, V] of the logits' dtype (may be the logits themselves: overwritten in place). dlogp or
+    dentropy may be None."""
+    import torch
+    _require_cuda(logits, tokens, lse, dlogp, entropy, dentropy, out)
+    dt, M, V, ld = _logit_rows(logits)
+    dev, f32 = logits.device, torch.float32
+    out, ldd = _dlogits(logits, out, M, V)
+    _row_array(tokens, "tokens", torch.int32, (M,), dev)
+    for t, name in ((lse, "lse"), (dlogp, "dlogp"), (entropy, "entropy"), (dentropy, "dentropy")):
+        _row_array(t, name, f32, (M,), dev)
+    with _on_device(logits):
+        st = lib().token_logprobs_backward(_ptr(logits), dt, M, V, ld, _ptr(tokens), float(scale), _ptr(lse),
+                                           _ptr(entropy), _ptr(dlogp), _ptr(dentropy), _ptr(out), ldd,
+                                           _stream(logits, stream))
+    _check(st, "token_logprobs_backward")
+    return out
+
+
+def topk_distill(logits, ids, teacher_logp, scale: float = 1.0, tail: bool = False, loss=None, lse=None,
+                 lse_tail=None, stream=None):
+    """Divergence of softmax(scale * logits) from a teacher's listed log-probs (ids int32 [M, k], teacher_logp
+    fp32 [M, k]; ids outside [0, V) are skipped) -> (loss, lse, lse_tail fp32 [M]). The teacher is normalised
+    over its list, or with tail=True everything unlisted is one more outcome (lse_tail is None without it)."""
+    import torch
+    _require_cuda(logits, ids, teacher_logp, loss, lse, lse_tail)
+    dt, M, V, ld = _logit_rows(logits)
+    dev, f32 = logits.device, torch.float32
+    k = ids.shape[1] if ids.dim() == 2 else 0
+    loss = _empty((M,), f32, dev) if loss is None else loss
+    lse = _empty((M,), f32, dev) if lse is None else lse
+    lse_tail = None if not tail else _empty((M,), f32, dev) if lse_tail is None else lse_tail
+    _row_array(ids, "ids", torch.int32, (M, k), dev)
+    _row_array(teacher_logp, "teacher_logp", f32, (M, k), dev)
+    for t, name in ((loss, "loss"), (lse, "lse"), (lse_tail, "lse_tail")):
+        _row_array(t, name, f32, (M,), dev)
+    with _on_device(logits):
+        st = lib().topk_distill(_ptr(logits), dt, M, V, ld, float(scale), _ptr(ids), _ptr(teacher_logp), k,
+                                DISTILL_TAIL if tail else DISTILL_NORMALIZED, _ptr(loss), _ptr(lse), _ptr(lse_tail),
+                                _stream(logits, stream))
+    _check(st, "topk_distill")
+    return loss, lse, lse_tail
+
+
+def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 1.0, tail: bool = False,
+                          lse_tail=None, out=None, stream=None):
+    """Gradient of sum(dloss * loss) to the logits, lse and lse_tail as topk_distill gave them -> out [M, V] of
+    the logits' dtype (may be the logits themselves: overwritten in place)."""
+    import torch
+    _require_cuda(logits, ids, teacher_logp, lse, dloss, lse_tail, out)
+    dt, M, V, ld = _logit_rows(logits)
+    dev, f32 = logits.device, torch.float32
+    k = ids.shape[1] if ids.dim() == 2 else 0
+    out, ldd = _dlogits(logits, out, M, V)
+    _row_array(ids, "ids", torch.int32, (M, k), dev)
+    _row_array(teacher_logp, "teacher_logp", f32, (M, k), dev)
+    for t, name in ((lse, "lse"), (dloss, "dloss"), (lse_tail, "lse_tail")):
+        _row_array(t, name, f32, (M,), dev)
+    with _on_device(logits):
+        st = lib().topk_distill_backward(_ptr(logits), dt, M, V, ld, float(scale), _ptr(ids), _ptr(teacher_logp), k,
+                                         DISTILL_TAIL if tail else DISTILL_NORMALIZED, _ptr(lse), _ptr(lse_tail),
+                                         _ptr(dloss), _ptr(out), ldd, _stream(logits, stream))
+    _check(st, "topk_distill_backward")
+    return out
 
 
 def nvfp4_quantize_batch(xs, codes=None, scales=None, g=None, workspace=None, stream=None):

@@ -3,10 +3,12 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
 #include "common.cuh"
+#include "logits.cuh"
 #include "sm100.cuh"
 
 namespace nvfp4rl {
@@ -191,6 +193,63 @@ nvfp4rl_status linear_common(bool w4a4, const uint16_t* x, int64_t M, int64_t K,
   return launch_linear(a, ws, ws_bytes, dev, static_cast<cudaStream_t>(stream));
 }
 
+// What the logits operators share: sizes, scale, the logits' alignment. *bytes: the span of the
+// rows from the first logit to the last. `skip`: nothing to do (M == 0).
+nvfp4rl_status check_logits(const void* x, int32_t dtype, int64_t M, int64_t V, int64_t ld, float scale, bool* skip,
+                            size_t* bytes) {
+  *skip = false;
+  if (dtype != NVFP4RL_BF16 && dtype != NVFP4RL_F32) return NVFP4RL_ERR_INVALID_ARG;
+  if (M < 0 || V <= 0 || ld < V) return NVFP4RL_ERR_INVALID_ARG;
+  if (!(scale >= 0x1p-20f && scale <= 0x1p20f)) return NVFP4RL_ERR_INVALID_ARG;
+  if (V > (int64_t(1) << 30) || M > 2147483647LL || ld > (int64_t(1) << 48)) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) {
+    *skip = true;
+    return NVFP4RL_OK;
+  }
+  if (ld > (int64_t(1) << 48) / M) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (!x) return NVFP4RL_ERR_INVALID_ARG;
+  const size_t esz = dtype == NVFP4RL_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(x) % esz) return NVFP4RL_ERR_MISALIGNED;
+  *bytes = (static_cast<size_t>(M - 1) * ld + V) * esz;
+  return NVFP4RL_OK;
+}
+
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+// Per-row arrays: 4-byte aligned, and no output over an input or another output (NULL: not there).
+template <int kOuts, int kIns>
+nvfp4rl_status check_spans(const Span (&outs)[kOuts], const Span (&ins)[kIns]) {
+  for (int i = 0; i < kOuts; ++i) {
+    if (!outs[i].p) continue;
+    for (int j = 0; j < kIns; ++j)
+      if (ins[j].p && overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return NVFP4RL_ERR_ALIAS;
+    for (int j = i + 1; j < kOuts; ++j)
+      if (outs[j].p && overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return NVFP4RL_ERR_ALIAS;
+  }
+  return NVFP4RL_OK;
+}
+
+bool aligned4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return false;
+  return true;
+}
+
+// A gradient's rows: their alignment and stride, and their place: over the logits exactly, or apart.
+nvfp4rl_status check_dlogits(const void* x, int64_t ld, size_t xbytes, const void* dx, int64_t ldd, int32_t dtype,
+                             int64_t M, int64_t V, size_t* bytes) {
+  if (!dx || ldd < V) return NVFP4RL_ERR_INVALID_ARG;
+  if (ldd > (int64_t(1) << 48) / M) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  const size_t esz = dtype == NVFP4RL_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(dx) % esz) return NVFP4RL_ERR_MISALIGNED;
+  *bytes = (static_cast<size_t>(M - 1) * ldd + V) * esz;
+  if (!(dx == x && ldd == ld) && overlap(dx, *bytes, x, xbytes)) return NVFP4RL_ERR_ALIAS;
+  return NVFP4RL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -278,6 +337,153 @@ nvfp4rl_status ais_mixing(const float* lr, const float* lt, const float* adv, in
   if (st != NVFP4RL_OK) return st;
   return launch_ais(lr, lt, adv, n, C, delta, gamma, beta, w_out, stats, workspace, dev,
                     static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status token_logprobs(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
+                              const int32_t* tokens, float scale, int32_t k, float* logp, float* entropy, float* lse,
+                              int32_t* top_ids, float* top_logp, void* stream) {
+  bool skip;
+  size_t xb;
+  nvfp4rl_status st = check_logits(logits, dtype, M, V, ld, scale, &skip, &xb);
+  if (st != NVFP4RL_OK) return st;
+  if (k < 0 || k > V) return NVFP4RL_ERR_INVALID_ARG;
+  if (k > kMaxListed) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (skip) return NVFP4RL_OK;
+  if (k == 0) {
+    top_ids = nullptr;
+    top_logp = nullptr;
+  }
+  if ((logp && !tokens) || (k > 0 && (!top_ids || !top_logp)) || (!logp && !entropy && !lse && k == 0))
+    return NVFP4RL_ERR_INVALID_ARG;
+  if (!aligned4({tokens, logp, entropy, lse, top_ids, top_logp})) return NVFP4RL_ERR_MISALIGNED;
+  const size_t mb = static_cast<size_t>(M) * 4, kb = mb * static_cast<size_t>(k);
+  const Span outs[5] = {{logp, mb}, {entropy, mb}, {lse, mb}, {top_ids, kb}, {top_logp, kb}};
+  const Span ins[2] = {{logits, xb}, {tokens, mb}};
+  if ((st = check_spans(outs, ins)) != NVFP4RL_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  LogitsArgs a{};
+  a.x = logits;
+  a.M = M;
+  a.V = V;
+  a.ld = ld;
+  a.scale = scale;
+  a.tokens = tokens;
+  a.k = k;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  return launch_logprobs(a, dtype, dev, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status token_logprobs_backward(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
+                                       const int32_t* tokens, float scale, const float* lse, const float* entropy,
+                                       const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
+                                       void* stream) {
+  bool skip;
+  size_t xb, db;
+  nvfp4rl_status st = check_logits(logits, dtype, M, V, ld, scale, &skip, &xb);
+  if (st != NVFP4RL_OK || skip) return st;
+  if (!lse || (!dlogp && !dentropy) || (dlogp && !tokens) || (dentropy && !entropy)) return NVFP4RL_ERR_INVALID_ARG;
+  if (!aligned4({tokens, lse, entropy, dlogp, dentropy})) return NVFP4RL_ERR_MISALIGNED;
+  if ((st = check_dlogits(logits, ld, xb, dlogits, ldd, dtype, M, V, &db)) != NVFP4RL_OK) return st;
+  const size_t mb = static_cast<size_t>(M) * 4;
+  const Span outs[1] = {{dlogits, db}};
+  const Span ins[5] = {{tokens, mb}, {lse, mb}, {entropy, mb}, {dlogp, mb}, {dentropy, mb}};
+  if ((st = check_spans(outs, ins)) != NVFP4RL_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  LogitsGradArgs a{};
+  a.x = logits;
+  a.M = M;
+  a.V = V;
+  a.ld = ld;
+  a.scale = scale;
+  a.tokens = tokens;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.dlogp = dlogp;
+  a.dentropy = dentropy;
+  a.dx = dlogits;
+  a.ldd = ldd;
+  return launch_logprobs_grad(a, dtype, dev, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status topk_distill(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld, float scale,
+                            const int32_t* ids, const float* teacher_logp, int32_t k, int32_t mode, float* loss,
+                            float* lse, float* lse_tail, void* stream) {
+  bool skip;
+  size_t xb;
+  nvfp4rl_status st = check_logits(logits, dtype, M, V, ld, scale, &skip, &xb);
+  if (st != NVFP4RL_OK) return st;
+  if (k < 1 || (mode != NVFP4RL_DISTILL_NORMALIZED && mode != NVFP4RL_DISTILL_TAIL)) return NVFP4RL_ERR_INVALID_ARG;
+  if (k > kMaxListed) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (skip) return NVFP4RL_OK;
+  if (mode != NVFP4RL_DISTILL_TAIL) lse_tail = nullptr;
+  if (!ids || !teacher_logp || !loss) return NVFP4RL_ERR_INVALID_ARG;
+  if (!aligned4({ids, teacher_logp, loss, lse, lse_tail})) return NVFP4RL_ERR_MISALIGNED;
+  const size_t mb = static_cast<size_t>(M) * 4, kb = mb * static_cast<size_t>(k);
+  const Span outs[3] = {{loss, mb}, {lse, mb}, {lse_tail, mb}};
+  const Span ins[3] = {{logits, xb}, {ids, kb}, {teacher_logp, kb}};
+  if ((st = check_spans(outs, ins)) != NVFP4RL_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  LogitsArgs a{};
+  a.x = logits;
+  a.M = M;
+  a.V = V;
+  a.ld = ld;
+  a.scale = scale;
+  a.k = k;
+  a.ids = ids;
+  a.teacher = teacher_logp;
+  a.tail = mode == NVFP4RL_DISTILL_TAIL;
+  a.loss = loss;
+  a.lse = lse;
+  a.lse_tail = lse_tail;
+  return launch_logprobs(a, dtype, dev, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status topk_distill_backward(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld, float scale,
+                                     const int32_t* ids, const float* teacher_logp, int32_t k, int32_t mode,
+                                     const float* lse, const float* lse_tail, const float* dloss, void* dlogits,
+                                     int64_t ldd, void* stream) {
+  bool skip;
+  size_t xb, db;
+  nvfp4rl_status st = check_logits(logits, dtype, M, V, ld, scale, &skip, &xb);
+  if (st != NVFP4RL_OK) return st;
+  if (k < 1 || (mode != NVFP4RL_DISTILL_NORMALIZED && mode != NVFP4RL_DISTILL_TAIL)) return NVFP4RL_ERR_INVALID_ARG;
+  if (k > kMaxListed) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (skip) return NVFP4RL_OK;
+  const bool tail = mode == NVFP4RL_DISTILL_TAIL;
+  if (!tail) lse_tail = nullptr;
+  if (!ids || !teacher_logp || !lse || !dloss || (tail && !lse_tail)) return NVFP4RL_ERR_INVALID_ARG;
+  if (!aligned4({ids, teacher_logp, lse, lse_tail, dloss})) return NVFP4RL_ERR_MISALIGNED;
+  if ((st = check_dlogits(logits, ld, xb, dlogits, ldd, dtype, M, V, &db)) != NVFP4RL_OK) return st;
+  const size_t mb = static_cast<size_t>(M) * 4, kb = mb * static_cast<size_t>(k);
+  const Span outs[1] = {{dlogits, db}};
+  const Span ins[5] = {{ids, kb}, {teacher_logp, kb}, {lse, mb}, {lse_tail, mb}, {dloss, mb}};
+  if ((st = check_spans(outs, ins)) != NVFP4RL_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  LogitsGradArgs a{};
+  a.x = logits;
+  a.M = M;
+  a.V = V;
+  a.ld = ld;
+  a.scale = scale;
+  a.lse = lse;
+  a.ids = ids;
+  a.teacher = teacher_logp;
+  a.k = k;
+  a.tail = tail;
+  a.lse_tail = lse_tail;
+  a.dloss = dloss;
+  a.dx = dlogits;
+  a.ldd = ldd;
+  return launch_logprobs_grad(a, dtype, dev, static_cast<cudaStream_t>(stream));
 }
 
 nvfp4rl_status nvfp4_kv_append(const uint16_t* k, const uint16_t* v, int64_t B, int64_t Hkv, int64_t D,

@@ -1,0 +1,129 @@
+// Shared pieces of the logits operators (logprobs.cu, logprobs_grad.cu).
+#pragma once
+
+#include "common.cuh"
+
+namespace nvfp4rl {
+
+// A logit at or below -2^100 is masked (p = 0); one above 2^100 (or NaN) spoils its row. With scale
+// within [2^-20, 2^20] every product scale * log2(e) * x of the others stays finite.
+constexpr float kLogitBound = 1.2676506002282294e30f;  // 2^100
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxListed = 256;  // alternatives or listed teacher columns per row
+
+// 2^x (ex2.approx: about 2 ulp; results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float logit(const uint16_t* x, int64_t i) {
+  return __uint_as_float(static_cast<uint32_t>(x[i]) << 16);
+}
+__device__ __forceinline__ float logit(const float* x, int64_t i) { return x[i]; }
+__device__ __forceinline__ void store_logit(uint16_t* y, int64_t i, float v) {
+  y[i] = static_cast<uint16_t>(f32_to_bf16_bits(v));
+}
+__device__ __forceinline__ void store_logit(float* y, int64_t i, float v) { y[i] = v; }
+
+struct LogitsArgs {
+  const void* x;
+  int64_t M, V, ld;
+  float scale;
+  // log-probs
+  const int32_t* tokens;
+  int k;
+  float *logp, *entropy, *lse;
+  int32_t* top_ids;
+  float* top_logp;
+  // distillation: k listed columns per row
+  const int32_t* ids;
+  const float* teacher;
+  bool tail;
+  float *loss, *lse_tail;
+};
+
+struct LogitsGradArgs {
+  const void* x;
+  int64_t M, V, ld;
+  float scale;
+  const int32_t* tokens;
+  const float *lse, *entropy, *dlogp, *dentropy;
+  const int32_t* ids;
+  const float* teacher;
+  int k;
+  bool tail;
+  const float *lse_tail, *dloss;
+  void* dx;
+  int64_t ldd;
+};
+
+nvfp4rl_status launch_logprobs(const LogitsArgs& a, int dtype, const DeviceInfo& dev, cudaStream_t st);
+nvfp4rl_status launch_logprobs_grad(const LogitsGradArgs& a, int dtype, const DeviceInfo& dev, cudaStream_t st);
+
+// A teacher's row, held by one warp: entries lane, lane + 32, ... of ids/teacher. q and ln q of each
+// entry, the bucket's mass and Q = sum q + q_0. `any`: an entry counts.
+struct TeacherRow {
+  float q0, mass;
+  bool any;
+};
+
+// ids_s, q_s, lq_s [k]: the entries' columns (-1: skipped), q and ln q. One whole warp calls.
+// 1 - sum q would lose the digits of a small rest in 32 bits: the largest q enters as -expm1(l).
+__device__ __forceinline__ TeacherRow teacher_row(const int32_t* ids, const float* teacher, int k, int64_t V, bool tail,
+                                                  int32_t* ids_s, float* q_s, float* lq_s) {
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY;
+  int counted = 0;
+  bool nan = false;
+  for (int i = lane; i < k; i += 32) {
+    const int32_t id = ids[i];
+    const bool valid = id >= 0 && id < V;
+    const float l = valid ? teacher[i] : -INFINITY;
+    ids_s[i] = valid ? id : -1;
+    lq_s[i] = l;
+    counted += valid;
+    nan |= l != l;
+    top = fmaxf(top, l);
+  }
+  top = warp_max(top);
+  counted = __reduce_add_sync(0xFFFFFFFFu, counted);
+  nan = __any_sync(0xFFFFFFFFu, nan);
+  TeacherRow r{0.0f, 0.0f, counted > 0 && (tail || nan || top != -INFINITY)};
+  if (!r.any) return r;
+  if (!tail) {
+    float total = 0.0f;
+    for (int i = lane; i < k; i += 32) {
+      const float e = lq_s[i] == -INFINITY ? 0.0f : expf(lq_s[i] - top);
+      q_s[i] = e;
+      total += e;
+    }
+    total = warp_sum(total);
+    const float ln_total = logf(total);
+    for (int i = lane; i < k; i += 32) {
+      q_s[i] /= total;
+      lq_s[i] = lq_s[i] - top - ln_total;
+    }
+    r.mass = nan ? NAN : 1.0f;
+    return r;
+  }
+  int first = kMaxListed;  // the entry that holds the largest l
+  for (int i = lane; i < k; i += 32)
+    if (lq_s[i] == top && ids_s[i] >= 0) first = min(first, i);
+  first = __reduce_min_sync(0xFFFFFFFFu, first);
+  float others = 0.0f;
+  for (int i = lane; i < k; i += 32) {
+    const float q = ids_s[i] < 0 ? 0.0f : expf(lq_s[i]);
+    q_s[i] = q;
+    if (i != first) others += q;
+  }
+  others = warp_sum(others);
+  const float rest = -expm1f(top) - others;
+  r.q0 = rest < 0.0f ? 0.0f : rest;
+  r.mass = (expf(top) + others) + r.q0;
+  return r;
+}
+
+}  // namespace nvfp4rl

@@ -61,6 +61,10 @@ def _declare(lib):
         "oracle_quantize_cached_rows": (None, [p, i, i64, i64, i64, f, p, p, p]),
         "oracle_ais": (None, [i64, p, p, p, d, d, d, d, p, p]),
         "oracle_attention_decode": (None, [p, p, p, f, p, p, f, p, i64, i64, i64, i64, i64, d, p]),
+        "oracle_token_logprobs_rows": (None, [p, i, i64, i64, i64, i64, p, d, i32, p, p, p, p, p]),
+        "oracle_token_logprobs_grad_rows": (None, [p, i, i64, i64, i64, i64, p, d, p, p, p]),
+        "oracle_topk_distill_rows": (None, [p, i, i64, i64, i64, i64, d, p, p, i32, i, p, p, p]),
+        "oracle_topk_distill_grad_rows": (None, [p, i, i64, i64, i64, i64, d, p, p, i32, i, p, p]),
         "oracle_aqn_sigma": (d, [d, d, i64, i64]),
         "oracle_rmsnorm_aqn_rows": (None, [p, i64, i64, i64, p, p, f, f, p]),
         "oracle_lora_down": (None, [p, i64, i64, p, i32, p]),
@@ -262,6 +266,79 @@ def attention_decode(q_bits, k_codes, k_scales, gk, v_codes, v_scales, gv, lens,
                                   b1 - b0, Hq, Hkv, D, Lmax, float(scale), _ptr(out[b0:b1]))
     _parallel(part, B)
     return out
+
+
+def _logits(x):
+    """Logits [M, ld] as bf16 bits (uint16) or fp32, with their dtype code."""
+    x = np.ascontiguousarray(x)
+    assert x.ndim == 2 and x.dtype in (np.uint16, np.float32)
+    return x, BF16 if x.dtype == np.uint16 else F32
+
+
+def _i32(a):
+    return None if a is None else np.ascontiguousarray(a, dtype=np.int32)
+
+
+def _f32(a):
+    return None if a is None else np.ascontiguousarray(a, dtype=np.float32)
+
+
+def token_logprobs(x, tokens, scale, k=0, V=None, L=None):
+    """Token log-probs, entropy, log-sum-exp (float64 [M]) and the k top alternatives (ids int32, log-probs
+    float64 [M, k]) of logits x [M, ld], columns [0, V)."""
+    L = L or lib()
+    x, dt = _logits(x)
+    M, ld = x.shape
+    V = V or ld
+    tokens = _i32(tokens)
+    logp, h, lse = np.zeros(M), np.zeros(M), np.zeros(M)
+    ids, top = np.zeros((M, k), np.int32), np.zeros((M, k))
+    _parallel(lambda a, b: L.oracle_token_logprobs_rows(_ptr(x), dt, V, ld, a, b, _ptr(tokens),
+                                                        float(np.float32(scale)), k, _ptr(logp), _ptr(h), _ptr(lse),
+                                                        _ptr(ids), _ptr(top)), M)
+    return logp, h, lse, ids, top
+
+
+def token_logprobs_grad(x, tokens, scale, dlogp=None, dentropy=None, V=None, L=None):
+    """Gradient of sum(dlogp logp) + sum(dentropy entropy) to the logits, float64 [M, V]."""
+    L = L or lib()
+    x, dt = _logits(x)
+    M, ld = x.shape
+    V = V or ld
+    tokens, dlogp, dentropy = _i32(tokens), _f32(dlogp), _f32(dentropy)
+    dx = np.zeros((M, V))
+    _parallel(lambda a, b: L.oracle_token_logprobs_grad_rows(_ptr(x), dt, V, ld, a, b, _ptr(tokens),
+                                                             float(np.float32(scale)), _ptr(dlogp), _ptr(dentropy),
+                                                             _ptr(dx)), M)
+    return dx
+
+
+def topk_distill(x, ids, teacher_logp, scale, tail, V=None, L=None):
+    """Distillation loss, log-sum-exp over the row and over its unlisted columns, float64 [M]."""
+    L = L or lib()
+    x, dt = _logits(x)
+    M, ld = x.shape
+    V = V or ld
+    ids, teacher = _i32(ids), _f32(teacher_logp)
+    loss, lse, rest = np.zeros(M), np.zeros(M), np.zeros(M)
+    _parallel(lambda a, b: L.oracle_topk_distill_rows(_ptr(x), dt, V, ld, a, b, float(np.float32(scale)), _ptr(ids),
+                                                      _ptr(teacher), ids.shape[1], int(tail), _ptr(loss), _ptr(lse),
+                                                      _ptr(rest)), M)
+    return loss, lse, rest
+
+
+def topk_distill_grad(x, ids, teacher_logp, scale, tail, dloss, V=None, L=None):
+    """Gradient of sum(dloss loss) to the logits, float64 [M, V]."""
+    L = L or lib()
+    x, dt = _logits(x)
+    M, ld = x.shape
+    V = V or ld
+    ids, teacher, dloss = _i32(ids), _f32(teacher_logp), _f32(dloss)
+    dx = np.zeros((M, V))
+    _parallel(lambda a, b: L.oracle_topk_distill_grad_rows(_ptr(x), dt, V, ld, a, b, float(np.float32(scale)),
+                                                           _ptr(ids), _ptr(teacher), ids.shape[1], int(tail),
+                                                           _ptr(dloss), _ptr(dx)), M)
+    return dx
 
 
 AIS_STATS = ("alpha", "alpha_ess", "alpha_mis", "alpha_var", "dbar", "cv2", "dsigma", "mean_w")

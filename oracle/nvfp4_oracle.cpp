@@ -347,6 +347,213 @@ void oracle_ais(int64_t n, const float* logp_rollout, const float* logp_train, c
     for (int64_t i = 0; i < n; ++i) w_out[i] = 1.0 + alpha * (w[i] - 1.0);
 }
 
+// ---- logits: token log-probs, entropy, top alternatives, top-k distillation -----------------------
+//
+// z_j = scale x_j; x_j <= -2^100 is masked (p_j = 0); a NaN or x_j > 2^100 spoils the row. Two passes
+// per row: the maximum, then the sums.
+
+}  // extern "C"
+
+namespace {
+
+struct LogitsRow {
+  bool bad = false;       // NaN, or a logit above 2^100
+  double lse = -INFINITY;  // top + ln_s; -inf: every column masked
+  double top = 0.0, ln_s = 0.0;
+  std::vector<double> z;   // -inf where masked
+};
+
+LogitsRow logits_row(const void* x, int dtype, int64_t V, int64_t first, double scale) {
+  const double bound = std::ldexp(1.0, 100);
+  LogitsRow r;
+  r.z.resize(V);
+  double top = -INFINITY;
+  for (int64_t j = 0; j < V; ++j) {
+    const double v = load_elem(x, dtype, first + j);
+    if (std::isnan(v) || v > bound) r.bad = true;
+    r.z[j] = v <= -bound ? -INFINITY : scale * v;
+    if (r.z[j] > top) top = r.z[j];
+  }
+  if (r.bad) {
+    r.lse = NAN;
+  } else if (top > -INFINITY) {
+    double s = 0.0;
+    for (int64_t j = 0; j < V; ++j) s += std::exp(r.z[j] - top);
+    r.top = top;
+    r.ln_s = std::log(s);
+    r.lse = top + r.ln_s;
+  }
+  return r;
+}
+
+// (z - top) - ln s: z - lse would lose everything beside a large common offset.
+double log_p(const LogitsRow& r, int64_t j) { return r.z[j] == -INFINITY ? -INFINITY : (r.z[j] - r.top) - r.ln_s; }
+
+double row_entropy(const LogitsRow& r) {
+  if (r.bad) return NAN;
+  double h = 0.0;
+  for (size_t j = 0; j < r.z.size(); ++j)
+    if (r.z[j] != -INFINITY) h -= std::exp(log_p(r, j)) * log_p(r, j);
+  return h;
+}
+
+// A teacher's row: q summed per listed column, the terms of the loss, the bucket.
+struct Teacher {
+  bool counts = false;
+  std::vector<int64_t> col;
+  std::vector<double> q, lq;
+  double q0 = 0.0;
+};
+
+Teacher teacher_of(const int32_t* ids, const float* l, int32_t k, int64_t V, bool tail) {
+  Teacher t;
+  double top = -INFINITY, total = 0.0;
+  for (int32_t i = 0; i < k; ++i)
+    if (ids[i] >= 0 && ids[i] < V) {
+      t.col.push_back(ids[i]);
+      t.lq.push_back(l[i]);
+      if (!(l[i] <= top)) top = l[i];
+    }
+  t.counts = !t.col.empty() && (tail || top != -INFINITY);
+  if (!t.counts) return t;
+  if (!tail) {
+    for (double v : t.lq) total += std::exp(v - top);
+    for (double& v : t.lq) v -= top + std::log(total);
+  }
+  double sum = 0.0;
+  for (double v : t.lq) {
+    t.q.push_back(std::exp(v));
+    sum += t.q.back();
+  }
+  if (tail && !(sum >= 1.0)) t.q0 = 1.0 - sum;
+  return t;
+}
+
+// ln sum exp z over the columns that no entry lists.
+double lse_unlisted(const LogitsRow& r, const Teacher& t) {
+  if (r.bad) return NAN;
+  std::vector<char> in(r.z.size(), 0);
+  for (int64_t c : t.col) in[c] = 1;
+  double top = -INFINITY, s = 0.0;
+  for (size_t j = 0; j < r.z.size(); ++j)
+    if (!in[j] && r.z[j] > top) top = r.z[j];
+  if (top == -INFINITY) return top;
+  for (size_t j = 0; j < r.z.size(); ++j)
+    if (!in[j]) s += std::exp(r.z[j] - top);
+  return top + std::log(s);
+}
+
+}  // namespace
+
+extern "C" {
+
+// Rows [row0, row1). tokens may be null; a row whose token is outside [0, V) is ignored.
+void oracle_token_logprobs_rows(const void* x, int dtype, int64_t V, int64_t ld, int64_t row0, int64_t row1,
+                                const int32_t* tokens, double scale, int32_t k, double* logp, double* entropy,
+                                double* lse, int32_t* top_ids, double* top_logp) {
+  const double bound = std::ldexp(1.0, 100);
+  for (int64_t m = row0; m < row1; ++m) {
+    const bool ignored = tokens && (tokens[m] < 0 || tokens[m] >= V);
+    for (int32_t i = 0; i < k; ++i) {
+      top_ids[m * k + i] = -1;
+      top_logp[m * k + i] = -INFINITY;
+    }
+    logp[m] = entropy[m] = lse[m] = 0.0;
+    if (ignored) continue;
+    const LogitsRow r = logits_row(x, dtype, V, m * ld, scale);
+    lse[m] = r.lse;
+    entropy[m] = row_entropy(r);
+    if (tokens) logp[m] = r.bad ? NAN : log_p(r, tokens[m]);
+    if (r.bad) {
+      for (int32_t i = 0; i < k; ++i) top_logp[m * k + i] = NAN;
+      continue;
+    }
+    std::vector<char> taken(V, 0);
+    for (int32_t i = 0; i < k; ++i) {
+      int64_t best = -1;
+      for (int64_t j = 0; j < V; ++j) {
+        const double v = load_elem(x, dtype, m * ld + j);
+        if (taken[j] || v <= -bound) continue;
+        if (best < 0 || v > load_elem(x, dtype, m * ld + best)) best = j;
+      }
+      if (best < 0) break;
+      taken[best] = 1;
+      top_ids[m * k + i] = static_cast<int32_t>(best);
+      top_logp[m * k + i] = log_p(r, best);
+    }
+  }
+}
+
+// dx [rows][V] of sum dlogp logp + dentropy entropy (either may be null).
+void oracle_token_logprobs_grad_rows(const void* x, int dtype, int64_t V, int64_t ld, int64_t row0, int64_t row1,
+                                     const int32_t* tokens, double scale, const float* dlogp, const float* dentropy,
+                                     double* dx) {
+  for (int64_t m = row0; m < row1; ++m) {
+    double* d = dx + m * V;
+    const double dl = dlogp ? dlogp[m] : 0.0, dh = dentropy ? dentropy[m] : 0.0;
+    for (int64_t j = 0; j < V; ++j) d[j] = 0.0;
+    if ((tokens && (tokens[m] < 0 || tokens[m] >= V)) || (dl == 0.0 && dh == 0.0)) continue;
+    const LogitsRow r = logits_row(x, dtype, V, m * ld, scale);
+    if (r.lse == -INFINITY) continue;
+    const double h = row_entropy(r);
+    for (int64_t j = 0; j < V; ++j) {
+      if (r.bad) {
+        d[j] = NAN;
+        continue;
+      }
+      const double lp = log_p(r, j);
+      if (lp != -INFINITY) d[j] = -std::exp(lp) * (dl + dh * (lp + h));
+      if (dlogp && j == tokens[m]) d[j] += dl;
+      d[j] *= scale;
+    }
+  }
+}
+
+void oracle_topk_distill_rows(const void* x, int dtype, int64_t V, int64_t ld, int64_t row0, int64_t row1, double scale,
+                              const int32_t* ids, const float* teacher, int32_t k, int tail, double* loss, double* lse,
+                              double* lse_tail) {
+  for (int64_t m = row0; m < row1; ++m) {
+    loss[m] = lse[m] = lse_tail[m] = 0.0;
+    const Teacher t = teacher_of(ids + m * k, teacher + m * k, k, V, tail != 0);
+    if (!t.counts) continue;
+    const LogitsRow r = logits_row(x, dtype, V, m * ld, scale);
+    lse[m] = r.lse;
+    lse_tail[m] = lse_unlisted(r, t);
+    double sum = r.bad ? NAN : 0.0;
+    for (size_t i = 0; i < t.col.size(); ++i)
+      if (t.q[i] != 0.0) sum += t.q[i] * (t.lq[i] - log_p(r, t.col[i]));
+    if (tail && t.q0 > 0.0 && lse_tail[m] != -INFINITY) sum += t.q0 * (std::log(t.q0) - (lse_tail[m] - r.lse));
+    loss[m] = sum;
+  }
+}
+
+void oracle_topk_distill_grad_rows(const void* x, int dtype, int64_t V, int64_t ld, int64_t row0, int64_t row1,
+                                   double scale, const int32_t* ids, const float* teacher, int32_t k, int tail,
+                                   const float* dloss, double* dx) {
+  for (int64_t m = row0; m < row1; ++m) {
+    double* d = dx + m * V;
+    for (int64_t j = 0; j < V; ++j) d[j] = 0.0;
+    Teacher t = teacher_of(ids + m * k, teacher + m * k, k, V, tail != 0);
+    if (!t.counts || dloss[m] == 0.0f) continue;
+    const LogitsRow r = logits_row(x, dtype, V, m * ld, scale);
+    if (r.lse == -INFINITY) continue;
+    const double rest = lse_unlisted(r, t);
+    if (rest == -INFINITY) t.q0 = 0.0;
+    std::vector<double> listed(V, -1.0);
+    double mass = t.q0;
+    for (size_t i = 0; i < t.col.size(); ++i) {
+      mass += t.q[i];
+      listed[t.col[i]] = std::max(listed[t.col[i]], 0.0);
+      listed[t.col[i]] += t.q[i];
+    }
+    for (int64_t j = 0; j < V; ++j) {
+      const double p = r.bad ? NAN : r.z[j] == -INFINITY ? 0.0 : std::exp(r.z[j] - r.lse);
+      const double share = r.bad ? NAN : t.q0 == 0.0 || r.z[j] == -INFINITY ? 0.0 : t.q0 * std::exp(r.z[j] - rest);
+      d[j] = (mass * p - (listed[j] >= 0.0 ? listed[j] : share)) * (scale * dloss[m]);
+    }
+  }
+}
+
 // AQN noise schedule: sigma_k = sigma0 * (sigmaK / sigma0)^(k / K).
 double oracle_aqn_sigma(double sigma0, double sigmaK, int64_t k, int64_t K) {
   return sigma0 * std::pow(sigmaK / sigma0, static_cast<double>(k) / static_cast<double>(K));
