@@ -28,6 +28,52 @@ __device__ __forceinline__ void store_logit(uint16_t* y, int64_t i, float v) {
 }
 __device__ __forceinline__ void store_logit(float* y, int64_t i, float v) { y[i] = v; }
 
+// Two fp32 values in one 64-bit register, for the packed fp32 instructions (one issue for two results).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// 16 bytes of logits, not kept in L1 (each is used once). An ordinary load: a gradient may lie over them.
+__device__ __forceinline__ uint4 ld_logits16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+// Logits per 16-byte vector, and the element of a vector at which the row at p starts.
+template <typename T>
+constexpr int kVecOf = 16 / static_cast<int>(sizeof(T));
+template <typename T>
+__device__ __forceinline__ int vec_phase(const T* p) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % kVecOf<T>);
+}
+
 struct LogitsArgs {
   const void* x;
   int64_t M, V, ld;

@@ -1,5 +1,16 @@
 // Gradients of the token log-probs, the entropy and the top-k distillation loss to the logits (sm_103a).
-// Elementwise given the forward call's lse; one CTA per row.
+//
+// Given the forward call's lse (and entropy, lse_tail) the gradient is elementwise: with t = log2 p_j = x c - R,
+// c = scale log2 e, R = lse log2 e,
+//   token log-prob and entropy:  dx_j = 2^t (alpha + beta t) [+ scale dlogp at the token],
+//     alpha = -scale (dlogp + dentropy H), beta = -scale dentropy ln 2;
+//   distillation, unlisted columns:  dx_j = alpha 2^t; NORMALIZED: alpha = scale dloss, R as above; TAIL: the factor
+//     Q - q_0 / p_0 would overflow for a small p_0, so alpha = scale dloss (Q p_0 - q_0) with R = lse_tail log2 e;
+//   listed columns:  dx_j = scale dloss (Q p_j - q_j), written over the above after a block barrier.
+// Bound by HBM: each logit is read once, each gradient written once. A CTA of 256 threads takes a chunk of one
+// row, 16-byte vectors aligned for the stores; where the row of logits starts at another element of a vector than the
+// row of gradients, a vector is put together from two aligned loads by funnel shifts (the second one hits L1/L2).
+// Vectors at a row's ends, whose 16 bytes are not all inside it, go element by element.
 #include "logits.cuh"
 
 namespace nvfp4rl {
@@ -7,93 +18,235 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T, bool kDistill>
-__global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradArgs a) {
-  __shared__ int32_t ids_s[kMaxListed];
-  __shared__ float q_s[kMaxListed], lq_s[kMaxListed];
+// The 8 (bf16) or 4 (fp32) logits that start s elements into the 32 bytes (a, b).
+template <typename T>
+__device__ __forceinline__ uint4 shift_vec(uint4 a, uint4 b, int s) {
+  const int words = sizeof(T) == 2 ? s >> 1 : s;  // uniform over the row
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (words & 1) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
+  }
+  if (words & 2) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  const uint32_t odd = sizeof(T) == 2 ? (s & 1) * 16 : 0;
+  return make_uint4(__funnelshift_r(w[0], w[1], odd), __funnelshift_r(w[1], w[2], odd),
+                    __funnelshift_r(w[2], w[3], odd), __funnelshift_r(w[3], w[4], odd));
+}
+
+struct RowCoef {
+  float c, R, alpha, beta;
+};
+
+template <bool kEntropy>
+__device__ __forceinline__ float grad1(float v, const RowCoef& r) {
+  // masked logits: t far below every exponent, 2^t = 0, and finite, as 0 beta t has to be 0
+  if (kEntropy) v = fmaxf(v, -kLogitBound);
+  const float t = fmaf(v, r.c, -r.R), e = exp2_approx(t);
+  return e * (kEntropy ? fmaf(r.beta, t, r.alpha) : r.alpha);
+}
+
+template <bool kEntropy>
+__device__ __forceinline__ F2 grad2(float lo, float hi, const RowCoef& r) {
+  if (kEntropy) {
+    lo = fmaxf(lo, -kLogitBound);
+    hi = fmaxf(hi, -kLogitBound);
+  }
+  const F2 t = fma2(pack2(lo, hi), pack2(r.c, r.c), pack2(-r.R, -r.R));
+  float t0, t1;
+  unpack2(t, t0, t1);
+  const F2 e = pack2(exp2_approx(t0), exp2_approx(t1));
+  return mul2(e, kEntropy ? fma2(pack2(r.beta, r.beta), t, pack2(r.alpha, r.alpha)) : pack2(r.alpha, r.alpha));
+}
+
+// The gradients of one vector; `hit` is added at element `at` (none: outside [0, VEC)).
+template <typename T, bool kEntropy>
+__device__ __forceinline__ uint4 grad_vec(uint4 x, const RowCoef& r, int at, float hit) {
+  constexpr int VEC = kVecOf<T>;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  float g[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) {
+    float lo, hi;
+    if (sizeof(T) == 2) {
+      lo = __uint_as_float(bf16_lo_bits(w[i]));
+      hi = __uint_as_float(bf16_hi_bits(w[i]));
+    } else {
+      lo = __uint_as_float(w[(2 * i) & 3]);
+      hi = __uint_as_float(w[(2 * i + 1) & 3]);
+    }
+    unpack2(grad2<kEntropy>(lo, hi, r), g[2 * i], g[2 * i + 1]);
+  }
+  if (static_cast<unsigned>(at) < static_cast<unsigned>(VEC)) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (i == at) g[i] += hit;
+  }
+  if (sizeof(T) == 2)
+    return make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4 % VEC], g[5 % VEC]),
+                      pack_bf16x2(g[6 % VEC], g[7 % VEC]));
+  return make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3]));
+}
+
+// kU: vectors per thread and step; kEntropy: the entropy term (token form only); kList: distillation;
+// kShift: rows of logits and gradients start at different elements of a vector (somewhere in the call).
+template <typename T, int kU, bool kEntropy, bool kList, bool kShift>
+__global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradArgs a, unsigned chunks, int steps) {
+  constexpr int VEC = kVecOf<T>;
+  __shared__ int32_t ids_s[kList ? kMaxListed : 1];
+  __shared__ float q_s[kList ? kMaxListed : 1], lq_s[kList ? kMaxListed : 1];
   __shared__ TeacherRow teacher_s;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t row = blockIdx.x;
+  const int64_t row = blockIdx.x / chunks;
+  // vectors and columns in 32 bits: V <= 2^30, and a chunk is longer than 2^17 vectors only where V < 2^20
+  const int V = static_cast<int>(a.V);
+  const int v_begin = static_cast<int>(blockIdx.x % chunks) * steps * (kU * kThreads);
   const T* x = static_cast<const T*>(a.x) + row * a.ld;
   T* dx = static_cast<T*>(a.dx) + row * a.ldd;
   const int tid = threadIdx.x;
-  const float c = a.scale * kLog2E;
+  const int out_phase = vec_phase(dx);
+  const int s = kShift ? (vec_phase(x) - out_phase) & (VEC - 1) : 0;
   const float lse = a.lse[row];
   bool dead = lse == -INFINITY;
-  int64_t token = -1;
-  // p_j (alpha + beta t_j), t_j = log2 p_j, and `hit` more at the token
-  float alpha = 0.0f, beta = 0.0f, hit = 0.0f, R = lse * kLog2E, mass = 0.0f;
-  if (kDistill) {
+  RowCoef r{a.scale * kLog2E, lse * kLog2E, 0.0f, 0.0f};
+  float hit = 0.0f, mass = 0.0f;
+  int token = -1;
+  // listed columns of this chunk: thread i holds entry i
+  int mine = -1;
+  float mine_x = 0.0f;
+  if (kList) {
     if (tid < 32) {
       const TeacherRow t = teacher_row(a.ids + row * a.k, a.teacher + row * a.k, a.k, a.V, a.tail, ids_s, q_s, lq_s);
       if (tid == 0) teacher_s = t;
     }
+    const float d = a.dloss[row];
     __syncthreads();
-    const float d = a.dloss[row] * a.scale;
-    dead |= !teacher_s.any || a.dloss[row] == 0.0f;
-    hit = d;
+    dead |= !teacher_s.any || d == 0.0f;
+    hit = d * a.scale;
     mass = teacher_s.mass;
-    alpha = mass * d;
+    r.alpha = mass * hit;
     if (a.tail) {
       const float rest = a.lse_tail[row];
       if (rest == -INFINITY) {
-        mass -= teacher_s.q0;
-        alpha = 0.0f;
+        mass -= teacher_s.q0;  // no bucket; the unlisted columns are masked
+        r.alpha = 0.0f;
       } else {
-        // (Q - q0 / p0) p = (Q p0 - q0) exp(z - lse_tail): nothing overflows for a tiny p0
-        alpha = (mass * expf(rest - lse) - teacher_s.q0) * d;
-        R = rest * kLog2E;
+        r.alpha = (mass * expf(rest - lse) - teacher_s.q0) * hit;
+        r.R = rest * kLog2E;
       }
     }
+    if (tid < a.k && !dead) {
+      mine = ids_s[tid];
+      const int v = (mine + out_phase) / VEC - v_begin;
+      if (mine >= 0 && v >= 0 && v < steps * (kU * kThreads))
+        mine_x = logit(x, mine);
+      else
+        mine = -1;
+    }
+    __syncthreads();  // the listed logits are read; a gradient in their place may be written
   } else {
+    const float dl = a.dlogp ? a.dlogp[row] : 0.0f, dh = kEntropy ? a.dentropy[row] : 0.0f;
     if (a.tokens) {
       token = a.tokens[row];
-      dead |= token < 0 || token >= a.V;
+      dead |= token < 0 || token >= V;
     }
-    const float dl = a.dlogp ? a.dlogp[row] : 0.0f, dh = a.dentropy ? a.dentropy[row] : 0.0f;
     dead |= dl == 0.0f && dh == 0.0f;
     hit = dl * a.scale;
-    alpha = -a.scale * (a.dentropy ? fmaf(dh, a.entropy[row], dl) : dl);
-    beta = -a.scale * dh * kLn2;
+    r.alpha = -a.scale * (kEntropy ? fmaf(dh, a.entropy[row], dl) : dl);
+    r.beta = -a.scale * dh * kLn2;
   }
-  for (int64_t j = tid; j < a.V; j += kThreads) {
-    float g = 0.0f;
-    if (!dead) {
-      const float v = fmaxf(logit(x, j), -kLogitBound);
-      const float t = fmaf(v, c, -R), e = v <= -kLogitBound ? 0.0f : exp2_approx(t);
-      g = e * fmaf(beta, t, alpha);
-      if (j == token) g += hit;
-      if (kDistill) {
-        float q = 0.0f;
-        bool in = false;
-        for (int i = 0; i < a.k; ++i)
-          if (ids_s[i] == j) {
-            q += q_s[i];
-            in = true;
-          }
-        if (in) g = hit * ((v <= -kLogitBound ? 0.0f : mass * exp2_approx(fmaf(v, c, -lse * kLog2E))) - q);
+  for (int step = 0; step < steps; ++step) {
+    const int v0 = v_begin + step * (kU * kThreads) + tid;
+    uint4 in[kU], in2[kShift ? kU : 1];
+    bool whole[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int col = (v0 + u * kThreads) * VEC - out_phase;
+      // every byte of the loads and of the store lies inside the row
+      whole[u] = kShift && s ? col >= s && col - s + 2 * VEC <= V : col >= 0 && col + VEC <= V;
+      if (whole[u] && !dead) {
+        in[u] = ld_logits16(x + col - s);
+        if (kShift && s) in2[u] = ld_logits16(x + col - s + VEC);
       }
-      if (lse != lse) g = NAN;
     }
-    store_logit(dx, j, g);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int col = (v0 + u * kThreads) * VEC - out_phase;
+      if (whole[u]) {
+        uint4 g = make_uint4(0, 0, 0, 0);
+        if (!dead) {
+          const uint4 xin = kShift && s ? shift_vec<T>(in[u], in2[kShift ? u : 0], s) : in[u];
+          g = grad_vec<T, kEntropy>(xin, r, kList || token < 0 ? -1 : token - col, hit);
+        }
+        __stcs(reinterpret_cast<uint4*>(dx + col), g);
+      } else if (col < V) {
+        for (int j = max(col, 0); j < min(col + VEC, V); ++j) {
+          float g = 0.0f;
+          if (!dead) g = grad1<kEntropy>(logit(x, j), r) + (!kList && j == token ? hit : 0.0f);
+          store_logit(dx, j, g);
+        }
+      }
+    }
+  }
+  if (kList) {
+    __syncthreads();  // the chunk's dense values are written
+    if (mine >= 0) {
+      // a column listed more than once is written by its first entry, with the sum of all
+      float q = 0.0f;
+      bool first = true;
+      for (int i = 0; i < a.k; ++i)
+        if (ids_s[i] == mine) {
+          first &= i >= tid;
+          q += q_s[i];
+        }
+      const float p = mine_x <= -kLogitBound && lse == lse ? 0.0f : exp2_approx(fmaf(mine_x, r.c, -lse * kLog2E));
+      if (first) store_logit(dx, mine, hit * (fmaf(mass, p, -q)));
+    }
   }
 }
 
-template <typename T, bool kDistill>
-nvfp4rl_status launch(const LogitsGradArgs& a, cudaStream_t st) {
-  if (launch_pdl(logits_grad_kernel<T, kDistill>, dim3(static_cast<unsigned>(a.M)), dim3(kThreads), 0, st, a) !=
-      cudaSuccess)
-    return NVFP4RL_ERR_CUDA;
-  return launch_status();
+template <typename T, int kU, bool kEntropy, bool kList>
+cudaError_t launch(const LogitsGradArgs& a, bool shift, unsigned grid, unsigned chunks, int steps, cudaStream_t st) {
+  if (shift)
+    return launch_pdl(logits_grad_kernel<T, kU, kEntropy, kList, true>, dim3(grid), dim3(kThreads), 0, st, a, chunks,
+                      steps);
+  return launch_pdl(logits_grad_kernel<T, kU, kEntropy, kList, false>, dim3(grid), dim3(kThreads), 0, st, a, chunks,
+                    steps);
+}
+
+template <typename T>
+nvfp4rl_status launch_type(const LogitsGradArgs& a, cudaStream_t st) {
+  constexpr int64_t VEC = kVecOf<T>;
+  const auto phase = [](const void* p) { return static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / sizeof(T)) % VEC; };
+  const bool shift = phase(a.x) != phase(a.dx) || (a.M > 1 && a.ld % VEC != a.ldd % VEC);
+  const int64_t vecs = (a.V + 2 * VEC - 2) / VEC;  // of the row, at its worst phase
+  const bool wide = a.M * ((vecs + 4 * kThreads - 1) / (4 * kThreads)) >= 4 * kNumSMsHint;
+  const int64_t per_step = (wide ? 4 : 1) * kThreads;
+  int64_t steps = a.ids && wide ? 4 : 1;  // a list costs its chunk a fixed part: larger chunks
+  while (steps * per_step < vecs && a.M * ((vecs + steps * per_step - 1) / (steps * per_step)) > (int64_t(1) << 30))
+    steps *= 2;
+  const int64_t chunks = (vecs + steps * per_step - 1) / (steps * per_step);
+  const unsigned grid = static_cast<unsigned>(a.M * chunks), ch = static_cast<unsigned>(chunks);
+  const int n = static_cast<int>(steps);
+  cudaError_t e;
+  if (wide)
+    e = a.ids ? launch<T, 4, false, true>(a, shift, grid, ch, n, st)
+              : a.dentropy ? launch<T, 4, true, false>(a, shift, grid, ch, n, st)
+                           : launch<T, 4, false, false>(a, shift, grid, ch, n, st);
+  else
+    e = a.ids ? launch<T, 1, false, true>(a, shift, grid, ch, n, st)
+              : a.dentropy ? launch<T, 1, true, false>(a, shift, grid, ch, n, st)
+                           : launch<T, 1, false, false>(a, shift, grid, ch, n, st);
+  return e == cudaSuccess ? launch_status() : NVFP4RL_ERR_CUDA;
 }
 
 }  // namespace
 
 nvfp4rl_status launch_logprobs_grad(const LogitsGradArgs& a, int dtype, const DeviceInfo&, cudaStream_t st) {
-  const bool distill = a.ids != nullptr;
-  if (dtype == NVFP4RL_BF16) return distill ? launch<uint16_t, true>(a, st) : launch<uint16_t, false>(a, st);
-  return distill ? launch<float, true>(a, st) : launch<float, false>(a, st);
+  return dtype == NVFP4RL_BF16 ? launch_type<uint16_t>(a, st) : launch_type<float>(a, st);
 }
 
 }  // namespace nvfp4rl
