@@ -1,18 +1,248 @@
 // Log-probs of given tokens, entropy and top alternatives of rows of logits, and the divergence from a
-// teacher's listed log-probs (sm_103a). One CTA per row.
+// teacher's listed log-probs (sm_103a). One pass over the logits.
+//
+// Every thread keeps a running reference R = c max(x) (c = scale log2 e), s = sum 2^t and w = sum 2^t t of the logits it
+// has seen, t = x c - R; a larger maximum rescales them. Over a row (R, s, w) merge by
+// s 2^(R_i - R), (w + (R_i - R) s) 2^(R_i - R), and
+//   lse = R ln 2 + ln s,   ln p_j = t_j ln 2 - ln s,   entropy = ln s - ln 2 (w / s).
+// Masked logits (at or below -2^100) enter the steps clamped to -2^100, where 2^t = 0 and t stays finite; a thread
+// that has seen nothing else adds nothing. A NaN stays in s.
+//
+// A row belongs to a cluster of 1 to 8 CTAs (a row alone would leave most SMs idle), each with a contiguous share; their
+// sums and alternatives meet in the first CTA's shared memory. A CTA of 256 threads takes 4 x 16 bytes per thread and
+// step; four CTAs on an SM hide one another's row ends. Bound by HBM: each logit is read once.
+//
+// Alternatives: the k-th largest of the threads' first maxima is a lower bound thr of the k-th largest logit. Columns that reach
+// it go to a candidate list in shared memory as 64-bit keys (value order, then the lower column). A list that
+// fills up is cut to little more than its k largest keys (histogram of the keys' range, refined where the k-th
+// falls), which raises thr: at the end the same cut, a rank by counting, and the result. What the list holds does
+// not depend on the order of the appends.
+//
+// Distillation with a tail bucket: listed columns are marked in a bit map in shared memory and masked as they are
+// read, so that the streamed sum is the tail's own, relative to its own maximum; the listed ones are gathered and
+// added at the end. 1 - sum p would lose a small tail.
+#include <atomic>
+
 #include "logits.cuh"
 
 namespace nvfp4rl {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kU = 4;                              // vectors per thread and step
+constexpr int kSlack = 32;                         // a cut leaves at most k + kSlack keys
+constexpr int kMaxKept = kMaxListed + kSlack;
+constexpr int kCandidates = kThreads * 8 + kMaxKept;  // one vector of every thread beside a list that was cut
+constexpr int kCutAt = 1024;                       // candidates at which a list is cut
+constexpr int kBins = 1024;
+constexpr int kMaxCluster = 8;
+constexpr int kMapColumns = 1 << 18;               // columns per bit map (32 KB)
+constexpr float kNoRef = -1.7014118346046923e38f;  // R of nothing: -2^127, below every c x
+static_assert(kMaxCluster * kMaxKept <= kCandidates, "the first CTA's list takes what every CTA of a cluster kept");
+static_assert(kThreads >= kMaxListed, "one thread per listed column");
+
+enum Mode { kLogprobs = 0, kNormalized = 1, kTailBucket = 2 };
+
+// ---- clusters ----
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address, in CTA `rank`, of what p is in this CTA's shared memory.
+__device__ __forceinline__ uint32_t map_shared(const void* p, uint32_t rank) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+// ---- keys: larger value first, then the lower column; 0 is no key ----
+
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 and +0 are one value
+  return (b >> 31) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t u) { return __uint_as_float((u >> 31) ? (u & 0x7FFFFFFFu) : ~u); }
+__device__ __forceinline__ unsigned long long rank_key(float v, int col) {
+  return (static_cast<unsigned long long>(order_bits(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(col));
+}
+__device__ __forceinline__ int key_column(unsigned long long key) {
+  return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+}
+
+struct TopShared {
+  unsigned long long key[kCandidates];
+  unsigned long long kept[kMaxKept];
+  int bins[kBins];
+  int warp_sum[kWarps];
+  int count, kept_count, above, bin;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Cuts the list's first n keys to those that include the k largest: at most k + kSlack, in key[0 .. count).
+// Returns the lower bound that the cut used (0: nothing was cut). All threads of the CTA call.
+__device__ unsigned long long cut_list(TopShared& sh, int n, int k) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kPer = (kCandidates + kThreads - 1) / kThreads;
+  unsigned long long mine[kPer], lo = ~0ull, hi = 0;
+  int keys = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = i * kThreads + tid;
+    mine[i] = j < n ? sh.key[j] : 0ull;
+    if (mine[i]) {
+      ++keys;
+      lo = min(lo, mine[i]);
+      hi = max(hi, mine[i]);
+    }
+  }
+  // the range of the keys, and their number: words 0..3 of the bins as scratch for the first reduction
+  keys = __reduce_add_sync(0xFFFFFFFFu, keys);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+  }
+  auto* ends = reinterpret_cast<unsigned long long*>(sh.bins);
+  if (lane == 0) {
+    ends[2 * warp] = lo;
+    ends[2 * warp + 1] = hi;
+    sh.warp_sum[warp] = keys;
+  }
+  if (tid == 0) sh.kept_count = 0;
+  __syncthreads();
+  keys = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    keys += sh.warp_sum[i];
+    lo = min(lo, ends[2 * i]);
+    hi = max(hi, ends[2 * i + 1]);
+  }
+  __syncthreads();
+  unsigned long long cut = 0;
+  if (keys > k + kSlack) {
+    int want = k;  // of the keys in [lo, hi]: those above are in
+    while (true) {
+      const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
+      const int shift = max(bits - 10, 0);  // (hi - lo) >> shift < 1024
+      for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (mine[i] >= lo && mine[i] <= hi && mine[i]) atomicAdd(&sh.bins[static_cast<int>((mine[i] - lo) >> shift)], 1);
+      __syncthreads();
+      // from the top: thread t holds bins 1023 - 4 t .. 1020 - 4 t
+      int b[4], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        b[i] = sh.bins[kBins - 1 - (4 * tid + i)];
+        sum += b[i];
+      }
+      int scan = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += v;
+      }
+      if (lane == 31) sh.warp_sum[warp] = scan;
+      __syncthreads();
+      int above = scan - sum;
+      for (int i = 0; i < warp; ++i) above += sh.warp_sum[i];
+      if (above < want && above + sum >= want) {  // the want-th key lies in one of this thread's bins
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (above < want && above + b[i] >= want) {
+            sh.bin = kBins - 1 - (4 * tid + i);
+            sh.above = above;
+            sh.count = above + b[i];
+            above = want;  // found
+          } else {
+            above += b[i];
+          }
+        }
+      }
+      __syncthreads();
+      const int bin = sh.bin, in = sh.above, with = sh.count;
+      cut = lo + (static_cast<unsigned long long>(bin) << shift);
+      // keys at or above the cut: k - want from earlier rounds, and `with`
+      if (k - want + with <= k + kSlack || shift == 0) break;
+      want -= in;
+      hi = min(hi, cut + ((1ull << shift) - 1));
+      lo = cut;
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (mine[i] && mine[i] >= cut) sh.kept[atomicAdd(&sh.kept_count, 1)] = mine[i];
+  __syncthreads();
+  const int kept = sh.kept_count;
+  for (int i = tid; i < kept; i += kThreads) sh.key[i] = sh.kept[i];
+  if (tid == 0) sh.count = kept;
+  __syncthreads();
+  return cut;
+}
+
+// ---- the streamed sums ----
+
+struct RowSum {
+  float R, s, w;
+};
+
+__device__ __forceinline__ void merge(RowSum& a, const RowSum& b) {
+  const float R = max_nan(a.R, b.R), da = a.R - R, db = b.R - R, fa = exp2_approx(da), fb = exp2_approx(db);
+  a.w = fmaf(da, a.s, a.w) * fa + fmaf(db, b.s, b.w) * fb;
+  a.s = a.s * fa + b.s * fb;
+  a.R = R;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 masked_vec() {
+  const uint32_t w = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  return make_uint4(w, w, w, w);
+}
+
+__device__ __forceinline__ float elem(const uint32_t (&w)[4], int i, uint16_t) {
+  return __uint_as_float((i & 1) ? bf16_hi_bits(w[i >> 1]) : bf16_lo_bits(w[i >> 1]));
+}
+__device__ __forceinline__ float elem(const uint32_t (&w)[4], int i, float) { return __uint_as_float(w[i & 3]); }
+
+template <typename T>
+__device__ __forceinline__ void set_masked(uint32_t (&w)[4], int i) {
+  if (sizeof(T) == 2)
+    w[i >> 1] = (i & 1) ? (w[i >> 1] & 0x0000FFFFu) | 0xFF800000u : (w[i >> 1] & 0xFFFF0000u) | 0x0000FF80u;
+  else
+    w[i & 3] = 0xFF800000u;
+}
 
 __device__ float block_max(float v, float* red) {
   v = warp_max(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   v = red[0];
-  for (int i = 1; i < kThreads / 32; ++i) v = fmaxf(v, red[i]);
+#pragma unroll
+  for (int i = 1; i < kWarps; ++i) v = fmaxf(v, red[i]);
   __syncthreads();
   return v;
 }
@@ -22,181 +252,430 @@ __device__ float block_sum(float v, float* red) {
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0.0f;
-  for (int i = 0; i < kThreads / 32; ++i) v += red[i];
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) v += red[i];
   __syncthreads();
   return v;
 }
 
-// Order of the alternatives as one integer: larger value first, then the lower column (-0 = +0).
-__device__ unsigned long long rank_key(float v, int64_t col) {
-  const uint32_t b = __float_as_uint(v + 0.0f);
-  const uint32_t u = (b >> 31) ? ~b : (b | 0x80000000u);
-  return (static_cast<unsigned long long>(u) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(col));
+struct Shared {
+  float red[kWarps];
+  RowSum sums[kWarps];
+  RowSum parts[kMaxCluster];
+  TeacherRow teacher;
+};
+struct ListShared {
+  int32_t ids[kMaxListed];
+  float q[kMaxListed], lq[kMaxListed];
+};
+
+// Columns whose logit reaches the bound go to the list; a full list drops them (the caller sees it by the count).
+template <typename T>
+__device__ __forceinline__ bool append(TopShared& sh, const uint32_t (&w)[4], int col, int V, float thr, bool equal) {
+  bool much = false;
+#pragma unroll
+  for (int i = 0; i < kVecOf<T>; ++i) {
+    const float v = elem(w, i, T());
+    if ((equal ? v >= thr : v > thr) && v > -kLogitBound && col + i >= 0 && col + i < V) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kCandidates) sh.key[at] = rank_key(v, col + i);
+      much |= at >= kCutAt;
+    }
+  }
+  return much;
 }
 
-template <typename T, bool kDistill>
-__global__ void __launch_bounds__(kThreads) logits_row_kernel(const LogitsArgs a) {
-  __shared__ float red[kThreads / 32];
-  __shared__ int32_t ids_s[kMaxListed];
-  __shared__ float q_s[kMaxListed], lq_s[kMaxListed];
-  __shared__ TeacherRow teacher_s;
-  __shared__ unsigned long long best;
+// kEntropy: w is kept; kTop: alternatives are listed (both kLogprobs only).
+template <typename T, int kMode, bool kEntropy, bool kTop>
+__global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArgs a, uint32_t cluster) {
+  constexpr int VEC = kVecOf<T>;
+  constexpr bool kDistill = kMode != kLogprobs;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ Shared sh;
+  TopShared& top = *reinterpret_cast<TopShared*>(dyn);                  // kTop
+  ListShared& list = *reinterpret_cast<ListShared*>(dyn);               // kDistill
+  uint32_t* map = reinterpret_cast<uint32_t*>(dyn + sizeof(ListShared));  // kTailBucket
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t row = blockIdx.x;
+  const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
+  const int64_t row = blockIdx.x / cluster;
   const T* x = static_cast<const T*>(a.x) + row * a.ld;
-  const int tid = threadIdx.x;
-  int64_t token = -1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int V = static_cast<int>(a.V), k = a.k;
+  int token = -1;
   if (kDistill) {
-    if (tid < 32) {
-      const TeacherRow t = teacher_row(a.ids + row * a.k, a.teacher + row * a.k, a.k, a.V, a.tail, ids_s, q_s, lq_s);
-      if (tid == 0) teacher_s = t;
+    if (warp == 0) {
+      const TeacherRow t = teacher_row(a.ids + row * k, a.teacher + row * k, k, a.V, a.tail, list.ids, list.q, list.lq);
+      if (lane == 0) sh.teacher = t;
     }
     __syncthreads();
-    if (!teacher_s.any) {
-      if (tid == 0) {
+    if (!sh.teacher.any) {  // every CTA of the cluster
+      if (rank == 0 && tid == 0) {
         a.loss[row] = 0.0f;
         if (a.lse) a.lse[row] = 0.0f;
-        if (a.tail && a.lse_tail) a.lse_tail[row] = 0.0f;
+        if (kMode == kTailBucket && a.lse_tail) a.lse_tail[row] = 0.0f;
       }
       return;
     }
   } else if (a.tokens) {
     token = a.tokens[row];
-    if (token < 0 || token >= a.V) {
-      if (tid == 0) {
-        if (a.logp) a.logp[row] = 0.0f;
-        if (a.entropy) a.entropy[row] = 0.0f;
-        if (a.lse) a.lse[row] = 0.0f;
-      }
-      for (int i = tid; i < a.k; i += kThreads) {
-        a.top_ids[row * a.k + i] = -1;
-        a.top_logp[row * a.k + i] = -INFINITY;
+    if (token < 0 || token >= V) {
+      if (rank == 0) {
+        if (tid == 0) {
+          if (a.logp) a.logp[row] = 0.0f;
+          if (a.entropy) a.entropy[row] = 0.0f;
+          if (a.lse) a.lse[row] = 0.0f;
+        }
+        if (kTop)
+          for (int i = tid; i < k; i += kThreads) {
+            a.top_ids[row * k + i] = -1;
+            a.top_logp[row * k + i] = -INFINITY;
+          }
       }
       return;
     }
   }
+
+  const float at_token = kMode == kLogprobs && tid == 0 && token >= 0 ? logit(x, token) : 0.0f;
   const float c = a.scale * kLog2E;
-  // the sums run over the columns that are not listed apart (TAIL), relative to their own maximum: a tail
-  // far below the row's maximum keeps its digits
-  const auto apart = [&](int64_t j) {
-    bool in = false;
-    if (kDistill && a.tail)
-      for (int i = 0; i < a.k; ++i) in |= ids_s[i] == j;
-    return in;
-  };
-  float m = -kLogitBound;
-  bool nan = false;
-  for (int64_t j = tid; j < a.V; j += kThreads) {
-    const float v = logit(x, j);
-    nan |= v != v || v > kLogitBound;
-    if (!apart(j)) m = fmaxf(m, v);
-  }
-  nan = __syncthreads_or(nan);
-  m = block_max(m, red);
-  const float R = m * c;
-  float s = 0.0f, w = 0.0f;
-  for (int64_t j = tid; j < a.V; j += kThreads) {
-    const float v = logit(x, j);
-    if (v <= -kLogitBound || apart(j)) continue;
-    const float t = fmaf(v, c, -R), e = exp2_approx(t);
-    s += e;
-    w = fmaf(e, t, w);
-  }
-  s = block_sum(s, red);
-  w = block_sum(w, red);
-  if (nan) s = NAN;
-  if (kDistill) {
-    const float s_tail = s;
-    float m2 = m;
-    if (a.tail) {
-      for (int i = tid; i < a.k; i += kThreads)
-        if (ids_s[i] >= 0) m2 = fmaxf(m2, logit(x, ids_s[i]));
-      m2 = block_max(m2, red);
-    }
-    const float R2 = m2 * c, down = R - R2;
-    if (a.tail) {
-      float more = 0.0f;
-      for (int i = tid; i < a.k; i += kThreads) {
-        bool first = ids_s[i] >= 0;
-        for (int j = 0; j < i; ++j) first &= ids_s[j] != ids_s[i];
-        if (!first) continue;
-        const float v = logit(x, ids_s[i]);
-        if (v > -kLogitBound) more += exp2_approx(fmaf(v, c, -R2));
+  const int phase = vec_phase(x);
+  const int vecs = (V + phase + VEC - 1) / VEC;  // vector v: columns v VEC - phase ..
+  const int share = (vecs + static_cast<int>(cluster) - 1) / static_cast<int>(cluster);
+  const int v_begin = static_cast<int>(rank) * share, v_end = min(v_begin + share, vecs);
+  float m = -kLogitBound, R = kNoRef, thr = -kLogitBound;
+  F2 s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
+  const F2 c2 = pack2(c, c);
+  if (kTop && tid == 0) top.count = 0;
+  constexpr int kMapVecs = kMapColumns / VEC;
+  int map_begin = v_begin;  // first vector of the bit map
+
+  for (int v0 = v_begin; v0 < v_end; v0 += kU * kThreads) {
+    if (kMode == kTailBucket && (v0 == v_begin || v0 - map_begin >= kMapVecs)) {
+      // the listed columns of the next kMapColumns columns
+      __syncthreads();
+      map_begin = v0;
+      const int words = (min(v_end - v0, kMapVecs) * VEC + 31) / 32;
+      for (int i = tid; i < words; i += kThreads) map[i] = 0;
+      __syncthreads();
+      if (tid < k && list.ids[tid] >= 0) {
+        const int v = (list.ids[tid] + phase) / VEC;
+        if (v >= v0 && v < min(v_end, v0 + kMapVecs)) {
+          const int bit = list.ids[tid] + phase - v0 * VEC;
+          atomicOr(&map[bit >> 5], 1u << (bit & 31));
+        }
       }
-      s = fmaf(s_tail, exp2_approx(down), block_sum(more, red));
+      __syncthreads();
     }
-    const bool empty = s == 0.0f;
-    const float ln_s = logf(s), ln_tail = logf(s_tail);
-    float part = 0.0f;
-    for (int i = tid; i < a.k; i += kThreads) {
-      if (ids_s[i] < 0 || q_s[i] == 0.0f) continue;
-      const float v = logit(x, ids_s[i]);
-      const float lp = empty || v <= -kLogitBound ? -INFINITY : fmaf(v, c, -R2) * kLn2 - ln_s;
-      part += q_s[i] * (lq_s[i] - lp);
+    uint4 in[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int v = v0 + u * kThreads + tid, col = v * VEC - phase;
+      in[u] = masked_vec<T>();
+      if (v < v_end) {
+        if (col >= 0 && col + VEC <= V) {
+          in[u] = ld_logits16(x + col);
+        } else {  // a row's end: its elements one by one
+          uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
+          for (int i = 0; i < VEC; ++i)
+            if (col + i >= 0 && col + i < V) {
+              const uint32_t b = __float_as_uint(logit(x, col + i));
+              if (sizeof(T) == 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (j == i) w[j] = b;
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (j == (i >> 1)) w[j] = (i & 1) ? (w[j] & 0xFFFFu) | b : (w[j] & 0xFFFF0000u) | (b >> 16);
+              }
+            }
+          in[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
     }
-    part = block_sum(part, red);
+    if (kMode == kTailBucket) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int v = v0 + u * kThreads + tid;
+        if (v < v_end) {
+          const int at = (v - map_begin) * VEC;
+          const uint32_t bits = (map[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
+          if (bits) {
+            uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+              if (bits >> i & 1) set_masked<T>(w, i);
+            in[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+    // the step's maximum, masked logits clamped to -2^100
+    float cm;
+    if (sizeof(T) == 2) {
+      uint32_t mx = 0xF180F180u;  // -2^100, twice
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        in[u].x = max_nan_bf16x2(in[u].x, 0xF180F180u);
+        in[u].y = max_nan_bf16x2(in[u].y, 0xF180F180u);
+        in[u].z = max_nan_bf16x2(in[u].z, 0xF180F180u);
+        in[u].w = max_nan_bf16x2(in[u].w, 0xF180F180u);
+        mx = max_nan_bf16x2(mx, max_nan_bf16x2(max_nan_bf16x2(in[u].x, in[u].y), max_nan_bf16x2(in[u].z, in[u].w)));
+      }
+      cm = max_nan(__uint_as_float(bf16_lo_bits(mx)), __uint_as_float(bf16_hi_bits(mx)));
+    } else {
+      cm = -kLogitBound;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        in[u].x = __float_as_uint(max_nan(__uint_as_float(in[u].x), -kLogitBound));
+        in[u].y = __float_as_uint(max_nan(__uint_as_float(in[u].y), -kLogitBound));
+        in[u].z = __float_as_uint(max_nan(__uint_as_float(in[u].z), -kLogitBound));
+        in[u].w = __float_as_uint(max_nan(__uint_as_float(in[u].w), -kLogitBound));
+        cm = max_nan(cm, max_nan(max_nan(__uint_as_float(in[u].x), __uint_as_float(in[u].y)),
+                                 max_nan(__uint_as_float(in[u].z), __uint_as_float(in[u].w))));
+      }
+    }
+    if (!(cm <= m)) {  // larger, or NaN (which stays)
+      const float Rn = cm * c, d = R - Rn, f = exp2_approx(d);
+      const F2 f2 = pack2(f, f);
+      if (kEntropy) w2 = mul2(fma2(pack2(d, d), s2, w2), f2);
+      s2 = mul2(s2, f2);
+      R = Rn;
+      m = cm;
+    }
+    if (!(m <= -kLogitBound)) {
+      const F2 r2 = pack2(-R, -R);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+          const F2 t = fma2(pack2(elem(w, 2 * i, T()), elem(w, 2 * i + 1, T())), c2, r2);
+          float t0, t1;
+          unpack2(t, t0, t1);
+          const F2 e = pack2(exp2_approx(t0), exp2_approx(t1));
+          s2 = add2(s2, e);
+          if (kEntropy) w2 = fma2(e, t, w2);
+        }
+      }
+    }
+    if (kTop) {
+      const bool first = v0 == v_begin;
+      if (first) {
+        // thr: the k-th largest of the threads' maxima, to 16 bits (rounded down)
+        const uint32_t key = order_bits(cm) >> 16;
+        uint32_t t = 0;
+#pragma unroll 1
+        for (int bit = 15; bit >= 0; --bit) {
+          const uint32_t next = t | (1u << bit);
+          if (__syncthreads_count(key >= next) >= k) t = next;
+        }
+        thr = fmaxf(order_value(t << 16), -kLogitBound);  // NaN (fewer than k threads saw one): the bound
+      }
+      bool much = false;
+      if (cm > thr || (first && cm == thr)) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
+          much |= append<T>(top, w, (v0 + u * kThreads + tid) * VEC - phase, V, thr, first);
+        }
+      }
+      if (__syncthreads_or(much)) {
+        const int n = top.count;
+        __syncthreads();
+        if (n <= kCandidates) {
+          const unsigned long long cut = cut_list(top, n, k);
+          if (cut) thr = fmaxf(thr, order_value(static_cast<uint32_t>(cut >> 32)));
+        } else {
+          // some of this step's columns found no place: what the step appended goes, and it is done again
+          // vector by vector, a list that was cut taking one vector of every thread
+          const int from = v0 * VEC - phase;
+          for (int i = tid; i < kCandidates; i += kThreads)
+            if (key_column(top.key[i]) >= from) top.key[i] = 0;
+          __syncthreads();
+          unsigned long long cut = cut_list(top, kCandidates, k);
+          bool equal = first;
+          if (cut) thr = fmaxf(thr, order_value(static_cast<uint32_t>(cut >> 32)));
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
+            append<T>(top, w, (v0 + u * kThreads + tid) * VEC - phase, V, thr, equal);
+            __syncthreads();
+            const int n1 = top.count;
+            __syncthreads();
+            cut = cut_list(top, n1, k);
+            if (cut) {
+              thr = fmaxf(thr, order_value(static_cast<uint32_t>(cut >> 32)));
+              equal = false;
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // the CTA's sums, then the cluster's, in a fixed order
+  RowSum sum{R, 0.0f, 0.0f};
+  {
+    float lo, hi;
+    unpack2(s2, lo, hi);
+    sum.s = lo + hi;
+    unpack2(w2, lo, hi);
+    sum.w = lo + hi;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    merge(sum, RowSum{__shfl_xor_sync(0xFFFFFFFFu, sum.R, o), __shfl_xor_sync(0xFFFFFFFFu, sum.s, o),
+                      __shfl_xor_sync(0xFFFFFFFFu, sum.w, o)});
+  if (lane == 0) sh.sums[warp] = sum;
+  __syncthreads();
+  sum = sh.sums[0];
+#pragma unroll
+  for (int i = 1; i < kWarps; ++i) merge(sum, sh.sums[i]);
+  if (kTop) cut_list(top, top.count, k);
+  if (cluster > 1) {
+    const int slots = k + kSlack;
+    cluster_sync();  // every CTA's list is its own until here
     if (tid == 0) {
-      if (a.tail && teacher_s.q0 > 0.0f && s_tail > 0.0f)
-        part += teacher_s.q0 * (logf(teacher_s.q0) - (fmaf(down, kLn2, ln_tail) - ln_s));
-      a.loss[row] = s != s ? NAN : part;
+      const uint32_t at = map_shared(&sh.parts[rank], 0);
+      st_cluster(at, sum.R);
+      st_cluster(at + 4, sum.s);
+      st_cluster(at + 8, sum.w);
+    }
+    if (kTop && rank > 0)
+      for (int i = tid; i < slots; i += kThreads)
+        st_cluster(map_shared(&top.key[rank * slots + i], 0), i < top.count ? top.key[i] : 0ull);
+    if (kTop && rank == 0)
+      for (int i = top.count + tid; i < slots; i += kThreads) top.key[i] = 0ull;
+    cluster_sync();
+    if (rank > 0) return;
+    sum = sh.parts[0];
+    for (uint32_t i = 1; i < cluster; ++i) merge(sum, sh.parts[i]);
+    if (kTop) cut_list(top, static_cast<int>(cluster) * slots, k);
+  }
+  if (sum.R > kLogitBound * c) sum.s = NAN;  // a logit above 2^100
+
+  if (kDistill) {
+    // listed columns: thread i holds entry i
+    const int32_t id = tid < k ? list.ids[tid] : -1;
+    const float v = id >= 0 ? logit(x, id) : -INFINITY;
+    const float s_tail = sum.s;
+    float R2 = sum.R;
+    if (kMode == kTailBucket) {
+      const bool bad = __syncthreads_or(v != v || v > kLogitBound);
+      R2 = fmaxf(R2, block_max(fmaxf(v, -kLogitBound) <= -kLogitBound ? kNoRef : v * c, sh.red));
+      bool once = id >= 0 && v > -kLogitBound;  // the first entry of its column
+      if (once)
+        for (int j = 0; j < tid; ++j) once &= list.ids[j] != id;
+      const float listed = block_sum(once ? exp2_approx(fmaf(v, c, -R2)) : 0.0f, sh.red);
+      sum.s = bad ? NAN : fmaf(s_tail, exp2_approx(sum.R - R2), listed);
+    }
+    const bool empty = sum.s == 0.0f;
+    const float ln_s = logf(sum.s), down = sum.R - R2;
+    float part = 0.0f;
+    if (id >= 0 && list.q[tid] != 0.0f) {
+      const float lp = empty || v <= -kLogitBound ? -INFINITY : fmaf(v, c, -R2) * kLn2 - ln_s;
+      part = list.q[tid] * (list.lq[tid] - lp);
+    }
+    part = block_sum(part, sh.red);
+    if (tid == 0) {
+      const float ln_tail = logf(s_tail), q0 = sh.teacher.q0;
+      if (kMode == kTailBucket && q0 > 0.0f && s_tail > 0.0f) part += q0 * (logf(q0) - (fmaf(down, kLn2, ln_tail) - ln_s));
+      a.loss[row] = sum.s != sum.s ? NAN : part;
       if (a.lse) a.lse[row] = empty ? -INFINITY : fmaf(R2, kLn2, ln_s);
-      if (a.tail && a.lse_tail) a.lse_tail[row] = s_tail == 0.0f ? -INFINITY : fmaf(R, kLn2, ln_tail);
+      if (kMode == kTailBucket && a.lse_tail)
+        a.lse_tail[row] = sum.s != sum.s ? NAN : s_tail == 0.0f ? -INFINITY : fmaf(sum.R, kLn2, ln_tail);
     }
     return;
   }
-  const bool empty = s == 0.0f;
-  const float ln_s = logf(s);
-  const float lse = empty ? -INFINITY : fmaf(R, kLn2, ln_s);
+
+  const bool bad = sum.s != sum.s, empty = sum.s == 0.0f;
+  const float ln_s = logf(sum.s);
   if (tid == 0) {
-    if (a.logp) {
-      const float v = logit(x, token);
-      a.logp[row] = s != s ? NAN : empty || v <= -kLogitBound ? -INFINITY : fmaf(v, c, -R) * kLn2 - ln_s;
-    }
-    if (a.entropy) {
-      const float h = empty ? 0.0f : ln_s - kLn2 * (w / s);
+    if (a.logp)
+      a.logp[row] = bad ? NAN : empty || at_token <= -kLogitBound ? -INFINITY
+                                                                  : fmaf(at_token, c, -sum.R) * kLn2 - ln_s;
+    if (kEntropy) {
+      const float h = empty ? 0.0f : ln_s - kLn2 * (sum.w / sum.s);
       a.entropy[row] = h < 0.0f ? 0.0f : h;
     }
-    if (a.lse) a.lse[row] = lse;
+    if (a.lse) a.lse[row] = empty ? -INFINITY : fmaf(sum.R, kLn2, ln_s);
   }
-  unsigned long long prev = ~0ull;
-  for (int i = 0; i < a.k; ++i) {
-    if (tid == 0) best = 0;
-    __syncthreads();
-    unsigned long long b = 0;
-    if (s == s)
-      for (int64_t j = tid; j < a.V; j += kThreads) {
-        const float v = logit(x, j);
-        const unsigned long long key = v > -kLogitBound ? rank_key(v, j) : 0ull;
-        if (key < prev && key > b) b = key;
+  if (kTop) {
+    const int n = top.count;  // k or a few more, or all there are
+    for (int i = tid; i < max(n, k); i += kThreads) {
+      if (i < n && !bad) {
+        const unsigned long long key = top.key[i];
+        int before = 0;
+        for (int j = 0; j < n; ++j) before += top.key[j] > key;
+        if (before < k) {
+          const int id = key_column(key);
+          a.top_ids[row * k + before] = id;
+          a.top_logp[row * k + before] =
+              fmaf(order_value(static_cast<uint32_t>(key >> 32)), c, -sum.R) * kLn2 - ln_s;
+        }
       }
-    atomicMax(&best, b);
-    __syncthreads();
-    prev = best;
-    if (tid == 0) {
-      const int32_t id = prev ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(prev)) : -1;
-      a.top_ids[row * a.k + i] = id;
-      a.top_logp[row * a.k + i] =
-          s != s ? NAN : id < 0 ? -INFINITY : fmaf(logit(x, id), c, -R) * kLn2 - ln_s;
+      if (i < k && (i >= n || bad)) {
+        a.top_ids[row * k + i] = -1;
+        a.top_logp[row * k + i] = bad ? NAN : -INFINITY;
+      }
     }
-    __syncthreads();
   }
 }
 
-template <typename T, bool kDistill>
-nvfp4rl_status launch(const LogitsArgs& a, cudaStream_t st) {
-  if (launch_pdl(logits_row_kernel<T, kDistill>, dim3(static_cast<unsigned>(a.M)), dim3(kThreads), 0, st, a) !=
-      cudaSuccess)
-    return NVFP4RL_ERR_CUDA;
-  return launch_status();
+template <typename T, int kMode, bool kEntropy, bool kTop>
+nvfp4rl_status launch(const LogitsArgs& a, unsigned cluster, const DeviceInfo& dev, cudaStream_t st) {
+  size_t smem = kTop ? sizeof(TopShared) : kMode == kLogprobs ? 0 : sizeof(ListShared);
+  if (kMode == kTailBucket) {
+    const int64_t share = (a.V + 2 * kVecOf<T>) / cluster + 2 * kVecOf<T>;
+    smem += align_up(static_cast<size_t>(std::min<int64_t>(share, kMapColumns) + 31) / 8 + 4, 16);
+  }
+  auto* kernel = logits_row_kernel<T, kMode, kEntropy, kTop>;
+  if (kTop || kMode == kTailBucket) {  // more than 48 KB of shared memory with the static part: asked for once per device
+    static std::atomic<uint64_t> asked{0};
+    const uint64_t bit = uint64_t(1) << (dev.device & 63);
+    if (!(asked.load(std::memory_order_relaxed) & bit)) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess)
+        return NVFP4RL_ERR_CUDA;
+      asked.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.M) * cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, cluster) == cudaSuccess ? launch_status() : NVFP4RL_ERR_CUDA;
+}
+
+template <typename T>
+nvfp4rl_status launch_type(const LogitsArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  // CTAs per row: as many as fill the SMs' four places each, and no share below one step
+  unsigned cluster = kMaxCluster;
+  while (cluster > 1 && (a.M * cluster > 4 * dev.sm_count || a.V < static_cast<int64_t>(cluster) * kThreads * kVecOf<T>))
+    cluster /= 2;
+  if (a.ids) return a.tail ? launch<T, kTailBucket, false, false>(a, cluster, dev, st)
+                           : launch<T, kNormalized, false, false>(a, cluster, dev, st);
+  if (a.k > 0)
+    return a.entropy ? launch<T, kLogprobs, true, true>(a, cluster, dev, st)
+                     : launch<T, kLogprobs, false, true>(a, cluster, dev, st);
+  return a.entropy ? launch<T, kLogprobs, true, false>(a, cluster, dev, st)
+                   : launch<T, kLogprobs, false, false>(a, cluster, dev, st);
 }
 
 }  // namespace
 
-nvfp4rl_status launch_logprobs(const LogitsArgs& a, int dtype, const DeviceInfo&, cudaStream_t st) {
-  const bool distill = a.ids != nullptr;
-  if (dtype == NVFP4RL_BF16) return distill ? launch<uint16_t, true>(a, st) : launch<uint16_t, false>(a, st);
-  return distill ? launch<float, true>(a, st) : launch<float, false>(a, st);
+nvfp4rl_status launch_logprobs(const LogitsArgs& a, int dtype, const DeviceInfo& dev, cudaStream_t st) {
+  return dtype == NVFP4RL_BF16 ? launch_type<uint16_t>(a, dev, st) : launch_type<float>(a, dev, st);
 }
 
 }  // namespace nvfp4rl

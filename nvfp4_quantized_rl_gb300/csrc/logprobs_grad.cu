@@ -40,12 +40,13 @@ struct RowCoef {
   float c, R, alpha, beta;
 };
 
+// One element, with the roundings of the packed form (no contraction): the bits do not depend on where a row lies.
 template <bool kEntropy>
 __device__ __forceinline__ float grad1(float v, const RowCoef& r) {
   // masked logits: t far below every exponent, 2^t = 0, and finite, as 0 beta t has to be 0
   if (kEntropy) v = fmaxf(v, -kLogitBound);
   const float t = fmaf(v, r.c, -r.R), e = exp2_approx(t);
-  return e * (kEntropy ? fmaf(r.beta, t, r.alpha) : r.alpha);
+  return __fmul_rn(e, kEntropy ? fmaf(r.beta, t, r.alpha) : r.alpha);
 }
 
 template <bool kEntropy>
@@ -82,7 +83,7 @@ __device__ __forceinline__ uint4 grad_vec(uint4 x, const RowCoef& r, int at, flo
   if (static_cast<unsigned>(at) < static_cast<unsigned>(VEC)) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-      if (i == at) g[i] += hit;
+      if (i == at) g[i] = __fadd_rn(g[i], hit);
   }
   if (sizeof(T) == 2)
     return make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4 % VEC], g[5 % VEC]),
@@ -185,7 +186,10 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
       } else if (col < V) {
         for (int j = max(col, 0); j < min(col + VEC, V); ++j) {
           float g = 0.0f;
-          if (!dead) g = grad1<kEntropy>(logit(x, j), r) + (!kList && j == token ? hit : 0.0f);
+          if (!dead) {
+            g = grad1<kEntropy>(logit(x, j), r);
+            if (!kList && j == token) g = __fadd_rn(g, hit);
+          }
           store_logit(dx, j, g);
         }
       }
