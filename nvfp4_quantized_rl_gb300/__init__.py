@@ -271,31 +271,43 @@ def ais_mixing(logp_rollout, logp_train, adv, C: float, delta: float, gamma: flo
 def _logit_rows(x, what="logits"):
     """dtype code, M, V and row stride of a 2-D bf16 or fp32 CUDA tensor whose columns are contiguous."""
     import torch
-    dt = BF16 if x.dtype == torch.bfloat16 else F32 if x.dtype == torch.float32 else None
+    dt = BF16 if x.dtype is torch.bfloat16 else F32 if x.dtype is torch.float32 else None
     if dt is None:
         raise TypeError(f"{what} must be bf16 or fp32")
     if x.dim() != 2:
         raise ValueError(f"{what} must be 2-D")
     M, V = x.shape
-    ld = max(x.stride(0), V) if M <= 1 else x.stride(0)
-    if (V > 1 and x.stride(1) != 1) or ld < V:
+    ld, step = x.stride()
+    if M <= 1 and ld < V:
+        ld = V
+    if (V > 1 and step != 1) or ld < V:
         raise ValueError(f"{what}: the columns of a row must be contiguous, and rows must not overlap")
     return dt, M, V, ld
 
 
 def _row_array(t, name, dtype, shape, device):
-    """Checks one per-row argument (None passes): contiguous, of this dtype and shape, on the logits' device."""
+    """The address of one per-row argument (None: NULL): contiguous, of this dtype and shape, on the logits'
+    device (its index)."""
     if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on the logits' device")
+    return t.data_ptr()
 
 
-def _on_device(t):
-    """The library launches on the current device: make it the tensor's."""
-    import contextlib
+def _logits_call(name, device, stream, *args):
+    """Calls the C function on the logits' device (the library launches on the current one) and its current
+    stream, or the stream given."""
     import torch
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device == torch.cuda.current_device():
+        st = getattr(lib(), name)(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib(), name)(*args, stream.cuda_stream)
+    if st != OK:
+        raise Nvfp4rlError(st, name)
 
 
 def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy: bool = True, logp=None, h=None,
@@ -305,37 +317,35 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy:
     int32 [M, k], top_logp fp32 [M, k]); None where tokens is None, entropy is False or k is 0. Rows whose
     token is outside [0, V) are ignored (0, and ids -1)."""
     import torch
-    _require_cuda(logits, tokens, logp, h, lse, top_ids, top_logp)
+    _require_cuda(logits)
     dt, M, V, ld = _logit_rows(logits)
-    dev, f32 = logits.device, torch.float32
-    if tokens is None and logp is not None:
+    dev, where, f32, i32 = logits.get_device(), logits.device, torch.float32, torch.int32
+    if tokens is not None:
+        logp = torch.empty(M, dtype=f32, device=where) if logp is None else logp
+    elif logp is not None:
         raise ValueError("logp needs tokens")
-    logp = _empty((M,), f32, dev) if logp is None and tokens is not None else logp
-    h = _empty((M,), f32, dev) if h is None and entropy else h if entropy else None
-    lse = _empty((M,), f32, dev) if lse is None else lse
+    h = None if not entropy else torch.empty(M, dtype=f32, device=where) if h is None else h
+    lse = torch.empty(M, dtype=f32, device=where) if lse is None else lse
     if k > 0:
-        top_ids = _empty((M, k), torch.int32, dev) if top_ids is None else top_ids
-        top_logp = _empty((M, k), f32, dev) if top_logp is None else top_logp
+        top_ids = torch.empty(M, k, dtype=i32, device=where) if top_ids is None else top_ids
+        top_logp = torch.empty(M, k, dtype=f32, device=where) if top_logp is None else top_logp
     else:
         top_ids = top_logp = None
-    _row_array(tokens, "tokens", torch.int32, (M,), dev)
-    _row_array(logp, "logp", f32, (M,), dev)
-    _row_array(h, "h", f32, (M,), dev)
-    _row_array(lse, "lse", f32, (M,), dev)
-    _row_array(top_ids, "top_ids", torch.int32, (M, k), dev)
-    _row_array(top_logp, "top_logp", f32, (M, k), dev)
-    with _on_device(logits):
-        st = lib().token_logprobs(_ptr(logits), dt, M, V, ld, _ptr(tokens), float(scale), k, _ptr(logp), _ptr(h),
-                                  _ptr(lse), _ptr(top_ids), _ptr(top_logp), _stream(logits, stream))
-    _check(st, "token_logprobs")
+    rows, listed = (M,), (M, k)
+    _logits_call("token_logprobs", dev, stream, logits.data_ptr(), dt, M, V, ld,
+                 _row_array(tokens, "tokens", i32, rows, dev), float(scale), k, _row_array(logp, "logp", f32, rows, dev),
+                 _row_array(h, "h", f32, rows, dev), _row_array(lse, "lse", f32, rows, dev),
+                 _row_array(top_ids, "top_ids", i32, listed, dev),
+                 _row_array(top_logp, "top_logp", f32, listed, dev))
     return logp, h, lse, top_ids, top_logp
 
 
 def _dlogits(logits, out, M, V):
     """The gradient's tensor (made when None) and its row stride."""
+    import torch
     if out is None:
-        out = _empty((M, V), logits.dtype, logits.device)
-    if out.dtype != logits.dtype or tuple(out.shape) != (M, V) or out.device != logits.device:
+        return torch.empty(M, V, dtype=logits.dtype, device=logits.device), V
+    if out.dtype is not logits.dtype or out.shape != (M, V) or out.device != logits.device:
         raise ValueError("out must have the logits' dtype, shape and device")
     return out, _logit_rows(out, "out")[3]
 
@@ -346,18 +356,14 @@ def token_logprobs_backward(logits, tokens, lse, dlogp, scale: float = 1.0, entr
     gave them -> out [M, V] of the logits' dtype (may be the logits themselves: overwritten in place). dlogp or
     dentropy may be None."""
     import torch
-    _require_cuda(logits, tokens, lse, dlogp, entropy, dentropy, out)
+    _require_cuda(logits)
     dt, M, V, ld = _logit_rows(logits)
-    dev, f32 = logits.device, torch.float32
+    dev, f32, rows = logits.get_device(), torch.float32, (M,)
     out, ldd = _dlogits(logits, out, M, V)
-    _row_array(tokens, "tokens", torch.int32, (M,), dev)
-    for t, name in ((lse, "lse"), (dlogp, "dlogp"), (entropy, "entropy"), (dentropy, "dentropy")):
-        _row_array(t, name, f32, (M,), dev)
-    with _on_device(logits):
-        st = lib().token_logprobs_backward(_ptr(logits), dt, M, V, ld, _ptr(tokens), float(scale), _ptr(lse),
-                                           _ptr(entropy), _ptr(dlogp), _ptr(dentropy), _ptr(out), ldd,
-                                           _stream(logits, stream))
-    _check(st, "token_logprobs_backward")
+    _logits_call("token_logprobs_backward", dev, stream, logits.data_ptr(), dt, M, V, ld,
+                 _row_array(tokens, "tokens", torch.int32, rows, dev), float(scale), _row_array(lse, "lse", f32, rows, dev),
+                 _row_array(entropy, "entropy", f32, rows, dev), _row_array(dlogp, "dlogp", f32, rows, dev),
+                 _row_array(dentropy, "dentropy", f32, rows, dev), out.data_ptr(), ldd)
     return out
 
 
@@ -367,22 +373,19 @@ def topk_distill(logits, ids, teacher_logp, scale: float = 1.0, tail: bool = Fal
     fp32 [M, k]; ids outside [0, V) are skipped) -> (loss, lse, lse_tail fp32 [M]). The teacher is normalised
     over its list, or with tail=True everything unlisted is one more outcome (lse_tail is None without it)."""
     import torch
-    _require_cuda(logits, ids, teacher_logp, loss, lse, lse_tail)
+    _require_cuda(logits)
     dt, M, V, ld = _logit_rows(logits)
-    dev, f32 = logits.device, torch.float32
+    dev, where, f32 = logits.get_device(), logits.device, torch.float32
     k = ids.shape[1] if ids.dim() == 2 else 0
-    loss = _empty((M,), f32, dev) if loss is None else loss
-    lse = _empty((M,), f32, dev) if lse is None else lse
-    lse_tail = None if not tail else _empty((M,), f32, dev) if lse_tail is None else lse_tail
-    _row_array(ids, "ids", torch.int32, (M, k), dev)
-    _row_array(teacher_logp, "teacher_logp", f32, (M, k), dev)
-    for t, name in ((loss, "loss"), (lse, "lse"), (lse_tail, "lse_tail")):
-        _row_array(t, name, f32, (M,), dev)
-    with _on_device(logits):
-        st = lib().topk_distill(_ptr(logits), dt, M, V, ld, float(scale), _ptr(ids), _ptr(teacher_logp), k,
-                                DISTILL_TAIL if tail else DISTILL_NORMALIZED, _ptr(loss), _ptr(lse), _ptr(lse_tail),
-                                _stream(logits, stream))
-    _check(st, "topk_distill")
+    loss = torch.empty(M, dtype=f32, device=where) if loss is None else loss
+    lse = torch.empty(M, dtype=f32, device=where) if lse is None else lse
+    lse_tail = None if not tail else torch.empty(M, dtype=f32, device=where) if lse_tail is None else lse_tail
+    rows, listed = (M,), (M, k)
+    _logits_call("topk_distill", dev, stream, logits.data_ptr(), dt, M, V, ld, float(scale),
+                 _row_array(ids, "ids", torch.int32, listed, dev),
+                 _row_array(teacher_logp, "teacher_logp", f32, listed, dev), k,
+                 DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(loss, "loss", f32, rows, dev),
+                 _row_array(lse, "lse", f32, rows, dev), _row_array(lse_tail, "lse_tail", f32, rows, dev))
     return loss, lse, lse_tail
 
 
@@ -391,20 +394,18 @@ def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 
     """Gradient of sum(dloss * loss) to the logits, lse and lse_tail as topk_distill gave them -> out [M, V] of
     the logits' dtype (may be the logits themselves: overwritten in place)."""
     import torch
-    _require_cuda(logits, ids, teacher_logp, lse, dloss, lse_tail, out)
+    _require_cuda(logits)
     dt, M, V, ld = _logit_rows(logits)
-    dev, f32 = logits.device, torch.float32
+    dev, f32 = logits.get_device(), torch.float32
     k = ids.shape[1] if ids.dim() == 2 else 0
     out, ldd = _dlogits(logits, out, M, V)
-    _row_array(ids, "ids", torch.int32, (M, k), dev)
-    _row_array(teacher_logp, "teacher_logp", f32, (M, k), dev)
-    for t, name in ((lse, "lse"), (dloss, "dloss"), (lse_tail, "lse_tail")):
-        _row_array(t, name, f32, (M,), dev)
-    with _on_device(logits):
-        st = lib().topk_distill_backward(_ptr(logits), dt, M, V, ld, float(scale), _ptr(ids), _ptr(teacher_logp), k,
-                                         DISTILL_TAIL if tail else DISTILL_NORMALIZED, _ptr(lse), _ptr(lse_tail),
-                                         _ptr(dloss), _ptr(out), ldd, _stream(logits, stream))
-    _check(st, "topk_distill_backward")
+    rows, listed = (M,), (M, k)
+    _logits_call("topk_distill_backward", dev, stream, logits.data_ptr(), dt, M, V, ld, float(scale),
+                 _row_array(ids, "ids", torch.int32, listed, dev),
+                 _row_array(teacher_logp, "teacher_logp", f32, listed, dev), k,
+                 DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(lse, "lse", f32, rows, dev),
+                 _row_array(lse_tail, "lse_tail", f32, rows, dev), _row_array(dloss, "dloss", f32, rows, dev),
+                 out.data_ptr(), ldd)
     return out
 
 

@@ -34,12 +34,12 @@ constexpr int kU = 4;                              // vectors per thread and ste
 constexpr int kSlack = 32;                         // a cut leaves at most k + kSlack keys
 constexpr int kMaxKept = kMaxListed + kSlack;
 constexpr int kCandidates = kThreads * 8 + kMaxKept;  // one vector of every thread beside a list that was cut
-constexpr int kCutAt = 1024;                       // candidates at which a list is cut
 constexpr int kBins = 1024;
 constexpr int kMaxCluster = 8;
 constexpr int kMapColumns = 1 << 18;               // columns per bit map (32 KB)
 constexpr float kNoRef = -1.7014118346046923e38f;  // R of nothing: -2^127, below every c x
 static_assert(kMaxCluster * kMaxKept <= kCandidates, "the first CTA's list takes what every CTA of a cluster kept");
+static_assert(kBins == 4 * kThreads, "four bins per thread");
 static_assert(kThreads >= kMaxListed, "one thread per listed column");
 
 enum Mode { kLogprobs = 0, kNormalized = 1, kTailBucket = 2 };
@@ -84,9 +84,12 @@ __device__ __forceinline__ int key_column(unsigned long long key) {
 struct TopShared {
   unsigned long long key[kCandidates];
   unsigned long long kept[kMaxKept];
+  uint4 vec[kThreads];  // a thread's vector with candidates, to take single elements from
   int bins[kBins];
+  unsigned long long ends[2 * kWarps];
   int warp_sum[kWarps];
-  int count, kept_count, above, bin;
+  uint32_t warp_bound[kWarps];
+  int count, kept_count, above, with, bin;
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -101,64 +104,56 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // Cuts the list's first n keys to those that include the k largest: at most k + kSlack, in key[0 .. count).
-// Returns the lower bound that the cut used (0: nothing was cut). All threads of the CTA call.
+// Returns the lower bound that the cut used (0: nothing was cut). All threads of the CTA call, after a barrier
+// that follows the last append.
 __device__ unsigned long long cut_list(TopShared& sh, int n, int k) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kPer = (kCandidates + kThreads - 1) / kThreads;
-  unsigned long long mine[kPer], lo = ~0ull, hi = 0;
+  unsigned long long lo = ~0ull, hi = 0;
   int keys = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int j = i * kThreads + tid;
-    mine[i] = j < n ? sh.key[j] : 0ull;
-    if (mine[i]) {
+  for (int j = tid; j < n; j += kThreads) {
+    const unsigned long long key = sh.key[j];
+    if (key) {
       ++keys;
-      lo = min(lo, mine[i]);
-      hi = max(hi, mine[i]);
+      lo = min(lo, key);
+      hi = max(hi, key);
     }
   }
-  // the range of the keys, and their number: words 0..3 of the bins as scratch for the first reduction
   keys = __reduce_add_sync(0xFFFFFFFFu, keys);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
     hi = max(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
   }
-  auto* ends = reinterpret_cast<unsigned long long*>(sh.bins);
   if (lane == 0) {
-    ends[2 * warp] = lo;
-    ends[2 * warp + 1] = hi;
+    sh.ends[2 * warp] = lo;
+    sh.ends[2 * warp + 1] = hi;
     sh.warp_sum[warp] = keys;
   }
   if (tid == 0) sh.kept_count = 0;
+  auto* bins4 = reinterpret_cast<int4*>(sh.bins);
+  bins4[tid] = make_int4(0, 0, 0, 0);
   __syncthreads();
   keys = 0;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) {
     keys += sh.warp_sum[i];
-    lo = min(lo, ends[2 * i]);
-    hi = max(hi, ends[2 * i + 1]);
+    lo = min(lo, sh.ends[2 * i]);
+    hi = max(hi, sh.ends[2 * i + 1]);
   }
-  __syncthreads();
   unsigned long long cut = 0;
   if (keys > k + kSlack) {
     int want = k;  // of the keys in [lo, hi]: those above are in
     while (true) {
       const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
       const int shift = max(bits - 10, 0);  // (hi - lo) >> shift < 1024
-      for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (mine[i] >= lo && mine[i] <= hi && mine[i]) atomicAdd(&sh.bins[static_cast<int>((mine[i] - lo) >> shift)], 1);
+      for (int j = tid; j < n; j += kThreads) {
+        const unsigned long long key = sh.key[j];
+        if (key >= lo && key <= hi) atomicAdd(&sh.bins[static_cast<int>((key - lo) >> shift)], 1);
+      }
       __syncthreads();
       // from the top: thread t holds bins 1023 - 4 t .. 1020 - 4 t
-      int b[4], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        b[i] = sh.bins[kBins - 1 - (4 * tid + i)];
-        sum += b[i];
-      }
+      const int4 b4 = bins4[kThreads - 1 - tid];
+      const int b[4] = {b4.w, b4.z, b4.y, b4.x}, sum = (b4.x + b4.y) + (b4.z + b4.w);
       int scan = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -168,14 +163,16 @@ __device__ unsigned long long cut_list(TopShared& sh, int n, int k) {
       if (lane == 31) sh.warp_sum[warp] = scan;
       __syncthreads();
       int above = scan - sum;
-      for (int i = 0; i < warp; ++i) above += sh.warp_sum[i];
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i)
+        if (i < warp) above += sh.warp_sum[i];
       if (above < want && above + sum >= want) {  // the want-th key lies in one of this thread's bins
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (above < want && above + b[i] >= want) {
             sh.bin = kBins - 1 - (4 * tid + i);
             sh.above = above;
-            sh.count = above + b[i];
+            sh.with = above + b[i];
             above = want;  // found
           } else {
             above += b[i];
@@ -183,19 +180,20 @@ __device__ unsigned long long cut_list(TopShared& sh, int n, int k) {
         }
       }
       __syncthreads();
-      const int bin = sh.bin, in = sh.above, with = sh.count;
-      cut = lo + (static_cast<unsigned long long>(bin) << shift);
-      // keys at or above the cut: k - want from earlier rounds, and `with`
-      if (k - want + with <= k + kSlack || shift == 0) break;
-      want -= in;
+      cut = lo + (static_cast<unsigned long long>(sh.bin) << shift);
+      // keys at or above the cut: k - want of earlier rounds, and `with`
+      if (k - want + sh.with <= k + kSlack || shift == 0) break;
+      want -= sh.above;
       hi = min(hi, cut + ((1ull << shift) - 1));
       lo = cut;
+      bins4[tid] = make_int4(0, 0, 0, 0);
       __syncthreads();
     }
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (mine[i] && mine[i] >= cut) sh.kept[atomicAdd(&sh.kept_count, 1)] = mine[i];
+  for (int j = tid; j < n; j += kThreads) {
+    const unsigned long long key = sh.key[j];
+    if (key && key >= cut) sh.kept[atomicAdd(&sh.kept_count, 1)] = key;
+  }
   __syncthreads();
   const int kept = sh.kept_count;
   for (int i = tid; i < kept; i += kThreads) sh.key[i] = sh.kept[i];
@@ -269,20 +267,43 @@ struct ListShared {
   float q[kMaxListed], lq[kMaxListed];
 };
 
-// Columns whose logit reaches the bound go to the list; a full list drops them (the caller sees it by the count).
+// The elements of a vector above the bound, as a mask: bit (i >> 1) + 16 (i & 1) for element i.
+__device__ __forceinline__ uint32_t above_mask(const uint4& x, float thr, uint16_t) {
+  const uint32_t t = __float_as_uint(thr) >> 16, t2 = t | (t << 16);
+  const auto gt = [&](uint32_t w) {
+    uint32_t r;
+    asm("set.gt.u32.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(t2));
+    return r;
+  };
+  return (gt(x.x) & 0x00010001u) | (gt(x.y) & 0x00020002u) | (gt(x.z) & 0x00040004u) | (gt(x.w) & 0x00080008u);
+}
+__device__ __forceinline__ uint32_t above_mask(const uint4& x, float thr, float) {
+  return (__uint_as_float(x.x) > thr ? 0x00001u : 0u) | (__uint_as_float(x.y) > thr ? 0x10000u : 0u) |
+         (__uint_as_float(x.z) > thr ? 0x00002u : 0u) | (__uint_as_float(x.w) > thr ? 0x20000u : 0u);
+}
+
+// The vector's columns above the bound go to the list; a full list drops them (the caller sees it by the count).
 template <typename T>
-__device__ __forceinline__ bool append(TopShared& sh, const uint32_t (&w)[4], int col, int V, float thr, bool equal) {
+__device__ __forceinline__ bool append(TopShared& sh, const uint4& x, int col, float thr, int cut_at) {
+  uint32_t mask = above_mask(x, thr, T());
   bool much = false;
-#pragma unroll
-  for (int i = 0; i < kVecOf<T>; ++i) {
-    const float v = elem(w, i, T());
-    if ((equal ? v >= thr : v > thr) && v > -kLogitBound && col + i >= 0 && col + i < V) {
+  if (mask) {
+    sh.vec[threadIdx.x] = x;
+    const T* mine = reinterpret_cast<const T*>(&sh.vec[threadIdx.x]);
+    do {
+      const int bit = __ffs(mask) - 1, i = 2 * (bit & 15) + (bit >> 4);
+      mask &= mask - 1;
       const int at = atomicAdd(&sh.count, 1);
-      if (at < kCandidates) sh.key[at] = rank_key(v, col + i);
-      much |= at >= kCutAt;
-    }
+      if (at < kCandidates) sh.key[at] = rank_key(logit(mine, i), col + i);
+      much |= at >= cut_at;
+    } while (mask);
   }
   return much;
+}
+
+// The bound that a cut at `cut` gives: later columns with its value rank behind the k kept.
+__device__ __forceinline__ void raise(float& thr, unsigned long long cut) {
+  if (cut) thr = fmaxf(thr, order_value(static_cast<uint32_t>(cut >> 32)));
 }
 
 // kEntropy: w is kept; kTop: alternatives are listed (both kLogprobs only).
@@ -346,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
   F2 s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
   const F2 c2 = pack2(c, c);
   if (kTop && tid == 0) top.count = 0;
+  const int cut_at = 2 * k + 64;  // candidates at which the list is cut
   constexpr int kMapVecs = kMapColumns / VEC;
   int map_begin = v_begin;  // first vector of the bit map
 
@@ -460,32 +482,34 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
       }
     }
     if (kTop) {
-      const bool first = v0 == v_begin;
-      if (first) {
-        // thr: the k-th largest of the threads' maxima, to 16 bits (rounded down)
+      if (v0 == v_begin) {
+        // Every warp's ceil(k / 8)-th largest thread maximum, to 16 bits; at least k maxima reach the least of them.
         const uint32_t key = order_bits(cm) >> 16;
+        const int each = (k + kWarps - 1) / kWarps;
         uint32_t t = 0;
 #pragma unroll 1
         for (int bit = 15; bit >= 0; --bit) {
           const uint32_t next = t | (1u << bit);
-          if (__syncthreads_count(key >= next) >= k) t = next;
+          if (__popc(__ballot_sync(0xFFFFFFFFu, key >= next)) >= each) t = next;
         }
-        thr = fmaxf(order_value(t << 16), -kLogitBound);  // NaN (fewer than k threads saw one): the bound
+        if (lane == 0) top.warp_bound[warp] = t;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) t = min(t, top.warp_bound[i]);
+        // this step's columns that equal it count: the bound is the value before it (-0 is +0)
+        t -= t == 0x8000u ? 2u : t > 0u ? 1u : 0u;
+        thr = fmaxf(order_value(sizeof(T) == 2 ? t << 16 : (t << 16) | 0xFFFFu), -kLogitBound);  // of NaN: the bound
       }
       bool much = false;
-      if (cm > thr || (first && cm == thr)) {
+      if (cm > thr) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
-          much |= append<T>(top, w, (v0 + u * kThreads + tid) * VEC - phase, V, thr, first);
-        }
+        for (int u = 0; u < kU; ++u)
+          much |= append<T>(top, in[u], (v0 + u * kThreads + tid) * VEC - phase, thr, cut_at);
       }
       if (__syncthreads_or(much)) {
         const int n = top.count;
-        __syncthreads();
         if (n <= kCandidates) {
-          const unsigned long long cut = cut_list(top, n, k);
-          if (cut) thr = fmaxf(thr, order_value(static_cast<uint32_t>(cut >> 32)));
+          raise(thr, cut_list(top, n, k));
         } else {
           // some of this step's columns found no place: what the step appended goes, and it is done again
           // vector by vector, a list that was cut taking one vector of every thread
@@ -493,21 +517,12 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
           for (int i = tid; i < kCandidates; i += kThreads)
             if (key_column(top.key[i]) >= from) top.key[i] = 0;
           __syncthreads();
-          unsigned long long cut = cut_list(top, kCandidates, k);
-          bool equal = first;
-          if (cut) thr = fmaxf(thr, order_value(static_cast<uint32_t>(cut >> 32)));
+          raise(thr, cut_list(top, kCandidates, k));
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            const uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
-            append<T>(top, w, (v0 + u * kThreads + tid) * VEC - phase, V, thr, equal);
+            append<T>(top, in[u], (v0 + u * kThreads + tid) * VEC - phase, thr, cut_at);
             __syncthreads();
-            const int n1 = top.count;
-            __syncthreads();
-            cut = cut_list(top, n1, k);
-            if (cut) {
-              thr = fmaxf(thr, order_value(static_cast<uint32_t>(cut >> 32)));
-              equal = false;
-            }
+            raise(thr, cut_list(top, top.count, k));
           }
         }
       }

@@ -104,7 +104,7 @@ def test_binding_refuses_cpu_and_wrong_tensors(nv):
             nv._logit_rows(bad)
     assert nv._logit_rows(torch.zeros(3, 9)[:, 1:6]) == (nv.F32, 3, 5, 9)
     assert nv._logit_rows(torch.zeros(1, 9).bfloat16()[:, :6]) == (nv.BF16, 1, 6, 9)
-    d = x.device
+    d = x.get_device()
     nv._row_array(torch.zeros(2, dtype=torch.int32), "tokens", torch.int32, (2,), d)
     for bad in (torch.zeros(2, dtype=torch.int64), torch.zeros(3, dtype=torch.int32),
                 torch.zeros(4, dtype=torch.int32)[::2]):
