@@ -268,7 +268,7 @@ NVFP4RL_API nvfp4rl_status ais_mixing(const float* logp_rollout, const float* lo
  *   left the list ends in (-1, -inf).
  * Arguments:
  *   tokens   int32 [M], or NULL (logp must then be NULL). A row whose token is outside [0, V)
- *            (padding) is not read: logp, entropy and lse 0, its list (-1, -inf).
+ *            (padding) is ignored, whatever it holds: logp, entropy and lse 0, its list (-1, -inf).
  *   k        alternatives per row, 0 .. min(V, 256); 0: top_ids and top_logp are not used.
  *   logp, entropy, lse  out, fp32 [M], each may be NULL. top_ids int32 [M][k], top_logp fp32 [M][k].
  * A row without an unmasked column: lse = logp = -inf, entropy 0. A NaN row lists (-1, NaN).
@@ -312,7 +312,7 @@ NVFP4RL_API nvfp4rl_status token_logprobs_backward(const void* logits, int32_t d
  *   ids      int32 [M][k], teacher_logp fp32 [M][k] (-inf: q_i = 0), k in [1, 256]; mode as above.
  *   loss     out, fp32 [M]. lse, lse_tail  out, fp32 [M] or NULL: ln sum exp(z) over the row, and over its
  *            unlisted columns (TAIL only), as topk_distill_backward takes them.
- * A row without an entry (or, NORMALIZED, with every l_i = -inf) is not read: loss, lse and lse_tail 0.
+ * A row without an entry (or, NORMALIZED, with every l_i = -inf) is ignored: loss, lse and lse_tail 0.
  * A NaN among a row's counted l_i gives a NaN loss.
  */
 NVFP4RL_API nvfp4rl_status topk_distill(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld, float scale,

@@ -31,14 +31,15 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kU = 4;                              // vectors per thread and step
-constexpr int kSlack = 32;                         // a cut leaves at most k + kSlack keys
-constexpr int kMaxKept = kMaxListed + kSlack;
+constexpr int kMaxKept = 256;                      // a cut leaves at most this many keys
 constexpr int kCandidates = kThreads * 8 + kMaxKept;  // one vector of every thread beside a list that was cut
 constexpr int kBins = 1024;
 constexpr int kMaxCluster = 8;
 constexpr int kMapColumns = 1 << 18;               // columns per bit map (32 KB)
 constexpr float kNoRef = -1.7014118346046923e38f;  // R of nothing: -2^127, below every c x
-static_assert(kMaxCluster * kMaxKept <= kCandidates, "the first CTA's list takes what every CTA of a cluster kept");
+static_assert(kMaxListed <= kMaxKept && kMaxKept <= kThreads, "a cut list holds the k alternatives, a key per thread");
+static_assert(kMaxCluster * kMaxListed <= kCandidates, "a cluster's lists fit the first CTA's");
+static_assert(sizeof(unsigned long long) * kCandidates % 16 == 0, "keys are read in pairs");
 static_assert(kBins == 4 * kThreads, "four bins per thread");
 static_assert(kThreads >= kMaxListed, "one thread per listed column");
 
@@ -51,9 +52,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // The address, in CTA `rank`, of what p is in this CTA's shared memory.
 __device__ __forceinline__ uint32_t map_shared(const void* p, uint32_t rank) {
   uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
@@ -90,6 +90,8 @@ struct TopShared {
   int warp_sum[kWarps];
   uint32_t warp_bound[kWarps];
   int count, kept_count, above, with, bin;
+  // of the cluster's first CTA, with more than one: what every CTA kept, k keys each
+  __device__ __forceinline__ unsigned long long* merged() { return reinterpret_cast<unsigned long long*>(this + 1); }
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -103,11 +105,11 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Cuts the list's first n keys to those that include the k largest: at most k + kSlack, in key[0 .. count).
-// Returns the lower bound that the cut used (0: nothing was cut). All threads of the CTA call, after a barrier
-// that follows the last append.
-__device__ unsigned long long cut_list(TopShared& sh, int n, int k) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Cuts a list of n keys, more than kMaxKept, to those that include the k largest: at most min(k + 32, kMaxKept), in
+// key[0 .. count). Returns the lower bound that the cut used (0: nothing was cut). All threads of the CTA call, after a
+// barrier that follows the last append. The histogram takes about 3100 cycles (its chain of barriers and scans).
+__device__ unsigned long long cut_long(TopShared& sh, int n, int k) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = min(k + 32, kMaxKept);
   unsigned long long lo = ~0ull, hi = 0;
   int keys = 0;
   for (int j = tid; j < n; j += kThreads) {
@@ -141,7 +143,7 @@ __device__ unsigned long long cut_list(TopShared& sh, int n, int k) {
     hi = max(hi, sh.ends[2 * i + 1]);
   }
   unsigned long long cut = 0;
-  if (keys > k + kSlack) {
+  if (keys > most) {
     int want = k;  // of the keys in [lo, hi]: those above are in
     while (true) {
       const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
@@ -181,8 +183,8 @@ __device__ unsigned long long cut_list(TopShared& sh, int n, int k) {
       }
       __syncthreads();
       cut = lo + (static_cast<unsigned long long>(sh.bin) << shift);
-      // keys at or above the cut: k - want of earlier rounds, and `with`
-      if (k - want + sh.with <= k + kSlack || shift == 0) break;
+      // keys at or above the cut: k - want of earlier rounds, and `with` (one key per bin at shift 0: k)
+      if (k - want + sh.with <= most || shift == 0) break;
       want -= sh.above;
       hi = min(hi, cut + ((1ull << shift) - 1));
       lo = cut;
@@ -200,6 +202,59 @@ __device__ unsigned long long cut_list(TopShared& sh, int n, int k) {
   if (tid == 0) sh.count = kept;
   __syncthreads();
   return cut;
+}
+
+// The k largest of at most kMaxKept keys, in order, in sh.key[0 .. count): every key counts those above it, with 4, 2 or 1
+// threads to a key, two keys a load. Returns the k-th (0: there are fewer). Called as cut_long.
+__device__ unsigned long long sort_short(TopShared& sh, int n, int k) {
+  const int p = n <= kThreads / 4 ? 2 : n <= kThreads / 2 ? 1 : 0, parts = 1 << p;
+  const int i = static_cast<int>(threadIdx.x) >> p, part = threadIdx.x & (parts - 1);
+  const unsigned long long key = i < n ? sh.key[i] : 0ull;
+  int rank = 0;
+  if (__any_sync(0xFFFFFFFFu, key != 0)) {
+    const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(sh.key);
+#pragma unroll 4
+    for (int j = part; 2 * j < n; j += parts) {
+      const ulonglong2 v = pairs[j];
+      rank += (v.x > key) + (v.y > key && 2 * j + 1 < n);
+    }
+    for (int o = 1; o < parts; o <<= 1) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, o);
+  }
+  const bool in = part == 0 && key && rank < k;
+  const int kept = __syncthreads_count(in);
+  if (in) sh.key[rank] = key;
+  if (threadIdx.x == 0) sh.count = kept;
+  __syncthreads();
+  return kept == k ? sh.key[k - 1] : 0ull;
+}
+
+// Of `lists` sorted lists of k keys each (0 where there is none, at the end) those that can be among the k largest, into
+// sh.key: ceil(k / lists) keys of every list reach the least of the lists' ceil(k / lists)-th keys.
+__device__ void gather_lists(TopShared& sh, const unsigned long long* from, int lists, int k) {
+  const int each = (k + lists - 1) / lists;
+  unsigned long long bound = ~0ull;
+  for (int l = 0; l < lists; ++l) bound = min(bound, from[l * k + each - 1]);
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < lists * k; i += kThreads) {
+    const unsigned long long key = from[i];
+    if (key && key >= bound) sh.key[atomicAdd(&sh.count, 1)] = key;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ unsigned long long cut_list(TopShared& sh, int n, int k) {
+  return n <= kMaxKept ? sort_short(sh, n, k) : cut_long(sh, n, k);
+}
+
+// The k largest of the list, in order, in key[0 .. count).
+__device__ void sort_list(TopShared& sh, int k) {
+  int n = sh.count;
+  if (n > kMaxKept) {
+    cut_long(sh, n, k);
+    n = sh.count;
+  }
+  sort_short(sh, n, k);
 }
 
 // ---- the streamed sums ----
@@ -232,6 +287,26 @@ __device__ __forceinline__ void set_masked(uint32_t (&w)[4], int i) {
     w[i >> 1] = (i & 1) ? (w[i >> 1] & 0x0000FFFFu) | 0xFF800000u : (w[i >> 1] & 0xFFFF0000u) | 0x0000FF80u;
   else
     w[i & 3] = 0xFF800000u;
+}
+
+// The vector at column col of a row of V: what lies outside is masked.
+template <typename T>
+__device__ __forceinline__ uint4 load_edge(const T* x, int col, int V) {
+  constexpr int VEC = kVecOf<T>;
+  if (col >= 0 && col + VEC <= V) return ld_logits16(x + col);
+  uint4 r = masked_vec<T>();
+#pragma unroll 1
+  for (int i = VEC - 1; i >= 0; --i) {  // the elements enter at the low end, the last one first
+    const bool in = col + i >= 0 && col + i < V;
+    if (sizeof(T) == 2) {
+      const uint32_t b = in ? __float_as_uint(logit(x, col + i)) >> 16 : 0xFF80u;
+      r = make_uint4((r.x << 16) | b, __funnelshift_l(r.x, r.y, 16), __funnelshift_l(r.y, r.z, 16),
+                     __funnelshift_l(r.z, r.w, 16));
+    } else {
+      r = make_uint4(in ? __float_as_uint(logit(x, col + i)) : 0xFF800000u, r.x, r.y, r.z);
+    }
+  }
+  return r;
 }
 
 __device__ float block_max(float v, float* red) {
@@ -282,21 +357,33 @@ __device__ __forceinline__ uint32_t above_mask(const uint4& x, float thr, float)
          (__uint_as_float(x.z) > thr ? 0x00002u : 0u) | (__uint_as_float(x.w) > thr ? 0x20000u : 0u);
 }
 
-// The vector's columns above the bound go to the list; a full list drops them (the caller sees it by the count).
-template <typename T>
-__device__ __forceinline__ bool append(TopShared& sh, const uint4& x, int col, float thr, int cut_at) {
-  uint32_t mask = above_mask(x, thr, T());
-  bool much = false;
-  if (mask) {
-    sh.vec[threadIdx.x] = x;
-    const T* mine = reinterpret_cast<const T*>(&sh.vec[threadIdx.x]);
-    do {
-      const int bit = __ffs(mask) - 1, i = 2 * (bit & 15) + (bit >> 4);
-      mask &= mask - 1;
-      const int at = atomicAdd(&sh.count, 1);
-      if (at < kCandidates) sh.key[at] = rank_key(logit(mine, i), col + i);
-      much |= at >= cut_at;
-    } while (mask);
+// The columns above the bound of the first N vectors in x go to the list; a full list drops them (the caller sees it by
+// the count). Vector u starts at column col + u kThreads VEC.
+template <typename T, int N>
+__device__ __forceinline__ bool append(TopShared& sh, const uint4* x, int col, float thr, int cut_at) {
+  constexpr int VEC = kVecOf<T>;
+  uint32_t mask[N];
+  int found = 0;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    mask[u] = above_mask(x[u], thr, T());
+    found += __popc(mask[u]);
+  }
+  if (!found) return false;
+  int at = atomicAdd(&sh.count, found);
+  const bool much = at + found > cut_at;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    if (mask[u]) {
+      sh.vec[threadIdx.x] = x[u];
+      const T* mine = reinterpret_cast<const T*>(&sh.vec[threadIdx.x]);
+      do {
+        const int bit = __ffs(mask[u]) - 1, i = 2 * (bit & 15) + (bit >> 4);
+        mask[u] &= mask[u] - 1;
+        if (at < kCandidates) sh.key[at] = rank_key(logit(mine, i), col + u * (kThreads * VEC) + i);
+        ++at;
+      } while (mask[u]);
+    }
   }
   return much;
 }
@@ -323,6 +410,25 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
   const T* x = static_cast<const T*>(a.x) + row * a.ld;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int V = static_cast<int>(a.V), k = a.k;
+  const int phase = vec_phase(x);
+  const int vecs = (V + phase + VEC - 1) / VEC;  // vector v: columns v VEC - phase ..
+  const int share = (vecs + static_cast<int>(cluster) - 1) / static_cast<int>(cluster);
+  const int v_begin = static_cast<int>(rank) * share, v_end = min(v_begin + share, vecs);
+  uint4 in[kU];
+  const auto load_step = [&](int v0) {
+    if (v0 * VEC >= phase && v0 + kU * kThreads <= v_end && (v0 + kU * kThreads) * VEC - phase <= V) {
+      const T* at = x + ((v0 + tid) * VEC - phase);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) in[u] = ld_logits16(at + u * (kThreads * VEC));
+    } else {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int v = v0 + u * kThreads + tid;
+        in[u] = v < v_end ? load_edge(x, v * VEC - phase, V) : masked_vec<T>();
+      }
+    }
+  };
+  load_step(v_begin);  // beside what the row needs else
   int token = -1;
   if (kDistill) {
     if (warp == 0) {
@@ -357,17 +463,14 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
     }
   }
 
+  if (cluster > 1) cluster_arrive();
   const float at_token = kMode == kLogprobs && tid == 0 && token >= 0 ? logit(x, token) : 0.0f;
   const float c = a.scale * kLog2E;
-  const int phase = vec_phase(x);
-  const int vecs = (V + phase + VEC - 1) / VEC;  // vector v: columns v VEC - phase ..
-  const int share = (vecs + static_cast<int>(cluster) - 1) / static_cast<int>(cluster);
-  const int v_begin = static_cast<int>(rank) * share, v_end = min(v_begin + share, vecs);
   float m = -kLogitBound, R = kNoRef, thr = -kLogitBound;
   F2 s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
   const F2 c2 = pack2(c, c);
   if (kTop && tid == 0) top.count = 0;
-  const int cut_at = 2 * k + 64;  // candidates at which the list is cut
+  const int cut_at = k <= 96 ? kMaxKept : 2 * k + 64;  // candidates above which the list is cut
   constexpr int kMapVecs = kMapColumns / VEC;
   int map_begin = v_begin;  // first vector of the bit map
 
@@ -388,33 +491,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
       }
       __syncthreads();
     }
-    uint4 in[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int v = v0 + u * kThreads + tid, col = v * VEC - phase;
-      in[u] = masked_vec<T>();
-      if (v < v_end) {
-        if (col >= 0 && col + VEC <= V) {
-          in[u] = ld_logits16(x + col);
-        } else {  // a row's end: its elements one by one
-          uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
-          for (int i = 0; i < VEC; ++i)
-            if (col + i >= 0 && col + i < V) {
-              const uint32_t b = __float_as_uint(logit(x, col + i));
-              if (sizeof(T) == 4) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (j == i) w[j] = b;
-              } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (j == (i >> 1)) w[j] = (i & 1) ? (w[j] & 0xFFFFu) | b : (w[j] & 0xFFFF0000u) | (b >> 16);
-              }
-            }
-          in[u] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-    }
+    if (v0 > v_begin) load_step(v0);
     if (kMode == kTailBucket) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -486,11 +563,19 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
         // Every warp's ceil(k / 8)-th largest thread maximum, to 16 bits; at least k maxima reach the least of them.
         const uint32_t key = order_bits(cm) >> 16;
         const int each = (k + kWarps - 1) / kWarps;
-        uint32_t t = 0;
+        uint32_t t = __reduce_max_sync(0xFFFFFFFFu, key);
+        if (each <= 4) {  // the next smaller maximum, till enough reach it
+          int reach = __popc(__ballot_sync(0xFFFFFFFFu, key == t));
+          while (reach < each) {
+            t = __reduce_max_sync(0xFFFFFFFFu, key < t ? key : 0u);
+            reach = __popc(__ballot_sync(0xFFFFFFFFu, key >= t));
+          }
+        } else {
+          uint32_t low = __reduce_min_sync(0xFFFFFFFFu, key);  // all reach it
 #pragma unroll 1
-        for (int bit = 15; bit >= 0; --bit) {
-          const uint32_t next = t | (1u << bit);
-          if (__popc(__ballot_sync(0xFFFFFFFFu, key >= next)) >= each) t = next;
+          for (uint32_t step = 0x80000000u >> __clz((t - low) | 1u); step; step >>= 1)
+            if (low + step <= t && __popc(__ballot_sync(0xFFFFFFFFu, key >= low + step)) >= each) low += step;
+          t = low;
         }
         if (lane == 0) top.warp_bound[warp] = t;
         __syncthreads();
@@ -501,11 +586,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
         thr = fmaxf(order_value(sizeof(T) == 2 ? t << 16 : (t << 16) | 0xFFFFu), -kLogitBound);  // of NaN: the bound
       }
       bool much = false;
-      if (cm > thr) {
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-          much |= append<T>(top, in[u], (v0 + u * kThreads + tid) * VEC - phase, thr, cut_at);
-      }
+      if (cm > thr) much = append<T, kU>(top, in, (v0 + tid) * VEC - phase, thr, cut_at);
       if (__syncthreads_or(much)) {
         const int n = top.count;
         if (n <= kCandidates) {
@@ -520,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
           raise(thr, cut_list(top, kCandidates, k));
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            append<T>(top, in[u], (v0 + u * kThreads + tid) * VEC - phase, thr, cut_at);
+            append<T, 1>(top, &in[u], (v0 + u * kThreads + tid) * VEC - phase, thr, cut_at);
             __syncthreads();
             raise(thr, cut_list(top, top.count, k));
           }
@@ -547,26 +628,25 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
   sum = sh.sums[0];
 #pragma unroll
   for (int i = 1; i < kWarps; ++i) merge(sum, sh.sums[i]);
-  if (kTop) cut_list(top, top.count, k);
+  if (kTop) sort_list(top, k);
   if (cluster > 1) {
-    const int slots = k + kSlack;
-    cluster_sync();  // every CTA's list is its own until here
+    cluster_wait();  // every CTA has started (the arrival at the kernel's start): its shared memory is there
     if (tid == 0) {
       const uint32_t at = map_shared(&sh.parts[rank], 0);
       st_cluster(at, sum.R);
       st_cluster(at + 4, sum.s);
       st_cluster(at + 8, sum.w);
     }
-    if (kTop && rank > 0)
-      for (int i = tid; i < slots; i += kThreads)
-        st_cluster(map_shared(&top.key[rank * slots + i], 0), i < top.count ? top.key[i] : 0ull);
-    if (kTop && rank == 0)
-      for (int i = top.count + tid; i < slots; i += kThreads) top.key[i] = 0ull;
-    cluster_sync();
+    if (kTop && tid < k) st_cluster(map_shared(top.merged() + rank * k + tid, 0), tid < top.count ? top.key[tid] : 0ull);
+    cluster_arrive();
+    cluster_wait();
     if (rank > 0) return;
     sum = sh.parts[0];
     for (uint32_t i = 1; i < cluster; ++i) merge(sum, sh.parts[i]);
-    if (kTop) cut_list(top, static_cast<int>(cluster) * slots, k);
+    if (kTop) {
+      gather_lists(top, top.merged(), static_cast<int>(cluster), k);
+      sort_list(top, k);
+    }
   }
   if (sum.R > kLogitBound * c) sum.s = NAN;  // a logit above 2^100
 
@@ -616,31 +696,17 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
     }
     if (a.lse) a.lse[row] = empty ? -INFINITY : fmaf(sum.R, kLn2, ln_s);
   }
-  if (kTop) {
-    const int n = top.count;  // k or a few more, or all there are
-    for (int i = tid; i < max(n, k); i += kThreads) {
-      if (i < n && !bad) {
-        const unsigned long long key = top.key[i];
-        int before = 0;
-        for (int j = 0; j < n; ++j) before += top.key[j] > key;
-        if (before < k) {
-          const int id = key_column(key);
-          a.top_ids[row * k + before] = id;
-          a.top_logp[row * k + before] =
-              fmaf(order_value(static_cast<uint32_t>(key >> 32)), c, -sum.R) * kLn2 - ln_s;
-        }
-      }
-      if (i < k && (i >= n || bad)) {
-        a.top_ids[row * k + i] = -1;
-        a.top_logp[row * k + i] = bad ? NAN : -INFINITY;
-      }
-    }
+  if (kTop && tid < k) {
+    const unsigned long long key = tid < top.count && !bad ? top.key[tid] : 0ull;
+    a.top_ids[row * k + tid] = key ? key_column(key) : -1;
+    a.top_logp[row * k + tid] =
+        bad ? NAN : key ? fmaf(order_value(static_cast<uint32_t>(key >> 32)), c, -sum.R) * kLn2 - ln_s : -INFINITY;
   }
 }
 
 template <typename T, int kMode, bool kEntropy, bool kTop>
 nvfp4rl_status launch(const LogitsArgs& a, unsigned cluster, const DeviceInfo& dev, cudaStream_t st) {
-  size_t smem = kTop ? sizeof(TopShared) : kMode == kLogprobs ? 0 : sizeof(ListShared);
+  size_t smem = kTop ? sizeof(TopShared) + (cluster > 1 ? static_cast<size_t>(cluster) * a.k * 8 : 0) : kMode == kLogprobs ? 0 : sizeof(ListShared);
   if (kMode == kTailBucket) {
     const int64_t share = (a.V + 2 * kVecOf<T>) / cluster + 2 * kVecOf<T>;
     smem += align_up(static_cast<size_t>(std::min<int64_t>(share, kMapColumns) + 31) / 8 + 4, 16);
