@@ -295,6 +295,15 @@ def _row_array(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
+def _row_out(t, name, dtype, shape, device):
+    """An output of that kind and its address: made here, or the caller's, checked."""
+    if t is not None:
+        return t, _row_array(t, name, dtype, shape, device)
+    import torch
+    t = torch.empty(*shape, dtype=dtype, device=device)
+    return t, t.data_ptr()
+
+
 def _logits_call(name, device, stream, *args):
     """Calls the C function on the logits' device (the library launches on the current one) and its current
     stream, or the stream given."""
@@ -319,33 +328,29 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy:
     import torch
     _require_cuda(logits)
     dt, M, V, ld = _logit_rows(logits)
-    dev, where, f32, i32 = logits.get_device(), logits.device, torch.float32, torch.int32
+    dev, f32, rows = logits.get_device(), torch.float32, (M,)
+    p_logp = p_h = p_ids = p_top = None
     if tokens is not None:
-        logp = torch.empty(M, dtype=f32, device=where) if logp is None else logp
+        logp, p_logp = _row_out(logp, "logp", f32, rows, dev)
     elif logp is not None:
         raise ValueError("logp needs tokens")
-    h = None if not entropy else torch.empty(M, dtype=f32, device=where) if h is None else h
-    lse = torch.empty(M, dtype=f32, device=where) if lse is None else lse
+    if entropy:
+        h, p_h = _row_out(h, "h", f32, rows, dev)
+    lse, p_lse = _row_out(lse, "lse", f32, rows, dev)
     if k > 0:
-        top_ids = torch.empty(M, k, dtype=i32, device=where) if top_ids is None else top_ids
-        top_logp = torch.empty(M, k, dtype=f32, device=where) if top_logp is None else top_logp
-    else:
-        top_ids = top_logp = None
-    rows, listed = (M,), (M, k)
+        top_ids, p_ids = _row_out(top_ids, "top_ids", torch.int32, (M, k), dev)
+        top_logp, p_top = _row_out(top_logp, "top_logp", f32, (M, k), dev)
     _logits_call("token_logprobs", dev, stream, logits.data_ptr(), dt, M, V, ld,
-                 _row_array(tokens, "tokens", i32, rows, dev), float(scale), k, _row_array(logp, "logp", f32, rows, dev),
-                 _row_array(h, "h", f32, rows, dev), _row_array(lse, "lse", f32, rows, dev),
-                 _row_array(top_ids, "top_ids", i32, listed, dev),
-                 _row_array(top_logp, "top_logp", f32, listed, dev))
-    return logp, h, lse, top_ids, top_logp
+                 _row_array(tokens, "tokens", torch.int32, rows, dev), float(scale), k, p_logp, p_h, p_lse, p_ids, p_top)
+    return logp, h if entropy else None, lse, top_ids if k > 0 else None, top_logp if k > 0 else None
 
 
 def _dlogits(logits, out, M, V):
     """The gradient's tensor (made when None) and its row stride."""
     import torch
     if out is None:
-        return torch.empty(M, V, dtype=logits.dtype, device=logits.device), V
-    if out.dtype is not logits.dtype or out.shape != (M, V) or out.device != logits.device:
+        return torch.empty(M, V, dtype=logits.dtype, device=logits.get_device()), V
+    if out.dtype is not logits.dtype or out.shape != (M, V) or out.get_device() != logits.get_device():
         raise ValueError("out must have the logits' dtype, shape and device")
     return out, _logit_rows(out, "out")[3]
 
@@ -375,18 +380,18 @@ def topk_distill(logits, ids, teacher_logp, scale: float = 1.0, tail: bool = Fal
     import torch
     _require_cuda(logits)
     dt, M, V, ld = _logit_rows(logits)
-    dev, where, f32 = logits.get_device(), logits.device, torch.float32
+    dev, f32 = logits.get_device(), torch.float32
     k = ids.shape[1] if ids.dim() == 2 else 0
-    loss = torch.empty(M, dtype=f32, device=where) if loss is None else loss
-    lse = torch.empty(M, dtype=f32, device=where) if lse is None else lse
-    lse_tail = None if not tail else torch.empty(M, dtype=f32, device=where) if lse_tail is None else lse_tail
-    rows, listed = (M,), (M, k)
+    rows, listed, p_tail = (M,), (M, k), None
+    loss, p_loss = _row_out(loss, "loss", f32, rows, dev)
+    lse, p_lse = _row_out(lse, "lse", f32, rows, dev)
+    if tail:
+        lse_tail, p_tail = _row_out(lse_tail, "lse_tail", f32, rows, dev)
     _logits_call("topk_distill", dev, stream, logits.data_ptr(), dt, M, V, ld, float(scale),
                  _row_array(ids, "ids", torch.int32, listed, dev),
                  _row_array(teacher_logp, "teacher_logp", f32, listed, dev), k,
-                 DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(loss, "loss", f32, rows, dev),
-                 _row_array(lse, "lse", f32, rows, dev), _row_array(lse_tail, "lse_tail", f32, rows, dev))
-    return loss, lse, lse_tail
+                 DISTILL_TAIL if tail else DISTILL_NORMALIZED, p_loss, p_lse, p_tail)
+    return loss, lse, lse_tail if tail else None
 
 
 def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 1.0, tail: bool = False,

@@ -107,7 +107,7 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
 
 // Cuts a list of n keys, more than kMaxKept, to those that include the k largest: at most min(k + 32, kMaxKept), in
 // key[0 .. count). Returns the lower bound that the cut used (0: nothing was cut). All threads of the CTA call, after a
-// barrier that follows the last append. The histogram takes about 3100 cycles (its chain of barriers and scans).
+// barrier that follows the last append. For keys in any range, equal values among them.
 __device__ unsigned long long cut_long(TopShared& sh, int n, int k) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = min(k + 32, kMaxKept);
   unsigned long long lo = ~0ull, hi = 0;
@@ -204,6 +204,68 @@ __device__ unsigned long long cut_long(TopShared& sh, int n, int k) {
   return cut;
 }
 
+// The same for a list whose values lie above thr and at most at the threads' maxima m: one histogram of the values'
+// order bits, without the reductions of the keys' range, and cut_long only where too many keys share the cut's bin.
+__device__ unsigned long long cut_values(TopShared& sh, int n, int k, float thr, float m) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = min(k + 32, kMaxKept);
+  const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, order_bits(m));
+  if (lane == 0) sh.warp_bound[warp] = top;
+  if (tid == 0) {
+    sh.kept_count = 0;
+    sh.bin = 0;  // fewer than k: all stay
+    sh.with = n;
+  }
+  auto* bins4 = reinterpret_cast<int4*>(sh.bins);
+  bins4[tid] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  const uint32_t lo = order_bits(thr);
+  uint32_t hi = lo;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) hi = max(hi, sh.warp_bound[i]);
+  const int shift = max(22 - __clz((hi - lo) | 1u), 0);  // (hi - lo) >> shift < 1024
+  for (int j = tid; j < n; j += kThreads)
+    atomicAdd(&sh.bins[(static_cast<uint32_t>(sh.key[j] >> 32) - lo) >> shift], 1);
+  __syncthreads();
+  const int4 b4 = bins4[kThreads - 1 - tid];  // from the top: thread t holds bins 1023 - 4 t .. 1020 - 4 t
+  const int sum = (b4.x + b4.y) + (b4.z + b4.w);
+  int scan = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) sh.warp_sum[warp] = scan;
+  __syncthreads();
+  int above = scan - sum;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i)
+    if (i < warp) above += sh.warp_sum[i];
+  if (above < k && above + sum >= k) {  // the k-th value lies in one of this thread's bins
+    int bin = kBins - 1 - 4 * tid, with = above + b4.w;
+    if (with < k) --bin, with += b4.z;
+    if (with < k) --bin, with += b4.y;
+    if (with < k) --bin, with += b4.x;
+    sh.bin = bin;
+    sh.with = with;
+  }
+  __syncthreads();
+  if (sh.with > most) {
+    __syncthreads();
+    return cut_long(sh, n, k);
+  }
+  const uint32_t cut = lo + (static_cast<uint32_t>(sh.bin) << shift);
+  for (int j = tid; j < n; j += kThreads) {
+    const unsigned long long key = sh.key[j];
+    if (static_cast<uint32_t>(key >> 32) >= cut) sh.kept[atomicAdd(&sh.kept_count, 1)] = key;
+  }
+  __syncthreads();
+  const int kept = sh.kept_count;
+  if (tid < kept) sh.key[tid] = sh.kept[tid];
+  if (tid == 0) sh.count = kept;
+  __syncthreads();
+  return static_cast<unsigned long long>(cut) << 32;
+}
+
 // The k largest of at most kMaxKept keys, in order, in sh.key[0 .. count): every key counts those above it, with 4, 2 or 1
 // threads to a key, two keys a load. Returns the k-th (0: there are fewer). Called as cut_long.
 __device__ unsigned long long sort_short(TopShared& sh, int n, int k) {
@@ -243,11 +305,7 @@ __device__ void gather_lists(TopShared& sh, const unsigned long long* from, int 
   __syncthreads();
 }
 
-__device__ __forceinline__ unsigned long long cut_list(TopShared& sh, int n, int k) {
-  return n <= kMaxKept ? sort_short(sh, n, k) : cut_long(sh, n, k);
-}
-
-// The k largest of the list, in order, in key[0 .. count).
+// The k largest of the list, in order, in key[0 .. count). Counting costs n^2 / 3 instructions of a warp, a cut about 1200.
 __device__ void sort_list(TopShared& sh, int k) {
   int n = sh.count;
   if (n > kMaxKept) {
@@ -342,9 +400,10 @@ struct ListShared {
   float q[kMaxListed], lq[kMaxListed];
 };
 
-// The elements of a vector above the bound, as a mask: bit (i >> 1) + 16 (i & 1) for element i.
+// The elements of a vector above the bound, as a mask: bit (i >> 1) + 16 (i & 1) for element i. The bound is rounded
+// down to bf16 (a negative one away from zero): no candidate is lost, the keys decide.
 __device__ __forceinline__ uint32_t above_mask(const uint4& x, float thr, uint16_t) {
-  const uint32_t t = __float_as_uint(thr) >> 16, t2 = t | (t << 16);
+  const uint32_t b = __float_as_uint(thr), t = (b >> 16) + (b > 0x80000000u && (b & 0xFFFFu)), t2 = t | (t << 16);
   const auto gt = [&](uint32_t w) {
     uint32_t r;
     asm("set.gt.u32.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(t2));
@@ -473,6 +532,8 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
   const int cut_at = k <= 96 ? kMaxKept : 2 * k + 64;  // candidates above which the list is cut
   constexpr int kMapVecs = kMapColumns / VEC;
   int map_begin = v_begin;  // first vector of the bit map
+  bool much = false;        // this thread saw the list longer than cut_at since the last look
+  int looked = v_begin;     // first vector appended since then
 
   for (int v0 = v_begin; v0 < v_end; v0 += kU * kThreads) {
     if (kMode == kTailBucket && (v0 == v_begin || v0 - map_begin >= kMapVecs)) {
@@ -585,31 +646,38 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
         t -= t == 0x8000u ? 2u : t > 0u ? 1u : 0u;
         thr = fmaxf(order_value(sizeof(T) == 2 ? t << 16 : (t << 16) | 0xFFFFu), -kLogitBound);  // of NaN: the bound
       }
-      bool much = false;
-      if (cm > thr) much = append<T, kU>(top, in, (v0 + tid) * VEC - phase, thr, cut_at);
-      if (__syncthreads_or(much)) {
+      if (cm > thr) much |= append<T, kU>(top, in, (v0 + tid) * VEC - phase, thr, cut_at);
+      // The list is looked at after the first two steps (the bound is still loose), every fourth and the last one:
+      // a barrier in each step, with nothing to cut, took 40% more time (2048 rows of 152064, k = 1).
+      const int step = (v0 - v_begin) / (kU * kThreads);
+      const bool look = step < 2 || (step & 3) == 3 || v0 + kU * kThreads >= v_end;
+      if (look && __syncthreads_or(much)) {
+        much = false;
         const int n = top.count;
         if (n <= kCandidates) {
-          raise(thr, cut_list(top, n, k));
+          raise(thr, cut_values(top, n, k, thr, m));
         } else {
-          // some of this step's columns found no place: what the step appended goes, and it is done again
+          // some columns found no place: what came since the last look goes, and is read and appended again
           // vector by vector, a list that was cut taking one vector of every thread
-          const int from = v0 * VEC - phase;
+          const int from = looked * VEC - phase;
           for (int i = tid; i < kCandidates; i += kThreads)
             if (key_column(top.key[i]) >= from) top.key[i] = 0;
           __syncthreads();
-          raise(thr, cut_list(top, kCandidates, k));
+          raise(thr, cut_long(top, kCandidates, k));
+          for (int v = looked; v <= v0; v += kU * kThreads) {
+            load_step(v);
 #pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            append<T, 1>(top, &in[u], (v0 + u * kThreads + tid) * VEC - phase, thr, cut_at);
-            __syncthreads();
-            raise(thr, cut_list(top, top.count, k));
+            for (int u = 0; u < kU; ++u) {
+              append<T, 1>(top, &in[u], (v + u * kThreads + tid) * VEC - phase, thr, cut_at);
+              __syncthreads();
+              raise(thr, cut_long(top, top.count, k));
+            }
           }
         }
       }
+      if (look) looked = v0 + kU * kThreads;
     }
   }
-
   // the CTA's sums, then the cluster's, in a fixed order
   RowSum sum{R, 0.0f, 0.0f};
   {
@@ -628,7 +696,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
   sum = sh.sums[0];
 #pragma unroll
   for (int i = 1; i < kWarps; ++i) merge(sum, sh.sums[i]);
-  if (kTop) sort_list(top, k);
+  if (kTop) {
+    if (top.count > 128) cut_values(top, top.count, k, thr, m);
+    sort_list(top, k);
+  }
   if (cluster > 1) {
     cluster_wait();  // every CTA has started (the arrival at the kernel's start): its shared memory is there
     if (tid == 0) {

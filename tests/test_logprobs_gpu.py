@@ -104,6 +104,16 @@ def test_top_alternatives_of_hard_rows(nv, dtype, V, k):
     check_forward(nv, x, V, np.arange(8, dtype=np.int32), 1.0, k, dtype, what=f"hard {V} {k} {dtype}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,V,k", [(3, 30000, 20), (3, 30000, 130), (700, 9000, 64), (700, 1100, 256)])
+def test_top_alternatives_below_zero(nv, dtype, M, V, k):
+    """Negative logits only: the list's bounds fall between values, and round away from zero."""
+    r = synth.rng(33, V, k)
+    x = (-np.abs(r.standard_normal((M, V))) * 4 - 3 * r.random((M, 1))).astype(np.float32)
+    rows = np.arange(M) % V
+    check_forward(nv, _bits(x) if dtype == "bf16" else x, V, rows.astype(np.int32), 1.0, k, dtype, what=f"{V} {k}")
+
+
 def _bits(x):
     """bf16 bits of fp32 values that may be infinite."""
     b = synth.bf16_bits(np.where(np.isfinite(x), x, 0.0))
