@@ -32,13 +32,13 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kU = 4;                              // vectors per thread and step
 constexpr int kMaxKept = 256;                      // a cut leaves at most this many keys
-constexpr int kCandidates = kThreads * 8 + kMaxKept;  // one vector of every thread beside a list that was cut
+constexpr int kCandidates = kThreads / 2 * 8 + kMaxKept;  // one vector of half the threads beside a list that was cut
+constexpr int kBlock = 32;                         // steps whose maxima are kept (one bit each in a mask)
 constexpr int kBins = 1024;
 constexpr int kMaxCluster = 8;
 constexpr int kMapColumns = 1 << 18;               // columns per bit map (32 KB)
 constexpr float kNoRef = -1.7014118346046923e38f;  // R of nothing: -2^127, below every c x
 static_assert(kMaxListed <= kMaxKept && kMaxKept <= kThreads, "a cut list holds the k alternatives, a key per thread");
-static_assert(kMaxCluster * kMaxListed <= kCandidates, "a cluster's lists fit the first CTA's");
 static_assert(sizeof(unsigned long long) * kCandidates % 16 == 0, "keys are read in pairs");
 static_assert(kBins == 4 * kThreads, "four bins per thread");
 static_assert(kThreads >= kMaxListed, "one thread per listed column");
@@ -85,10 +85,11 @@ struct TopShared {
   unsigned long long key[kCandidates];
   unsigned long long kept[kMaxKept];
   uint4 vec[kThreads];  // a thread's vector with candidates, to take single elements from
+  uint16_t step_max[kBlock][kThreads];  // the upper half of every thread's maximum in each step of a block
   int bins[kBins];
   unsigned long long ends[2 * kWarps];
   int warp_sum[kWarps];
-  uint32_t warp_bound[kWarps];
+  uint32_t warp_bound[kWarps], warp_top[kWarps];
   int count, kept_count, above, with, bin;
   // of the cluster's first CTA, with more than one: what every CTA kept, k keys each
   __device__ __forceinline__ unsigned long long* merged() { return reinterpret_cast<unsigned long long*>(this + 1); }
@@ -103,6 +104,36 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// The bin that holds the want-th largest entry of the histogram, and how many entries lie above it and with it. Left as
+// they are where the histogram holds fewer. Called after a barrier, ends with one.
+__device__ void find_bin(TopShared& sh, int want) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int4 b4 = reinterpret_cast<const int4*>(sh.bins)[kThreads - 1 - tid];  // bins 1023 - 4 tid .. 1020 - 4 tid
+  const int sum = (b4.x + b4.y) + (b4.z + b4.w);
+  int scan = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) sh.warp_sum[warp] = scan;
+  __syncthreads();
+  int above = scan - sum;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i)
+    if (i < warp) above += sh.warp_sum[i];
+  if (above < want && above + sum >= want) {  // in one of this thread's bins
+    int bin = kBins - 1 - 4 * tid, in = b4.w;
+    if (above + in < want) --bin, above += in, in = b4.z;
+    if (above + in < want) --bin, above += in, in = b4.y;
+    if (above + in < want) --bin, above += in, in = b4.x;
+    sh.bin = bin;
+    sh.above = above;
+    sh.with = above + in;
+  }
+  __syncthreads();
 }
 
 // Cuts a list of n keys, more than kMaxKept, to those that include the k largest: at most min(k + 32, kMaxKept), in
@@ -153,35 +184,7 @@ __device__ unsigned long long cut_long(TopShared& sh, int n, int k) {
         if (key >= lo && key <= hi) atomicAdd(&sh.bins[static_cast<int>((key - lo) >> shift)], 1);
       }
       __syncthreads();
-      // from the top: thread t holds bins 1023 - 4 t .. 1020 - 4 t
-      const int4 b4 = bins4[kThreads - 1 - tid];
-      const int b[4] = {b4.w, b4.z, b4.y, b4.x}, sum = (b4.x + b4.y) + (b4.z + b4.w);
-      int scan = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-        if (lane >= o) scan += v;
-      }
-      if (lane == 31) sh.warp_sum[warp] = scan;
-      __syncthreads();
-      int above = scan - sum;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i)
-        if (i < warp) above += sh.warp_sum[i];
-      if (above < want && above + sum >= want) {  // the want-th key lies in one of this thread's bins
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (above < want && above + b[i] >= want) {
-            sh.bin = kBins - 1 - (4 * tid + i);
-            sh.above = above;
-            sh.with = above + b[i];
-            above = want;  // found
-          } else {
-            above += b[i];
-          }
-        }
-      }
-      __syncthreads();
+      find_bin(sh, want);
       cut = lo + (static_cast<unsigned long long>(sh.bin) << shift);
       // keys at or above the cut: k - want of earlier rounds, and `with` (one key per bin at shift 0: k)
       if (k - want + sh.with <= most || shift == 0) break;
@@ -226,29 +229,7 @@ __device__ unsigned long long cut_values(TopShared& sh, int n, int k, float thr,
   for (int j = tid; j < n; j += kThreads)
     atomicAdd(&sh.bins[(static_cast<uint32_t>(sh.key[j] >> 32) - lo) >> shift], 1);
   __syncthreads();
-  const int4 b4 = bins4[kThreads - 1 - tid];  // from the top: thread t holds bins 1023 - 4 t .. 1020 - 4 t
-  const int sum = (b4.x + b4.y) + (b4.z + b4.w);
-  int scan = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-    if (lane >= o) scan += v;
-  }
-  if (lane == 31) sh.warp_sum[warp] = scan;
-  __syncthreads();
-  int above = scan - sum;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i)
-    if (i < warp) above += sh.warp_sum[i];
-  if (above < k && above + sum >= k) {  // the k-th value lies in one of this thread's bins
-    int bin = kBins - 1 - 4 * tid, with = above + b4.w;
-    if (with < k) --bin, with += b4.z;
-    if (with < k) --bin, with += b4.y;
-    if (with < k) --bin, with += b4.x;
-    sh.bin = bin;
-    sh.with = with;
-  }
-  __syncthreads();
+  find_bin(sh, k);
   if (sh.with > most) {
     __syncthreads();
     return cut_long(sh, n, k);
@@ -293,16 +274,30 @@ __device__ unsigned long long sort_short(TopShared& sh, int n, int k) {
 // Of `lists` sorted lists of k keys each (0 where there is none, at the end) those that can be among the k largest, into
 // sh.key: ceil(k / lists) keys of every list reach the least of the lists' ceil(k / lists)-th keys.
 __device__ void gather_lists(TopShared& sh, const unsigned long long* from, int lists, int k) {
-  const int each = (k + lists - 1) / lists;
+  const int each = (k + lists - 1) / lists, tid = threadIdx.x;
   unsigned long long bound = ~0ull;
   for (int l = 0; l < lists; ++l) bound = min(bound, from[l * k + each - 1]);
-  if (threadIdx.x == 0) sh.count = 0;
+  if (tid == 0) sh.count = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < lists * k; i += kThreads) {
+  for (int i = tid; i < lists * k; i += kThreads) {
     const unsigned long long key = from[i];
-    if (key && key >= bound) sh.key[atomicAdd(&sh.count, 1)] = key;
+    if (key && key >= bound) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kCandidates) sh.key[at] = key;
+    }
   }
   __syncthreads();
+  if (sh.count <= kCandidates) return;
+  // (a list is short, so that the bound is 0) list by list, cut to a list's length each time
+  int n = 0;
+  __syncthreads();
+  for (int l = 0; l < lists; ++l) {
+    if (tid < k) sh.key[n + tid] = from[l * k + tid];
+    __syncthreads();
+    cut_long(sh, n + k, k);
+    n = sh.count;
+    __syncthreads();
+  }
 }
 
 // The k largest of the list, in order, in key[0 .. count). Counting costs n^2 / 3 instructions of a warp, a cut about 1200.
@@ -345,6 +340,23 @@ __device__ __forceinline__ void set_masked(uint32_t (&w)[4], int i) {
     w[i >> 1] = (i & 1) ? (w[i >> 1] & 0x0000FFFFu) | 0xFF800000u : (w[i >> 1] & 0xFFFF0000u) | 0x0000FF80u;
   else
     w[i & 3] = 0xFF800000u;
+}
+
+__device__ __forceinline__ uint4 clamp_masked(const uint4& x, uint16_t) {
+  constexpr uint32_t kLow = 0xF180F180u;  // -2^100, twice
+  return make_uint4(max_nan_bf16x2(x.x, kLow), max_nan_bf16x2(x.y, kLow), max_nan_bf16x2(x.z, kLow),
+                    max_nan_bf16x2(x.w, kLow));
+}
+__device__ __forceinline__ uint4 clamp_masked(const uint4& x, float) {
+  const auto f = [](uint32_t w) { return __float_as_uint(max_nan(__uint_as_float(w), -kLogitBound)); };
+  return make_uint4(f(x.x), f(x.y), f(x.z), f(x.w));
+}
+__device__ __forceinline__ float vector_max(const uint4& x, uint16_t) {
+  const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(x.x, x.y), max_nan_bf16x2(x.z, x.w));
+  return max_nan(__uint_as_float(bf16_lo_bits(m)), __uint_as_float(bf16_hi_bits(m)));
+}
+__device__ __forceinline__ float vector_max(const uint4& x, float) {
+  return max_nan(max_nan(__uint_as_float(x.x), __uint_as_float(x.y)), max_nan(__uint_as_float(x.z), __uint_as_float(x.w)));
 }
 
 // The vector at column col of a row of V: what lies outside is masked.
@@ -416,40 +428,100 @@ __device__ __forceinline__ uint32_t above_mask(const uint4& x, float thr, float)
          (__uint_as_float(x.z) > thr ? 0x00002u : 0u) | (__uint_as_float(x.w) > thr ? 0x20000u : 0u);
 }
 
-// The columns above the bound of the first N vectors in x go to the list; a full list drops them (the caller sees it by
-// the count). Vector u starts at column col + u kThreads VEC.
-template <typename T, int N>
-__device__ __forceinline__ bool append(TopShared& sh, const uint4* x, int col, float thr, int cut_at) {
-  constexpr int VEC = kVecOf<T>;
-  uint32_t mask[N];
-  int found = 0;
-#pragma unroll
-  for (int u = 0; u < N; ++u) {
-    mask[u] = above_mask(x[u], thr, T());
-    found += __popc(mask[u]);
-  }
-  if (!found) return false;
-  int at = atomicAdd(&sh.count, found);
-  const bool much = at + found > cut_at;
-#pragma unroll
-  for (int u = 0; u < N; ++u) {
-    if (mask[u]) {
-      sh.vec[threadIdx.x] = x[u];
-      const T* mine = reinterpret_cast<const T*>(&sh.vec[threadIdx.x]);
-      do {
-        const int bit = __ffs(mask[u]) - 1, i = 2 * (bit & 15) + (bit >> 4);
-        mask[u] &= mask[u] - 1;
-        if (at < kCandidates) sh.key[at] = rank_key(logit(mine, i), col + u * (kThreads * VEC) + i);
-        ++at;
-      } while (mask[u]);
-    }
-  }
-  return much;
+// The vector's columns above the bound go to the list; a full list drops them (the caller sees it by the count).
+template <typename T>
+__device__ __forceinline__ void append(TopShared& sh, const uint4& x, int col, float thr) {
+  uint32_t mask = above_mask(x, thr, T());
+  if (!mask) return;
+  int at = atomicAdd(&sh.count, __popc(mask));
+  sh.vec[threadIdx.x] = x;
+  const T* mine = reinterpret_cast<const T*>(&sh.vec[threadIdx.x]);
+  do {
+    const int bit = __ffs(mask) - 1, i = 2 * (bit & 15) + (bit >> 4);
+    mask &= mask - 1;
+    if (at < kCandidates) sh.key[at] = rank_key(logit(mine, i), col + i);
+    ++at;
+  } while (mask);
 }
 
 // The bound that a cut at `cut` gives: later columns with its value rank behind the k kept.
 __device__ __forceinline__ void raise(float& thr, unsigned long long cut) {
   if (cut) thr = fmaxf(thr, order_value(static_cast<uint32_t>(cut >> 32)));
+}
+
+// The value before the least one with these upper 16 order bits (-0 is +0).
+template <typename T>
+__device__ __forceinline__ float before(uint32_t t) {
+  t -= t == 0x8000u ? 2u : t > 0u ? 1u : 0u;
+  return order_value(sizeof(T) == 2 ? t << 16 : (t << 16) | 0xFFFFu);
+}
+
+// A lower bound of the k-th largest logit, for columns above it: every warp's ceil(k / 8)-th largest thread maximum, to 16
+// bits; at least k maxima reach the least of them, and the bound is the value before that one.
+template <typename T>
+__device__ __forceinline__ float first_bound(TopShared& sh, float m, int k) {
+  const uint32_t key = order_bits(fmaxf(m, -kLogitBound)) >> 16;
+  const int each = (k + kWarps - 1) / kWarps;
+  uint32_t t = __reduce_max_sync(0xFFFFFFFFu, key);
+  if (each <= 4) {  // the next smaller maximum, till enough reach it
+    int reach = __popc(__ballot_sync(0xFFFFFFFFu, key == t));
+    while (reach < each) {
+      t = __reduce_max_sync(0xFFFFFFFFu, key < t ? key : 0u);
+      reach = __popc(__ballot_sync(0xFFFFFFFFu, key >= t));
+    }
+  } else {
+    uint32_t low = __reduce_min_sync(0xFFFFFFFFu, key);  // all reach it
+#pragma unroll 1
+    for (uint32_t step = 0x80000000u >> __clz((t - low) | 1u); step; step >>= 1)
+      if (low + step <= t && __popc(__ballot_sync(0xFFFFFFFFu, key >= low + step)) >= each) low += step;
+    t = low;
+  }
+  if ((threadIdx.x & 31) == 0) sh.warp_bound[threadIdx.x >> 5] = t;
+  reinterpret_cast<int4*>(sh.bins)[threadIdx.x] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) t = min(t, sh.warp_bound[i]);
+  return fmaxf(before<T>(t), -kLogitBound);  // of NaN: the bound
+}
+
+// A step's maximum of this thread, in order, to 16 bits (rounded down).
+__device__ __forceinline__ uint32_t step_order(const TopShared& sh, int step) {
+  return order_bits(__uint_as_float(static_cast<uint32_t>(sh.step_max[step][threadIdx.x]) << 16)) >> 16;
+}
+
+// Where the first bound lets many more than k steps pass (mask: this thread's): the k-th largest of all the block's step
+// maxima is a lower bound too, found by one histogram of them. Returns the steps that pass it.
+template <typename T>
+__device__ uint32_t refine_bound(TopShared& sh, uint32_t mask, int k, float& thr) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int all = __reduce_add_sync(0xFFFFFFFFu, __popc(mask));
+  uint32_t hi = 0;
+  for (uint32_t left = mask; left; left &= left - 1) hi = max(hi, step_order(sh, __ffs(left) - 1));
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+  if (lane == 0) {
+    sh.warp_sum[warp] = all;
+    sh.warp_top[warp] = hi;
+  }
+  __syncthreads();
+  int steps = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    steps += sh.warp_sum[i];
+    hi = max(hi, sh.warp_top[i]);
+  }
+  if (steps <= k + 48) return mask;
+  const uint32_t lo = order_bits(thr) >> 16;
+  const int shift = max(22 - __clz((hi - lo) | 1u), 0);  // (hi - lo) >> shift < 1024
+  for (uint32_t left = mask; left; left &= left - 1)
+    atomicAdd(&sh.bins[(step_order(sh, __ffs(left) - 1) - lo) >> shift], 1);
+  __syncthreads();
+  find_bin(sh, k);
+  const uint32_t t = lo + (static_cast<uint32_t>(sh.bin) << shift);  // at least k steps reach it
+  uint32_t pass = 0;
+  for (uint32_t left = mask; left; left &= left - 1)
+    if (step_order(sh, __ffs(left) - 1) >= t) pass |= left & (0u - left);
+  thr = fmaxf(thr, before<T>(t));
+  return pass;
 }
 
 // kEntropy: w is kept; kTop: alternatives are listed (both kLogprobs only).
@@ -529,11 +601,9 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
   F2 s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
   const F2 c2 = pack2(c, c);
   if (kTop && tid == 0) top.count = 0;
-  const int cut_at = k <= 96 ? kMaxKept : 2 * k + 64;  // candidates above which the list is cut
   constexpr int kMapVecs = kMapColumns / VEC;
   int map_begin = v_begin;  // first vector of the bit map
-  bool much = false;        // this thread saw the list longer than cut_at since the last look
-  int looked = v_begin;     // first vector appended since then
+  int block_begin = v_begin;  // first vector of the block
 
   for (int v0 = v_begin; v0 < v_end; v0 += kU * kThreads) {
     if (kMode == kTailBucket && (v0 == v_begin || v0 - map_begin >= kMapVecs)) {
@@ -570,31 +640,13 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
         }
       }
     }
-    // the step's maximum, masked logits clamped to -2^100
-    float cm;
-    if (sizeof(T) == 2) {
-      uint32_t mx = 0xF180F180u;  // -2^100, twice
+    if (kEntropy) {  // masked logits clamped to -2^100: 2^t t has to be 0 there (2^t alone is, for -inf too)
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        in[u].x = max_nan_bf16x2(in[u].x, 0xF180F180u);
-        in[u].y = max_nan_bf16x2(in[u].y, 0xF180F180u);
-        in[u].z = max_nan_bf16x2(in[u].z, 0xF180F180u);
-        in[u].w = max_nan_bf16x2(in[u].w, 0xF180F180u);
-        mx = max_nan_bf16x2(mx, max_nan_bf16x2(max_nan_bf16x2(in[u].x, in[u].y), max_nan_bf16x2(in[u].z, in[u].w)));
-      }
-      cm = max_nan(__uint_as_float(bf16_lo_bits(mx)), __uint_as_float(bf16_hi_bits(mx)));
-    } else {
-      cm = -kLogitBound;
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        in[u].x = __float_as_uint(max_nan(__uint_as_float(in[u].x), -kLogitBound));
-        in[u].y = __float_as_uint(max_nan(__uint_as_float(in[u].y), -kLogitBound));
-        in[u].z = __float_as_uint(max_nan(__uint_as_float(in[u].z), -kLogitBound));
-        in[u].w = __float_as_uint(max_nan(__uint_as_float(in[u].w), -kLogitBound));
-        cm = max_nan(cm, max_nan(max_nan(__uint_as_float(in[u].x), __uint_as_float(in[u].y)),
-                                 max_nan(__uint_as_float(in[u].z), __uint_as_float(in[u].w))));
-      }
+      for (int u = 0; u < kU; ++u) in[u] = clamp_masked(in[u], T());
     }
+    float cm = vector_max(in[0], T());
+#pragma unroll
+    for (int u = 1; u < kU; ++u) cm = max_nan(cm, vector_max(in[u], T()));
     if (!(cm <= m)) {  // larger, or NaN (which stays)
       const float Rn = cm * c, d = R - Rn, f = exp2_approx(d);
       const F2 f2 = pack2(f, f);
@@ -620,64 +672,54 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
       }
     }
     if (kTop) {
-      if (v0 == v_begin) {
-        // Every warp's ceil(k / 8)-th largest thread maximum, to 16 bits; at least k maxima reach the least of them.
-        const uint32_t key = order_bits(cm) >> 16;
-        const int each = (k + kWarps - 1) / kWarps;
-        uint32_t t = __reduce_max_sync(0xFFFFFFFFu, key);
-        if (each <= 4) {  // the next smaller maximum, till enough reach it
-          int reach = __popc(__ballot_sync(0xFFFFFFFFu, key == t));
-          while (reach < each) {
-            t = __reduce_max_sync(0xFFFFFFFFu, key < t ? key : 0u);
-            reach = __popc(__ballot_sync(0xFFFFFFFFu, key >= t));
-          }
-        } else {
-          uint32_t low = __reduce_min_sync(0xFFFFFFFFu, key);  // all reach it
-#pragma unroll 1
-          for (uint32_t step = 0x80000000u >> __clz((t - low) | 1u); step; step >>= 1)
-            if (low + step <= t && __popc(__ballot_sync(0xFFFFFFFFu, key >= low + step)) >= each) low += step;
-          t = low;
-        }
-        if (lane == 0) top.warp_bound[warp] = t;
+      const int step = (v0 - block_begin) / (kU * kThreads);
+      top.step_max[step][tid] = static_cast<uint16_t>(__float_as_uint(cm) >> 16);
+      if (step < kBlock - 1 && v0 + kU * kThreads < v_end) continue;
+      // The block's end (of the row, but for the longest): the steps that hold a candidate are read again.
+      if (block_begin == v_begin) thr = first_bound<T>(top, m, k);  // and the bins are clear
+      const uint32_t least = max(order_bits(thr) >> 16, (order_bits(-kLogitBound) >> 16) + 1);  // not the masked
+      uint32_t mask = 0;
+      for (int i = 0; i <= step; ++i)
+        if (step_order(top, i) >= least) mask |= 1u << i;
+      if (block_begin == v_begin) mask = refine_bound<T>(top, mask, k, thr);
+      while (mask) {
+        const int v = block_begin + (__ffs(mask) - 1) * (kU * kThreads);
+        mask &= mask - 1;
+        load_step(v);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (vector_max(in[u], T()) > thr) append<T>(top, in[u], (v + u * kThreads + tid) * VEC - phase, thr);
+      }
+      __syncthreads();
+      const int n = top.count;
+      if (n > kCandidates) {
+        // More than find a place (equal values): what the block appended goes, and it is appended again in parts
+        // that a list that was cut can take, one vector of half the threads.
+        const int from = block_begin * VEC - phase;
+        for (int i = tid; i < kCandidates; i += kThreads)
+          if (key_column(top.key[i]) >= from) top.key[i] = 0;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) t = min(t, top.warp_bound[i]);
-        // this step's columns that equal it count: the bound is the value before it (-0 is +0)
-        t -= t == 0x8000u ? 2u : t > 0u ? 1u : 0u;
-        thr = fmaxf(order_value(sizeof(T) == 2 ? t << 16 : (t << 16) | 0xFFFFu), -kLogitBound);  // of NaN: the bound
-      }
-      if (cm > thr) much |= append<T, kU>(top, in, (v0 + tid) * VEC - phase, thr, cut_at);
-      // The list is looked at after the first two steps (the bound is still loose), every fourth and the last one:
-      // a barrier in each step, with nothing to cut, took 40% more time (2048 rows of 152064, k = 1).
-      const int step = (v0 - v_begin) / (kU * kThreads);
-      const bool look = step < 2 || (step & 3) == 3 || v0 + kU * kThreads >= v_end;
-      if (look && __syncthreads_or(much)) {
-        much = false;
-        const int n = top.count;
-        if (n <= kCandidates) {
-          raise(thr, cut_values(top, n, k, thr, m));
-        } else {
-          // some columns found no place: what came since the last look goes, and is read and appended again
-          // vector by vector, a list that was cut taking one vector of every thread
-          const int from = looked * VEC - phase;
-          for (int i = tid; i < kCandidates; i += kThreads)
-            if (key_column(top.key[i]) >= from) top.key[i] = 0;
-          __syncthreads();
-          raise(thr, cut_long(top, kCandidates, k));
-          for (int v = looked; v <= v0; v += kU * kThreads) {
-            load_step(v);
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              append<T, 1>(top, &in[u], (v + u * kThreads + tid) * VEC - phase, thr, cut_at);
-              __syncthreads();
-              raise(thr, cut_long(top, top.count, k));
+        raise(thr, cut_long(top, kCandidates, k));
+#pragma unroll 1
+        for (int v = block_begin; v <= v0 + (kU - 1) * kThreads; v += kThreads)
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (tid / (kThreads / 2) == half && v + tid < v_end) {
+              const int col = (v + tid) * VEC - phase;
+              append<T>(top, load_edge(x, col, V), col, thr);
             }
+            __syncthreads();
+            const int now = top.count;
+            if (now > kMaxKept) raise(thr, cut_long(top, now, k));
+            __syncthreads();
           }
-        }
+      } else if (v0 + kU * kThreads < v_end && n > k) {
+        raise(thr, cut_values(top, n, k, thr, m));
       }
-      if (look) looked = v0 + kU * kThreads;
+      block_begin = v0 + kU * kThreads;
     }
   }
+
   // the CTA's sums, then the cluster's, in a fixed order
   RowSum sum{R, 0.0f, 0.0f};
   {

@@ -98,10 +98,11 @@ def test_top_alternatives_of_hard_rows(nv, dtype, V, k):
             np.where(np.arange(V) >= V - k - 3, 5.0, -1.0),                     # all of them at the end
             np.where(np.arange(V) % 37 == 5, up, -np.inf),                      # few left
             np.where(r.random(V) < 0.5, 0.0, -0.0),                             # the two zeros are one value
-            -np.abs(r.standard_normal(V)) - 2.0 ** 60]
+            -np.abs(r.standard_normal(V)) - 2.0 ** 60,
+            np.where((np.arange(V) > 4) & (np.arange(V) < V // 2), -np.inf, r.standard_normal(V))]  # a share nearly empty
     x = np.stack(rows).astype(np.float32)
     x = _bits(x) if dtype == "bf16" else x
-    check_forward(nv, x, V, np.arange(8, dtype=np.int32), 1.0, k, dtype, what=f"hard {V} {k} {dtype}")
+    check_forward(nv, x, V, np.arange(9, dtype=np.int32), 1.0, k, dtype, what=f"hard {V} {k} {dtype}")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
