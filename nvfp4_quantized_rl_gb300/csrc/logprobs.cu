@@ -9,8 +9,8 @@
 // that has seen nothing else adds nothing. A NaN stays in s.
 //
 // A row belongs to a cluster of 1 to 8 CTAs (a row alone would leave most SMs idle), each with a contiguous share; their
-// sums and alternatives meet in the first CTA's shared memory. A CTA of 256 threads takes 4 x 16 bytes per thread and
-// step; four CTAs on an SM hide one another's row ends. Bound by HBM: each logit is read once.
+// sums and alternatives meet in the first CTA's shared memory. A CTA of 256 threads takes 5 x 16 bytes per thread and
+// step; four or five CTAs on an SM hide one another's row ends. Bound by HBM: each logit is read once.
 //
 // Alternatives: the k-th largest of the threads' first maxima is a lower bound thr of the k-th largest logit. Columns that reach
 // it go to a candidate list in shared memory as 64-bit keys (value order, then the lower column). A list that
@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kU = 4;                              // vectors per thread and step
+constexpr int kU = 5;                              // vectors per thread and step
 constexpr int kMaxKept = 256;                      // a cut leaves at most this many keys
 constexpr int kCandidates = kThreads / 2 * 8 + kMaxKept;  // one vector of half the threads beside a list that was cut
 constexpr int kBlock = 32;                         // steps whose maxima are kept (one bit each in a mask)
@@ -524,9 +524,14 @@ __device__ uint32_t refine_bound(TopShared& sh, uint32_t mask, int k, float& thr
   return pass;
 }
 
+// CTAs to an SM: five where 48 registers do. 2048 x 152064 bf16 (floor 92 us), without alternatives: 4 vectors and 4 CTAs
+// 106 us, 4 and 5 99 us, 5 and 5 96 us, 6 and 5 98 us, 8 and 4 99 us; with 64 of them 137, 138, 132, 131, 139 us.
+template <bool kTop>
+constexpr int kPerSm = kTop ? 4 : 5;
+
 // kEntropy: w is kept; kTop: alternatives are listed (both kLogprobs only).
 template <typename T, int kMode, bool kEntropy, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArgs a, uint32_t cluster) {
+__global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(const LogitsArgs a, uint32_t cluster) {
   constexpr int VEC = kVecOf<T>;
   constexpr bool kDistill = kMode != kLogprobs;
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_row_kernel(const LogitsArg
   F2 s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
   const F2 c2 = pack2(c, c);
   if (kTop && tid == 0) top.count = 0;
-  constexpr int kMapVecs = kMapColumns / VEC;
+  constexpr int kMapVecs = kMapColumns / VEC / (kU * kThreads) * (kU * kThreads);
   int map_begin = v_begin;  // first vector of the bit map
   int block_begin = v_begin;  // first vector of the block
 
@@ -855,7 +860,7 @@ template <typename T>
 nvfp4rl_status launch_type(const LogitsArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   // CTAs per row: as many as fill the SMs' four places each, and no share below one step
   unsigned cluster = kMaxCluster;
-  while (cluster > 1 && (a.M * cluster > 4 * dev.sm_count || a.V < static_cast<int64_t>(cluster) * kThreads * kVecOf<T>))
+  while (cluster > 1 && (a.M * cluster > (a.k > 0 && !a.ids ? kPerSm<true> : kPerSm<false>) * dev.sm_count || a.V < static_cast<int64_t>(cluster) * kThreads * kVecOf<T>))
     cluster /= 2;
   if (a.ids) return a.tail ? launch<T, kTailBucket, false, false>(a, cluster, dev, st)
                            : launch<T, kNormalized, false, false>(a, cluster, dev, st);
