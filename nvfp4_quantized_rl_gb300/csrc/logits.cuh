@@ -126,8 +126,9 @@ __device__ __forceinline__ TeacherRow teacher_row(const int32_t* ids, const floa
   bool nan = false;
   for (int i = lane; i < k; i += 32) {
     const int32_t id = ids[i];
+    const float listed = teacher[i];
     const bool valid = id >= 0 && id < V;
-    const float l = valid ? teacher[i] : -INFINITY;
+    const float l = valid ? listed : -INFINITY;
     ids_s[i] = valid ? id : -1;
     lq_s[i] = l;
     counted += valid;

@@ -17,6 +17,7 @@ namespace nvfp4rl {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kListCtas = 4 * kNumSMsHint;
 
 // The 8 (bf16) or 4 (fp32) logits that start s elements into the 32 bytes (a, b).
 template <typename T>
@@ -96,7 +97,7 @@ __device__ __forceinline__ uint4 grad_vec(uint4 x, const RowCoef& r, int at, flo
 template <typename T, int kU, bool kEntropy, bool kList, bool kShift>
 __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradArgs a, unsigned chunks, int steps) {
   constexpr int VEC = kVecOf<T>;
-  __shared__ int32_t ids_s[kList ? kMaxListed : 1];
+  __shared__ __align__(16) int32_t ids_s[kList ? kMaxListed : 4];
   __shared__ float q_s[kList ? kMaxListed : 1], lq_s[kList ? kMaxListed : 1];
   __shared__ TeacherRow teacher_s;
   griddep_wait();
@@ -118,19 +119,46 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
   // listed columns of this chunk: thread i holds entry i
   int mine = -1;
   float mine_x = 0.0f;
+  uint4 in[kU], in2[kShift ? kU : 1];
+  bool whole[kU];
+  const auto load_step = [&](int step) {
+    const int v0 = v_begin + step * (kU * kThreads) + tid;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int col = (v0 + u * kThreads) * VEC - out_phase;
+      // every byte of the loads and of the store lies inside the row
+      whole[u] = kShift && s ? col >= s && col - s + 2 * VEC <= V : col >= 0 && col + VEC <= V;
+      if (whole[u] && !dead) {
+        in[u] = ld_logits16(x + col - s);
+        if (kShift && s) in2[u] = ld_logits16(x + col - s + VEC);
+      }
+    }
+  };
   if (kList) {
+    // all of these are under way together: the row's scalars, the listed logits of this chunk, the first vectors, and
+    // the teacher's softmax in the first warp
+    const float d = a.dloss[row], rest = a.tail ? a.lse_tail[row] : 0.0f;
+    if (tid < a.k) {
+      mine = a.ids[row * a.k + tid];
+      const int v = (mine + out_phase) / VEC - v_begin;
+      if (mine >= 0 && mine < V && v >= 0 && v < steps * (kU * kThreads))
+        mine_x = logit(x, mine);
+      else
+        mine = -1;
+    }
+    dead |= d == 0.0f;
+    load_step(0);
     if (tid < 32) {
       const TeacherRow t = teacher_row(a.ids + row * a.k, a.teacher + row * a.k, a.k, a.V, a.tail, ids_s, q_s, lq_s);
       if (tid == 0) teacher_s = t;
+      if (tid < 3 && a.k + tid < kMaxListed) ids_s[a.k + tid] = -1;
     }
-    const float d = a.dloss[row];
-    __syncthreads();
-    dead |= !teacher_s.any || d == 0.0f;
+    __syncthreads();  // the listed logits are read; a gradient in their place may be written
+    dead |= !teacher_s.any;
     hit = d * a.scale;
     mass = teacher_s.mass;
     r.alpha = mass * hit;
     if (a.tail) {
-      const float rest = a.lse_tail[row];
       if (rest == -INFINITY) {
         mass -= teacher_s.q0;  // no bucket; the unlisted columns are masked
         r.alpha = 0.0f;
@@ -139,15 +167,7 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
         r.R = rest * kLog2E;
       }
     }
-    if (tid < a.k && !dead) {
-      mine = ids_s[tid];
-      const int v = (mine + out_phase) / VEC - v_begin;
-      if (mine >= 0 && v >= 0 && v < steps * (kU * kThreads))
-        mine_x = logit(x, mine);
-      else
-        mine = -1;
-    }
-    __syncthreads();  // the listed logits are read; a gradient in their place may be written
+    if (dead) mine = -1;
   } else {
     const float dl = a.dlogp ? a.dlogp[row] : 0.0f, dh = kEntropy ? a.dentropy[row] : 0.0f;
     if (a.tokens) {
@@ -161,18 +181,7 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
   }
   for (int step = 0; step < steps; ++step) {
     const int v0 = v_begin + step * (kU * kThreads) + tid;
-    uint4 in[kU], in2[kShift ? kU : 1];
-    bool whole[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int col = (v0 + u * kThreads) * VEC - out_phase;
-      // every byte of the loads and of the store lies inside the row
-      whole[u] = kShift && s ? col >= s && col - s + 2 * VEC <= V : col >= 0 && col + VEC <= V;
-      if (whole[u] && !dead) {
-        in[u] = ld_logits16(x + col - s);
-        if (kShift && s) in2[u] = ld_logits16(x + col - s + VEC);
-      }
-    }
+    if (!kList || step > 0) load_step(step);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int col = (v0 + u * kThreads) * VEC - out_phase;
@@ -201,11 +210,18 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
       // a column listed more than once is written by its first entry, with the sum of all
       float q = 0.0f;
       bool first = true;
-      for (int i = 0; i < a.k; ++i)
-        if (ids_s[i] == mine) {
-          first &= i >= tid;
-          q += q_s[i];
+      for (int i = 0; i < a.k; i += 4) {  // four ids a load; behind the k-th they are -1
+        const int4 id = *reinterpret_cast<const int4*>(ids_s + i);
+        if (id.x == mine || id.y == mine || id.z == mine || id.w == mine) {
+          const int same[4] = {id.x, id.y, id.z, id.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (same[j] == mine) {
+              first &= i + j >= tid;
+              q += q_s[i + j];
+            }
         }
+      }
       const float p = mine_x <= -kLogitBound && lse == lse ? 0.0f : exp2_approx(fmaf(mine_x, r.c, -lse * kLog2E));
       if (first) store_logit(dx, mine, hit * (fmaf(mass, p, -q)));
     }
@@ -229,7 +245,9 @@ nvfp4rl_status launch_type(const LogitsGradArgs& a, cudaStream_t st) {
   const int64_t vecs = (a.V + 2 * VEC - 2) / VEC;  // of the row, at its worst phase
   const bool wide = a.M * ((vecs + 4 * kThreads - 1) / (4 * kThreads)) >= 4 * kNumSMsHint;
   const int64_t per_step = (wide ? 4 : 1) * kThreads;
-  int64_t steps = a.ids && wide ? 4 : 1;  // a list costs its chunk a fixed part: larger chunks
+  // a list costs its chunk a fixed part: larger chunks, where enough CTAs are left
+  int64_t steps = 1;
+  while (a.ids && wide && steps < 4 && a.M * ((vecs + 2 * steps * per_step - 1) / (2 * steps * per_step)) >= kListCtas) steps *= 2;
   while (steps * per_step < vecs && a.M * ((vecs + steps * per_step - 1) / (steps * per_step)) > (int64_t(1) << 30))
     steps *= 2;
   const int64_t chunks = (vecs + steps * per_step - 1) / (steps * per_step);
