@@ -304,17 +304,33 @@ def _row_out(t, name, dtype, shape, device):
     return t, t.data_ptr()
 
 
+_logits_entry = {}  # the logits operators' C functions, once loaded
+
+
+def _current(device):
+    """(current device, handle of the current stream of `device`): the raw handle where torch gives it, which spares a
+    Stream object on the calls of a decode step."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    stream = raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+    return torch.cuda.current_device(), stream
+
+
 def _logits_call(name, device, stream, *args):
     """Calls the C function on the logits' device (the library launches on the current one) and its current
     stream, or the stream given."""
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device == torch.cuda.current_device():
-        st = getattr(lib(), name)(*args, stream.cuda_stream)
+    fn = _logits_entry.get(name)
+    if fn is None:
+        fn = _logits_entry[name] = getattr(lib(), name)
+    at, handle = _current(device)
+    if stream is not None:
+        handle = stream.cuda_stream
+    if device == at:
+        st = fn(*args, handle)
     else:
+        import torch
         with torch.cuda.device(device):
-            st = getattr(lib(), name)(*args, stream.cuda_stream)
+            st = fn(*args, handle)
     if st != OK:
         raise Nvfp4rlError(st, name)
 
