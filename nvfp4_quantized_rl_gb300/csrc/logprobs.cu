@@ -35,6 +35,7 @@ constexpr int kMaxKept = 256;                      // a cut leaves at most this 
 constexpr int kCandidates = kThreads / 2 * 8 + kMaxKept;  // one vector of half the threads beside a list that was cut
 constexpr int kBlock = 32;                         // steps whose maxima are kept (one bit each in a mask)
 constexpr int kBins = 1024;
+constexpr int kParts = 1024;                       // thread-steps read again together
 constexpr int kMaxCluster = 8;
 constexpr int kMapColumns = 1 << 18;               // columns per bit map (32 KB)
 constexpr float kNoRef = -1.7014118346046923e38f;  // R of nothing: -2^127, below every c x
@@ -86,11 +87,12 @@ struct TopShared {
   unsigned long long kept[kMaxKept];
   uint4 vec[kThreads];  // a thread's vector with candidates, to take single elements from
   uint16_t step_max[kBlock][kThreads];  // the upper half of every thread's maximum in each step of a block
+  uint16_t part[kParts];                // step * kThreads + thread of those that hold candidates
   int bins[kBins];
   unsigned long long ends[2 * kWarps];
   int warp_sum[kWarps];
   uint32_t warp_bound[kWarps], warp_top[kWarps];
-  int count, kept_count, above, with, bin;
+  int count, kept_count, above, with, bin, part_count;
   // of the cluster's first CTA, with more than one: what every CTA kept, k keys each
   __device__ __forceinline__ unsigned long long* merged() { return reinterpret_cast<unsigned long long*>(this + 1); }
 };
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
   float m = -kLogitBound, R = kNoRef, thr = -kLogitBound;
   F2 s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
   const F2 c2 = pack2(c, c);
-  if (kTop && tid == 0) top.count = 0;
+  if (kTop && tid == 0) top.count = top.part_count = 0;
   constexpr int kMapVecs = kMapColumns / VEC / (kU * kThreads) * (kU * kThreads);
   int map_begin = v_begin;  // first vector of the bit map
   int block_begin = v_begin;  // first vector of the block
@@ -681,21 +683,57 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
       top.step_max[step][tid] = static_cast<uint16_t>(__float_as_uint(cm) >> 16);
       if (step < kBlock - 1 && v0 + kU * kThreads < v_end) continue;
       // The block's end (of the row, but for the longest): the steps that hold a candidate are read again.
-      if (block_begin == v_begin) thr = first_bound<T>(top, m, k);  // and the bins are clear
+      if (block_begin == v_begin)
+        thr = first_bound<T>(top, m, k);  // and the bins are clear
+      else
+        __syncthreads();  // part_count is 0
       const uint32_t least = max(order_bits(thr) >> 16, (order_bits(-kLogitBound) >> 16) + 1);  // not the masked
       uint32_t mask = 0;
       for (int i = 0; i <= step; ++i)
         if (step_order(top, i) >= least) mask |= 1u << i;
       if (block_begin == v_begin) mask = refine_bound<T>(top, mask, k, thr);
-      while (mask) {
-        const int v = block_begin + (__ffs(mask) - 1) * (kU * kThreads);
-        mask &= mask - 1;
-        load_step(v);
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-          if (vector_max(in[u], T()) > thr) append<T>(top, in[u], (v + u * kThreads + tid) * VEC - phase, thr);
+      // The thread-steps with candidates are listed, and their vectors dealt out to the threads: all loads of a row's
+      // end go out together (thread by thread their latencies would add up, 6000 cycles under load).
+      if (mask) {
+        int at = atomicAdd(&top.part_count, __popc(mask));
+        for (uint32_t left = mask; left; left &= left - 1, ++at)
+          if (at < kParts) top.part[at] = static_cast<uint16_t>((__ffs(left) - 1) * kThreads + tid);
       }
       __syncthreads();
+      const int parts = top.part_count;
+      if (parts <= kParts) {
+        constexpr int kBatch = 3;
+        for (int i = tid; i < parts * kU; i += kBatch * kThreads) {
+          uint4 y[kBatch];
+          int col[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int q = i + j * kThreads;
+            y[j] = masked_vec<T>();
+            col[j] = 0;
+            if (q < parts * kU) {
+              const int part = top.part[q / kU];
+              const int v = block_begin + (part / kThreads * kU + q % kU) * kThreads + part % kThreads;
+              col[j] = v * VEC - phase;
+              if (v < v_end) y[j] = load_edge(x, col[j], V);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            if (vector_max(y[j], T()) > thr) append<T>(top, y[j], col[j], thr);
+        }
+      } else {
+        while (mask) {
+          const int v = block_begin + (__ffs(mask) - 1) * (kU * kThreads);
+          mask &= mask - 1;
+          load_step(v);
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+            if (vector_max(in[u], T()) > thr) append<T>(top, in[u], (v + u * kThreads + tid) * VEC - phase, thr);
+        }
+      }
+      __syncthreads();
+      if (tid == 0) top.part_count = 0;
       const int n = top.count;
       if (n > kCandidates) {
         // More than find a place (equal values): what the block appended goes, and it is appended again in parts
