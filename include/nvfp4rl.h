@@ -246,13 +246,13 @@ NVFP4RL_API nvfp4rl_status ais_mixing(const float* logp_rollout, const float* lo
  *   logits   [M][ld] bf16 bits or fp32 (dtype), columns [0, V) of each row, ld >= V: a vocabulary
  *            inside padded rows (a linear's N is a multiple of 128) is taken as it lies, and columns
  *            [V, ld) are neither read nor written. Aligned to an element (2 or 4 bytes); rows may start
- *            anywhere. V <= 2^30, M <= 2^31 - 1, M * ld <= 2^48.
+ *            anywhere. V <= 2^22, M <= 2^31 - 1, M * ld <= 2^48.
  *   scale    z = scale * x (the inverse sampling temperature), in [2^-20, 2^20]; p = softmax(z) over
  *            the row's V columns.
  *   A logit at or below -2^100 (-inf, the type's lowest value) is MASKED: its p is 0. A row that
  *   holds a NaN or a logit above 2^100 has NaN for every result. Other rows are not affected.
  *   Per-row arrays are fp32 or int32, aligned to 4 bytes.
- *   Sums run in fp32 (a few hundred terms per thread, then a tree), exponentials are ex2.approx of
+ *   Sums run in fp32 (V / 512 terms per lane, then a tree), exponentials are ex2.approx of
  *   scores in log2 units. No workspace, no atomics on floating values: equal inputs give equal bits.
  * Errors: NVFP4RL_ERR_INVALID_ARG (bad dtype or mode, negative sizes, ld < V, k out of range, scale
  *   out of range, NULL pointers), NVFP4RL_ERR_UNSUPPORTED_SHAPE (V, M, M * ld or k too large),

@@ -307,30 +307,29 @@ def _row_out(t, name, dtype, shape, device):
 _logits_entry = {}  # the logits operators' C functions, once loaded
 
 
-def _current(device):
-    """(current device, handle of the current stream of `device`): the raw handle where torch gives it, which spares a
-    Stream object on the calls of a decode step."""
+def _on_stream(stream, logits, fn, *args):
+    """fn on a stream given by the caller: as the current stream, so that the outputs made are that stream's too."""
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    stream = raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
-    return torch.cuda.current_device(), stream
+    if stream.device != logits.device:
+        raise ValueError("the stream and the logits are on different devices")
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
-def _logits_call(name, device, stream, *args):
+def _logits_call(name, device, *args):
     """Calls the C function on the logits' device (the library launches on the current one) and its current
-    stream, or the stream given."""
+    stream: the raw handle where torch gives it, which spares a Stream object on the calls of a decode step."""
+    import torch
     fn = _logits_entry.get(name)
     if fn is None:
         fn = _logits_entry[name] = getattr(lib(), name)
-    at, handle = _current(device)
-    if stream is not None:
-        handle = stream.cuda_stream
-    if device == at:
-        st = fn(*args, handle)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    stream = raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+    if device == torch.cuda.current_device():
+        st = fn(*args, stream)
     else:
-        import torch
         with torch.cuda.device(device):
-            st = fn(*args, handle)
+            st = fn(*args, stream)
     if st != OK:
         raise Nvfp4rlError(st, name)
 
@@ -343,6 +342,9 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy:
     token is outside [0, V) are ignored (0, and ids -1)."""
     import torch
     _require_cuda(logits)
+    if stream is not None:
+        return _on_stream(stream, logits, token_logprobs, logits, tokens, scale, k, entropy, logp, h, lse,
+                          top_ids, top_logp)
     dt, M, V, ld = _logit_rows(logits)
     dev, f32, rows = logits.get_device(), torch.float32, (M,)
     p_logp = p_h = p_ids = p_top = None
@@ -356,7 +358,7 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy:
     if k > 0:
         top_ids, p_ids = _row_out(top_ids, "top_ids", torch.int32, (M, k), dev)
         top_logp, p_top = _row_out(top_logp, "top_logp", f32, (M, k), dev)
-    _logits_call("token_logprobs", dev, stream, logits.data_ptr(), dt, M, V, ld,
+    _logits_call("token_logprobs", dev, logits.data_ptr(), dt, M, V, ld,
                  _row_array(tokens, "tokens", torch.int32, rows, dev), float(scale), k, p_logp, p_h, p_lse, p_ids, p_top)
     return logp, h if entropy else None, lse, top_ids if k > 0 else None, top_logp if k > 0 else None
 
@@ -378,10 +380,13 @@ def token_logprobs_backward(logits, tokens, lse, dlogp, scale: float = 1.0, entr
     dentropy may be None."""
     import torch
     _require_cuda(logits)
+    if stream is not None:
+        return _on_stream(stream, logits, token_logprobs_backward, logits, tokens, lse, dlogp, scale, entropy,
+                          dentropy, out)
     dt, M, V, ld = _logit_rows(logits)
     dev, f32, rows = logits.get_device(), torch.float32, (M,)
     out, ldd = _dlogits(logits, out, M, V)
-    _logits_call("token_logprobs_backward", dev, stream, logits.data_ptr(), dt, M, V, ld,
+    _logits_call("token_logprobs_backward", dev, logits.data_ptr(), dt, M, V, ld,
                  _row_array(tokens, "tokens", torch.int32, rows, dev), float(scale), _row_array(lse, "lse", f32, rows, dev),
                  _row_array(entropy, "entropy", f32, rows, dev), _row_array(dlogp, "dlogp", f32, rows, dev),
                  _row_array(dentropy, "dentropy", f32, rows, dev), out.data_ptr(), ldd)
@@ -395,6 +400,8 @@ def topk_distill(logits, ids, teacher_logp, scale: float = 1.0, tail: bool = Fal
     over its list, or with tail=True everything unlisted is one more outcome (lse_tail is None without it)."""
     import torch
     _require_cuda(logits)
+    if stream is not None:
+        return _on_stream(stream, logits, topk_distill, logits, ids, teacher_logp, scale, tail, loss, lse, lse_tail)
     dt, M, V, ld = _logit_rows(logits)
     dev, f32 = logits.get_device(), torch.float32
     k = ids.shape[1] if ids.dim() == 2 else 0
@@ -403,7 +410,7 @@ def topk_distill(logits, ids, teacher_logp, scale: float = 1.0, tail: bool = Fal
     lse, p_lse = _row_out(lse, "lse", f32, rows, dev)
     if tail:
         lse_tail, p_tail = _row_out(lse_tail, "lse_tail", f32, rows, dev)
-    _logits_call("topk_distill", dev, stream, logits.data_ptr(), dt, M, V, ld, float(scale),
+    _logits_call("topk_distill", dev, logits.data_ptr(), dt, M, V, ld, float(scale),
                  _row_array(ids, "ids", torch.int32, listed, dev),
                  _row_array(teacher_logp, "teacher_logp", f32, listed, dev), k,
                  DISTILL_TAIL if tail else DISTILL_NORMALIZED, p_loss, p_lse, p_tail)
@@ -416,12 +423,15 @@ def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 
     the logits' dtype (may be the logits themselves: overwritten in place)."""
     import torch
     _require_cuda(logits)
+    if stream is not None:
+        return _on_stream(stream, logits, topk_distill_backward, logits, ids, teacher_logp, lse, dloss, scale,
+                          tail, lse_tail, out)
     dt, M, V, ld = _logit_rows(logits)
     dev, f32 = logits.get_device(), torch.float32
     k = ids.shape[1] if ids.dim() == 2 else 0
     out, ldd = _dlogits(logits, out, M, V)
     rows, listed = (M,), (M, k)
-    _logits_call("topk_distill_backward", dev, stream, logits.data_ptr(), dt, M, V, ld, float(scale),
+    _logits_call("topk_distill_backward", dev, logits.data_ptr(), dt, M, V, ld, float(scale),
                  _row_array(ids, "ids", torch.int32, listed, dev),
                  _row_array(teacher_logp, "teacher_logp", f32, listed, dev), k,
                  DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(lse, "lse", f32, rows, dev),

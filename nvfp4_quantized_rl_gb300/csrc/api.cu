@@ -201,7 +201,7 @@ nvfp4rl_status check_logits(const void* x, int32_t dtype, int64_t M, int64_t V, 
   if (dtype != NVFP4RL_BF16 && dtype != NVFP4RL_F32) return NVFP4RL_ERR_INVALID_ARG;
   if (M < 0 || V <= 0 || ld < V) return NVFP4RL_ERR_INVALID_ARG;
   if (!(scale >= 0x1p-20f && scale <= 0x1p20f)) return NVFP4RL_ERR_INVALID_ARG;
-  if (V > (int64_t(1) << 30) || M > 2147483647LL || ld > (int64_t(1) << 48)) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (V > kMaxVocab || M > 2147483647LL || ld > (int64_t(1) << 48)) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) {
     *skip = true;
     return NVFP4RL_OK;

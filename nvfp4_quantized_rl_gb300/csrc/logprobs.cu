@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
       __syncthreads();
       const int parts = top.part_count;
       if (parts <= kParts) {
-        constexpr int kBatch = 3;
+        constexpr int kBatch = 2;
         for (int i = tid; i < parts * kU; i += kBatch * kThreads) {
           uint4 y[kBatch];
           int col[kBatch];
@@ -896,9 +896,10 @@ nvfp4rl_status launch(const LogitsArgs& a, unsigned cluster, const DeviceInfo& d
 
 template <typename T>
 nvfp4rl_status launch_type(const LogitsArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  // CTAs per row: as many as fill the SMs' four places each, and no share below one step
+  // CTAs per row: two to an SM at most, and no share below one step. 152064 columns, 5 alternatives: 64 rows with 8 CTAs
+  // each 11.6 us, with 4 10.1, with 2 11.9; 152 rows with 2 15.9 us, with 1 20.0; 200 rows with 2 23.1 us, with 1 22.2.
   unsigned cluster = kMaxCluster;
-  while (cluster > 1 && (a.M * cluster > (a.k > 0 && !a.ids ? kPerSm<true> : kPerSm<false>) * dev.sm_count || a.V < static_cast<int64_t>(cluster) * kThreads * kVecOf<T>))
+  while (cluster > 1 && (a.M * cluster > 2 * dev.sm_count || a.V < static_cast<int64_t>(cluster) * kThreads * kVecOf<T>))
     cluster /= 2;
   if (a.ids) return a.tail ? launch<T, kTailBucket, false, false>(a, cluster, dev, st)
                            : launch<T, kNormalized, false, false>(a, cluster, dev, st);

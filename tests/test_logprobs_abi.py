@@ -19,7 +19,7 @@ def _sizes(call):
     assert call(dtype=2) == 1 and call(M=-1) == 1 and call(V=0) == 1 and call(ld=99) == 1 and call(x=None) == 1
     for s in (0.0, -1.0, float("nan"), float("inf"), 2.0 ** -21, 2.0 ** 21):
         assert call(scale=s) == 1, s
-    assert call(V=(1 << 30) + 1, ld=1 << 31) == 3 and call(M=1 << 31) == 3
+    assert call(V=(1 << 22) + 1, ld=1 << 23) == 3 and call(M=1 << 31) == 3
     assert call(M=1 << 20, ld=1 << 29) == 3 and call(M=4, ld=1 << 62) == 3  # more than 2^48 elements
     assert call(x=A0 + 1) == 2 and call(dtype=1, x=A0 + 2) == 2
     assert call(M=0, x=None) == 0

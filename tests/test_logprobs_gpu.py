@@ -383,6 +383,82 @@ def test_offsets_beyond_32_bits(nv):
     assert torch.all((d[rows].double() - ref).abs() <= ref.abs() * (2.0 ** -8 + 4e-4) + 1e-7 * dl[rows].abs()[:, None])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_vocabulary(nv, dtype):
+    """More columns than one block of step maxima and one bit map hold, in rows with one CTA each (64 bits by torch)."""
+    M, V, k = 160, 400003, 70
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = (torch.randn(M, V, generator=g, device="cuda") * 2).to(t)
+    ramp = torch.linspace(-9, 9, V, device="cuda").to(t)
+    x[1] = 1.5
+    x[2] = ramp
+    x[3] = (torch.rand(V, generator=g, device="cuda") < 0.5).to(t)
+    x[4, :350000] = -torch.inf
+    x[5, :-3] = torch.finfo(t).min
+    x[6] = ramp.flip(0)
+    x[7] = -5 - torch.rand(V, generator=g, device="cuda").to(t)
+    x[8, 390000:] = 3.0                      # ties for the last places, in the last block
+    tok = torch.randint(0, V, (M,), generator=g, device="cuda").int()
+    tok[5] = V - 1
+    logp, h, lse, ids, top = nv.token_logprobs(x, tok, k=k)
+    rows = torch.arange(12, device="cuda")
+    f = x[rows].double()
+    z = torch.where(f <= G.MASKED, -torch.inf, f)
+    lp = torch.log_softmax(z, 1)
+    order = torch.sort(f, dim=1, descending=True, stable=True).indices[:, :k]
+    want = torch.where(z.gather(1, order) > -torch.inf, order, -1)
+    assert torch.equal(ids[rows].long(), want)
+    ref_lse = torch.logsumexp(z, 1)
+    ref_h = -(lp.exp() * torch.where(lp == -torch.inf, 0.0, lp)).sum(1)
+    # S of _logits.py with V / 512 additions in a chain, E[D] <= ln V
+    tol = (3 * 13 + 4 + V / 512 + 64) * G.U + 8 * G.U * (ref_lse.abs() + 13)
+    assert torch.all((lse[rows].double() - ref_lse).abs() <= tol)
+    assert torch.all((h[rows].double() - ref_h).abs() <= tol * (1 + 3 * 13))
+    got, ref = logp[rows].double(), lp.gather(1, tok[rows].long()[:, None])[:, 0]
+    fin = torch.isfinite(ref)
+    assert torch.equal(fin, torch.isfinite(got)) and torch.all(((got - ref).abs() <= tol + 8 * G.U * ref.abs())[fin])
+    # the bit map's borders: vectors of 8 or 4 columns around 2^18, the first and the last column
+    edge = torch.tensor([0, 1, 262139, 262142, 262143, 262144, 262145, 262150, V - 2, V - 1], device="cuda")
+    tid = edge.expand(M, -1).int().contiguous()
+    tl = torch.log_softmax(torch.randn(M, 11, generator=g, device="cuda"), 1)[:, :10].contiguous()
+    live = torch.tensor([0, 3, 7, 9, 10, 11], device="cuda")  # rows whose listed columns are all unmasked
+    loss, lse2, rest = nv.topk_distill(x, tid, tl, tail=True)
+    lp, q = lp[live], tl[live].double().exp()
+    q0 = 1 - q.sum(1)
+    ref_rest = torch.logsumexp(z[live].scatter(1, edge.expand(6, -1), -torch.inf), 1)
+    ref = (q * (tl[live].double() - lp[:, edge])).sum(1) + q0 * (q0.log() - (ref_rest - ref_lse[live]))
+    assert torch.all((rest[live].double() - ref_rest).abs() <= tol[live])
+    assert torch.all((loss[live].double() - ref).abs() <= 2 * tol[live] + 64 * G.U * (1 + ref.abs()))
+    d = nv.topk_distill_backward(x, tid, tl, lse2, torch.ones(M, device="cuda"), tail=True, lse_tail=rest)[live].double()
+    p0 = (ref_rest - ref_lse[live]).exp()
+    ref = lp.exp() * (1 - q0 / p0)[:, None]
+    ref[:, edge] = lp[:, edge].exp() - q
+    half = 2.0 ** -8 if dtype == "bf16" else G.U
+    assert torch.all((d - ref).abs() <= ref.abs() * half + lp.exp() * (4 * tol[live] + 64 * G.U)[:, None] * (1 + q0 / p0)[:, None]
+                     + 32 * G.U * ((ref != 0) * q.max()))
+
+
+def test_stream_argument(nv):
+    x = dev(G.make(12, 9001, "bf16", 5))
+    tok = torch.arange(12, dtype=torch.int32, device="cuda")
+    _, ids, l = teacher_case(12, 9001, 5, "bf16", 17)
+    ids, l = P.dev(ids), P.dev(l)
+    one = torch.ones(12, device="cuda")
+
+    def all_four(s):
+        a = nv.token_logprobs(x, tok, k=4, stream=s)
+        b = nv.topk_distill(x, ids, l, stream=s)
+        return [*a, *b[:2], nv.token_logprobs_backward(x, tok, a[2], one, stream=s),
+                nv.topk_distill_backward(x, ids, l, b[1], one, stream=s)]
+    want = all_four(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = all_four(s)
+    s.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
 def test_same_bits_on_every_call_and_stream(nv):
     x = dev(G.make(40, 30011, "bf16", 5))
     tok = torch.arange(40, dtype=torch.int32, device="cuda")
