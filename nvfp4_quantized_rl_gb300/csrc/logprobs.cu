@@ -491,6 +491,13 @@ __device__ __forceinline__ uint32_t step_order(const TopShared& sh, int step) {
   return order_bits(__uint_as_float(static_cast<uint32_t>(sh.step_max[step][threadIdx.x]) << 16)) >> 16;
 }
 
+// Whether this thread's logits of a step may exceed the bound: exactly for bf16, with a rounded maximum for fp32.
+template <typename T>
+__device__ __forceinline__ bool may_exceed(const TopShared& sh, int step, float thr) {
+  if (sizeof(T) == 2) return __uint_as_float(static_cast<uint32_t>(sh.step_max[step][threadIdx.x]) << 16) > thr;
+  return step_order(sh, step) >= max(order_bits(thr) >> 16, (order_bits(-kLogitBound) >> 16) + 1);  // not the masked
+}
+
 // Where the first bound lets many more than k steps pass (mask: this thread's): the k-th largest of all the block's step
 // maxima is a lower bound too, found by one histogram of them. Returns the steps that pass it.
 template <typename T>
@@ -687,10 +694,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
         thr = first_bound<T>(top, m, k);  // and the bins are clear
       else
         __syncthreads();  // part_count is 0
-      const uint32_t least = max(order_bits(thr) >> 16, (order_bits(-kLogitBound) >> 16) + 1);  // not the masked
       uint32_t mask = 0;
       for (int i = 0; i <= step; ++i)
-        if (step_order(top, i) >= least) mask |= 1u << i;
+        if (may_exceed<T>(top, i, thr)) mask |= 1u << i;
       if (block_begin == v_begin) mask = refine_bound<T>(top, mask, k, thr);
       // The thread-steps with candidates are listed, and their vectors dealt out to the threads: all loads of a row's
       // end go out together (thread by thread their latencies would add up, 6000 cycles under load).
@@ -722,33 +728,30 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
           for (int j = 0; j < kBatch; ++j)
             if (vector_max(y[j], T()) > thr) append<T>(top, y[j], col[j], thr);
         }
-      } else {
-        while (mask) {
-          const int v = block_begin + (__ffs(mask) - 1) * (kU * kThreads);
-          mask &= mask - 1;
-          load_step(v);
-#pragma unroll
-          for (int u = 0; u < kU; ++u)
-            if (vector_max(in[u], T()) > thr) append<T>(top, in[u], (v + u * kThreads + tid) * VEC - phase, thr);
-        }
       }
       __syncthreads();
       if (tid == 0) top.part_count = 0;
-      const int n = top.count;
+      const int n = parts <= kParts ? top.count : kCandidates + 1;
       if (n > kCandidates) {
         // More than find a place (equal values): what the block appended goes, and it is appended again in parts
-        // that a list that was cut can take, one vector of half the threads.
+        // that a list that was cut can take, one vector of half the threads. The first cuts raise the bound, and what
+        // cannot exceed it any more is passed over.
         const int from = block_begin * VEC - phase;
-        for (int i = tid; i < kCandidates; i += kThreads)
+        const int held = min(top.count, kCandidates);
+        for (int i = tid; i < held; i += kThreads)
           if (key_column(top.key[i]) >= from) top.key[i] = 0;
         __syncthreads();
-        raise(thr, cut_long(top, kCandidates, k));
+        raise(thr, cut_long(top, held, k));
 #pragma unroll 1
-        for (int v = block_begin; v <= v0 + (kU - 1) * kThreads; v += kThreads)
+        for (int i = 0; i <= step; ++i) {
+          if (!__syncthreads_or(may_exceed<T>(top, i, thr))) continue;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            if (tid / (kThreads / 2) == half && v + tid < v_end) {
-              const int col = (v + tid) * VEC - phase;
+          for (int half = 0; half < 2 * kU; ++half) {
+            const int v = block_begin + (i * kU + (half >> 1)) * kThreads + tid;
+            const bool mine = tid / (kThreads / 2) == (half & 1) && v < v_end && may_exceed<T>(top, i, thr);
+            if (!__syncthreads_or(mine)) continue;
+            if (mine) {
+              const int col = v * VEC - phase;
               append<T>(top, load_edge(x, col, V), col, thr);
             }
             __syncthreads();
@@ -756,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
             if (now > kMaxKept) raise(thr, cut_long(top, now, k));
             __syncthreads();
           }
+        }
       } else if (v0 + kU * kThreads < v_end && n > k) {
         raise(thr, cut_values(top, n, k, thr, m));
       }
