@@ -110,68 +110,63 @@ struct LogitsGradArgs {
 nvfp4rl_status launch_logprobs(const LogitsArgs& a, int dtype, const DeviceInfo& dev, cudaStream_t st);
 nvfp4rl_status launch_logprobs_grad(const LogitsGradArgs& a, int dtype, const DeviceInfo& dev, cudaStream_t st);
 
-// A teacher's row, held by one warp: entries lane, lane + 32, ... of ids/teacher. q and ln q of each
-// entry, the bucket's mass and Q = sum q + q_0. `any`: an entry counts.
+// ---- a teacher's row, one entry to a thread of a CTA of 256 ----
+
+constexpr int kListWarps = 8;
+static_assert(32 * kListWarps >= kMaxListed, "one thread per listed column");
+
+// Block reductions with one barrier each; `red` (kListWarps values of its own for every use in a row) is free again
+// after the CTA's next barrier.
+__device__ __forceinline__ float cta_max(float v, float* red) {
+  v = warp_max(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int i = 1; i < kListWarps; ++i) v = fmaxf(v, red[i]);
+  return v;
+}
+__device__ __forceinline__ float2 cta_sum(float2 v, float2* red) {
+  v = make_float2(warp_sum(v.x), warp_sum(v.y));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int i = 1; i < kListWarps; ++i) v = make_float2(v.x + red[i].x, v.y + red[i].y);
+  return v;
+}
+
+// The bucket's mass and Q = sum q + q_0. `any`: an entry counts (NORMALIZED: one above -inf).
 struct TeacherRow {
   float q0, mass;
   bool any;
 };
 
-// ids_s, q_s, lq_s [k]: the entries' columns (-1: skipped), q and ln q. One whole warp calls.
+struct TeacherShared {
+  float top[kListWarps];
+  float2 sum[kListWarps];
+};
+
+// This thread's entry: column id (-1: none, or skipped) with log-prob l; gives its q and ln q. All threads call.
 // 1 - sum q would lose the digits of a small rest in 32 bits: the largest q enters as -expm1(l).
-__device__ __forceinline__ TeacherRow teacher_row(const int32_t* ids, const float* teacher, int k, int64_t V, bool tail,
-                                                  int32_t* ids_s, float* q_s, float* lq_s) {
-  const int lane = threadIdx.x & 31;
-  float top = -INFINITY;
-  int counted = 0;
-  bool nan = false;
-  for (int i = lane; i < k; i += 32) {
-    const int32_t id = ids[i];
-    const float listed = teacher[i];
-    const bool valid = id >= 0 && id < V;
-    const float l = valid ? listed : -INFINITY;
-    ids_s[i] = valid ? id : -1;
-    lq_s[i] = l;
-    counted += valid;
-    nan |= l != l;
-    top = fmaxf(top, l);
-  }
-  top = warp_max(top);
-  counted = __reduce_add_sync(0xFFFFFFFFu, counted);
-  nan = __any_sync(0xFFFFFFFFu, nan);
-  TeacherRow r{0.0f, 0.0f, counted > 0 && (tail || nan || top != -INFINITY)};
-  if (!r.any) return r;
+__device__ __forceinline__ TeacherRow teacher_row(TeacherShared& sh, int id, float l, bool tail, float& q, float& lq) {
+  const bool counts = id >= 0;
+  // a NaN hides from the maximum, and shows in the sums
+  const float top = cta_max(counts ? l : -INFINITY, sh.top);
   if (!tail) {
-    float total = 0.0f;
-    for (int i = lane; i < k; i += 32) {
-      const float e = lq_s[i] == -INFINITY ? 0.0f : expf(lq_s[i] - top);
-      q_s[i] = e;
-      total += e;
-    }
-    total = warp_sum(total);
-    const float ln_total = logf(total);
-    for (int i = lane; i < k; i += 32) {
-      q_s[i] /= total;
-      lq_s[i] = lq_s[i] - top - ln_total;
-    }
-    r.mass = nan ? NAN : 1.0f;
-    return r;
+    q = counts && l != -INFINITY ? expf(l - top) : 0.0f;
+    const float total = cta_sum(make_float2(q, 0.0f), sh.sum).x;
+    q /= total;
+    lq = (l - top) - logf(total);
+    return TeacherRow{0.0f, total != total ? NAN : 1.0f, total != 0.0f};
   }
-  int first = kMaxListed;  // the entry that holds the largest l
-  for (int i = lane; i < k; i += 32)
-    if (lq_s[i] == top && ids_s[i] >= 0) first = min(first, i);
-  first = __reduce_min_sync(0xFFFFFFFFu, first);
-  float others = 0.0f;
-  for (int i = lane; i < k; i += 32) {
-    const float q = ids_s[i] < 0 ? 0.0f : expf(lq_s[i]);
-    q_s[i] = q;
-    if (i != first) others += q;
-  }
-  others = warp_sum(others);
-  const float rest = -expm1f(top) - others;
-  r.q0 = rest < 0.0f ? 0.0f : rest;
-  r.mass = (expf(top) + others) + r.q0;
-  return r;
+  q = counts ? expf(l) : 0.0f;
+  lq = l;
+  // the others' sum, and how many hold the largest
+  const float2 sum = cta_sum(make_float2(l == top ? 0.0f : q, counts && l == top ? 1.0f : 0.0f), sh.sum);
+  const float largest = expf(top), others = fmaf(fmaxf(sum.y - 1.0f, 0.0f), largest, sum.x);
+  const float rest = -expm1f(top) - others, q0 = rest < 0.0f ? 0.0f : rest;
+  return TeacherRow{q0, (largest + others) + q0, true};
 }
 
 }  // namespace nvfp4rl

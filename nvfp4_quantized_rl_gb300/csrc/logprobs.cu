@@ -5,22 +5,27 @@
 // has seen, t = x c - R; a larger maximum rescales them. Over a row (R, s, w) merge by
 // s 2^(R_i - R), (w + (R_i - R) s) 2^(R_i - R), and
 //   lse = R ln 2 + ln s,   ln p_j = t_j ln 2 - ln s,   entropy = ln s - ln 2 (w / s).
-// Masked logits (at or below -2^100) enter the steps clamped to -2^100, where 2^t = 0 and t stays finite; a thread
-// that has seen nothing else adds nothing. A NaN stays in s.
+// A masked logit (at or below -2^100) gives 2^t = 0; where t itself is summed it is clamped to -2^100, which keeps t
+// finite. A thread that has seen nothing else adds nothing. A NaN stays in s.
 //
-// A row belongs to a cluster of 1 to 8 CTAs (a row alone would leave most SMs idle), each with a contiguous share; their
-// sums and alternatives meet in the first CTA's shared memory. A CTA of 256 threads takes 5 x 16 bytes per thread and
-// step; four or five CTAs on an SM hide one another's row ends. Bound by HBM: each logit is read once.
+// Each logit is read once: bound by HBM (8192 x 152064 bf16 with entropy 352 us, 1.04 of the copy rate), and near it by
+// issue slots, which is why the arithmetic is packed (8 instructions for two logits) and nothing else runs in the loop.
+// A CTA of 256 threads takes 5 x 16 bytes per thread and step; several CTAs on an SM hide one another's row ends. What
+// did not help: a cp.async ring that runs ahead over the rows' ends (410 us for 367 at the time: its copies and
+// shared-memory loads cost issue slots), and CTAs that stay for several rows. Few rows are split over clusters of 2 to
+// 8 CTAs, whose sums and alternatives meet in the first CTA's shared memory (one row with 20 alternatives 8 us).
 //
-// Alternatives: the k-th largest of the threads' first maxima is a lower bound thr of the k-th largest logit. Columns that reach
-// it go to a candidate list in shared memory as 64-bit keys (value order, then the lower column). A list that
-// fills up is cut to little more than its k largest keys (histogram of the keys' range, refined where the k-th
-// falls), which raises thr: at the end the same cut, a rank by counting, and the result. What the list holds does
-// not depend on the order of the appends.
+// Alternatives: the loop only keeps the upper half of each thread's maximum per step. At the row's end the k-th largest
+// of those maxima (of the threads' first, then by a histogram of the steps') bounds the k-th largest logit from below;
+// the few thread-steps that reach it are read again, dealt out over the CTA, and the logits above the bound go to a
+// list in shared memory as 64-bit keys (value order, then the lower column). A list that is too long is cut by a
+// histogram; the rest is ranked by counting. The result does not depend on the order of the appends. 64 of each of
+// 2048 x 152064 bf16: 122 us, 0.75 of the copy rate (96 us without); testing every logit against a bound in the loop
+// took 164 us.
 //
 // Distillation with a tail bucket: listed columns are marked in a bit map in shared memory and masked as they are
 // read, so that the streamed sum is the tail's own, relative to its own maximum; the listed ones are gathered and
-// added at the end. 1 - sum p would lose a small tail.
+// added at the end. 1 - sum p would lose a small tail. 4096 x 152064 bf16, 64 listed: 194 us, 0.95 of the copy rate.
 #include <atomic>
 
 #include "logits.cuh"
@@ -42,7 +47,7 @@ constexpr float kNoRef = -1.7014118346046923e38f;  // R of nothing: -2^127, belo
 static_assert(kMaxListed <= kMaxKept && kMaxKept <= kThreads, "a cut list holds the k alternatives, a key per thread");
 static_assert(sizeof(unsigned long long) * kCandidates % 16 == 0, "keys are read in pairs");
 static_assert(kBins == 4 * kThreads, "four bins per thread");
-static_assert(kThreads >= kMaxListed, "one thread per listed column");
+static_assert(kThreads >= kMaxListed && kWarps == kListWarps, "one thread per listed column");
 
 enum Mode { kLogprobs = 0, kNormalized = 1, kTailBucket = 2 };
 
@@ -381,37 +386,15 @@ __device__ __forceinline__ uint4 load_edge(const T* x, int col, int V) {
   return r;
 }
 
-__device__ float block_max(float v, float* red) {
-  v = warp_max(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) v = fmaxf(v, red[i]);
-  __syncthreads();
-  return v;
-}
-
-__device__ float block_sum(float v, float* red) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) v += red[i];
-  __syncthreads();
-  return v;
-}
-
 struct Shared {
-  float red[kWarps];
   RowSum sums[kWarps];
   RowSum parts[kMaxCluster];
-  TeacherRow teacher;
 };
 struct ListShared {
   int32_t ids[kMaxListed];
-  float q[kMaxListed], lq[kMaxListed];
+  TeacherShared teacher;
+  float top[kWarps];
+  float2 sum[2][kWarps];
 };
 
 // The elements of a vector above the bound, as a mask: bit (i >> 1) + 16 (i & 1) for element i. The bound is rounded
@@ -574,20 +557,43 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
     }
   };
   load_step(v_begin);  // beside what the row needs else
-  int token = -1;
+  constexpr int kMapVecs = kMapColumns / VEC / (kU * kThreads) * (kU * kThreads);
+  int map_begin = v_begin;  // first vector of the bit map
+  const auto clear_map = [&]() {
+    const int words = (min(v_end - map_begin, kMapVecs) * VEC + 31) / 32;
+    for (int i = tid; i < words; i += kThreads) map[i] = 0;
+  };
+  // listed columns: thread i holds entry i
+  int id = -1, token = -1;
+  float listed_l = -INFINITY, listed_x = -INFINITY;
+  const auto mark_map = [&]() -> bool {  // whether the column was marked already
+    const int v = id >= 0 ? (id + phase) / VEC : -1;
+    if (v < map_begin || v >= min(v_end, map_begin + kMapVecs)) return false;
+    const int bit = id + phase - map_begin * VEC;
+    const uint32_t was = atomicOr(&map[bit >> 5], 1u << (bit & 31));
+    return was >> (bit & 31) & 1u;
+  };
+  bool twice = true;  // a column may be listed twice
   if (kDistill) {
-    if (warp == 0) {
-      const TeacherRow t = teacher_row(a.ids + row * k, a.teacher + row * k, k, a.V, a.tail, list.ids, list.q, list.lq);
-      if (lane == 0) sh.teacher = t;
+    if (tid < k) {
+      id = a.ids[row * k + tid];
+      listed_l = a.teacher[row * k + tid];
+      if (id < 0 || id >= V) id = -1;
+      list.ids[tid] = id;
     }
-    __syncthreads();
-    if (!sh.teacher.any) {  // every CTA of the cluster
+    if (kMode == kTailBucket) clear_map();
+    if (!__syncthreads_or(id >= 0)) {  // in every CTA of the cluster
       if (rank == 0 && tid == 0) {
         a.loss[row] = 0.0f;
         if (a.lse) a.lse[row] = 0.0f;
         if (kMode == kTailBucket && a.lse_tail) a.lse_tail[row] = 0.0f;
       }
       return;
+    }
+    if (rank == 0 && id >= 0) listed_x = logit(x, id);
+    if (kMode == kTailBucket) {
+      twice = __syncthreads_or(mark_map());
+      twice |= cluster > 1 || v_end - v_begin > kMapVecs;  // other maps may know of others
     }
   } else if (a.tokens) {
     token = a.tokens[row];
@@ -615,25 +621,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
   F2 s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
   const F2 c2 = pack2(c, c);
   if (kTop && tid == 0) top.count = top.part_count = 0;
-  constexpr int kMapVecs = kMapColumns / VEC / (kU * kThreads) * (kU * kThreads);
-  int map_begin = v_begin;  // first vector of the bit map
   int block_begin = v_begin;  // first vector of the block
 
   for (int v0 = v_begin; v0 < v_end; v0 += kU * kThreads) {
-    if (kMode == kTailBucket && (v0 == v_begin || v0 - map_begin >= kMapVecs)) {
-      // the listed columns of the next kMapColumns columns
+    if (kMode == kTailBucket && v0 - map_begin >= kMapVecs) {  // the listed columns of the next kMapVecs vectors
       __syncthreads();
       map_begin = v0;
-      const int words = (min(v_end - v0, kMapVecs) * VEC + 31) / 32;
-      for (int i = tid; i < words; i += kThreads) map[i] = 0;
+      clear_map();
       __syncthreads();
-      if (tid < k && list.ids[tid] >= 0) {
-        const int v = (list.ids[tid] + phase) / VEC;
-        if (v >= v0 && v < min(v_end, v0 + kMapVecs)) {
-          const int bit = list.ids[tid] + phase - v0 * VEC;
-          atomicOr(&map[bit >> 5], 1u << (bit & 31));
-        }
-      }
+      mark_map();
       __syncthreads();
     }
     if (v0 > v_begin) load_step(v0);
@@ -811,33 +807,34 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
   if (sum.R > kLogitBound * c) sum.s = NAN;  // a logit above 2^100
 
   if (kDistill) {
-    // listed columns: thread i holds entry i
-    const int32_t id = tid < k ? list.ids[tid] : -1;
-    const float v = id >= 0 ? logit(x, id) : -INFINITY;
+    float q, lq;
+    const TeacherRow t = teacher_row(list.teacher, id, listed_l, kMode == kTailBucket, q, lq);
     const float s_tail = sum.s;
     float R2 = sum.R;
     if (kMode == kTailBucket) {
-      const bool bad = __syncthreads_or(v != v || v > kLogitBound);
-      R2 = fmaxf(R2, block_max(fmaxf(v, -kLogitBound) <= -kLogitBound ? kNoRef : v * c, sh.red));
-      bool once = id >= 0 && v > -kLogitBound;  // the first entry of its column
-      if (once)
+      R2 = fmaxf(R2, cta_max(listed_x <= -kLogitBound ? kNoRef : listed_x * c, list.top));
+      const bool bad = listed_x != listed_x || listed_x > kLogitBound;
+      bool once = id >= 0 && listed_x > -kLogitBound;  // the first entry of its column
+      if (once && twice)
         for (int j = 0; j < tid; ++j) once &= list.ids[j] != id;
-      const float listed = block_sum(once ? exp2_approx(fmaf(v, c, -R2)) : 0.0f, sh.red);
-      sum.s = bad ? NAN : fmaf(s_tail, exp2_approx(sum.R - R2), listed);
+      const float e = bad ? NAN : once ? exp2_approx(fmaf(listed_x, c, -R2)) : 0.0f;
+      sum.s = fmaf(s_tail, exp2_approx(sum.R - R2), cta_sum(make_float2(e, 0.0f), list.sum[0]).x);
     }
     const bool empty = sum.s == 0.0f;
     const float ln_s = logf(sum.s), down = sum.R - R2;
     float part = 0.0f;
-    if (id >= 0 && list.q[tid] != 0.0f) {
-      const float lp = empty || v <= -kLogitBound ? -INFINITY : fmaf(v, c, -R2) * kLn2 - ln_s;
-      part = list.q[tid] * (list.lq[tid] - lp);
+    if (id >= 0 && q != 0.0f) {
+      const float lp = empty || listed_x <= -kLogitBound ? -INFINITY : fmaf(listed_x, c, -R2) * kLn2 - ln_s;
+      part = q * (lq - lp);
     }
-    part = block_sum(part, sh.red);
+    part = cta_sum(make_float2(part, 0.0f), list.sum[1]).x;
     if (tid == 0) {
-      const float ln_tail = logf(s_tail), q0 = sh.teacher.q0;
-      if (kMode == kTailBucket && q0 > 0.0f && s_tail > 0.0f) part += q0 * (logf(q0) - (fmaf(down, kLn2, ln_tail) - ln_s));
-      a.loss[row] = sum.s != sum.s ? NAN : part;
-      if (a.lse) a.lse[row] = empty ? -INFINITY : fmaf(R2, kLn2, ln_s);
+      const float ln_tail = logf(s_tail);
+      if (kMode == kTailBucket && t.q0 > 0.0f && s_tail > 0.0f)
+        part += t.q0 * (logf(t.q0) - (fmaf(down, kLn2, ln_tail) - ln_s));
+      // NORMALIZED with every l_i at -inf: the row does not count
+      a.loss[row] = !t.any ? 0.0f : sum.s != sum.s ? NAN : part;
+      if (a.lse) a.lse[row] = !t.any ? 0.0f : empty ? -INFINITY : fmaf(R2, kLn2, ln_s);
       if (kMode == kTailBucket && a.lse_tail)
         a.lse_tail[row] = sum.s != sum.s ? NAN : s_tail == 0.0f ? -INFINITY : fmaf(sum.R, kLn2, ln_tail);
     }

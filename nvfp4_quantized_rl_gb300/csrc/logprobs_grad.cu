@@ -17,6 +17,7 @@ namespace nvfp4rl {
 namespace {
 
 constexpr int kThreads = 256;
+static_assert(kThreads == 32 * kListWarps && kMaxListed <= kThreads, "one thread per listed column");
 constexpr int64_t kListCtas = 4 * kNumSMsHint;
 
 // The 8 (bf16) or 4 (fp32) logits that start s elements into the 32 bytes (a, b).
@@ -98,8 +99,8 @@ template <typename T, int kU, bool kEntropy, bool kList, bool kShift>
 __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradArgs a, unsigned chunks, int steps) {
   constexpr int VEC = kVecOf<T>;
   __shared__ __align__(16) int32_t ids_s[kList ? kMaxListed : 4];
-  __shared__ float q_s[kList ? kMaxListed : 1], lq_s[kList ? kMaxListed : 1];
-  __shared__ TeacherRow teacher_s;
+  __shared__ float q_s[kList ? kMaxListed : 1];
+  __shared__ TeacherShared teacher_s;
   griddep_wait();
   griddep_launch_dependents();
   const int64_t row = blockIdx.x / chunks;
@@ -135,35 +136,39 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
     }
   };
   if (kList) {
-    // all of these are under way together: the row's scalars, the listed logits of this chunk, the first vectors, and
-    // the teacher's softmax in the first warp
+    // all of these are under way together: the row's scalars, its list, the first vectors and the listed logits of
+    // this chunk
     const float d = a.dloss[row], rest = a.tail ? a.lse_tail[row] : 0.0f;
+    int id = -1;
+    float l = -INFINITY, q, lq;
     if (tid < a.k) {
-      mine = a.ids[row * a.k + tid];
-      const int v = (mine + out_phase) / VEC - v_begin;
-      if (mine >= 0 && mine < V && v >= 0 && v < steps * (kU * kThreads))
-        mine_x = logit(x, mine);
-      else
-        mine = -1;
+      id = a.ids[row * a.k + tid];
+      l = a.teacher[row * a.k + tid];
     }
     dead |= d == 0.0f;
     load_step(0);
-    if (tid < 32) {
-      const TeacherRow t = teacher_row(a.ids + row * a.k, a.teacher + row * a.k, a.k, a.V, a.tail, ids_s, q_s, lq_s);
-      if (tid == 0) teacher_s = t;
-      if (tid < 3 && a.k + tid < kMaxListed) ids_s[a.k + tid] = -1;
+    if (id >= V) id = -1;
+    if (id >= 0) {
+      const int v = (id + out_phase) / VEC - v_begin;
+      if (v >= 0 && v < steps * (kU * kThreads)) {
+        mine = id;
+        mine_x = logit(x, id);
+      }
     }
-    __syncthreads();  // the listed logits are read; a gradient in their place may be written
-    dead |= !teacher_s.any;
+    ids_s[tid] = id >= 0 ? id : -1;
+    // its barriers: the listed logits are read before a gradient in their place may be written
+    const TeacherRow t = teacher_row(teacher_s, id >= 0 ? id : -1, l, a.tail, q, lq);
+    q_s[tid] = q;
+    dead |= !__syncthreads_or(id >= 0) || !t.any;
     hit = d * a.scale;
-    mass = teacher_s.mass;
+    mass = t.mass;
     r.alpha = mass * hit;
     if (a.tail) {
       if (rest == -INFINITY) {
-        mass -= teacher_s.q0;  // no bucket; the unlisted columns are masked
+        mass -= t.q0;  // no bucket; the unlisted columns are masked
         r.alpha = 0.0f;
       } else {
-        r.alpha = (mass * expf(rest - lse) - teacher_s.q0) * hit;
+        r.alpha = (mass * expf(rest - lse) - t.q0) * hit;
         r.R = rest * kLog2E;
       }
     }
