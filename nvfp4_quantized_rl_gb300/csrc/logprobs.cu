@@ -33,21 +33,15 @@
 namespace nvfp4rl {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 256;                      // of a CTA, but for long rows with few alternatives (kNarrow)
+constexpr int kNarrow = 128;
 constexpr int kU = 5;                              // vectors per thread and step
-constexpr int kMaxKept = 256;                      // a cut leaves at most this many keys
-constexpr int kCandidates = kThreads / 2 * 8 + kMaxKept;  // one vector of half the threads beside a list that was cut
 constexpr int kBlock = 32;                         // steps whose maxima are kept (one bit each in a mask)
-constexpr int kBins = 1024;
 constexpr int kParts = 1024;                       // thread-steps read again together
 constexpr int kMaxCluster = 8;
 constexpr int kMapColumns = 1 << 18;               // columns per bit map (32 KB)
 constexpr float kNoRef = -1.7014118346046923e38f;  // R of nothing: -2^127, below every c x
-static_assert(kMaxListed <= kMaxKept && kMaxKept <= kThreads, "a cut list holds the k alternatives, a key per thread");
-static_assert(sizeof(unsigned long long) * kCandidates % 16 == 0, "keys are read in pairs");
-static_assert(kBins == 4 * kThreads, "four bins per thread");
-static_assert(kThreads >= kMaxListed && kWarps == kListWarps, "one thread per listed column");
+static_assert(kThreads >= kMaxListed && kThreads == 32 * kListWarps, "one thread per listed column");
 
 enum Mode { kLogprobs = 0, kNormalized = 1, kTailBucket = 2 };
 
@@ -87,12 +81,20 @@ __device__ __forceinline__ int key_column(unsigned long long key) {
   return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
 }
 
+// The alternatives' shared memory of a CTA of NT threads.
+template <int NT>
 struct TopShared {
+  static constexpr int kWarps = NT / 32;
+  static constexpr int kMaxKept = NT;                      // a cut leaves at most this many keys, one to a thread
+  static constexpr int kCandidates = NT / 2 * 8 + kMaxKept;  // one vector of half the threads beside a list that was cut
+  static constexpr int kBins = 4 * NT;
+  static constexpr int kLogBins = NT == 256 ? 10 : 9;
+  static_assert(1 << kLogBins == kBins && kCandidates % 2 == 0, "four bins to a thread; keys are read in pairs");
   unsigned long long key[kCandidates];
   unsigned long long kept[kMaxKept];
-  uint4 vec[kThreads];  // a thread's vector with candidates, to take single elements from
-  uint16_t step_max[kBlock][kThreads];  // the upper half of every thread's maximum in each step of a block
-  uint16_t part[kParts];                // step * kThreads + thread of those that hold candidates
+  uint4 vec[NT];  // a thread's vector with candidates, to take single elements from
+  uint16_t step_max[kBlock][NT];  // the upper half of every thread's maximum in each step of a block
+  uint16_t part[kParts];                // step * NT + thread of those that hold candidates
   int bins[kBins];
   unsigned long long ends[2 * kWarps];
   int warp_sum[kWarps];
@@ -115,9 +117,10 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
 
 // The bin that holds the want-th largest entry of the histogram, and how many entries lie above it and with it. Left as
 // they are where the histogram holds fewer. Called after a barrier, ends with one.
-__device__ void find_bin(TopShared& sh, int want) {
+template <int NT>
+__device__ void find_bin(TopShared<NT>& sh, int want) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int4 b4 = reinterpret_cast<const int4*>(sh.bins)[kThreads - 1 - tid];  // bins 1023 - 4 tid .. 1020 - 4 tid
+  const int4 b4 = reinterpret_cast<const int4*>(sh.bins)[NT - 1 - tid];  // from the top: bins kBins - 1 - 4 tid and the three below
   const int sum = (b4.x + b4.y) + (b4.z + b4.w);
   int scan = sum;
 #pragma unroll
@@ -129,10 +132,10 @@ __device__ void find_bin(TopShared& sh, int want) {
   __syncthreads();
   int above = scan - sum;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i)
+  for (int i = 0; i < TopShared<NT>::kWarps; ++i)
     if (i < warp) above += sh.warp_sum[i];
   if (above < want && above + sum >= want) {  // in one of this thread's bins
-    int bin = kBins - 1 - 4 * tid, in = b4.w;
+    int bin = TopShared<NT>::kBins - 1 - 4 * tid, in = b4.w;
     if (above + in < want) --bin, above += in, in = b4.z;
     if (above + in < want) --bin, above += in, in = b4.y;
     if (above + in < want) --bin, above += in, in = b4.x;
@@ -146,11 +149,12 @@ __device__ void find_bin(TopShared& sh, int want) {
 // Cuts a list of n keys, more than kMaxKept, to those that include the k largest: at most min(k + 32, kMaxKept), in
 // key[0 .. count). Returns the lower bound that the cut used (0: nothing was cut). All threads of the CTA call, after a
 // barrier that follows the last append. For keys in any range, equal values among them.
-__device__ unsigned long long cut_long(TopShared& sh, int n, int k) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = min(k + 32, kMaxKept);
+template <int NT>
+__device__ unsigned long long cut_long(TopShared<NT>& sh, int n, int k) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = min(k + 32, TopShared<NT>::kMaxKept);
   unsigned long long lo = ~0ull, hi = 0;
   int keys = 0;
-  for (int j = tid; j < n; j += kThreads) {
+  for (int j = tid; j < n; j += NT) {
     const unsigned long long key = sh.key[j];
     if (key) {
       ++keys;
@@ -175,7 +179,7 @@ __device__ unsigned long long cut_long(TopShared& sh, int n, int k) {
   __syncthreads();
   keys = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
+  for (int i = 0; i < TopShared<NT>::kWarps; ++i) {
     keys += sh.warp_sum[i];
     lo = min(lo, sh.ends[2 * i]);
     hi = max(hi, sh.ends[2 * i + 1]);
@@ -185,8 +189,8 @@ __device__ unsigned long long cut_long(TopShared& sh, int n, int k) {
     int want = k;  // of the keys in [lo, hi]: those above are in
     while (true) {
       const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
-      const int shift = max(bits - 10, 0);  // (hi - lo) >> shift < 1024
-      for (int j = tid; j < n; j += kThreads) {
+      const int shift = max(bits - TopShared<NT>::kLogBins, 0);  // (hi - lo) >> shift < kBins
+      for (int j = tid; j < n; j += NT) {
         const unsigned long long key = sh.key[j];
         if (key >= lo && key <= hi) atomicAdd(&sh.bins[static_cast<int>((key - lo) >> shift)], 1);
       }
@@ -202,13 +206,13 @@ __device__ unsigned long long cut_long(TopShared& sh, int n, int k) {
       __syncthreads();
     }
   }
-  for (int j = tid; j < n; j += kThreads) {
+  for (int j = tid; j < n; j += NT) {
     const unsigned long long key = sh.key[j];
     if (key && key >= cut) sh.kept[atomicAdd(&sh.kept_count, 1)] = key;
   }
   __syncthreads();
   const int kept = sh.kept_count;
-  for (int i = tid; i < kept; i += kThreads) sh.key[i] = sh.kept[i];
+  for (int i = tid; i < kept; i += NT) sh.key[i] = sh.kept[i];
   if (tid == 0) sh.count = kept;
   __syncthreads();
   return cut;
@@ -216,8 +220,9 @@ __device__ unsigned long long cut_long(TopShared& sh, int n, int k) {
 
 // The same for a list whose values lie above thr and at most at the threads' maxima m: one histogram of the values'
 // order bits, without the reductions of the keys' range, and cut_long only where too many keys share the cut's bin.
-__device__ unsigned long long cut_values(TopShared& sh, int n, int k, float thr, float m) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = min(k + 32, kMaxKept);
+template <int NT>
+__device__ unsigned long long cut_values(TopShared<NT>& sh, int n, int k, float thr, float m) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = min(k + 32, TopShared<NT>::kMaxKept);
   const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, order_bits(m));
   if (lane == 0) sh.warp_bound[warp] = top;
   if (tid == 0) {
@@ -231,9 +236,9 @@ __device__ unsigned long long cut_values(TopShared& sh, int n, int k, float thr,
   const uint32_t lo = order_bits(thr);
   uint32_t hi = lo;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) hi = max(hi, sh.warp_bound[i]);
-  const int shift = max(22 - __clz((hi - lo) | 1u), 0);  // (hi - lo) >> shift < 1024
-  for (int j = tid; j < n; j += kThreads)
+  for (int i = 0; i < TopShared<NT>::kWarps; ++i) hi = max(hi, sh.warp_bound[i]);
+  const int shift = max(32 - TopShared<NT>::kLogBins - __clz((hi - lo) | 1u), 0);  // (hi - lo) >> shift < kBins
+  for (int j = tid; j < n; j += NT)
     atomicAdd(&sh.bins[(static_cast<uint32_t>(sh.key[j] >> 32) - lo) >> shift], 1);
   __syncthreads();
   find_bin(sh, k);
@@ -242,7 +247,7 @@ __device__ unsigned long long cut_values(TopShared& sh, int n, int k, float thr,
     return cut_long(sh, n, k);
   }
   const uint32_t cut = lo + (static_cast<uint32_t>(sh.bin) << shift);
-  for (int j = tid; j < n; j += kThreads) {
+  for (int j = tid; j < n; j += NT) {
     const unsigned long long key = sh.key[j];
     if (static_cast<uint32_t>(key >> 32) >= cut) sh.kept[atomicAdd(&sh.kept_count, 1)] = key;
   }
@@ -256,8 +261,9 @@ __device__ unsigned long long cut_values(TopShared& sh, int n, int k, float thr,
 
 // The k largest of at most kMaxKept keys, in order, in sh.key[0 .. count): every key counts those above it, with 4, 2 or 1
 // threads to a key, two keys a load. Returns the k-th (0: there are fewer). Called as cut_long.
-__device__ unsigned long long sort_short(TopShared& sh, int n, int k) {
-  const int p = n <= kThreads / 4 ? 2 : n <= kThreads / 2 ? 1 : 0, parts = 1 << p;
+template <int NT>
+__device__ unsigned long long sort_short(TopShared<NT>& sh, int n, int k) {
+  const int p = n <= NT / 4 ? 2 : n <= NT / 2 ? 1 : 0, parts = 1 << p;
   const int i = static_cast<int>(threadIdx.x) >> p, part = threadIdx.x & (parts - 1);
   const unsigned long long key = i < n ? sh.key[i] : 0ull;
   int rank = 0;
@@ -280,21 +286,22 @@ __device__ unsigned long long sort_short(TopShared& sh, int n, int k) {
 
 // Of `lists` sorted lists of k keys each (0 where there is none, at the end) those that can be among the k largest, into
 // sh.key: ceil(k / lists) keys of every list reach the least of the lists' ceil(k / lists)-th keys.
-__device__ void gather_lists(TopShared& sh, const unsigned long long* from, int lists, int k) {
+template <int NT>
+__device__ void gather_lists(TopShared<NT>& sh, const unsigned long long* from, int lists, int k) {
   const int each = (k + lists - 1) / lists, tid = threadIdx.x;
   unsigned long long bound = ~0ull;
   for (int l = 0; l < lists; ++l) bound = min(bound, from[l * k + each - 1]);
   if (tid == 0) sh.count = 0;
   __syncthreads();
-  for (int i = tid; i < lists * k; i += kThreads) {
+  for (int i = tid; i < lists * k; i += NT) {
     const unsigned long long key = from[i];
     if (key && key >= bound) {
       const int at = atomicAdd(&sh.count, 1);
-      if (at < kCandidates) sh.key[at] = key;
+      if (at < TopShared<NT>::kCandidates) sh.key[at] = key;
     }
   }
   __syncthreads();
-  if (sh.count <= kCandidates) return;
+  if (sh.count <= TopShared<NT>::kCandidates) return;
   // (a list is short, so that the bound is 0) list by list, cut to a list's length each time
   int n = 0;
   __syncthreads();
@@ -308,9 +315,10 @@ __device__ void gather_lists(TopShared& sh, const unsigned long long* from, int 
 }
 
 // The k largest of the list, in order, in key[0 .. count). Counting costs n^2 / 3 instructions of a warp, a cut about 1200.
-__device__ void sort_list(TopShared& sh, int k) {
+template <int NT>
+__device__ void sort_list(TopShared<NT>& sh, int k) {
   int n = sh.count;
-  if (n > kMaxKept) {
+  if (n > TopShared<NT>::kMaxKept) {
     cut_long(sh, n, k);
     n = sh.count;
   }
@@ -387,14 +395,14 @@ __device__ __forceinline__ uint4 load_edge(const T* x, int col, int V) {
 }
 
 struct Shared {
-  RowSum sums[kWarps];
+  RowSum sums[kThreads / 32];
   RowSum parts[kMaxCluster];
 };
 struct ListShared {
   int32_t ids[kMaxListed];
   TeacherShared teacher;
-  float top[kWarps];
-  float2 sum[2][kWarps];
+  float top[kListWarps];
+  float2 sum[2][kListWarps];
 };
 
 // The elements of a vector above the bound, as a mask: bit (i >> 1) + 16 (i & 1) for element i. The bound is rounded
@@ -414,8 +422,8 @@ __device__ __forceinline__ uint32_t above_mask(const uint4& x, float thr, float)
 }
 
 // The vector's columns above the bound go to the list; a full list drops them (the caller sees it by the count).
-template <typename T>
-__device__ __forceinline__ void append(TopShared& sh, const uint4& x, int col, float thr) {
+template <int NT, typename T>
+__device__ __forceinline__ void append(TopShared<NT>& sh, const uint4& x, int col, float thr) {
   uint32_t mask = above_mask(x, thr, T());
   if (!mask) return;
   int at = atomicAdd(&sh.count, __popc(mask));
@@ -424,7 +432,7 @@ __device__ __forceinline__ void append(TopShared& sh, const uint4& x, int col, f
   do {
     const int bit = __ffs(mask) - 1, i = 2 * (bit & 15) + (bit >> 4);
     mask &= mask - 1;
-    if (at < kCandidates) sh.key[at] = rank_key(logit(mine, i), col + i);
+    if (at < TopShared<NT>::kCandidates) sh.key[at] = rank_key(logit(mine, i), col + i);
     ++at;
   } while (mask);
 }
@@ -443,10 +451,10 @@ __device__ __forceinline__ float before(uint32_t t) {
 
 // A lower bound of the k-th largest logit, for columns above it: every warp's ceil(k / 8)-th largest thread maximum, to 16
 // bits; at least k maxima reach the least of them, and the bound is the value before that one.
-template <typename T>
-__device__ __forceinline__ float first_bound(TopShared& sh, float m, int k) {
+template <int NT, typename T>
+__device__ __forceinline__ float first_bound(TopShared<NT>& sh, float m, int k) {
   const uint32_t key = order_bits(fmaxf(m, -kLogitBound)) >> 16;
-  const int each = (k + kWarps - 1) / kWarps;
+  const int each = (k + TopShared<NT>::kWarps - 1) / TopShared<NT>::kWarps;
   uint32_t t = __reduce_max_sync(0xFFFFFFFFu, key);
   if (each <= 4) {  // the next smaller maximum, till enough reach it
     int reach = __popc(__ballot_sync(0xFFFFFFFFu, key == t));
@@ -465,26 +473,27 @@ __device__ __forceinline__ float first_bound(TopShared& sh, float m, int k) {
   reinterpret_cast<int4*>(sh.bins)[threadIdx.x] = make_int4(0, 0, 0, 0);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) t = min(t, sh.warp_bound[i]);
+  for (int i = 0; i < TopShared<NT>::kWarps; ++i) t = min(t, sh.warp_bound[i]);
   return fmaxf(before<T>(t), -kLogitBound);  // of NaN: the bound
 }
 
 // A step's maximum of this thread, in order, to 16 bits (rounded down).
-__device__ __forceinline__ uint32_t step_order(const TopShared& sh, int step) {
+template <int NT>
+__device__ __forceinline__ uint32_t step_order(const TopShared<NT>& sh, int step) {
   return order_bits(__uint_as_float(static_cast<uint32_t>(sh.step_max[step][threadIdx.x]) << 16)) >> 16;
 }
 
 // Whether this thread's logits of a step may exceed the bound: exactly for bf16, with a rounded maximum for fp32.
-template <typename T>
-__device__ __forceinline__ bool may_exceed(const TopShared& sh, int step, float thr) {
+template <int NT, typename T>
+__device__ __forceinline__ bool may_exceed(const TopShared<NT>& sh, int step, float thr) {
   if (sizeof(T) == 2) return __uint_as_float(static_cast<uint32_t>(sh.step_max[step][threadIdx.x]) << 16) > thr;
   return step_order(sh, step) >= max(order_bits(thr) >> 16, (order_bits(-kLogitBound) >> 16) + 1);  // not the masked
 }
 
 // Where the first bound lets many more than k steps pass (mask: this thread's): the k-th largest of all the block's step
 // maxima is a lower bound too, found by one histogram of them. Returns the steps that pass it.
-template <typename T>
-__device__ uint32_t refine_bound(TopShared& sh, uint32_t mask, int k, float& thr) {
+template <int NT, typename T>
+__device__ uint32_t refine_bound(TopShared<NT>& sh, uint32_t mask, int k, float& thr) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int all = __reduce_add_sync(0xFFFFFFFFu, __popc(mask));
   uint32_t hi = 0;
@@ -497,13 +506,13 @@ __device__ uint32_t refine_bound(TopShared& sh, uint32_t mask, int k, float& thr
   __syncthreads();
   int steps = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
+  for (int i = 0; i < TopShared<NT>::kWarps; ++i) {
     steps += sh.warp_sum[i];
     hi = max(hi, sh.warp_top[i]);
   }
   if (steps <= k + 48) return mask;
   const uint32_t lo = order_bits(thr) >> 16;
-  const int shift = max(22 - __clz((hi - lo) | 1u), 0);  // (hi - lo) >> shift < 1024
+  const int shift = max(32 - TopShared<NT>::kLogBins - __clz((hi - lo) | 1u), 0);  // (hi - lo) >> shift < kBins
   for (uint32_t left = mask; left; left &= left - 1)
     atomicAdd(&sh.bins[(step_order(sh, __ffs(left) - 1) - lo) >> shift], 1);
   __syncthreads();
@@ -518,17 +527,18 @@ __device__ uint32_t refine_bound(TopShared& sh, uint32_t mask, int k, float& thr
 
 // CTAs to an SM: five where 48 registers do. 2048 x 152064 bf16 (floor 92 us), without alternatives: 4 vectors and 4 CTAs
 // 106 us, 4 and 5 99 us, 5 and 5 96 us, 6 and 5 98 us, 8 and 4 99 us; with 64 of them 137, 138, 132, 131, 139 us.
-template <bool kTop>
-constexpr int kPerSm = kTop ? 4 : 5;
+template <bool kTop, int NT>
+constexpr int kPerSm = !kTop ? 5 : NT == kThreads ? 4 : 7;
 
 // kEntropy: w is kept; kTop: alternatives are listed (both kLogprobs only).
-template <typename T, int kMode, bool kEntropy, bool kTop>
-__global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(const LogitsArgs a, uint32_t cluster) {
+template <typename T, int kMode, bool kEntropy, bool kTop, int NT>
+__global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const LogitsArgs a, uint32_t cluster) {
   constexpr int VEC = kVecOf<T>;
   constexpr bool kDistill = kMode != kLogprobs;
+  static_assert(NT == kThreads || kTop, "one thread per listed column");
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Shared sh;
-  TopShared& top = *reinterpret_cast<TopShared*>(dyn);                  // kTop
+  TopShared<NT>& top = *reinterpret_cast<TopShared<NT>*>(dyn);                  // kTop
   ListShared& list = *reinterpret_cast<ListShared*>(dyn);               // kDistill
   uint32_t* map = reinterpret_cast<uint32_t*>(dyn + sizeof(ListShared));  // kTailBucket
   griddep_wait();
@@ -544,24 +554,24 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
   const int v_begin = static_cast<int>(rank) * share, v_end = min(v_begin + share, vecs);
   uint4 in[kU];
   const auto load_step = [&](int v0) {
-    if (v0 * VEC >= phase && v0 + kU * kThreads <= v_end && (v0 + kU * kThreads) * VEC - phase <= V) {
+    if (v0 * VEC >= phase && v0 + kU * NT <= v_end && (v0 + kU * NT) * VEC - phase <= V) {
       const T* at = x + ((v0 + tid) * VEC - phase);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) in[u] = ld_logits16(at + u * (kThreads * VEC));
+      for (int u = 0; u < kU; ++u) in[u] = ld_logits16(at + u * (NT * VEC));
     } else {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int v = v0 + u * kThreads + tid;
+        const int v = v0 + u * NT + tid;
         in[u] = v < v_end ? load_edge(x, v * VEC - phase, V) : masked_vec<T>();
       }
     }
   };
   load_step(v_begin);  // beside what the row needs else
-  constexpr int kMapVecs = kMapColumns / VEC / (kU * kThreads) * (kU * kThreads);
+  constexpr int kMapVecs = kMapColumns / VEC / (kU * NT) * (kU * NT);
   int map_begin = v_begin;  // first vector of the bit map
   const auto clear_map = [&]() {
     const int words = (min(v_end - map_begin, kMapVecs) * VEC + 31) / 32;
-    for (int i = tid; i < words; i += kThreads) map[i] = 0;
+    for (int i = tid; i < words; i += NT) map[i] = 0;
   };
   // listed columns: thread i holds entry i
   int id = -1, token = -1;
@@ -605,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
           if (a.lse) a.lse[row] = 0.0f;
         }
         if (kTop)
-          for (int i = tid; i < k; i += kThreads) {
+          for (int i = tid; i < k; i += NT) {
             a.top_ids[row * k + i] = -1;
             a.top_logp[row * k + i] = -INFINITY;
           }
@@ -623,7 +633,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
   if (kTop && tid == 0) top.count = top.part_count = 0;
   int block_begin = v_begin;  // first vector of the block
 
-  for (int v0 = v_begin; v0 < v_end; v0 += kU * kThreads) {
+  const auto warp_sums = [&]() {  // the warp's sums to shared memory; a barrier has to follow
+    float lo, hi, wlo, whi;
+    unpack2(s2, lo, hi);
+    unpack2(w2, wlo, whi);
+    RowSum sum{R, lo + hi, wlo + whi};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      merge(sum, RowSum{__shfl_xor_sync(0xFFFFFFFFu, sum.R, o), __shfl_xor_sync(0xFFFFFFFFu, sum.s, o),
+                        __shfl_xor_sync(0xFFFFFFFFu, sum.w, o)});
+    if (lane == 0) sh.sums[warp] = sum;
+  };
+
+  for (int v0 = v_begin; v0 < v_end; v0 += kU * NT) {
     if (kMode == kTailBucket && v0 - map_begin >= kMapVecs) {  // the listed columns of the next kMapVecs vectors
       __syncthreads();
       map_begin = v0;
@@ -636,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
     if (kMode == kTailBucket) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int v = v0 + u * kThreads + tid;
+        const int v = v0 + u * NT + tid;
         if (v < v_end) {
           const int at = (v - map_begin) * VEC;
           const uint32_t bits = (map[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
@@ -682,105 +704,96 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
       }
     }
     if (kTop) {
-      const int step = (v0 - block_begin) / (kU * kThreads);
+      const int step = (v0 - block_begin) / (kU * NT);
       top.step_max[step][tid] = static_cast<uint16_t>(__float_as_uint(cm) >> 16);
-      if (step < kBlock - 1 && v0 + kU * kThreads < v_end) continue;
+      if (step < kBlock - 1 && v0 + kU * NT < v_end) continue;
+      if (v0 + kU * NT >= v_end) warp_sums();
       // The block's end (of the row, but for the longest): the steps that hold a candidate are read again.
       if (block_begin == v_begin)
-        thr = first_bound<T>(top, m, k);  // and the bins are clear
+        thr = first_bound<NT, T>(top, m, k);  // and the bins are clear
       else
         __syncthreads();  // part_count is 0
       uint32_t mask = 0;
       for (int i = 0; i <= step; ++i)
-        if (may_exceed<T>(top, i, thr)) mask |= 1u << i;
-      if (block_begin == v_begin) mask = refine_bound<T>(top, mask, k, thr);
+        if (may_exceed<NT, T>(top, i, thr)) mask |= 1u << i;
+      if (block_begin == v_begin) mask = refine_bound<NT, T>(top, mask, k, thr);
       // The thread-steps with candidates are listed, and their vectors dealt out to the threads: all loads of a row's
       // end go out together (thread by thread their latencies would add up, 6000 cycles under load).
       if (mask) {
         int at = atomicAdd(&top.part_count, __popc(mask));
         for (uint32_t left = mask; left; left &= left - 1, ++at)
-          if (at < kParts) top.part[at] = static_cast<uint16_t>((__ffs(left) - 1) * kThreads + tid);
+          if (at < kParts) top.part[at] = static_cast<uint16_t>((__ffs(left) - 1) * NT + tid);
       }
       __syncthreads();
       const int parts = top.part_count;
       if (parts <= kParts) {
         constexpr int kBatch = 2;
-        for (int i = tid; i < parts * kU; i += kBatch * kThreads) {
+        for (int i = tid; i < parts * kU; i += kBatch * NT) {
           uint4 y[kBatch];
           int col[kBatch];
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
-            const int q = i + j * kThreads;
+            const int q = i + j * NT;
             y[j] = masked_vec<T>();
             col[j] = 0;
             if (q < parts * kU) {
               const int part = top.part[q / kU];
-              const int v = block_begin + (part / kThreads * kU + q % kU) * kThreads + part % kThreads;
+              const int v = block_begin + (part / NT * kU + q % kU) * NT + part % NT;
               col[j] = v * VEC - phase;
               if (v < v_end) y[j] = load_edge(x, col[j], V);
             }
           }
 #pragma unroll
           for (int j = 0; j < kBatch; ++j)
-            if (vector_max(y[j], T()) > thr) append<T>(top, y[j], col[j], thr);
+            if (vector_max(y[j], T()) > thr) append<NT, T>(top, y[j], col[j], thr);
         }
       }
       __syncthreads();
       if (tid == 0) top.part_count = 0;
-      const int n = parts <= kParts ? top.count : kCandidates + 1;
-      if (n > kCandidates) {
+      const int n = parts <= kParts ? top.count : TopShared<NT>::kCandidates + 1;
+      if (n > TopShared<NT>::kCandidates) {
         // More than find a place (equal values): what the block appended goes, and it is appended again in parts
         // that a list that was cut can take, one vector of half the threads. The first cuts raise the bound, and what
         // cannot exceed it any more is passed over.
         const int from = block_begin * VEC - phase;
-        const int held = min(top.count, kCandidates);
-        for (int i = tid; i < held; i += kThreads)
+        const int held = min(top.count, TopShared<NT>::kCandidates);
+        for (int i = tid; i < held; i += NT)
           if (key_column(top.key[i]) >= from) top.key[i] = 0;
         __syncthreads();
         raise(thr, cut_long(top, held, k));
 #pragma unroll 1
         for (int i = 0; i <= step; ++i) {
-          if (!__syncthreads_or(may_exceed<T>(top, i, thr))) continue;
+          if (!__syncthreads_or(may_exceed<NT, T>(top, i, thr))) continue;
 #pragma unroll 1
           for (int half = 0; half < 2 * kU; ++half) {
-            const int v = block_begin + (i * kU + (half >> 1)) * kThreads + tid;
-            const bool mine = tid / (kThreads / 2) == (half & 1) && v < v_end && may_exceed<T>(top, i, thr);
+            const int v = block_begin + (i * kU + (half >> 1)) * NT + tid;
+            const bool mine = tid / (NT / 2) == (half & 1) && v < v_end && may_exceed<NT, T>(top, i, thr);
             if (!__syncthreads_or(mine)) continue;
             if (mine) {
               const int col = v * VEC - phase;
-              append<T>(top, load_edge(x, col, V), col, thr);
+              append<NT, T>(top, load_edge(x, col, V), col, thr);
             }
             __syncthreads();
             const int now = top.count;
-            if (now > kMaxKept) raise(thr, cut_long(top, now, k));
+            if (now > TopShared<NT>::kMaxKept) raise(thr, cut_long(top, now, k));
             __syncthreads();
           }
         }
-      } else if (v0 + kU * kThreads < v_end && n > k) {
+      } else if (v0 + kU * NT < v_end && n > k) {
         raise(thr, cut_values(top, n, k, thr, m));
       }
-      block_begin = v0 + kU * kThreads;
+      block_begin = v0 + kU * NT;
     }
   }
 
   // the CTA's sums, then the cluster's, in a fixed order
-  RowSum sum{R, 0.0f, 0.0f};
-  {
-    float lo, hi;
-    unpack2(s2, lo, hi);
-    sum.s = lo + hi;
-    unpack2(w2, lo, hi);
-    sum.w = lo + hi;
+  if (!kTop || v_begin >= v_end) {
+    warp_sums();
+    __syncthreads();
   }
+  RowSum sum = sh.sums[0];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    merge(sum, RowSum{__shfl_xor_sync(0xFFFFFFFFu, sum.R, o), __shfl_xor_sync(0xFFFFFFFFu, sum.s, o),
-                      __shfl_xor_sync(0xFFFFFFFFu, sum.w, o)});
-  if (lane == 0) sh.sums[warp] = sum;
-  __syncthreads();
-  sum = sh.sums[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) merge(sum, sh.sums[i]);
+  for (int i = 1; i < TopShared<NT>::kWarps; ++i) merge(sum, sh.sums[i]);
   if (kTop) {
     if (top.count > 128) cut_values(top, top.count, k, thr, m);
     sort_list(top, k);
@@ -861,14 +874,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kTop>) logits_row_kernel(cons
   }
 }
 
-template <typename T, int kMode, bool kEntropy, bool kTop>
+template <typename T, int kMode, bool kEntropy, bool kTop, int NT = kThreads>
 nvfp4rl_status launch(const LogitsArgs& a, unsigned cluster, const DeviceInfo& dev, cudaStream_t st) {
-  size_t smem = kTop ? sizeof(TopShared) + (cluster > 1 ? static_cast<size_t>(cluster) * a.k * 8 : 0) : kMode == kLogprobs ? 0 : sizeof(ListShared);
+  size_t smem = kTop ? sizeof(TopShared<NT>) + (cluster > 1 ? static_cast<size_t>(cluster) * a.k * 8 : 0) : kMode == kLogprobs ? 0 : sizeof(ListShared);
   if (kMode == kTailBucket) {
     const int64_t share = (a.V + 2 * kVecOf<T>) / cluster + 2 * kVecOf<T>;
     smem += align_up(static_cast<size_t>(std::min<int64_t>(share, kMapColumns) + 31) / 8 + 4, 16);
   }
-  auto* kernel = logits_row_kernel<T, kMode, kEntropy, kTop>;
+  auto* kernel = logits_row_kernel<T, kMode, kEntropy, kTop, NT>;
   if (kTop || kMode == kTailBucket) {  // more than 48 KB of shared memory with the static part: asked for once per device
     static std::atomic<uint64_t> asked{0};
     const uint64_t bit = uint64_t(1) << (dev.device & 63);
@@ -880,7 +893,7 @@ nvfp4rl_status launch(const LogitsArgs& a, unsigned cluster, const DeviceInfo& d
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.M) * cluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -904,6 +917,11 @@ nvfp4rl_status launch_type(const LogitsArgs& a, const DeviceInfo& dev, cudaStrea
     cluster /= 2;
   if (a.ids) return a.tail ? launch<T, kTailBucket, false, false>(a, cluster, dev, st)
                            : launch<T, kNormalized, false, false>(a, cluster, dev, st);
+  // One row to a CTA: narrow ones, more of them, lose less to a row's end (2048 x 152064, 20 alternatives 117 us with 256
+  // threads, 108 with 128; 64 of them 124 and 119); a list of theirs holds 128 keys. Split rows take 256 (64 rows 11.4 and 12.9 us).
+  if (a.k > 0 && cluster == 1 && a.k + 32 <= kNarrow)
+    return a.entropy ? launch<T, kLogprobs, true, true, kNarrow>(a, cluster, dev, st)
+                     : launch<T, kLogprobs, false, true, kNarrow>(a, cluster, dev, st);
   if (a.k > 0)
     return a.entropy ? launch<T, kLogprobs, true, true>(a, cluster, dev, st)
                      : launch<T, kLogprobs, false, true>(a, cluster, dev, st);
