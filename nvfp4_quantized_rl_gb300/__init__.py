@@ -269,9 +269,12 @@ def ais_mixing(logp_rollout, logp_train, adv, C: float, delta: float, gamma: flo
 
 
 def _logit_rows(x, what="logits"):
-    """dtype code, M, V and row stride of a 2-D bf16 or fp32 CUDA tensor whose columns are contiguous."""
+    """dtype code, M, V, row stride and device index of a 2-D bf16 or fp32 CUDA tensor with contiguous columns."""
     import torch
-    dt = BF16 if x.dtype is torch.bfloat16 else F32 if x.dtype is torch.float32 else None
+    dtype, device = x.dtype, x.get_device()
+    if device < 0:
+        raise ValueError("nvfp4rl works on CUDA tensors only (no CPU path)")
+    dt = BF16 if dtype is torch.bfloat16 else F32 if dtype is torch.float32 else None
     if dt is None:
         raise TypeError(f"{what} must be bf16 or fp32")
     if x.dim() != 2:
@@ -282,7 +285,7 @@ def _logit_rows(x, what="logits"):
         ld = V
     if (V > 1 and step != 1) or ld < V:
         raise ValueError(f"{what}: the columns of a row must be contiguous, and rows must not overlap")
-    return dt, M, V, ld
+    return dt, M, V, ld, device
 
 
 def _row_array(t, name, dtype, shape, device):
@@ -293,15 +296,6 @@ def _row_array(t, name, dtype, shape, device):
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on the logits' device")
     return t.data_ptr()
-
-
-def _row_out(t, name, dtype, shape, device):
-    """An output of that kind and its address: made here, or the caller's, checked."""
-    if t is not None:
-        return t, _row_array(t, name, dtype, shape, device)
-    import torch
-    t = torch.empty(*shape, dtype=dtype, device=device)
-    return t, t.data_ptr()
 
 
 _logits_entry = {}  # the logits operators' C functions, once loaded
@@ -341,34 +335,50 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy:
     int32 [M, k], top_logp fp32 [M, k]); None where tokens is None, entropy is False or k is 0. Rows whose
     token is outside [0, V) are ignored (0, and ids -1)."""
     import torch
-    _require_cuda(logits)
     if stream is not None:
         return _on_stream(stream, logits, token_logprobs, logits, tokens, scale, k, entropy, logp, h, lse,
                           top_ids, top_logp)
-    dt, M, V, ld = _logit_rows(logits)
-    dev, f32, rows = logits.get_device(), torch.float32, (M,)
-    p_logp = p_h = p_ids = p_top = None
+    dt, M, V, ld, dev = _logit_rows(logits)
+    empty, f32, i32, rows = torch.empty, torch.float32, torch.int32, (M,)
+    p_tok = p_logp = p_h = p_ids = p_top = None
     if tokens is not None:
-        logp, p_logp = _row_out(logp, "logp", f32, rows, dev)
+        p_tok = _row_array(tokens, "tokens", i32, rows, dev)
+        p_logp = _row_array(logp, "logp", f32, rows, dev)
+        if p_logp is None:
+            logp = empty(M, dtype=f32, device=dev)
+            p_logp = logp.data_ptr()
     elif logp is not None:
         raise ValueError("logp needs tokens")
-    if entropy:
-        h, p_h = _row_out(h, "h", f32, rows, dev)
-    lse, p_lse = _row_out(lse, "lse", f32, rows, dev)
+    if not entropy:
+        h = None
+    elif h is None:
+        h = empty(M, dtype=f32, device=dev)
+        p_h = h.data_ptr()
+    else:
+        p_h = _row_array(h, "h", f32, rows, dev)
+    if lse is None:
+        lse = empty(M, dtype=f32, device=dev)
+        p_lse = lse.data_ptr()
+    else:
+        p_lse = _row_array(lse, "lse", f32, rows, dev)
     if k > 0:
-        top_ids, p_ids = _row_out(top_ids, "top_ids", torch.int32, (M, k), dev)
-        top_logp, p_top = _row_out(top_logp, "top_logp", f32, (M, k), dev)
-    _logits_call("token_logprobs", dev, logits.data_ptr(), dt, M, V, ld,
-                 _row_array(tokens, "tokens", torch.int32, rows, dev), float(scale), k, p_logp, p_h, p_lse, p_ids, p_top)
-    return logp, h if entropy else None, lse, top_ids if k > 0 else None, top_logp if k > 0 else None
+        top_ids = empty(M, k, dtype=i32, device=dev) if top_ids is None else top_ids
+        top_logp = empty(M, k, dtype=f32, device=dev) if top_logp is None else top_logp
+        p_ids = _row_array(top_ids, "top_ids", i32, (M, k), dev)
+        p_top = _row_array(top_logp, "top_logp", f32, (M, k), dev)
+    else:
+        top_ids = top_logp = None
+    _logits_call("token_logprobs", dev, logits.data_ptr(), dt, M, V, ld, p_tok, float(scale), k, p_logp, p_h, p_lse,
+                 p_ids, p_top)
+    return logp, h, lse, top_ids, top_logp
 
 
-def _dlogits(logits, out, M, V):
+def _dlogits(logits, out, M, V, device):
     """The gradient's tensor (made when None) and its row stride."""
     import torch
     if out is None:
-        return torch.empty(M, V, dtype=logits.dtype, device=logits.get_device()), V
-    if out.dtype is not logits.dtype or out.shape != (M, V) or out.get_device() != logits.get_device():
+        return torch.empty(M, V, dtype=logits.dtype, device=device), V
+    if out.dtype is not logits.dtype or out.shape != (M, V) or out.get_device() != device:
         raise ValueError("out must have the logits' dtype, shape and device")
     return out, _logit_rows(out, "out")[3]
 
@@ -379,13 +389,12 @@ def token_logprobs_backward(logits, tokens, lse, dlogp, scale: float = 1.0, entr
     gave them -> out [M, V] of the logits' dtype (may be the logits themselves: overwritten in place). dlogp or
     dentropy may be None."""
     import torch
-    _require_cuda(logits)
     if stream is not None:
         return _on_stream(stream, logits, token_logprobs_backward, logits, tokens, lse, dlogp, scale, entropy,
                           dentropy, out)
-    dt, M, V, ld = _logit_rows(logits)
-    dev, f32, rows = logits.get_device(), torch.float32, (M,)
-    out, ldd = _dlogits(logits, out, M, V)
+    dt, M, V, ld, dev = _logit_rows(logits)
+    f32, rows = torch.float32, (M,)
+    out, ldd = _dlogits(logits, out, M, V, dev)
     _logits_call("token_logprobs_backward", dev, logits.data_ptr(), dt, M, V, ld,
                  _row_array(tokens, "tokens", torch.int32, rows, dev), float(scale), _row_array(lse, "lse", f32, rows, dev),
                  _row_array(entropy, "entropy", f32, rows, dev), _row_array(dlogp, "dlogp", f32, rows, dev),
@@ -399,22 +408,20 @@ def topk_distill(logits, ids, teacher_logp, scale: float = 1.0, tail: bool = Fal
     fp32 [M, k]; ids outside [0, V) are skipped) -> (loss, lse, lse_tail fp32 [M]). The teacher is normalised
     over its list, or with tail=True everything unlisted is one more outcome (lse_tail is None without it)."""
     import torch
-    _require_cuda(logits)
     if stream is not None:
         return _on_stream(stream, logits, topk_distill, logits, ids, teacher_logp, scale, tail, loss, lse, lse_tail)
-    dt, M, V, ld = _logit_rows(logits)
-    dev, f32 = logits.get_device(), torch.float32
+    dt, M, V, ld, dev = _logit_rows(logits)
+    empty, f32, rows = torch.empty, torch.float32, (M,)
     k = ids.shape[1] if ids.dim() == 2 else 0
-    rows, listed, p_tail = (M,), (M, k), None
-    loss, p_loss = _row_out(loss, "loss", f32, rows, dev)
-    lse, p_lse = _row_out(lse, "lse", f32, rows, dev)
-    if tail:
-        lse_tail, p_tail = _row_out(lse_tail, "lse_tail", f32, rows, dev)
+    loss = empty(M, dtype=f32, device=dev) if loss is None else loss
+    lse = empty(M, dtype=f32, device=dev) if lse is None else lse
+    lse_tail = None if not tail else empty(M, dtype=f32, device=dev) if lse_tail is None else lse_tail
     _logits_call("topk_distill", dev, logits.data_ptr(), dt, M, V, ld, float(scale),
-                 _row_array(ids, "ids", torch.int32, listed, dev),
-                 _row_array(teacher_logp, "teacher_logp", f32, listed, dev), k,
-                 DISTILL_TAIL if tail else DISTILL_NORMALIZED, p_loss, p_lse, p_tail)
-    return loss, lse, lse_tail if tail else None
+                 _row_array(ids, "ids", torch.int32, (M, k), dev),
+                 _row_array(teacher_logp, "teacher_logp", f32, (M, k), dev), k,
+                 DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(loss, "loss", f32, rows, dev),
+                 _row_array(lse, "lse", f32, rows, dev), _row_array(lse_tail, "lse_tail", f32, rows, dev))
+    return loss, lse, lse_tail
 
 
 def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 1.0, tail: bool = False,
@@ -422,18 +429,16 @@ def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 
     """Gradient of sum(dloss * loss) to the logits, lse and lse_tail as topk_distill gave them -> out [M, V] of
     the logits' dtype (may be the logits themselves: overwritten in place)."""
     import torch
-    _require_cuda(logits)
     if stream is not None:
         return _on_stream(stream, logits, topk_distill_backward, logits, ids, teacher_logp, lse, dloss, scale,
                           tail, lse_tail, out)
-    dt, M, V, ld = _logit_rows(logits)
-    dev, f32 = logits.get_device(), torch.float32
+    dt, M, V, ld, dev = _logit_rows(logits)
+    f32, rows = torch.float32, (M,)
     k = ids.shape[1] if ids.dim() == 2 else 0
-    out, ldd = _dlogits(logits, out, M, V)
-    rows, listed = (M,), (M, k)
+    out, ldd = _dlogits(logits, out, M, V, dev)
     _logits_call("topk_distill_backward", dev, logits.data_ptr(), dt, M, V, ld, float(scale),
-                 _row_array(ids, "ids", torch.int32, listed, dev),
-                 _row_array(teacher_logp, "teacher_logp", f32, listed, dev), k,
+                 _row_array(ids, "ids", torch.int32, (M, k), dev),
+                 _row_array(teacher_logp, "teacher_logp", f32, (M, k), dev), k,
                  DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(lse, "lse", f32, rows, dev),
                  _row_array(lse_tail, "lse_tail", f32, rows, dev), _row_array(dloss, "dloss", f32, rows, dev),
                  out.data_ptr(), ldd)

@@ -95,18 +95,30 @@ def test_binding_refuses_cpu_and_wrong_tensors(nv):
         nv.token_logprobs(x)
     with pytest.raises(ValueError):
         nv.topk_distill(x, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1))
-    # the checks that need no GPU, by the helpers that every call uses
+    # the checks that need no GPU, by the helpers that every call uses (a tensor that says it is on device 0)
+    class OnGpu:
+        def __init__(self, t):
+            self.t = t
+
+        def get_device(self):
+            return 0
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
     for bad in (x.half(), x.to(torch.int16)):
         with pytest.raises(TypeError):
-            nv._logit_rows(bad)
-    for bad in (x[0], x.t(), x[:, ::2], x[:1].expand(3, 8)):
+            nv._logit_rows(OnGpu(bad))
+    for bad in (x, OnGpu(x[0]), OnGpu(x.t()), OnGpu(x[:, ::2]), OnGpu(x[:1].expand(3, 8))):
         with pytest.raises(ValueError):
             nv._logit_rows(bad)
-    assert nv._logit_rows(torch.zeros(3, 9)[:, 1:6]) == (nv.F32, 3, 5, 9)
-    assert nv._logit_rows(torch.zeros(1, 9).bfloat16()[:, :6]) == (nv.BF16, 1, 6, 9)
-    d = x.get_device()
-    nv._row_array(torch.zeros(2, dtype=torch.int32), "tokens", torch.int32, (2,), d)
+    assert nv._logit_rows(OnGpu(torch.zeros(3, 9)[:, 1:6])) == (nv.F32, 3, 5, 9, 0)
+    assert nv._logit_rows(OnGpu(torch.zeros(1, 9).bfloat16()[:, :6])) == (nv.BF16, 1, 6, 9, 0)
+    ok = OnGpu(torch.zeros(2, dtype=torch.int32))
+    assert nv._row_array(ok, "tokens", torch.int32, (2,), 0) == ok.t.data_ptr()
+    assert nv._row_array(None, "tokens", torch.int32, (2,), 0) is None
     for bad in (torch.zeros(2, dtype=torch.int64), torch.zeros(3, dtype=torch.int32),
                 torch.zeros(4, dtype=torch.int32)[::2]):
         with pytest.raises(ValueError):
-            nv._row_array(bad, "tokens", torch.int32, (2,), d)
+            nv._row_array(OnGpu(bad), "tokens", torch.int32, (2,), 0)
+    with pytest.raises(ValueError):
+        nv._row_array(ok, "tokens", torch.int32, (2,), 1)  # another device than the logits'
