@@ -20,8 +20,8 @@
 // the few thread-steps that reach it are read again, dealt out over the CTA, and the logits above the bound go to a
 // list in shared memory as 64-bit keys (value order, then the lower column). A list that is too long is cut by a
 // histogram; the rest is ranked by counting. The result does not depend on the order of the appends. 64 of each of
-// 2048 x 152064 bf16: 122 us, 0.75 of the copy rate (96 us without); testing every logit against a bound in the loop
-// took 164 us.
+// 2048 x 152064 bf16: 119 us, 0.77 of the copy rate (96 us without any), bound by the latency of the row's end; testing
+// every logit against a bound in the loop took 164 us. Rows of equal logits are dearer (2048 rows of zeros 147 us).
 //
 // Distillation with a tail bucket: listed columns are marked in a bit map in shared memory and masked as they are
 // read, so that the streamed sum is the tail's own, relative to its own maximum; the listed ones are gathered and
@@ -526,7 +526,8 @@ __device__ uint32_t refine_bound(TopShared<NT>& sh, uint32_t mask, int k, float&
 }
 
 // CTAs to an SM: five where 48 registers do. 2048 x 152064 bf16 (floor 92 us), without alternatives: 4 vectors and 4 CTAs
-// 106 us, 4 and 5 99 us, 5 and 5 96 us, 6 and 5 98 us, 8 and 4 99 us; with 64 of them 137, 138, 132, 131, 139 us.
+// 106 us, 4 and 5 99 us, 5 and 5 96 us, 6 and 5 98 us, 8 and 4 99 us. With 64 alternatives: 4 CTAs of 256 threads 124 us,
+// 5 163 us (spills), 6, 7, 8 CTAs of 128 threads 134, 119, 121 us.
 template <bool kTop, int NT>
 constexpr int kPerSm = !kTop ? 5 : NT == kThreads ? 4 : 7;
 
