@@ -492,6 +492,52 @@ def test_same_bits_on_every_call_and_stream(nv):
     assert all(torch.equal(p, q) for p, q in zip(first, kept))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [2.0 ** -20, 1e-3, 300.0, 2.0 ** 20])
+def test_scales_at_the_ends(nv, dtype, scale):
+    """The tolerances grow with |z| and |lse|, which fp32 holds to half an ulp; the order of the alternatives is the logits'."""
+    M, V = 4, 2500
+    x = G.make(M, V, dtype, 101)
+    tok = np.array([3, 2499, -1, 7], np.int32)
+    check_forward(nv, x, V, tok, scale, 40, dtype, what=f"scale {scale} {dtype}")
+    one = np.ones(M, np.float32)
+    if scale < 1000.0:  # above, lse itself is off by more than a nat
+        check_backward(nv, x, V, tok, scale, dtype, one, None, what=f"scale {scale} {dtype}")
+
+
+def test_a_graph_replays_on_new_contents(nv):
+    """A captured step, in place and over few rows (clusters) and many, reads what lies in its tensors at replay time."""
+    for M, V, k in ((3, 20001, 20), (700, 3001, 33)):
+        x, ids, l = teacher_case(M, V, k, "bf16", 111)
+        x = dev(x)
+        tok = torch.arange(M, dtype=torch.int32, device="cuda")
+        ids, l, one = P.dev(ids), P.dev(l), torch.ones(M, device="cuda")
+        logits = x.clone()
+
+        def step():
+            a = nv.token_logprobs(logits, tok, k=k)
+            b = nv.topk_distill(logits, ids, l, tail=True)
+            d = nv.topk_distill_backward(logits, ids, l, b[1], one, tail=True, lse_tail=b[2])
+            return [*a, *b, d, nv.token_logprobs_backward(logits, tok, a[2], one, entropy=a[1], dentropy=one, out=logits)]
+        step()
+        torch.cuda.synchronize()
+        logits.copy_(x)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kept = step()
+        for seed in (1, 2):
+            new = dev(G.make(M, V, "bf16", seed))
+            tok.copy_(torch.randint(-1, V, (M,), device="cuda").int())
+            logits.copy_(new)
+            g.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in kept]
+            logits.copy_(new)
+            want = step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_policy_step_from_linear_to_gradient(nv):
     """The run they are made for: logits of the same tokens from the W4A16 rollout head and from the bf16 trainer
     head, log-probs of both, AIS weights, and the gradient of the weighted policy objective to the trainer's logits;
