@@ -111,29 +111,31 @@ struct LogitsGradArgs {
 nvfp4rl_status launch_logprobs(const LogitsArgs& a, int dtype, const DeviceInfo& dev, cudaStream_t st);
 nvfp4rl_status launch_logprobs_grad(const LogitsGradArgs& a, int dtype, const DeviceInfo& dev, cudaStream_t st);
 
-// ---- a teacher's row, one entry to a thread of a CTA of 256 ----
+// ---- a teacher's row, one entry to a thread of a CTA of kW warps ----
 
-constexpr int kListWarps = 8;
+constexpr int kListWarps = 8;  // of the widest CTA
 static_assert(32 * kListWarps >= kMaxListed, "one thread per listed column");
 
-// Block reductions with one barrier each; `red` (kListWarps values of its own for every use in a row) is free again
+// Block reductions with one barrier each; `red` (kW values of its own for every use in a row) is free again
 // after the CTA's next barrier.
+template <int kW>
 __device__ __forceinline__ float cta_max(float v, float* red) {
   v = warp_max(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   v = red[0];
 #pragma unroll
-  for (int i = 1; i < kListWarps; ++i) v = fmaxf(v, red[i]);
+  for (int i = 1; i < kW; ++i) v = fmaxf(v, red[i]);
   return v;
 }
+template <int kW>
 __device__ __forceinline__ float2 cta_sum(float2 v, float2* red) {
   v = make_float2(warp_sum(v.x), warp_sum(v.y));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   v = red[0];
 #pragma unroll
-  for (int i = 1; i < kListWarps; ++i) v = make_float2(v.x + red[i].x, v.y + red[i].y);
+  for (int i = 1; i < kW; ++i) v = make_float2(v.x + red[i].x, v.y + red[i].y);
   return v;
 }
 
@@ -150,13 +152,14 @@ struct TeacherShared {
 
 // This thread's entry: column id (-1: none, or skipped) with log-prob l; gives its q and ln q. All threads call.
 // 1 - sum q would lose the digits of a small rest in 32 bits: the largest q enters as -expm1(l).
+template <int kW>
 __device__ __forceinline__ TeacherRow teacher_row(TeacherShared& sh, int id, float l, bool tail, float& q, float& lq) {
   const bool counts = id >= 0;
   // a NaN hides from the maximum, and shows in the sums
-  const float top = cta_max(counts ? l : -INFINITY, sh.top);
+  const float top = cta_max<kW>(counts ? l : -INFINITY, sh.top);
   if (!tail) {
     q = counts && l != -INFINITY ? expf(l - top) : 0.0f;
-    const float total = cta_sum(make_float2(q, 0.0f), sh.sum).x;
+    const float total = cta_sum<kW>(make_float2(q, 0.0f), sh.sum).x;
     q /= total;
     lq = (l - top) - logf(total);
     return TeacherRow{0.0f, total != total ? NAN : 1.0f, total != 0.0f};
@@ -164,7 +167,7 @@ __device__ __forceinline__ TeacherRow teacher_row(TeacherShared& sh, int id, flo
   q = counts ? expf(l) : 0.0f;
   lq = l;
   // the others' sum, and how many hold the largest
-  const float2 sum = cta_sum(make_float2(l == top ? 0.0f : q, counts && l == top ? 1.0f : 0.0f), sh.sum);
+  const float2 sum = cta_sum<kW>(make_float2(l == top ? 0.0f : q, counts && l == top ? 1.0f : 0.0f), sh.sum);
   const float largest = expf(top), others = fmaf(fmaxf(sum.y - 1.0f, 0.0f), largest, sum.x);
   const float rest = -expm1f(top) - others, q0 = rest < 0.0f ? 0.0f : rest;
   return TeacherRow{q0, (largest + others) + q0, true};

@@ -33,8 +33,7 @@
 namespace nvfp4rl {
 namespace {
 
-constexpr int kThreads = 256;                      // of a CTA, but for long rows with few alternatives (kNarrow)
-constexpr int kNarrow = 128;
+constexpr int kThreads = 256;                      // of the widest CTA
 constexpr int kU = 5;                              // vectors per thread and step
 constexpr int kBlock = 32;                         // steps whose maxima are kept (one bit each in a mask)
 constexpr int kParts = 1024;                       // thread-steps read again together
@@ -88,7 +87,7 @@ struct TopShared {
   static constexpr int kMaxKept = NT;                      // a cut leaves at most this many keys, one to a thread
   static constexpr int kCandidates = NT / 2 * 8 + kMaxKept;  // one vector of half the threads beside a list that was cut
   static constexpr int kBins = 4 * NT;
-  static constexpr int kLogBins = NT == 256 ? 10 : 9;
+  static constexpr int kLogBins = NT == 256 ? 10 : NT == 128 ? 9 : 8;
   static_assert(1 << kLogBins == kBins && kCandidates % 2 == 0, "four bins to a thread; keys are read in pairs");
   unsigned long long key[kCandidates];
   unsigned long long kept[kMaxKept];
@@ -525,18 +524,17 @@ __device__ uint32_t refine_bound(TopShared<NT>& sh, uint32_t mask, int k, float&
   return pass;
 }
 
-// CTAs to an SM: five where 48 registers do. 2048 x 152064 bf16 (floor 92 us), without alternatives: 4 vectors and 4 CTAs
-// 106 us, 4 and 5 99 us, 5 and 5 96 us, 6 and 5 98 us, 8 and 4 99 us. With 64 alternatives: 4 CTAs of 256 threads 124 us,
-// 5 163 us (spills), 6, 7, 8 CTAs of 128 threads 134, 119, 121 us.
+// CTAs to an SM. Five of 256 threads where 48 registers do: 2048 x 152064 bf16 (floor 92 us), without alternatives, 4
+// vectors and 4 CTAs 106 us, 4 and 5 99 us, 5 and 5 96 us, 6 and 5 98 us, 8 and 4 99 us. With 64 alternatives: 4 CTAs of
+// 256 threads 124 us, 5 163 us (spills), 6, 7, 8 CTAs of 128 threads 134, 119, 121 us.
 template <bool kTop, int NT>
-constexpr int kPerSm = !kTop ? 5 : NT == kThreads ? 4 : 7;
+constexpr int kPerSm = NT == 256 ? (kTop ? 4 : 5) : NT == 128 ? (kTop ? 7 : 10) : (kTop ? 13 : 18);
 
 // kEntropy: w is kept; kTop: alternatives are listed (both kLogprobs only).
 template <typename T, int kMode, bool kEntropy, bool kTop, int NT>
 __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const LogitsArgs a, uint32_t cluster) {
   constexpr int VEC = kVecOf<T>;
   constexpr bool kDistill = kMode != kLogprobs;
-  static_assert(NT == kThreads || kTop, "one thread per listed column");
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Shared sh;
   TopShared<NT>& top = *reinterpret_cast<TopShared<NT>*>(dyn);                  // kTop
@@ -822,17 +820,17 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
 
   if (kDistill) {
     float q, lq;
-    const TeacherRow t = teacher_row(list.teacher, id, listed_l, kMode == kTailBucket, q, lq);
+    const TeacherRow t = teacher_row<NT / 32>(list.teacher, id, listed_l, kMode == kTailBucket, q, lq);
     const float s_tail = sum.s;
     float R2 = sum.R;
     if (kMode == kTailBucket) {
-      R2 = fmaxf(R2, cta_max(listed_x <= -kLogitBound ? kNoRef : listed_x * c, list.top));
+      R2 = fmaxf(R2, cta_max<NT / 32>(listed_x <= -kLogitBound ? kNoRef : listed_x * c, list.top));
       const bool bad = listed_x != listed_x || listed_x > kLogitBound;
       bool once = id >= 0 && listed_x > -kLogitBound;  // the first entry of its column
       if (once && twice)
         for (int j = 0; j < tid; ++j) once &= list.ids[j] != id;
       const float e = bad ? NAN : once ? exp2_approx(fmaf(listed_x, c, -R2)) : 0.0f;
-      sum.s = fmaf(s_tail, exp2_approx(sum.R - R2), cta_sum(make_float2(e, 0.0f), list.sum[0]).x);
+      sum.s = fmaf(s_tail, exp2_approx(sum.R - R2), cta_sum<NT / 32>(make_float2(e, 0.0f), list.sum[0]).x);
     }
     const bool empty = sum.s == 0.0f;
     const float ln_s = logf(sum.s), down = sum.R - R2;
@@ -841,7 +839,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
       const float lp = empty || listed_x <= -kLogitBound ? -INFINITY : fmaf(listed_x, c, -R2) * kLn2 - ln_s;
       part = q * (lq - lp);
     }
-    part = cta_sum(make_float2(part, 0.0f), list.sum[1]).x;
+    part = cta_sum<NT / 32>(make_float2(part, 0.0f), list.sum[1]).x;
     if (tid == 0) {
       const float ln_tail = logf(s_tail);
       if (kMode == kTailBucket && t.q0 > 0.0f && s_tail > 0.0f)
@@ -875,7 +873,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
   }
 }
 
-template <typename T, int kMode, bool kEntropy, bool kTop, int NT = kThreads>
+template <typename T, int kMode, bool kEntropy, bool kTop, int NT>
 nvfp4rl_status launch(const LogitsArgs& a, unsigned cluster, const DeviceInfo& dev, cudaStream_t st) {
   size_t smem = kTop ? sizeof(TopShared<NT>) + (cluster > 1 ? static_cast<size_t>(cluster) * a.k * 8 : 0) : kMode == kLogprobs ? 0 : sizeof(ListShared);
   if (kMode == kTailBucket) {
@@ -909,6 +907,40 @@ nvfp4rl_status launch(const LogitsArgs& a, unsigned cluster, const DeviceInfo& d
   return cudaLaunchKernelEx(&cfg, kernel, a, cluster) == cudaSuccess ? launch_status() : NVFP4RL_ERR_CUDA;
 }
 
+template <typename T, int NT>
+nvfp4rl_status launch_width(const LogitsArgs& a, unsigned cluster, const DeviceInfo& dev, cudaStream_t st) {
+  if (a.ids) return a.tail ? launch<T, kTailBucket, false, false, NT>(a, cluster, dev, st)
+                           : launch<T, kNormalized, false, false, NT>(a, cluster, dev, st);
+  if (a.k > 0)
+    return a.entropy ? launch<T, kLogprobs, true, true, NT>(a, cluster, dev, st)
+                     : launch<T, kLogprobs, false, true, NT>(a, cluster, dev, st);
+  return a.entropy ? launch<T, kLogprobs, true, false, NT>(a, cluster, dev, st)
+                   : launch<T, kLogprobs, false, false, NT>(a, cluster, dev, st);
+}
+
+// Threads per row, of rows that are not split: narrow CTAs, more of them, where there are enough rows to fill the SMs, the
+// rows are short or their ends dear. Measured with 256, 128, 64 threads, bf16, in us (ent: entropy, top: 20 alternatives,
+// tail: 32 listed): 400 x 16000 ent 6.7, 5.3, 6.6, top 9.4, 7.9, 9.8, tail 9.1, 7.4, 9.4; 1064 x 8000 ent 7.4, 6.6, 6.6,
+// top 14.1, 9.3, 9.8, tail 10.9, 9.3, 8.1; 2128 x 16000 ent 19.1, 16.6, 16.0, top 30.4, 22.7, 17.9, tail 25.0, 19.7, 19.0;
+// 760 x 50257 ent 15.4, 16.9, 23.0, top 24.3, 21.0, 26.9, tail 19.0, 18.9, 26.3; 400 x 152064 ent 30.7, 34.7, 54.1, top 29.5,
+// 36.0, 59.7; 2128 x 152064 ent 99, 108, 108, top 115.8, 109.5, 109.6, tail 104, 117, 140.
+int width_of(const LogitsArgs& a, int64_t vecs, int sms) {
+  const bool list = a.ids != nullptr, top = !list && a.k > 0;
+  int w = 256;
+  if (a.M > 2 * sms) {
+    if (vecs > 12288)
+      w = top && a.M > 4 * sms ? 128 : 256;
+    else if (top)
+      w = a.M <= 4 * sms && vecs > 2560 ? 256 : a.M > 8 * sms && vecs <= 5120 ? 64 : 128;
+    else
+      w = a.M > 6 * sms && vecs <= 2560 ? 64 : list || vecs <= 5120 ? 128 : 256;
+  }
+  // a narrow CTA's list holds as many keys, its teacher as many entries, as it has threads
+  const int least = top ? a.k + 32 : list ? a.k : 0;
+  while (w < 256 && least > w) w *= 2;
+  return w;
+}
+
 template <typename T>
 nvfp4rl_status launch_type(const LogitsArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   // CTAs per row: two to an SM at most, and no share below one step. 152064 columns, 5 alternatives: 64 rows with 8 CTAs
@@ -916,18 +948,11 @@ nvfp4rl_status launch_type(const LogitsArgs& a, const DeviceInfo& dev, cudaStrea
   unsigned cluster = kMaxCluster;
   while (cluster > 1 && (a.M * cluster > 2 * dev.sm_count || a.V < static_cast<int64_t>(cluster) * kThreads * kVecOf<T>))
     cluster /= 2;
-  if (a.ids) return a.tail ? launch<T, kTailBucket, false, false>(a, cluster, dev, st)
-                           : launch<T, kNormalized, false, false>(a, cluster, dev, st);
-  // One row to a CTA: narrow ones, more of them, lose less to a row's end (2048 x 152064, 20 alternatives 117 us with 256
-  // threads, 108 with 128; 64 of them 124 and 119); a list of theirs holds 128 keys. Split rows take 256 (64 rows 11.4 and 12.9 us).
-  if (a.k > 0 && cluster == 1 && a.k + 32 <= kNarrow)
-    return a.entropy ? launch<T, kLogprobs, true, true, kNarrow>(a, cluster, dev, st)
-                     : launch<T, kLogprobs, false, true, kNarrow>(a, cluster, dev, st);
-  if (a.k > 0)
-    return a.entropy ? launch<T, kLogprobs, true, true>(a, cluster, dev, st)
-                     : launch<T, kLogprobs, false, true>(a, cluster, dev, st);
-  return a.entropy ? launch<T, kLogprobs, true, false>(a, cluster, dev, st)
-                   : launch<T, kLogprobs, false, false>(a, cluster, dev, st);
+  switch (cluster > 1 ? 256 : width_of(a, a.V / kVecOf<T>, dev.sm_count)) {
+    case 64: return launch_width<T, 64>(a, cluster, dev, st);
+    case 128: return launch_width<T, 128>(a, cluster, dev, st);
+    default: return launch_width<T, 256>(a, cluster, dev, st);
+  }
 }
 
 }  // namespace

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
     }
     ids_s[tid] = id >= 0 ? id : -1;
     // its barriers: the listed logits are read before a gradient in their place may be written
-    const TeacherRow t = teacher_row(teacher_s, id >= 0 ? id : -1, l, a.tail, q, lq);
+    const TeacherRow t = teacher_row<kListWarps>(teacher_s, id >= 0 ? id : -1, l, a.tail, q, lq);
     q_s[tid] = q;
     dead |= !__syncthreads_or(id >= 0) || !t.any;
     hit = d * a.scale;

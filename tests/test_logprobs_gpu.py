@@ -61,7 +61,8 @@ def check_forward(nv, x, V, tok, scale, k, dtype, shift=0, what=""):
 @pytest.mark.parametrize("M,V,k,scale,pad,shift", [
     (1, 1, 1, 1.0, 0, 0), (1, 7, 7, 1.0, 0, 0), (3, 8, 3, 0.7, 0, 1), (5, 33, 0, 1.25, 0, 3), (2, 1000, 20, 1.0, 24, 0),
     (4, 5003, 64, 0.5, 0, 0), (3, 8192, 128, 1.0, 1, 5), (1, 20001, 256, 2.0, 0, 7), (130, 1537, 5, 1.0, 0, 0),
-    (333, 257, 33, 1.0, 7, 2), (20, 16385, 1, 1.0, 0, 0), (640, 2049, 2, 0.9, 3, 0)])
+    (333, 257, 33, 1.0, 7, 2), (20, 16385, 1, 1.0, 0, 0), (640, 2049, 2, 0.9, 3, 0), (1300, 301, 5, 1.0, 0, 1),
+    (1301, 1500, 32, 1.0, 4, 0), (1000, 77, 0, 1.0, 0, 0), (950, 3003, 96, 0.6, 0, 0)])
 def test_logprobs_match_the_oracle(nv, dtype, M, V, k, scale, pad, shift):
     x = G.make(M, V, dtype, 11, ld=V + pad)
     r = synth.rng(5, M, V)
@@ -90,8 +91,10 @@ def test_masks_and_bad_rows(nv, dtype, V):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("V,k", [(300, 256), (5000, 1), (5000, 256), (70001, 40), (70001, 256)])
-def test_top_alternatives_of_hard_rows(nv, dtype, V, k):
+@pytest.mark.parametrize("V,k,times", [(300, 256, 1), (5000, 1, 1), (5000, 256, 1), (70001, 40, 1), (70001, 256, 1),
+                                       (3001, 40, 80), (3001, 1, 150), (3001, 32, 150), (12001, 20, 40)])
+def test_top_alternatives_of_hard_rows(nv, dtype, V, k, times):
+    """One CTA or a cluster to a row, and (`times` over) the narrower CTAs of many rows."""
     r = synth.rng(31, V, k)
     up = np.arange(V, dtype=np.float32) / V * 20 - 10
     rows = [up, up[::-1], np.zeros(V), np.where(r.random(V) < 0.5, 1.0, 0.0),  # rising, falling, constant, two values
@@ -101,8 +104,8 @@ def test_top_alternatives_of_hard_rows(nv, dtype, V, k):
             -np.abs(r.standard_normal(V)) - 2.0 ** 60,
             np.where((np.arange(V) > 4) & (np.arange(V) < V // 2), -np.inf, r.standard_normal(V))]  # a share nearly empty
     x = np.stack(rows).astype(np.float32)
-    x = _bits(x) if dtype == "bf16" else x
-    check_forward(nv, x, V, np.arange(9, dtype=np.int32), 1.0, k, dtype, what=f"hard {V} {k} {dtype}")
+    x = np.tile(_bits(x) if dtype == "bf16" else x, (times, 1))
+    check_forward(nv, x, V, np.arange(9 * times, dtype=np.int32) % V, 1.0, k, dtype, what=f"hard {V} {k} {dtype}")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -305,7 +308,8 @@ def check_distill(nv, x, V, ids, l, scale, tail, dtype, dloss, shift=0, out=None
 @pytest.mark.parametrize("M,V,k,scale,pad,shift,twice", [
     (1, 1, 1, 1.0, 0, 0, False), (2, 7, 7, 1.0, 0, 1, False), (3, 8, 3, 0.7, 5, 0, True), (4, 33, 40, 1.0, 0, 0, False),
     (5, 1000, 20, 1.25, 0, 3, False), (2, 5003, 64, 1.0, 0, 0, True), (130, 1537, 5, 0.5, 7, 0, False),
-    (3, 20001, 256, 1.0, 0, 0, True), (20, 4097, 100, 1.0, 1, 0, False), (400, 300, 33, 1.0, 0, 0, True)])
+    (3, 20001, 256, 1.0, 0, 0, True), (20, 4097, 100, 1.0, 1, 0, False), (400, 300, 33, 1.0, 0, 0, True),
+    (1000, 203, 20, 1.0, 5, 1, True), (930, 1111, 64, 0.8, 0, 0, False), (500, 700, 128, 1.0, 0, 0, True)])
 def test_distill_matches_the_oracle(nv, dtype, tail, M, V, k, scale, pad, shift, twice):
     x, ids, l = teacher_case(M, V, k, dtype, 71, twice, pad_entries=min(3, k - 1), ld=V + pad)
     if M > 2:
