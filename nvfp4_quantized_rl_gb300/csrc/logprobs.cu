@@ -10,10 +10,11 @@
 //
 // Each logit is read once: bound by HBM (8192 x 152064 bf16 with entropy 352 us, 1.04 of the copy rate), and near it by
 // issue slots, which is why the arithmetic is packed (8 instructions for two logits) and nothing else runs in the loop.
-// A CTA of 256 threads takes 5 x 16 bytes per thread and step; several CTAs on an SM hide one another's row ends. What
-// did not help: a cp.async ring that runs ahead over the rows' ends (410 us for 367 at the time: its copies and
-// shared-memory loads cost issue slots), and CTAs that stay for several rows. Few rows are split over clusters of 2 to
-// 8 CTAs, whose sums and alternatives meet in the first CTA's shared memory (one row with 20 alternatives 8 us).
+// A thread takes 5 x 16 bytes a step; several CTAs of 64 to 256 threads on an SM, a row to each, hide one another's row
+// ends. What did not help: a cp.async ring that runs ahead over the rows' ends (410 us for 367 at the time: its copies
+// and shared-memory loads cost issue slots), loading a step ahead into registers, and CTAs that stay for several rows.
+// Few rows are split over clusters of 2 to 8 CTAs, whose sums and alternatives meet in the first CTA's shared memory
+// (one row with 20 alternatives 8 us).
 //
 // Alternatives: the loop only keeps the upper half of each thread's maximum per step. At the row's end the k-th largest
 // of those maxima (of the threads' first, then by a histogram of the steps') bounds the k-th largest logit from below;

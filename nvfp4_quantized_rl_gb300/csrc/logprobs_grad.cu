@@ -8,19 +8,17 @@
 //     Q - q_0 / p_0 would overflow for a small p_0, so alpha = scale dloss (Q p_0 - q_0) with R = lse_tail log2 e;
 //   listed columns:  dx_j = scale dloss (Q p_j - q_j), written over the above after a block barrier.
 // Bound by HBM: each logit is read once, each gradient written once (4096 x 152064 bf16 with entropy 335 us, 1.03 of the
-// copy rate counted in the bytes it cannot do without; distillation with 64 listed 376 us, 0.98). A CTA of 256 threads
-// takes a chunk of one row, 16-byte vectors aligned for the stores; where the row of logits starts at another element of
+// copy rate counted in the bytes it cannot do without; distillation with 64 listed 371 us, 0.99). A CTA takes
+// a chunk of one row, 16-byte vectors aligned for the stores; where the row of logits starts at another element of
 // a vector than the row of gradients, a vector is put together from two aligned loads by funnel shifts (the second one
 // hits L1/L2). Vectors at a row's ends, whose 16 bytes are not all inside it, go element by element. A list costs every
-// chunk the same (the teacher's row, the barriers): chunks of four steps where the CTAs suffice (two steps 485 us, eight
-// 388); an fp32 batch of 100 rows stays at 0.69 (19 us).
+// chunk the same (the teacher's row, the barriers): chunks of four steps where the CTAs suffice (eight: 378 us);
+// an fp32 batch of 100 rows stays at 0.72 (18.5 us).
 #include "logits.cuh"
 
 namespace nvfp4rl {
 namespace {
 
-constexpr int kThreads = 256;
-static_assert(kThreads == 32 * kListWarps && kMaxListed <= kThreads, "one thread per listed column");
 constexpr int64_t kListCtas = 4 * kNumSMsHint;
 
 // The 8 (bf16) or 4 (fp32) logits that start s elements into the 32 bytes (a, b).
@@ -109,10 +107,10 @@ __device__ __forceinline__ uint4 grad_vec(uint4 x, const RowCoef& r, int at, flo
   return make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3]));
 }
 
-// kU: vectors per thread and step; kEntropy: the entropy term (token form only); kList: distillation;
+// NT: threads, at least as many as listed columns; kU: vectors per thread and step; kEntropy: the entropy term (token form only); kList: distillation;
 // kShift: rows of logits and gradients start at different elements of a vector (somewhere in the call).
-template <typename T, int kU, bool kEntropy, bool kList, bool kShift>
-__global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradArgs a, unsigned chunks, int steps) {
+template <typename T, int NT, int kU, bool kEntropy, bool kList, bool kShift>
+__global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a, unsigned chunks, int steps) {
   constexpr int VEC = kVecOf<T>;
   __shared__ __align__(16) int32_t ids_s[kList ? kMaxListed : 4];
   __shared__ float q_s[kList ? kMaxListed : 1];
@@ -122,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
   const int64_t row = blockIdx.x / chunks;
   // vectors and columns in 32 bits: V <= 2^30, and a chunk is longer than 2^17 vectors only where V < 2^20
   const int V = static_cast<int>(a.V);
-  const int v_begin = static_cast<int>(blockIdx.x % chunks) * steps * (kU * kThreads);
+  const int v_begin = static_cast<int>(blockIdx.x % chunks) * steps * (kU * NT);
   const T* x = static_cast<const T*>(a.x) + row * a.ld;
   T* dx = static_cast<T*>(a.dx) + row * a.ldd;
   const int tid = threadIdx.x;
@@ -140,10 +138,10 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
   uint4 in[kU], in2[kShift ? kU : 1];
   bool whole[kU];
   const auto load_step = [&](int step) {
-    const int v0 = v_begin + step * (kU * kThreads) + tid;
+    const int v0 = v_begin + step * (kU * NT) + tid;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int col = (v0 + u * kThreads) * VEC - out_phase;
+      const int col = (v0 + u * NT) * VEC - out_phase;
       // every byte of the loads and of the store lies inside the row
       whole[u] = kShift && s ? col >= s && col - s + 2 * VEC <= V : col >= 0 && col + VEC <= V;
       if (whole[u] && !dead) {
@@ -167,14 +165,14 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
     if (id >= V) id = -1;
     if (id >= 0) {
       const int v = (id + out_phase) / VEC - v_begin;
-      if (v >= 0 && v < steps * (kU * kThreads)) {
+      if (v >= 0 && v < steps * (kU * NT)) {
         mine = id;
         mine_x = logit(x, id);
       }
     }
     ids_s[tid] = id >= 0 ? id : -1;
     // its barriers: the listed logits are read before a gradient in their place may be written
-    const TeacherRow t = teacher_row<kListWarps>(teacher_s, id >= 0 ? id : -1, l, a.tail, q, lq);
+    const TeacherRow t = teacher_row<NT / 32>(teacher_s, id >= 0 ? id : -1, l, a.tail, q, lq);
     q_s[tid] = q;
     dead |= !__syncthreads_or(id >= 0) || !t.any;
     hit = d * a.scale;
@@ -202,11 +200,11 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
     r.beta = -a.scale * dh * kLn2 * f;
   }
   for (int step = 0; step < steps; ++step) {
-    const int v0 = v_begin + step * (kU * kThreads) + tid;
+    const int v0 = v_begin + step * (kU * NT) + tid;
     if (!kList || step > 0) load_step(step);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int col = (v0 + u * kThreads) * VEC - out_phase;
+      const int col = (v0 + u * NT) * VEC - out_phase;
       if (whole[u]) {
         uint4 g = make_uint4(0, 0, 0, 0);
         if (!dead) {
@@ -251,23 +249,23 @@ __global__ void __launch_bounds__(kThreads) logits_grad_kernel(const LogitsGradA
   }
 }
 
-template <typename T, int kU, bool kEntropy, bool kList>
+template <typename T, int NT, int kU, bool kEntropy, bool kList>
 cudaError_t launch(const LogitsGradArgs& a, bool shift, unsigned grid, unsigned chunks, int steps, cudaStream_t st) {
   if (shift)
-    return launch_pdl(logits_grad_kernel<T, kU, kEntropy, kList, true>, dim3(grid), dim3(kThreads), 0, st, a, chunks,
+    return launch_pdl(logits_grad_kernel<T, NT, kU, kEntropy, kList, true>, dim3(grid), dim3(NT), 0, st, a, chunks,
                       steps);
-  return launch_pdl(logits_grad_kernel<T, kU, kEntropy, kList, false>, dim3(grid), dim3(kThreads), 0, st, a, chunks,
+  return launch_pdl(logits_grad_kernel<T, NT, kU, kEntropy, kList, false>, dim3(grid), dim3(NT), 0, st, a, chunks,
                     steps);
 }
 
-template <typename T>
-nvfp4rl_status launch_type(const LogitsGradArgs& a, cudaStream_t st) {
+template <typename T, int NT>
+nvfp4rl_status launch_width(const LogitsGradArgs& a, cudaStream_t st) {
   constexpr int64_t VEC = kVecOf<T>;
   const auto phase = [](const void* p) { return static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / sizeof(T)) % VEC; };
   const bool shift = phase(a.x) != phase(a.dx) || (a.M > 1 && a.ld % VEC != a.ldd % VEC);
   const int64_t vecs = (a.V + 2 * VEC - 2) / VEC;  // of the row, at its worst phase
-  const bool wide = a.M * ((vecs + 4 * kThreads - 1) / (4 * kThreads)) >= 4 * kNumSMsHint;
-  const int64_t per_step = (wide ? 4 : 1) * kThreads;
+  const bool wide = a.M * ((vecs + 4 * NT - 1) / (4 * NT)) >= 4 * kNumSMsHint;
+  const int64_t per_step = (wide ? 4 : 1) * NT;
   // a list costs its chunk a fixed part: larger chunks, where enough CTAs are left
   int64_t steps = 1;
   while (a.ids && wide && steps < 4 && a.M * ((vecs + 2 * steps * per_step - 1) / (2 * steps * per_step)) >= kListCtas) steps *= 2;
@@ -277,15 +275,27 @@ nvfp4rl_status launch_type(const LogitsGradArgs& a, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(a.M * chunks), ch = static_cast<unsigned>(chunks);
   const int n = static_cast<int>(steps);
   cudaError_t e;
-  if (wide)
-    e = a.ids ? launch<T, 4, false, true>(a, shift, grid, ch, n, st)
-              : a.dentropy ? launch<T, 4, true, false>(a, shift, grid, ch, n, st)
-                           : launch<T, 4, false, false>(a, shift, grid, ch, n, st);
-  else
-    e = a.ids ? launch<T, 1, false, true>(a, shift, grid, ch, n, st)
-              : a.dentropy ? launch<T, 1, true, false>(a, shift, grid, ch, n, st)
-                           : launch<T, 1, false, false>(a, shift, grid, ch, n, st);
+  if constexpr (NT == 128) {
+    if (!a.ids) {
+      if (wide)
+        e = a.dentropy ? launch<T, NT, 4, true, false>(a, shift, grid, ch, n, st)
+                       : launch<T, NT, 4, false, false>(a, shift, grid, ch, n, st);
+      else
+        e = a.dentropy ? launch<T, NT, 1, true, false>(a, shift, grid, ch, n, st)
+                       : launch<T, NT, 1, false, false>(a, shift, grid, ch, n, st);
+      return e == cudaSuccess ? launch_status() : NVFP4RL_ERR_CUDA;
+    }
+  }
+  e = wide ? launch<T, NT, 4, false, true>(a, shift, grid, ch, n, st) : launch<T, NT, 1, false, true>(a, shift, grid, ch, n, st);
   return e == cudaSuccess ? launch_status() : NVFP4RL_ERR_CUDA;
+}
+
+// As many threads as the list has entries, at least 64: with 64 listed, 256, 128 and 64 threads took 381, 370, 371 us at
+// 4096 x 152064 bf16, 39, 20, 14.5 us at 4096 x 1001. Without a list 128: 8.9 and 6.6 us at 4096 x 1001, else alike.
+template <typename T>
+nvfp4rl_status launch_type(const LogitsGradArgs& a, cudaStream_t st) {
+  if (!a.ids || (a.k > 64 && a.k <= 128)) return launch_width<T, 128>(a, st);
+  return a.k <= 64 ? launch_width<T, 64>(a, st) : launch_width<T, 256>(a, st);
 }
 
 }  // namespace
