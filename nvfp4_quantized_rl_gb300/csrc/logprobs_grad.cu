@@ -275,7 +275,7 @@ nvfp4rl_status launch_width(const LogitsGradArgs& a, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(a.M * chunks), ch = static_cast<unsigned>(chunks);
   const int n = static_cast<int>(steps);
   cudaError_t e;
-  if constexpr (NT == 128) {
+  if constexpr (NT > 64) {
     if (!a.ids) {
       if (wide)
         e = a.dentropy ? launch<T, NT, 4, true, false>(a, shift, grid, ch, n, st)
@@ -291,11 +291,13 @@ nvfp4rl_status launch_width(const LogitsGradArgs& a, cudaStream_t st) {
 }
 
 // As many threads as the list has entries, at least 64: with 64 listed, 256, 128 and 64 threads took 381, 370, 371 us at
-// 4096 x 152064 bf16, 39, 20, 14.5 us at 4096 x 1001. Without a list 128: 8.9 and 6.6 us at 4096 x 1001, else alike.
+// 4096 x 152064 bf16, 39, 20, 14.5 us at 4096 x 1001. Without a list 256 for long rows (351.2 us, with 128 352.7), 128 for
+// short ones (6.6 us at 4096 x 1001, with 256 9.1).
 template <typename T>
 nvfp4rl_status launch_type(const LogitsGradArgs& a, cudaStream_t st) {
-  if (!a.ids || (a.k > 64 && a.k <= 128)) return launch_width<T, 128>(a, st);
-  return a.k <= 64 ? launch_width<T, 64>(a, st) : launch_width<T, 256>(a, st);
+  if (a.ids && a.k <= 64) return launch_width<T, 64>(a, st);
+  const bool narrow = a.ids ? a.k <= 128 : a.V <= 4096 * kVecOf<T>;
+  return narrow ? launch_width<T, 128>(a, st) : launch_width<T, 256>(a, st);
 }
 
 }  // namespace
