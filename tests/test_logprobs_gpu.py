@@ -363,6 +363,43 @@ def test_distill_gradient_places(nv, dtype):
     assert torch.equal(inplace, apart)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_subnormal_logits(nv, dtype):
+    """Values below the smallest normal one are values: they order the alternatives, and give the uniform p."""
+    V = 4000
+    r = synth.rng(121)
+    bits = r.integers(1, 0x80 if dtype == "bf16" else 0x7FFFFF, (2, V))
+    bits = np.where(r.random((2, V)) < 0.5, bits, bits | (0x8000 if dtype == "bf16" else 0x80000000))
+    x = bits.astype(np.uint16) if dtype == "bf16" else bits.astype(np.uint32).view(np.float32)
+    check_forward(nv, x, V, np.array([5, 6], np.int32), 1.0, 50, dtype, what=f"subnormal {dtype}")
+    check_forward(nv, np.tile(x, (700, 1)), V, np.arange(1400, dtype=np.int32), 1.0, 20, dtype, what=f"subnormal {dtype}")
+
+
+def test_many_tiny_rows(nv):
+    """Two hundred thousand rows of five columns (router logits' kind)."""
+    M, V = 200003, 5
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(M, V, generator=g, device="cuda").bfloat16()
+    tok = torch.randint(-1, V, (M,), generator=g, device="cuda").int()
+    logp, h, lse, ids, top = nv.token_logprobs(x, tok, k=2)
+    lp = torch.log_softmax(x.double(), 1)
+    live = tok >= 0
+    safe = tok.long().clamp_min(0)[:, None]
+    # (3 E[D] + 4 + V / 64 + 64) u + 8 u (|z| + ln 5) with |z| < 8, D < 16
+    tol = 300 * G.U
+    assert torch.all((logp.double() - torch.where(live, lp.gather(1, safe)[:, 0], 0.0)).abs() < tol)
+    order = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :2]
+    assert torch.equal(ids.long(), torch.where(live[:, None], order, -1))
+    one = torch.ones(M, device="cuda")
+    d = nv.token_logprobs_backward(x, tok, lse, one).double()
+    ref = torch.where(live[:, None], torch.zeros_like(lp).scatter_(1, safe, 1.0) - lp.exp(), 0.0)
+    assert torch.all((d - ref).abs() <= ref.abs() * 2.0 ** -8 + tol)
+    loss, lse2, rest = nv.topk_distill(x, ids, top, tail=True)  # a teacher that is the student
+    assert torch.all(loss.abs() < 10 * tol)
+    dd = nv.topk_distill_backward(x, ids, top, lse2, one, tail=True, lse_tail=rest)
+    assert torch.all(dd.double().abs() < 20 * tol)
+
+
 def test_offsets_beyond_32_bits(nv):
     """2.4 billion logits: the last rows lie behind element 2^31 (and 4 GB)."""
     M, V = 16000, 151665
