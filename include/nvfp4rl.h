@@ -289,7 +289,7 @@ NVFP4RL_API nvfp4rl_status token_logprobs(const void* logits, int32_t dtype, int
  *            logits themselves (the same pointer and ldd == ld: overwritten in place), and may
  *            overlap nothing otherwise.
  * Rows whose token is outside [0, V), whose dlogp and dentropy are both 0, or whose lse is -inf get
- * zeros and are not read.
+ * zeros, whatever they hold (they are not read).
  */
 NVFP4RL_API nvfp4rl_status token_logprobs_backward(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
                                                    const int32_t* tokens, float scale, const float* lse,
@@ -325,7 +325,7 @@ NVFP4RL_API nvfp4rl_status topk_distill(const void* logits, int32_t dtype, int64
  *   scale dloss (Q - q_0 / p_0) p_j at the others, Q = sum_i q_i + q_0 (NORMALIZED: Q = 1, q_0 = 0).
  * Arguments as topk_distill; lse, lse_tail as it wrote them (lse_tail is used by TAIL only, which needs it); dloss fp32 [M];
  *   dlogits, ldd as token_logprobs_backward.
- * Rows without an entry, with dloss 0, or with lse = -inf get zeros and are not read.
+ * Rows without an entry, with dloss 0, or with lse = -inf get zeros, whatever they hold.
  */
 NVFP4RL_API nvfp4rl_status topk_distill_backward(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
                                                  float scale, const int32_t* ids, const float* teacher_logp, int32_t k,
