@@ -5,6 +5,8 @@
 // has seen, t = x c - R; a larger maximum rescales them. Over a row (R, s, w) merge by
 // s 2^(R_i - R), (w + (R_i - R) s) 2^(R_i - R), and
 //   lse = R ln 2 + ln s,   ln p_j = t_j ln 2 - ln s,   entropy = ln s - ln 2 (w / s).
+// R is rounded, which shifts every t and s alike and drops out, but past 2^24 (a row, or a thread's part of one, of nothing
+// but -1e10 or -1e30) 2^t would overflow: there t = (x - max) c, and R has a low part.
 // A masked logit (at or below -2^100) gives 2^t = 0; where t itself is summed it is clamped to -2^100, which keeps t
 // finite. A thread that has seen nothing else adds nothing. A NaN stays in s.
 //
@@ -40,7 +42,7 @@ constexpr int kBlock = 32;                         // steps whose maxima are kep
 constexpr int kParts = 1024;                       // thread-steps read again together
 constexpr int kMaxCluster = 8;
 constexpr int kMapColumns = 1 << 18;               // columns per bit map (32 KB)
-constexpr float kNoRef = -1.7014118346046923e38f;  // R of nothing: -2^127, below every c x
+constexpr float kFarRef = 0x1p24f;                 // |R| above which R's rounding is a whole score or more
 static_assert(kThreads >= kMaxListed && kThreads == 32 * kListWarps, "one thread per listed column");
 
 enum Mode { kLogprobs = 0, kNormalized = 1, kTailBucket = 2 };
@@ -327,15 +329,38 @@ __device__ void sort_list(TopShared<NT>& sh, int k) {
 
 // ---- the streamed sums ----
 
+// s, w relative to the largest logit m
 struct RowSum {
-  float R, s, w;
+  float m, s, w;
 };
 
-__device__ __forceinline__ void merge(RowSum& a, const RowSum& b) {
-  const float R = max_nan(a.R, b.R), da = a.R - R, db = b.R - R, fa = exp2_approx(da), fb = exp2_approx(db);
+// The reference of a maximum m: R = fl(m c), and its low part, kept where R is far.
+__device__ __forceinline__ float ref_of(float m, float c) { return __fmul_rn(m, c); }
+__device__ __forceinline__ float ref_low(float m, float R, float c) { return fabsf(R) > kFarRef ? fmaf(m, c, -R) : 0.0f; }
+// The score of x relative to m.
+__device__ __forceinline__ float score_from(float x, float m, float c) {
+  const float R = ref_of(m, c);
+  return fmaf(x, c, -R) - ref_low(m, R, c);
+}
+// The reference of a relative to that of b.
+__device__ __forceinline__ float ref_diff(float a, float b, float c) {
+  const float Ra = ref_of(a, c), Rb = ref_of(b, c);
+  return (Ra - Rb) + (ref_low(a, Ra, c) - ref_low(b, Rb, c));
+}
+// The same for a <= b, no lower than where 2^d is 0: d s stays finite.
+__device__ __forceinline__ float ref_down(float a, float b, float c) { return fmaxf(ref_diff(a, b, c), -16384.0f); }
+// ln sum exp: scale m and ln s, without what the rounding of a near R put into s.
+__device__ __forceinline__ float ref_lse(float m, float c, float scale, float ln_s) {
+  const float R = ref_of(m, c);
+  return fmaf(m, scale, fabsf(R) > kFarRef ? ln_s : fmaf(-fmaf(m, c, -R), kLn2, ln_s));
+}
+
+__device__ __forceinline__ void merge(RowSum& a, const RowSum& b, float c) {
+  const float m = max_nan(a.m, b.m), da = ref_down(a.m, m, c), db = ref_down(b.m, m, c);
+  const float fa = exp2_approx(da), fb = exp2_approx(db);
   a.w = fmaf(da, a.s, a.w) * fa + fmaf(db, b.s, b.w) * fb;
   a.s = a.s * fa + b.s * fb;
-  a.R = R;
+  a.m = m;
 }
 
 template <typename T>
@@ -364,6 +389,20 @@ __device__ __forceinline__ uint4 clamp_masked(const uint4& x, uint16_t) {
 }
 __device__ __forceinline__ uint4 clamp_masked(const uint4& x, float) {
   const auto f = [](uint32_t w) { return __float_as_uint(max_nan(__uint_as_float(w), -kLogitBound)); };
+  return make_uint4(f(x.x), f(x.y), f(x.z), f(x.w));
+}
+// x - m. Rounding to bf16 is free here: bf16 logits below a far m are 2^15 scores or more below it.
+__device__ __forceinline__ uint4 minus_max(const uint4& x, float m, uint16_t) {
+  const uint32_t m2 = (__float_as_uint(m) >> 16) * 0x10001u;
+  const auto f = [&](uint32_t w) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(m2));
+    return r;
+  };
+  return make_uint4(f(x.x), f(x.y), f(x.z), f(x.w));
+}
+__device__ __forceinline__ uint4 minus_max(const uint4& x, float m, float) {
+  const auto f = [&](uint32_t w) { return __float_as_uint(__uint_as_float(w) - m); };
   return make_uint4(f(x.x), f(x.y), f(x.z), f(x.w));
 }
 __device__ __forceinline__ float vector_max(const uint4& x, uint16_t) {
@@ -627,7 +666,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
   if (cluster > 1) cluster_arrive();
   const float at_token = kMode == kLogprobs && tid == 0 && token >= 0 ? logit(x, token) : 0.0f;
   const float c = a.scale * kLog2E;
-  float m = -kLogitBound, R = kNoRef, thr = -kLogitBound;
+  float m = -kLogitBound, R = 0.0f, thr = -kLogitBound;
   F2 s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
   const F2 c2 = pack2(c, c);
   if (kTop && tid == 0) top.count = top.part_count = 0;
@@ -637,11 +676,11 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
     float lo, hi, wlo, whi;
     unpack2(s2, lo, hi);
     unpack2(w2, wlo, whi);
-    RowSum sum{R, lo + hi, wlo + whi};
+    RowSum sum{m, lo + hi, wlo + whi};
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-      merge(sum, RowSum{__shfl_xor_sync(0xFFFFFFFFu, sum.R, o), __shfl_xor_sync(0xFFFFFFFFu, sum.s, o),
-                        __shfl_xor_sync(0xFFFFFFFFu, sum.w, o)});
+      merge(sum, RowSum{__shfl_xor_sync(0xFFFFFFFFu, sum.m, o), __shfl_xor_sync(0xFFFFFFFFu, sum.s, o),
+                        __shfl_xor_sync(0xFFFFFFFFu, sum.w, o)}, c);
     if (lane == 0) sh.sums[warp] = sum;
   };
 
@@ -680,15 +719,21 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
 #pragma unroll
     for (int u = 1; u < kU; ++u) cm = max_nan(cm, vector_max(in[u], T()));
     if (!(cm <= m)) {  // larger, or NaN (which stays)
-      const float Rn = cm * c, d = R - Rn, f = exp2_approx(d);
+      const float d = ref_down(m, cm, c), f = exp2_approx(d);
       const F2 f2 = pack2(f, f);
       if (kEntropy) w2 = mul2(fma2(pack2(d, d), s2, w2), f2);
       s2 = mul2(s2, f2);
-      R = Rn;
       m = cm;
+      R = ref_of(m, c);
     }
     if (!(m <= -kLogitBound)) {
-      const F2 r2 = pack2(-R, -R);
+      float ref = -R;
+      if (fabsf(R) > kFarRef) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) in[u] = minus_max(in[u], m, T());
+        ref = 0.0f;
+      }
+      const F2 r2 = pack2(ref, ref);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
@@ -793,7 +838,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
   }
   RowSum sum = sh.sums[0];
 #pragma unroll
-  for (int i = 1; i < TopShared<NT>::kWarps; ++i) merge(sum, sh.sums[i]);
+  for (int i = 1; i < TopShared<NT>::kWarps; ++i) merge(sum, sh.sums[i], c);
   if (kTop) {
     if (top.count > 128) cut_values(top, top.count, k, thr, m);
     sort_list(top, k);
@@ -802,7 +847,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
     cluster_wait();  // every CTA has started (the arrival at the kernel's start): its shared memory is there
     if (tid == 0) {
       const uint32_t at = map_shared(&sh.parts[rank], 0);
-      st_cluster(at, sum.R);
+      st_cluster(at, sum.m);
       st_cluster(at + 4, sum.s);
       st_cluster(at + 8, sum.w);
     }
@@ -811,45 +856,45 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
     cluster_wait();
     if (rank > 0) return;
     sum = sh.parts[0];
-    for (uint32_t i = 1; i < cluster; ++i) merge(sum, sh.parts[i]);
+    for (uint32_t i = 1; i < cluster; ++i) merge(sum, sh.parts[i], c);
     if (kTop) {
       gather_lists(top, top.merged(), static_cast<int>(cluster), k);
       sort_list(top, k);
     }
   }
-  if (sum.R > kLogitBound * c) sum.s = NAN;  // a logit above 2^100
+  if (sum.m > kLogitBound) sum.s = NAN;  // a logit above 2^100
 
   if (kDistill) {
     float q, lq;
     const TeacherRow t = teacher_row<NT / 32>(list.teacher, id, listed_l, kMode == kTailBucket, q, lq);
     const float s_tail = sum.s;
-    float R2 = sum.R;
+    float m2 = sum.m;
     if (kMode == kTailBucket) {
-      R2 = fmaxf(R2, cta_max<NT / 32>(listed_x <= -kLogitBound ? kNoRef : listed_x * c, list.top));
+      m2 = fmaxf(m2, cta_max<NT / 32>(fmaxf(listed_x, -kLogitBound), list.top));
       const bool bad = listed_x != listed_x || listed_x > kLogitBound;
       bool once = id >= 0 && listed_x > -kLogitBound;  // the first entry of its column
       if (once && twice)
         for (int j = 0; j < tid; ++j) once &= list.ids[j] != id;
-      const float e = bad ? NAN : once ? exp2_approx(fmaf(listed_x, c, -R2)) : 0.0f;
-      sum.s = fmaf(s_tail, exp2_approx(sum.R - R2), cta_sum<NT / 32>(make_float2(e, 0.0f), list.sum[0]).x);
+      const float e = bad ? NAN : once ? exp2_approx(score_from(listed_x, m2, c)) : 0.0f;
+      sum.s = fmaf(s_tail, exp2_approx(ref_down(sum.m, m2, c)), cta_sum<NT / 32>(make_float2(e, 0.0f), list.sum[0]).x);
     }
     const bool empty = sum.s == 0.0f;
-    const float ln_s = logf(sum.s), down = sum.R - R2;
+    const float ln_s = logf(sum.s);
     float part = 0.0f;
     if (id >= 0 && q != 0.0f) {
-      const float lp = empty || listed_x <= -kLogitBound ? -INFINITY : fmaf(listed_x, c, -R2) * kLn2 - ln_s;
+      const float lp = empty || listed_x <= -kLogitBound ? -INFINITY : score_from(listed_x, m2, c) * kLn2 - ln_s;
       part = q * (lq - lp);
     }
     part = cta_sum<NT / 32>(make_float2(part, 0.0f), list.sum[1]).x;
     if (tid == 0) {
       const float ln_tail = logf(s_tail);
       if (kMode == kTailBucket && t.q0 > 0.0f && s_tail > 0.0f)
-        part += t.q0 * (logf(t.q0) - (fmaf(down, kLn2, ln_tail) - ln_s));
+        part += t.q0 * (logf(t.q0) - (fmaf(ref_diff(sum.m, m2, c), kLn2, ln_tail) - ln_s));
       // NORMALIZED with every l_i at -inf: the row does not count
       a.loss[row] = !t.any ? 0.0f : sum.s != sum.s ? NAN : part;
-      if (a.lse) a.lse[row] = !t.any ? 0.0f : empty ? -INFINITY : fmaf(R2, kLn2, ln_s);
+      if (a.lse) a.lse[row] = !t.any ? 0.0f : empty ? -INFINITY : ref_lse(m2, c, a.scale, ln_s);
       if (kMode == kTailBucket && a.lse_tail)
-        a.lse_tail[row] = sum.s != sum.s ? NAN : s_tail == 0.0f ? -INFINITY : fmaf(sum.R, kLn2, ln_tail);
+        a.lse_tail[row] = sum.s != sum.s ? NAN : s_tail == 0.0f ? -INFINITY : ref_lse(sum.m, c, a.scale, ln_tail);
     }
     return;
   }
@@ -859,18 +904,18 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
   if (tid == 0) {
     if (a.logp)
       a.logp[row] = bad ? NAN : empty || at_token <= -kLogitBound ? -INFINITY
-                                                                  : fmaf(at_token, c, -sum.R) * kLn2 - ln_s;
+                                                                  : score_from(at_token, sum.m, c) * kLn2 - ln_s;
     if (kEntropy) {
       const float h = empty ? 0.0f : ln_s - kLn2 * (sum.w / sum.s);
       a.entropy[row] = h < 0.0f ? 0.0f : h;
     }
-    if (a.lse) a.lse[row] = empty ? -INFINITY : fmaf(sum.R, kLn2, ln_s);
+    if (a.lse) a.lse[row] = empty ? -INFINITY : ref_lse(sum.m, c, a.scale, ln_s);
   }
   if (kTop && tid < k) {
     const unsigned long long key = tid < top.count && !bad ? top.key[tid] : 0ull;
     a.top_ids[row * k + tid] = key ? key_column(key) : -1;
     a.top_logp[row * k + tid] =
-        bad ? NAN : key ? fmaf(order_value(static_cast<uint32_t>(key >> 32)), c, -sum.R) * kLn2 - ln_s : -INFINITY;
+        bad ? NAN : key ? score_from(order_value(static_cast<uint32_t>(key >> 32)), sum.m, c) * kLn2 - ln_s : -INFINITY;
   }
 }
 

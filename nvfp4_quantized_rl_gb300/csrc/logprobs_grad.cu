@@ -39,9 +39,19 @@ __device__ __forceinline__ uint4 shift_vec(uint4 a, uint4 b, int s) {
                     __funnelshift_r(w[2], w[3], odd), __funnelshift_r(w[3], w[4], odd));
 }
 
+// lse: the reference of p, R = lse log2 e. x is clamped at `low`, where 2^t is 0 and beta t finite (0 beta t has to be 0).
 struct RowCoef {
-  float c, c_low, R, alpha, beta;
+  float c, c_low, R, alpha, beta, low, scale, lse;
 };
+
+// Past 2^20 the rounding of lse itself is a score of 2^-5 or more (and past 2^32 what R's took would overflow in 2^t):
+// score_far takes its place. (Not for -inf, NaN.)
+__device__ __forceinline__ bool is_far(float lse) { return fabsf(lse) > 0x1p20f && fabsf(lse) < INFINITY; }
+
+// t at such sizes, where lse comes to be z_max without a trace of ln s: p = 1 at the largest logits, never more.
+__device__ __forceinline__ float score_far(float v, const RowCoef& r) {
+  return fminf(fmaxf((__fmul_rn(v, r.scale) - r.lse) * kLog2E, -0x1p17f), 0.0f);
+}
 
 // t = x c - R, with the rounding of c made good for fp32 logits (29 2^-24 of p at z = 20; a bf16 result does not show it).
 template <typename T>
@@ -51,24 +61,32 @@ __device__ __forceinline__ float score(float v, const RowCoef& r) {
 
 // What the rounding of R = lse log2 e took: p = 2^(x c - R) times this, which goes into a row's factors.
 __device__ __forceinline__ float ref_factor(float lse, float R) {
+  if (is_far(lse)) return 1.0f;
   const float low = fmaf(lse, kLog2E, -R) + lse * kLog2ELow, d = -low * kLn2;
   return fabsf(d) < 0.01f ? fmaf(fmaf(0.5f * d, d, d), 1.0f, 1.0f) : expf(d);
 }
 
+__device__ __forceinline__ float low_of(float R, float c) { return fmaxf((R - 0x1p17f) / c, -kLogitBound); }
+
 // One element, with the roundings of the packed form (no contraction): the bits do not depend on where a row lies.
 template <typename T, bool kEntropy>
 __device__ __forceinline__ float grad1(float v, const RowCoef& r) {
-  // masked logits: t far below every exponent, 2^t = 0, and finite, as 0 beta t has to be 0
-  if (kEntropy || sizeof(T) == 4) v = fmaxf(v, -kLogitBound);
-  const float t = score<T>(v, r), e = exp2_approx(t);
+  float t;
+  if (is_far(r.lse)) {
+    t = score_far(v, r);
+  } else {
+    if (kEntropy || sizeof(T) == 4) v = fmaxf(v, r.low);
+    t = score<T>(v, r);
+  }
+  const float e = exp2_approx(t);
   return __fmul_rn(e, kEntropy ? fmaf(r.beta, t, r.alpha) : r.alpha);
 }
 
 template <typename T, bool kEntropy>
 __device__ __forceinline__ F2 grad2(float lo, float hi, const RowCoef& r) {
   if (kEntropy || sizeof(T) == 4) {
-    lo = fmaxf(lo, -kLogitBound);
-    hi = fmaxf(hi, -kLogitBound);
+    lo = fmaxf(lo, r.low);
+    hi = fmaxf(hi, r.low);
   }
   const F2 x = pack2(lo, hi), ref = pack2(-r.R, -r.R);
   const F2 t = fma2(x, pack2(r.c, r.c), sizeof(T) == 4 ? fma2(x, pack2(r.c_low, r.c_low), ref) : ref);
@@ -129,7 +147,9 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
   const float lse = a.lse[row];
   bool dead = lse == -INFINITY;
   const float c = a.scale * kLog2E, R = lse * kLog2E, f = ref_factor(lse, R);
-  RowCoef r{c, fmaf(a.scale, kLog2E, -c) + a.scale * kLog2ELow, R, 0.0f, 0.0f};
+  RowCoef r{c, fmaf(a.scale, kLog2E, -c) + a.scale * kLog2ELow, R, 0.0f, 0.0f, low_of(R, c), a.scale, lse};
+  const float rest = kList && a.tail ? a.lse_tail[row] : 0.0f;
+  const bool far = is_far(lse) || is_far(rest);  // element by element
   float hit = 0.0f, mass = 0.0f;
   int token = -1;
   // listed columns of this chunk: thread i holds entry i
@@ -143,7 +163,7 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
     for (int u = 0; u < kU; ++u) {
       const int col = (v0 + u * NT) * VEC - out_phase;
       // every byte of the loads and of the store lies inside the row
-      whole[u] = kShift && s ? col >= s && col - s + 2 * VEC <= V : col >= 0 && col + VEC <= V;
+      whole[u] = !far && (kShift && s ? col >= s && col - s + 2 * VEC <= V : col >= 0 && col + VEC <= V);
       if (whole[u] && !dead) {
         in[u] = ld_logits16(x + col - s);
         if (kShift && s) in2[u] = ld_logits16(x + col - s + VEC);
@@ -153,7 +173,7 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
   if (kList) {
     // all of these are under way together: the row's scalars, its list, the first vectors and the listed logits of
     // this chunk
-    const float d = a.dloss[row], rest = a.tail ? a.lse_tail[row] : 0.0f;
+    const float d = a.dloss[row];
     int id = -1;
     float l = -INFINITY, q, lq;
     if (tid < a.k) {
@@ -183,7 +203,9 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
         mass -= t.q0;  // no bucket; the unlisted columns are masked
         r.alpha = 0.0f;
       } else {
+        r.lse = rest;
         r.R = rest * kLog2E;
+        r.low = low_of(r.R, c);
         r.alpha = (mass * expf(rest - lse) - t.q0) * hit * ref_factor(rest, r.R);
       }
     }
@@ -243,7 +265,9 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
         }
       }
       r.R = R;
-      const float p = mine_x <= -kLogitBound && lse == lse ? 0.0f : exp2_approx(score<T>(mine_x, r)) * f;
+      r.lse = lse;
+      const float t = is_far(lse) ? score_far(mine_x, r) : score<T>(mine_x, r);
+      const float p = mine_x <= -kLogitBound && lse == lse ? 0.0f : exp2_approx(t) * f;
       if (first) store_logit(dx, mine, hit * (fmaf(mass, p, -q)));
     }
   }

@@ -624,3 +624,195 @@ def test_policy_step_from_linear_to_gradient(nv):
     assert np.all(f64(loss)[on] >= -1e-4) and np.abs(f64(loss) - o_l).max() < 1e-3 and np.all(f64(loss)[~on] == 0)
     o_g = oracle.topk_distill_grad(bits_r, ids.cpu().numpy(), top.cpu().numpy(), 1.0, True, np.ones(M, np.float32), V=V)
     assert np.abs(f64(gd) - o_g).max() < 4e-3  # half an ulp of bf16 at 1 and the bound above
+
+
+# ---- logits far from 0: offsets, and masks that are large finite numbers ----
+
+def relative(x, scale, V):
+    """From 64-bit scores relative to each row's maximum (z itself would lose them): ln p, entropy, ln s, E[D]."""
+    d = G.values(x[:, :V])
+    d = (d - d.max(1, keepdims=True)) * float(np.float32(scale))
+    s = np.exp(d).sum(1)
+    lp = d - np.log(s)[:, None]
+    D = np.where(np.isfinite(d), -d, 0.0)
+    p = np.exp(lp)
+    ED = (p * D).sum(1)
+    return lp, np.log(s) + ED, np.log(s), ED
+
+
+def far_rows(M, V, dtype, fill, seed):
+    """Rows that are `fill` but for: nothing; a few ordinary columns; the last column; all but one ordinary; differing
+    fills; an ordinary row moved by fill (fp32 keeps little or nothing of it)."""
+    x = G.make(M, V, "f32", seed)
+    keep = x.copy()
+    r = synth.rng(seed, M, 3)
+    x[:] = fill
+    for m in range(1, M):
+        kind = m % 6
+        if kind == 1:
+            c = r.choice(V, size=5, replace=False)
+            x[m, c] = keep[m, c]
+        elif kind == 2:
+            x[m, -1] = keep[m, -1]
+        elif kind == 3:
+            x[m] = keep[m]
+            x[m, r.integers(V)] = fill
+        elif kind == 4:
+            x[m] = fill * (1.0 + 0.5 * r.random(V))
+        elif kind == 5:
+            x[m] = fill + keep[m]
+    x = x.astype(np.float32)
+    return synth.bf16_bits(x) if dtype == "bf16" else x
+
+
+FILLS = [-1e4, -1e7, -1e9, -1e10, -1e30, 1e10, 3e29]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fill", FILLS)
+@pytest.mark.parametrize("M,V", [(7, 5003), (7, 40000), (700, 1501)])
+def test_forward_far_from_zero(nv, dtype, fill, M, V):
+    for scale in (1.0, 0.7):
+        x = far_rows(M, V, dtype, fill, 71)
+        lp, h, ln_s, ED = relative(x, scale, V)
+        tok = np.argmax(G.values(x), axis=1).astype(np.int32)
+        tok[::2] = (np.arange(M)[::2] * 7919) % V
+        S = (3 * ED + 4 + V / 64 + 64) * G.U  # as in _logits.py; scores beyond 2^24 are rounded once more, 2 u D
+        S += 2 * G.U * ED
+        xd, td = dev(x), P.dev(tok)
+        for k in (0, 5, 40):
+            logp, hd, lse, ids, top = nv.token_logprobs(xd, td, scale, k=k)
+            at = lp[np.arange(M), tok]
+            far = np.abs(at + ln_s)
+            G.close(f64(logp), at, S + 10 * G.U * (far + ln_s), f"logp k={k}")
+            G.close(f64(hd), h, S * (1 + 3 * ED) + 8 * G.U * (ED + ln_s), f"entropy k={k}")
+            z = G.values(x).max(1) * float(np.float32(scale))
+            G.close(f64(lse), z + ln_s, S + 8 * G.U * (np.abs(z) + ln_s), f"lse k={k}")
+            if k:
+                order = np.argsort(-G.values(x), axis=1, kind="stable")[:, :k]
+                assert np.array_equal(ids.cpu().numpy(), order)
+                want = np.take_along_axis(lp, order, 1)
+                G.close(f64(top), want, S[:, None] + 10 * G.U * (np.abs(want + ln_s[:, None]) + ln_s[:, None]), "top")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fill", FILLS)
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_far_from_zero(nv, dtype, fill, tail):
+    M, V, k = 37, 3001, 9
+    x = far_rows(M, V, dtype, fill, 72)
+    ids, t = G.teacher(M, k, V, 73)
+    ids[::3, 0] = np.argmax(G.values(x), axis=1)[::3]
+    ids[::3, 1:] = (ids[::3, :1] + 1 + np.arange(k - 1)) % V
+    lp, _, ln_s, ED = relative(x, 1.0, V)
+    li = np.take_along_axis(lp, ids.astype(np.int64), 1)
+    lq = t.astype(np.float64)
+    if not tail:
+        lq = lq - np.log(np.exp(lq).sum(1, keepdims=True))
+    q = np.exp(lq)
+    ref = (q * (lq - li)).sum(1)
+    size = (q * (np.abs(lq) + np.abs(li))).sum(1)
+    S = (5 * np.log(V) + 4 + V / 64 + 64) * G.U  # E[D] = entropy - ln s, of the row as of its unlisted columns, is below ln V
+    if tail:
+        un = lp.copy()
+        un[~np.isfinite(un)] = -np.inf
+        np.put_along_axis(un, ids.astype(np.int64), -np.inf, 1)
+        top = un.max(1)
+        rest = top + np.log(np.exp(un - top[:, None]).sum(1))  # ln p_0
+        q0 = 1 - q.sum(1)
+        ref += q0 * (np.log(q0) - rest)
+        size += q0 * (np.abs(np.log(q0)) + np.abs(rest))
+    loss, lse, lse_tail = nv.topk_distill(dev(x), P.dev(ids), P.dev(t), tail=tail)
+    # each term q (ln q - ln p): ln q by (8 |ln q| + 40) u, ln p by S and 10 u |ln p|, the sum of k + 1 terms by (k + 8) u;
+    # q_0, by the errors of k + 1 exponentials and their sum, (k + 12) u absolute
+    extra = (k + 12) * G.U * np.abs(np.log(q0) - rest) if tail else 0.0
+    G.close(f64(loss), ref, 2 * S + (k + 60) * G.U * (size + 1) + extra, "loss")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fill", FILLS)
+@pytest.mark.parametrize("shift", [0, 3])
+def test_gradients_far_from_zero(nv, dtype, fill, shift):
+    """Masks far below ordinary logits, and rows that are far as a whole with one largest logit: p is 0 and 1."""
+    M, V, k = 6, 2049, 5
+    x = G.make(M, V, "f32", 74)
+    x[1, ::2] = fill if fill < 0 else -fill
+    x[2] = fill * (1.5 if fill < 0 else 0.5)
+    x[2, 77] = fill
+    x[3] = fill if fill < 0 else -fill
+    x[3, 1024:1030] = [1.0, 2.0, 0.5, -1.0, 3.0, 0.0]
+    x[4] = np.where(np.arange(V) % 3 == 0, -np.inf, fill * (1.5 if fill < 0 else 0.5))
+    x[4, 78] = fill
+    x = synth.bf16_bits(x) if dtype == "bf16" else x
+    scale = 1.25
+    lp, h, ln_s, ED = relative(x, scale, V)
+    p = np.exp(lp)
+    tok = np.array([5, 1, 77, 1026, 5, 0], np.int32)
+    dl = np.linspace(-1.0, 1.5, M).astype(np.float32)
+    dh = np.linspace(0.5, -0.7, M).astype(np.float32)
+    xd, td = dev(x, shift=shift), P.dev(tok)
+    _, hd, lse, _, _ = nv.token_logprobs(xd, td, scale)
+    hit = np.zeros((M, V))
+    hit[np.arange(M), tok] = 1.0
+    l64 = f64(lse)
+    # p by (3 |z| + 3 |lse| + 8) u and lse's own error where z is not far; far rows hold one p of 1
+    e = np.where(np.abs(l64) > 2.0 ** 20, 16 * G.U, G.U * (6 * np.abs(l64) + 3 * np.abs(ED) + 60 + V / 64 + 8 * np.abs(l64)))
+    for g_h in (None, dh):
+        got = nv.token_logprobs_backward(xd, td, lse, P.dev(dl), scale, entropy=hd, dentropy=None if g_h is None else P.dev(g_h))
+        ln = np.where(p > 0, lp, 0.0)
+        ref = dl[:, None] * (hit - p) - (0.0 if g_h is None else g_h[:, None] * p * (ln + h[:, None]))
+        part = np.abs(dl)[:, None] + np.abs(dh)[:, None] * (np.abs(ln) + h[:, None] + 1)
+        tol = 4 * e[:, None] * p * part + 16 * G.U * hit + G.half_ulp(ref, dtype) + 2.0 ** -120
+        G.close(f64(got.float()), ref * scale, tol * scale + G.half_ulp(ref * scale, dtype), f"dlogits entropy {g_h is not None}")
+    ids = np.stack([np.array([77, 1024, 1028, 5, 2000], np.int32)] * M)
+    t = np.log(np.array([0.4, 0.2, 0.1, 0.1, 0.05], np.float32))[None].repeat(M, 0)
+    q = np.zeros((M, V))
+    np.put_along_axis(q, ids.astype(np.int64), np.exp(t.astype(np.float64)), 1)
+    for tail in (False, True):
+        loss, l2, lt = nv.topk_distill(xd, P.dev(ids), P.dev(t), scale, tail=tail)
+        got = f64(nv.topk_distill_backward(xd, P.dev(ids), P.dev(t), l2, P.dev(dl), scale, tail=tail, lse_tail=lt).float())
+        if not tail:
+            ref = dl[:, None] * (p - q / q.sum(1, keepdims=True))
+        else:
+            un = np.where(q > 0, -np.inf, lp)
+            top = un.max(1, keepdims=True)
+            b = np.exp(un - top)
+            b /= b.sum(1, keepdims=True)  # the bucket's own softmax
+            ref = dl[:, None] * (p - q - (1 - q.sum(1, keepdims=True)) * b)
+        assert np.all(np.isfinite(got))
+        rows = np.ones(M, bool)
+        if tail:  # a bucket of equal far logits: each counts as the largest one, as lse_tail holds no more
+            rows &= np.abs(f64(lt)) < 2.0 ** 20
+            assert np.all(np.abs(got) <= 2.0 * scale * np.abs(dl)[:, None])
+        listed = q > 0
+        size = p + q + np.abs(ref)
+        tol = (4 * e[:, None] + 60 * G.U) * size * 2 + G.half_ulp(ref, dtype) + 2.0 ** -120
+        if tail:
+            tol = tol + (4 * e[:, None] + 160 * G.U) * np.where(listed, 0.0, b)
+        G.close(got[rows], (ref * scale)[rows], (tol * scale + G.half_ulp(ref * scale, dtype))[rows], f"distill tail {tail}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scales_at_the_ends_of_their_range(nv, dtype):
+    """2^20 and 2^-20 with masked columns and logits of either bound: nothing turns into NaN."""
+    M, V = 5, 6007
+    x = G.make(M, V, "f32", 75)
+    x[:, 1::7] = -np.inf
+    x[1] *= 2.0 ** -18
+    x[2] = -(2.0 ** 99)
+    x[2, -1] = 2.0 ** 99
+    x[3, :4000] = -(2.0 ** 99)
+    x = synth.bf16_bits(x) if dtype == "bf16" else x
+    tok = np.full(M, 6006, np.int32)
+    one = np.ones(M, np.float32)
+    for scale in (2.0 ** 20, 2.0 ** -20):
+        lp, h, ln_s, ED = relative(x, scale, V)
+        logp, hd, lse, _, _ = nv.token_logprobs(dev(x), P.dev(tok), scale, k=3)
+        S = (5 * ED + 4 + V / 64 + 64) * G.U
+        G.close(f64(hd), h, S * (1 + 3 * ED) + 8 * G.U * (ED + ln_s), "entropy")
+        G.close(f64(logp), lp[:, -1], S + 10 * G.U * (np.abs(lp[:, -1] + ln_s) + ln_s), "logp")
+        for dh in (0.5, 1000.0):
+            got = nv.token_logprobs_backward(dev(x), P.dev(tok), lse, P.dev(one), scale, entropy=hd, dentropy=P.dev(one * dh))
+            got = f64(got.float())
+            assert np.all(np.isfinite(got))
+            assert np.all(got[:, 1::7][G.values(x)[:, 1::7] == -np.inf] == 0)
