@@ -111,6 +111,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float warp_max_nan(float a) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -342,25 +347,45 @@ __device__ __forceinline__ float score_from(float x, float m, float c) {
   const float R = ref_of(m, c);
   return fmaf(x, c, -R) - ref_low(m, R, c);
 }
-// The reference of a relative to that of b.
-__device__ __forceinline__ float ref_diff(float a, float b, float c) {
-  const float Ra = ref_of(a, c), Rb = ref_of(b, c);
-  return (Ra - Rb) + (ref_low(a, Ra, c) - ref_low(b, Rb, c));
+// The reference of a relative to that of b. (Far bf16 maxima are equal or 2^15 scores apart: no low parts.)
+template <typename T>
+__device__ __forceinline__ float ref_diff(float a, float Ra, float b, float Rb, float c) {
+  const float d = Ra - Rb;
+  return sizeof(T) == 4 ? d + (ref_low(a, Ra, c) - ref_low(b, Rb, c)) : d;
 }
 // The same for a <= b, no lower than where 2^d is 0: d s stays finite.
-__device__ __forceinline__ float ref_down(float a, float b, float c) { return fmaxf(ref_diff(a, b, c), -16384.0f); }
+template <typename T>
+__device__ __forceinline__ float ref_down(float a, float Ra, float b, float Rb, float c) {
+  return fmaxf(ref_diff<T>(a, Ra, b, Rb, c), -16384.0f);
+}
 // ln sum exp: scale m and ln s, without what the rounding of a near R put into s.
 __device__ __forceinline__ float ref_lse(float m, float c, float scale, float ln_s) {
   const float R = ref_of(m, c);
   return fmaf(m, scale, fabsf(R) > kFarRef ? ln_s : fmaf(-fmaf(m, c, -R), kLn2, ln_s));
 }
 
-__device__ __forceinline__ void merge(RowSum& a, const RowSum& b, float c) {
-  const float m = max_nan(a.m, b.m), da = ref_down(a.m, m, c), db = ref_down(b.m, m, c);
-  const float fa = exp2_approx(da), fb = exp2_approx(db);
-  a.w = fmaf(da, a.s, a.w) * fa + fmaf(db, b.s, b.w) * fb;
-  a.s = a.s * fa + b.s * fb;
-  a.m = m;
+// a, relative to a maximum m of several.
+template <typename T>
+__device__ __forceinline__ RowSum moved(const RowSum& a, float m, float c) {
+  const float d = ref_down<T>(a.m, ref_of(a.m, c), m, ref_of(m, c), c), f = exp2_approx(d);
+  return RowSum{m, a.s * f, fmaf(d, a.s, a.w) * f};
+}
+// The sum of n parts, n <= N, in their order.
+template <typename T, int N>
+__device__ __forceinline__ RowSum merged(const RowSum* parts, int n, float c) {
+  float m = parts[0].m;
+#pragma unroll
+  for (int i = 1; i < N; ++i)
+    if (i < n) m = max_nan(m, parts[i].m);
+  RowSum sum{m, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < n) {
+      const RowSum a = moved<T>(parts[i], m, c);
+      sum.s += a.s;
+      sum.w += a.w;
+    }
+  return sum;
 }
 
 template <typename T>
@@ -666,7 +691,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
   if (cluster > 1) cluster_arrive();
   const float at_token = kMode == kLogprobs && tid == 0 && token >= 0 ? logit(x, token) : 0.0f;
   const float c = a.scale * kLog2E;
-  float m = -kLogitBound, R = 0.0f, thr = -kLogitBound;
+  float m = -kLogitBound, R = ref_of(m, c), thr = -kLogitBound;
   F2 s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
   const F2 c2 = pack2(c, c);
   if (kTop && tid == 0) top.count = top.part_count = 0;
@@ -676,11 +701,9 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
     float lo, hi, wlo, whi;
     unpack2(s2, lo, hi);
     unpack2(w2, wlo, whi);
-    RowSum sum{m, lo + hi, wlo + whi};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      merge(sum, RowSum{__shfl_xor_sync(0xFFFFFFFFu, sum.m, o), __shfl_xor_sync(0xFFFFFFFFu, sum.s, o),
-                        __shfl_xor_sync(0xFFFFFFFFu, sum.w, o)}, c);
+    RowSum sum = moved<T>(RowSum{m, lo + hi, wlo + whi}, warp_max_nan(m), c);
+    sum.s = warp_sum(sum.s);
+    if (kEntropy) sum.w = warp_sum(sum.w);
     if (lane == 0) sh.sums[warp] = sum;
   };
 
@@ -719,12 +742,12 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
 #pragma unroll
     for (int u = 1; u < kU; ++u) cm = max_nan(cm, vector_max(in[u], T()));
     if (!(cm <= m)) {  // larger, or NaN (which stays)
-      const float d = ref_down(m, cm, c), f = exp2_approx(d);
+      const float Rn = ref_of(cm, c), d = ref_down<T>(m, R, cm, Rn, c), f = exp2_approx(d);
       const F2 f2 = pack2(f, f);
       if (kEntropy) w2 = mul2(fma2(pack2(d, d), s2, w2), f2);
       s2 = mul2(s2, f2);
+      R = Rn;
       m = cm;
-      R = ref_of(m, c);
     }
     if (!(m <= -kLogitBound)) {
       float ref = -R;
@@ -836,9 +859,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
     warp_sums();
     __syncthreads();
   }
-  RowSum sum = sh.sums[0];
-#pragma unroll
-  for (int i = 1; i < TopShared<NT>::kWarps; ++i) merge(sum, sh.sums[i], c);
+  RowSum sum = merged<T, NT / 32>(sh.sums, NT / 32, c);
   if (kTop) {
     if (top.count > 128) cut_values(top, top.count, k, thr, m);
     sort_list(top, k);
@@ -855,8 +876,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
     cluster_arrive();
     cluster_wait();
     if (rank > 0) return;
-    sum = sh.parts[0];
-    for (uint32_t i = 1; i < cluster; ++i) merge(sum, sh.parts[i], c);
+    sum = merged<T, kMaxCluster>(sh.parts, static_cast<int>(cluster), c);
     if (kTop) {
       gather_lists(top, top.merged(), static_cast<int>(cluster), k);
       sort_list(top, k);
@@ -868,6 +888,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
     float q, lq;
     const TeacherRow t = teacher_row<NT / 32>(list.teacher, id, listed_l, kMode == kTailBucket, q, lq);
     const float s_tail = sum.s;
+    const float R1 = ref_of(sum.m, c);
     float m2 = sum.m;
     if (kMode == kTailBucket) {
       m2 = fmaxf(m2, cta_max<NT / 32>(fmaxf(listed_x, -kLogitBound), list.top));
@@ -876,7 +897,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
       if (once && twice)
         for (int j = 0; j < tid; ++j) once &= list.ids[j] != id;
       const float e = bad ? NAN : once ? exp2_approx(score_from(listed_x, m2, c)) : 0.0f;
-      sum.s = fmaf(s_tail, exp2_approx(ref_down(sum.m, m2, c)), cta_sum<NT / 32>(make_float2(e, 0.0f), list.sum[0]).x);
+      sum.s = fmaf(s_tail, exp2_approx(ref_down<T>(sum.m, R1, m2, ref_of(m2, c), c)), cta_sum<NT / 32>(make_float2(e, 0.0f), list.sum[0]).x);
     }
     const bool empty = sum.s == 0.0f;
     const float ln_s = logf(sum.s);
@@ -889,7 +910,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
     if (tid == 0) {
       const float ln_tail = logf(s_tail);
       if (kMode == kTailBucket && t.q0 > 0.0f && s_tail > 0.0f)
-        part += t.q0 * (logf(t.q0) - (fmaf(ref_diff(sum.m, m2, c), kLn2, ln_tail) - ln_s));
+        part += t.q0 * (logf(t.q0) - (fmaf(ref_diff<T>(sum.m, R1, m2, ref_of(m2, c), c), kLn2, ln_tail) - ln_s));
       // NORMALIZED with every l_i at -inf: the row does not count
       a.loss[row] = !t.any ? 0.0f : sum.s != sum.s ? NAN : part;
       if (a.lse) a.lse[row] = !t.any ? 0.0f : empty ? -INFINITY : ref_lse(m2, c, a.scale, ln_s);
