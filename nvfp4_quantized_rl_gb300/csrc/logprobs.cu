@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(NT, kPerSm<kTop, NT>) logits_row_kernel(const 
       if (kEntropy) w2 = mul2(fma2(pack2(d, d), s2, w2), f2);
       s2 = mul2(s2, f2);
       R = Rn;
-      m = cm;
+      m = max_nan(m, cm);  // a NaN stays: no listed value lies above the largest m (cut_values)
     }
     if (!(m <= -kLogitBound)) {
       float ref = -R;

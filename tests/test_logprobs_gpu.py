@@ -816,3 +816,23 @@ def test_scales_at_the_ends_of_their_range(nv, dtype):
             got = f64(got.float())
             assert np.all(np.isfinite(got))
             assert np.all(got[:, 1::7][G.values(x)[:, 1::7] == -np.inf] == 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,V", [(2, 60000), (40, 90001), (700, 30001), (2500, 9001)])
+def test_alternatives_of_a_row_with_a_nan_behind_its_largest_logits(nv, dtype, M, V):
+    """The NaN comes after the thread has seen logits far above all it sees later; many candidates are listed."""
+    x = G.make(M, V, "f32", 76)
+    r = synth.rng(77, M, V)
+    for m in range(0, M, 2):
+        x[m, :V // 8] = (1e3 * 10.0 ** (30 * r.random(V // 8)) * np.where(r.random(V // 8) < 0.5, 1, -1)).clip(-1e30, 1e30)
+        x[m, V // 2 + 11 * m % (V // 3)::97] = np.nan
+    x = synth.bf16_bits(x) if dtype == "bf16" else x
+    for k in (1, 20, 64, 200):
+        logp, h, lse, ids, top = nv.token_logprobs(dev(x), P.dev(np.arange(M, dtype=np.int32)), k=k)
+        torch.cuda.synchronize()
+        for t in (logp, h, lse, top):
+            assert bool(torch.isnan(t[::2]).all()) and not bool(torch.isnan(t[1::2]).any())
+        assert bool((ids[::2] == -1).all())
+        order = np.argsort(-G.values(x[1::2]), axis=1, kind="stable")[:, :k]
+        assert np.array_equal(ids[1::2].cpu().numpy(), order)
