@@ -254,8 +254,8 @@ NVFP4RL_API nvfp4rl_status ais_mixing(const float* logp_rollout, const float* lo
  *   Per-row arrays are fp32 or int32, aligned to 4 bytes.
  *   Sums run in fp32 (V / 512 terms per lane, then a tree), exponentials are ex2.approx of
  *   scores in log2 units, relative to the largest logit: an offset of a row's logits costs the forward calls
- *   nothing. The gradients take p from lse, whose rounding alone is |lse| 2^-24 of p; a row with
- *   |lse| above 2^20 (nothing in it but, say, -1e9) has p = 1 at each of its largest logits. No workspace, no atomics on floating values: equal inputs give equal bits.
+ *   nothing. The gradients take p from lse (and lse_tail), whose rounding is up to |lse| 2^-24 of p;
+ *   rows where one is past 2^12 (nothing in them but, say, -1e9) get their sums anew, a few times slower. No workspace, no atomics on floating values: equal inputs give equal bits.
  * Errors: NVFP4RL_ERR_INVALID_ARG (bad dtype or mode, negative sizes, ld < V, k out of range, scale
  *   out of range, NULL pointers), NVFP4RL_ERR_UNSUPPORTED_SHAPE (V, M, M * ld or k too large),
  *   NVFP4RL_ERR_MISALIGNED, NVFP4RL_ERR_ALIAS. M == 0 is a no-op.

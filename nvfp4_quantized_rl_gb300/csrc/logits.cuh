@@ -106,6 +106,7 @@ struct LogitsGradArgs {
   const float *lse_tail, *dloss;
   void* dx;
   int64_t ldd;
+  float low;  // set by the launch
 };
 
 nvfp4rl_status launch_logprobs(const LogitsArgs& a, int dtype, const DeviceInfo& dev, cudaStream_t st);

@@ -8,12 +8,14 @@
 //     Q - q_0 / p_0 would overflow for a small p_0, so alpha = scale dloss (Q p_0 - q_0) with R = lse_tail log2 e;
 //   listed columns:  dx_j = scale dloss (Q p_j - q_j), written over the above after a block barrier.
 // Bound by HBM: each logit is read once, each gradient written once (4096 x 152064 bf16 with entropy 335 us, 1.03 of the
-// copy rate counted in the bytes it cannot do without; distillation with 64 listed 371 us, 0.99). A CTA takes
+// copy rate counted in the bytes it cannot do without; distillation with 64 listed 375 us, 0.98). A CTA takes
 // a chunk of one row, 16-byte vectors aligned for the stores; where the row of logits starts at another element of
 // a vector than the row of gradients, a vector is put together from two aligned loads by funnel shifts (the second one
 // hits L1/L2). Vectors at a row's ends, whose 16 bytes are not all inside it, go element by element. A list costs every
 // chunk the same (the teacher's row, the barriers): chunks of four steps where the CTAs suffice (eight: 378 us);
-// an fp32 batch of 100 rows stays at 0.72 (18.5 us).
+// an fp32 batch of 100 rows stays at 0.69 (19.1 us).
+// Rows of scores past 2^12, where lse itself is too coarse, get their sums anew from one CTA (far_row): 4096 x 152064 bf16 of
+// them 2.0 ms, with a list 2.8 ms, one alone 0.2 and 0.6 ms.
 #include "logits.cuh"
 
 namespace nvfp4rl {
@@ -39,19 +41,14 @@ __device__ __forceinline__ uint4 shift_vec(uint4 a, uint4 b, int s) {
                     __funnelshift_r(w[2], w[3], odd), __funnelshift_r(w[3], w[4], odd));
 }
 
-// lse: the reference of p, R = lse log2 e. x is clamped at `low`, where 2^t is 0 and beta t finite (0 beta t has to be 0).
+// x is clamped at low = -2^17 / c, where 2^t is 0 (|R| is below 2^13) and beta t finite: 0 beta t has to be 0.
 struct RowCoef {
-  float c, c_low, R, alpha, beta, low, scale, lse;
+  float c, c_low, R, alpha, beta, low;
 };
 
-// Past 2^20 the rounding of lse itself is a score of 2^-5 or more (and past 2^32 what R's took would overflow in 2^t):
-// score_far takes its place. (Not for -inf, NaN.)
-__device__ __forceinline__ bool is_far(float lse) { return fabsf(lse) > 0x1p20f && fabsf(lse) < INFINITY; }
-
-// t at such sizes, where lse comes to be z_max without a trace of ln s: p = 1 at the largest logits, never more.
-__device__ __forceinline__ float score_far(float v, const RowCoef& r) {
-  return fminf(fmaxf((__fmul_rn(v, r.scale) - r.lse) * kLog2E, -0x1p17f), 0.0f);
-}
+// Past 2^12 lse as a 32-bit number takes more than 2^-13 from p (past 2^24 it holds no trace of ln s): far_row takes the
+// row. (Not for -inf, NaN.)
+__device__ __forceinline__ bool is_far(float lse) { return fabsf(lse) > 0x1p12f && fabsf(lse) < INFINITY; }
 
 // t = x c - R, with the rounding of c made good for fp32 logits (29 2^-24 of p at z = 20; a bf16 result does not show it).
 template <typename T>
@@ -61,24 +58,15 @@ __device__ __forceinline__ float score(float v, const RowCoef& r) {
 
 // What the rounding of R = lse log2 e took: p = 2^(x c - R) times this, which goes into a row's factors.
 __device__ __forceinline__ float ref_factor(float lse, float R) {
-  if (is_far(lse)) return 1.0f;
   const float low = fmaf(lse, kLog2E, -R) + lse * kLog2ELow, d = -low * kLn2;
   return fabsf(d) < 0.01f ? fmaf(fmaf(0.5f * d, d, d), 1.0f, 1.0f) : expf(d);
 }
 
-__device__ __forceinline__ float low_of(float R, float c) { return fmaxf((R - 0x1p17f) / c, -kLogitBound); }
-
 // One element, with the roundings of the packed form (no contraction): the bits do not depend on where a row lies.
 template <typename T, bool kEntropy>
 __device__ __forceinline__ float grad1(float v, const RowCoef& r) {
-  float t;
-  if (is_far(r.lse)) {
-    t = score_far(v, r);
-  } else {
-    if (kEntropy || sizeof(T) == 4) v = fmaxf(v, r.low);
-    t = score<T>(v, r);
-  }
-  const float e = exp2_approx(t);
+  if (kEntropy || sizeof(T) == 4) v = fmaxf(v, r.low);
+  const float t = score<T>(v, r), e = exp2_approx(t);
   return __fmul_rn(e, kEntropy ? fmaf(r.beta, t, r.alpha) : r.alpha);
 }
 
@@ -125,6 +113,102 @@ __device__ __forceinline__ uint4 grad_vec(uint4 x, const RowCoef& r, int at, flo
   return make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3]));
 }
 
+// A row whose lse does not hold its sums: one CTA forms them anew, relative to the maxima, and writes the whole row.
+struct FarShared {
+  float hit, mass, q0;
+  float dh, h;          // scale dentropy, entropy
+  int token;
+};
+struct FarReduce {
+  float top[2][kListWarps];
+  float2 sum[kListWarps];
+};
+
+template <typename T, int NT, typename F>
+__device__ __forceinline__ void for_row(const T* x, int V, const F& f) {
+  for (int j0 = threadIdx.x; j0 < V; j0 += 8 * NT) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = j0 + u * NT < V ? logit(x, j0 + u * NT) : -INFINITY;
+#pragma unroll 1
+    for (int u = 0; u < 8 && j0 + u * NT < V; ++u) {
+      f(j0 + u * NT, v[0]);
+#pragma unroll
+      for (int i = 0; i < 7; ++i) v[i] = v[i + 1];
+    }
+  }
+}
+
+template <typename T, int NT, bool kEntropy, bool kList>
+__device__ __forceinline__ void far_row(const LogitsGradArgs& a, const T* x, T* dx, const int32_t* ids_s, const float* q_s,
+                                        const FarShared& sh, FarReduce& red) {
+  const float hit = sh.hit, dh = sh.dh, h = sh.h;
+  const int token = sh.token;
+  const int V = static_cast<int>(a.V);
+  const float c = a.scale * kLog2E;
+  const bool tail = kList && a.tail;
+  const auto listed = [&](int j) {
+    bool in = false;
+    for (int i = 0; i < a.k && !in; i += 4) {
+      const int4 id = *reinterpret_cast<const int4*>(ids_s + i);
+      in = id.x == j || id.y == j || id.z == j || id.w == j;
+    }
+    return in;
+  };
+  // listed columns: thread i holds entry i; the first entry of a column writes it, with the sum of all
+  int mine = -1;
+  float mine_x = -INFINITY, mine_q = 0.0f;
+  if (kList && threadIdx.x < a.k && ids_s[threadIdx.x] >= 0) {
+    mine = ids_s[threadIdx.x];
+    mine_x = logit(x, mine);
+    for (int i = 0; i < a.k; ++i) {
+      if (ids_s[i] != mine) continue;
+      mine_q += q_s[i];
+      if (i < static_cast<int>(threadIdx.x)) mine = -1;
+    }
+  }
+  float m = -kLogitBound, m_rest = -kLogitBound;
+  for_row<T, NT>(x, V, [&](int j, float v) {
+    m = fmaxf(m, v);
+    if (tail && v > m_rest && !listed(j)) m_rest = v;
+  });
+  m = cta_max<NT / 32>(m, red.top[0]);
+  m_rest = cta_max<NT / 32>(m_rest, red.top[1]);
+  const auto exp_from = [&](float v, float top) {
+    return v <= -kLogitBound || v > top ? 0.0f : exp2_approx((v - top) * c);
+  };
+  float2 s = make_float2(0.0f, 0.0f);
+  for_row<T, NT>(x, V, [&](int, float v) {
+    s.x += exp_from(v, m);
+    if (tail) s.y += exp_from(v, m_rest);
+  });
+  // the listed columns' terms come out of the second sum: at most k of 1, beside at least one unlisted of 1
+  if (tail && mine >= 0) s.y -= exp_from(mine_x, m_rest);
+  s = cta_sum<NT / 32>(s, red.sum);
+  const float ln_s = logf(s.x), to_p = 1.0f / s.x, to_b = tail && m_rest > -kLogitBound ? sh.q0 / s.y : 0.0f;
+  for_row<T, NT>(x, V, [&](int j, float v) {
+    const float p = exp_from(v, m) * to_p;
+    float g;
+    if (kList) {
+      g = hit * fmaf(sh.mass, p, -(exp_from(v, m_rest) * to_b));
+    } else {
+      g = hit * ((j == token ? 1.0f : 0.0f) - p);
+      if (kEntropy && p > 0.0f) g -= dh * p * (fmaf(v - m, a.scale, -ln_s) + h);
+    }
+    store_logit(dx, j, g);
+  });
+  if (kList) {
+    __syncthreads();
+    if (mine >= 0) store_logit(dx, mine, hit * fmaf(sh.mass, exp_from(mine_x, m) * to_p, -mine_q));
+  }
+}
+
+// The same as a call, which spares the token form's loop (4096 x 152064 334 us, inlined 337; the list's is better inlined: 376, 380).
+template <typename T, int NT, bool kEntropy>
+__device__ __noinline__ void far_row_called(const LogitsGradArgs& a, const T* x, T* dx, const FarShared& sh, FarReduce& red) {
+  far_row<T, NT, kEntropy, false>(a, x, dx, nullptr, nullptr, sh, red);
+}
+
 // NT: threads, at least as many as listed columns; kU: vectors per thread and step; kEntropy: the entropy term (token form only); kList: distillation;
 // kShift: rows of logits and gradients start at different elements of a vector (somewhere in the call).
 template <typename T, int NT, int kU, bool kEntropy, bool kList, bool kShift>
@@ -133,6 +217,8 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
   __shared__ __align__(16) int32_t ids_s[kList ? kMaxListed : 4];
   __shared__ float q_s[kList ? kMaxListed : 1];
   __shared__ TeacherShared teacher_s;
+  __shared__ FarShared far_s;
+  __shared__ FarReduce far_red;
   griddep_wait();
   griddep_launch_dependents();
   const int64_t row = blockIdx.x / chunks;
@@ -147,9 +233,9 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
   const float lse = a.lse[row];
   bool dead = lse == -INFINITY;
   const float c = a.scale * kLog2E, R = lse * kLog2E, f = ref_factor(lse, R);
-  RowCoef r{c, fmaf(a.scale, kLog2E, -c) + a.scale * kLog2ELow, R, 0.0f, 0.0f, low_of(R, c), a.scale, lse};
+  RowCoef r{c, fmaf(a.scale, kLog2E, -c) + a.scale * kLog2ELow, R, 0.0f, 0.0f, a.low};
   const float rest = kList && a.tail ? a.lse_tail[row] : 0.0f;
-  const bool far = is_far(lse) || is_far(rest);  // element by element
+  const bool far = is_far(lse) || is_far(rest);
   float hit = 0.0f, mass = 0.0f;
   int token = -1;
   // listed columns of this chunk: thread i holds entry i
@@ -163,7 +249,7 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
     for (int u = 0; u < kU; ++u) {
       const int col = (v0 + u * NT) * VEC - out_phase;
       // every byte of the loads and of the store lies inside the row
-      whole[u] = !far && (kShift && s ? col >= s && col - s + 2 * VEC <= V : col >= 0 && col + VEC <= V);
+      whole[u] = kShift && s ? col >= s && col - s + 2 * VEC <= V : col >= 0 && col + VEC <= V;
       if (whole[u] && !dead) {
         in[u] = ld_logits16(x + col - s);
         if (kShift && s) in2[u] = ld_logits16(x + col - s + VEC);
@@ -203,12 +289,11 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
         mass -= t.q0;  // no bucket; the unlisted columns are masked
         r.alpha = 0.0f;
       } else {
-        r.lse = rest;
         r.R = rest * kLog2E;
-        r.low = low_of(r.R, c);
         r.alpha = (mass * expf(rest - lse) - t.q0) * hit * ref_factor(rest, r.R);
       }
     }
+    if (far && tid == 0) far_s = FarShared{hit, mass, t.q0, 0.0f, 0.0f, -1};
     if (dead) mine = -1;
   } else {
     const float dl = a.dlogp ? a.dlogp[row] : 0.0f, dh = kEntropy ? a.dentropy[row] : 0.0f;
@@ -221,7 +306,14 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
     r.alpha = -a.scale * (kEntropy ? fmaf(dh, a.entropy[row], dl) : dl) * f;
     r.beta = -a.scale * dh * kLn2 * f;
   }
-  for (int step = 0; step < steps; ++step) {
+  const bool anew = far && !dead;
+  if (anew) {
+    if (!kList && tid == 0)
+      far_s = FarShared{hit, 0.0f, 0.0f, kEntropy ? a.scale * a.dentropy[row] : 0.0f, kEntropy ? a.entropy[row] : 0.0f,
+                        token};
+    __syncthreads();
+  }
+  for (int step = 0; step < steps && !anew; ++step) {
     const int v0 = v_begin + step * (kU * NT) + tid;
     if (!kList || step > 0) load_step(step);
 #pragma unroll
@@ -248,7 +340,7 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
   }
   if (kList) {
     __syncthreads();  // the chunk's dense values are written
-    if (mine >= 0) {
+    if (mine >= 0 && !anew) {
       // a column listed more than once is written by its first entry, with the sum of all
       float q = 0.0f;
       bool first = true;
@@ -265,11 +357,15 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
         }
       }
       r.R = R;
-      r.lse = lse;
-      const float t = is_far(lse) ? score_far(mine_x, r) : score<T>(mine_x, r);
-      const float p = mine_x <= -kLogitBound && lse == lse ? 0.0f : exp2_approx(t) * f;
+      const float p = mine_x <= -kLogitBound && lse == lse ? 0.0f : exp2_approx(score<T>(mine_x, r)) * f;
       if (first) store_logit(dx, mine, hit * (fmaf(mass, p, -q)));
     }
+  }
+  if (anew && v_begin == 0) {
+    if (kList)
+      far_row<T, NT, kEntropy, kList>(a, x, dx, ids_s, q_s, far_s, far_red);
+    else
+      far_row_called<T, NT, kEntropy>(a, x, dx, far_s, far_red);
   }
 }
 
@@ -326,7 +422,9 @@ nvfp4rl_status launch_type(const LogitsGradArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-nvfp4rl_status launch_logprobs_grad(const LogitsGradArgs& a, int dtype, const DeviceInfo&, cudaStream_t st) {
+nvfp4rl_status launch_logprobs_grad(const LogitsGradArgs& a0, int dtype, const DeviceInfo&, cudaStream_t st) {
+  LogitsGradArgs a = a0;
+  a.low = -0x1p17f / (a.scale * kLog2E);
   return dtype == NVFP4RL_BF16 ? launch_type<uint16_t>(a, st) : launch_type<float>(a, st);
 }
 

@@ -732,64 +732,74 @@ def test_distill_far_from_zero(nv, dtype, fill, tail):
 @pytest.mark.parametrize("fill", FILLS)
 @pytest.mark.parametrize("shift", [0, 3])
 def test_gradients_far_from_zero(nv, dtype, fill, shift):
-    """Masks far below ordinary logits, and rows that are far as a whole with one largest logit: p is 0 and 1."""
-    M, V, k = 6, 2049, 5
+    """Masks far below ordinary logits, rows that are far as a whole (one largest logit, equal ones, ordinary ones moved),
+    and far buckets of unlisted columns. A row's gradients add up to 0."""
+    M, V, k = 8, 2049, 5
     x = G.make(M, V, "f32", 74)
-    x[1, ::2] = fill if fill < 0 else -fill
+    low = -abs(fill)
+    x[1, ::2] = low
     x[2] = fill * (1.5 if fill < 0 else 0.5)
     x[2, 77] = fill
-    x[3] = fill if fill < 0 else -fill
-    x[3, 1024:1030] = [1.0, 2.0, 0.5, -1.0, 3.0, 0.0]
+    x[3] = low
+    x[3, [77, 1024, 1028, 5, 2000]] = [1.0, 2.0, 0.5, -1.0, 3.0]
     x[4] = np.where(np.arange(V) % 3 == 0, -np.inf, fill * (1.5 if fill < 0 else 0.5))
     x[4, 78] = fill
+    x[6] = fill
+    x[7] += np.float32(fill)
     x = synth.bf16_bits(x) if dtype == "bf16" else x
     scale = 1.25
     lp, h, ln_s, ED = relative(x, scale, V)
     p = np.exp(lp)
-    tok = np.array([5, 1, 77, 1026, 5, 0], np.int32)
+    ln = np.where(p > 0, lp, 0.0)
+    tok = np.array([5, 1, 77, 1026, 5, 0, 9, 11], np.int32)
     dl = np.linspace(-1.0, 1.5, M).astype(np.float32)
     dh = np.linspace(0.5, -0.7, M).astype(np.float32)
     xd, td = dev(x, shift=shift), P.dev(tok)
     _, hd, lse, _, _ = nv.token_logprobs(xd, td, scale)
     hit = np.zeros((M, V))
     hit[np.arange(M), tok] = 1.0
-    l64 = f64(lse)
-    # p by (3 |z| + 3 |lse| + 8) u and lse's own error where z is not far; far rows hold one p of 1
-    e = np.where(np.abs(l64) > 2.0 ** 20, 16 * G.U, G.U * (6 * np.abs(l64) + 3 * np.abs(ED) + 60 + V / 64 + 8 * np.abs(l64)))
+
+    def p_error(ref_lse, lp):
+        """Of p taken from ref_lse, relative: its rounding and that of |z| <= |lse| + |ln p| (3 u each, 8 u for lse's own
+        sums), or up to 2^12; past it the sums are formed anew, which leaves what the forward call has."""
+        S = (3 * ED + 4 + V / 64 + 64) * G.U
+        far = np.abs(ref_lse) > 2.0 ** 12
+        return S[:, None] + G.U * (6 * np.abs(lp) + 40 + np.where(far, 0.0, 14 * np.abs(np.where(far, 0.0, ref_lse)))[:, None])
+
+    e = p_error(f64(lse), ln)
     for g_h in (None, dh):
-        got = nv.token_logprobs_backward(xd, td, lse, P.dev(dl), scale, entropy=hd, dentropy=None if g_h is None else P.dev(g_h))
-        ln = np.where(p > 0, lp, 0.0)
+        got = f64(nv.token_logprobs_backward(xd, td, lse, P.dev(dl), scale, entropy=hd,
+                                             dentropy=None if g_h is None else P.dev(g_h)).float())
         ref = dl[:, None] * (hit - p) - (0.0 if g_h is None else g_h[:, None] * p * (ln + h[:, None]))
         part = np.abs(dl)[:, None] + np.abs(dh)[:, None] * (np.abs(ln) + h[:, None] + 1)
-        tol = 4 * e[:, None] * p * part + 16 * G.U * hit + G.half_ulp(ref, dtype) + 2.0 ** -120
-        G.close(f64(got.float()), ref * scale, tol * scale + G.half_ulp(ref * scale, dtype), f"dlogits entropy {g_h is not None}")
+        tol = 4 * e * p * part + 16 * G.U * hit + 2.0 ** -120
+        G.close(got, ref * scale, tol * scale + G.half_ulp(ref * scale, dtype), f"dlogits entropy {g_h is not None}")
     ids = np.stack([np.array([77, 1024, 1028, 5, 2000], np.int32)] * M)
     t = np.log(np.array([0.4, 0.2, 0.1, 0.1, 0.05], np.float32))[None].repeat(M, 0)
     q = np.zeros((M, V))
     np.put_along_axis(q, ids.astype(np.int64), np.exp(t.astype(np.float64)), 1)
     for tail in (False, True):
         loss, l2, lt = nv.topk_distill(xd, P.dev(ids), P.dev(t), scale, tail=tail)
-        got = f64(nv.topk_distill_backward(xd, P.dev(ids), P.dev(t), l2, P.dev(dl), scale, tail=tail, lse_tail=lt).float())
-        if not tail:
-            ref = dl[:, None] * (p - q / q.sum(1, keepdims=True))
-        else:
+        in_place = xd.clone()
+        assert in_place.stride() == xd.stride()
+        got = nv.topk_distill_backward(xd, P.dev(ids), P.dev(t), l2, P.dev(dl), scale, tail=tail, lse_tail=lt)
+        nv.topk_distill_backward(in_place, P.dev(ids), P.dev(t), l2, P.dev(dl), scale, tail=tail, lse_tail=lt, out=in_place)
+        assert torch.equal(got, in_place)
+        got = f64(got.float())
+        b, Q = np.zeros_like(p), q.sum(1, keepdims=True)
+        if tail:
             un = np.where(q > 0, -np.inf, lp)
             top = un.max(1, keepdims=True)
-            with np.errstate(invalid="ignore"):  # every unlisted column masked
-                b = np.exp(un - top)
-            b /= b.sum(1, keepdims=True)  # the bucket's own softmax
-            ref = dl[:, None] * (p - q - (1 - q.sum(1, keepdims=True)) * b)
-        assert np.all(np.isfinite(got))
-        rows = np.ones(M, bool)
-        if tail:  # a bucket of equal far logits: each counts as the largest one, as lse_tail holds no more
-            rows &= np.abs(f64(lt)) < 2.0 ** 20
-            assert np.all(np.abs(got) <= 2.0 * scale * np.abs(dl)[:, None])
-        listed = q > 0
-        size = p + q + np.abs(ref)
-        tol = (4 * e[:, None] + 60 * G.U) * size * 2 + G.half_ulp(ref, dtype) + 2.0 ** -120
-        if tail:
-            tol = tol + (4 * e[:, None] + 160 * G.U) * np.where(listed, 0.0, b)
-        G.close(got[rows], (ref * scale)[rows], (tol * scale + G.half_ulp(ref * scale, dtype))[rows], f"distill tail {tail}")
+            there = np.isfinite(top)
+            b = np.where(there, np.exp(un - np.where(there, top, 0.0)), 0.0)
+            b /= np.where(there, b.sum(1, keepdims=True), 1.0)  # the bucket's own softmax
+            Q = np.where(there, 1.0, Q)
+            ref = dl[:, None] * (Q * p - q - np.where(there, 1 - q.sum(1, keepdims=True), 0.0) * b)
+            e = np.maximum(e, p_error(f64(lt), np.where(b > 0, np.log(np.maximum(b, 1e-300)), 0.0)))
+        else:
+            ref = dl[:, None] * (p - q / Q)
+        tol = 4 * e * (p + b) + 60 * G.U * (p + q + b) + 2.0 ** -120
+        G.close(got, ref * scale, tol * scale * np.abs(dl)[:, None] + G.half_ulp(ref * scale, dtype), f"distill tail {tail}")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
