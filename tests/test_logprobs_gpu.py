@@ -768,8 +768,12 @@ def test_gradients_far_from_zero(nv, dtype, fill, shift):
 
     e = p_error(f64(lse), ln)
     for g_h in (None, dh):
-        got = f64(nv.token_logprobs_backward(xd, td, lse, P.dev(dl), scale, entropy=hd,
-                                             dentropy=None if g_h is None else P.dev(g_h)).float())
+        kw = dict(entropy=hd, dentropy=None if g_h is None else P.dev(g_h))
+        got = nv.token_logprobs_backward(xd, td, lse, P.dev(dl), scale, **kw)
+        in_place = xd.clone()
+        nv.token_logprobs_backward(in_place, td, lse, P.dev(dl), scale, out=in_place, **kw)
+        assert torch.equal(got, in_place)
+        got = f64(got.float())
         ref = dl[:, None] * (hit - p) - (0.0 if g_h is None else g_h[:, None] * p * (ln + h[:, None]))
         part = np.abs(dl)[:, None] + np.abs(dh)[:, None] * (np.abs(ln) + h[:, None] + 1)
         tol = 4 * e * p * part + 16 * G.U * hit + 2.0 ** -120
