@@ -124,8 +124,9 @@ struct FarReduce {
   float2 sum[kListWarps];
 };
 
-template <typename T, int NT, typename F>
-__device__ __forceinline__ void for_row(const T* x, int V, const F& f) {
+// f takes every column and its logit, in groups of at most 8 per thread; `end` is called after each group.
+template <typename T, int NT, typename F, typename E>
+__device__ __forceinline__ void for_row(const T* x, int V, const F& f, const E& end) {
   for (int j0 = threadIdx.x; j0 < V; j0 += 8 * NT) {
     float v[8];
 #pragma unroll
@@ -136,8 +137,24 @@ __device__ __forceinline__ void for_row(const T* x, int V, const F& f) {
 #pragma unroll
       for (int i = 0; i < 7; ++i) v[i] = v[i + 1];
     }
+    end();
   }
 }
+template <typename T, int NT, typename F>
+__device__ __forceinline__ void for_row(const T* x, int V, const F& f) {
+  for_row<T, NT>(x, V, f, [] {});
+}
+
+// A sum that keeps what its additions lose: 65536 equal terms in one chain (64 threads, the longest rows) drift by
+// 2^-11 of the sum, which would go into every gradient of the row; groups of 8 added this way stay within 10 2^-24.
+struct LongSum {
+  float s, lost;
+  __device__ __forceinline__ void add(float v) {
+    const float y = __fsub_rn(v, lost), t = __fadd_rn(s, y);
+    lost = __fsub_rn(__fsub_rn(t, s), y);
+    s = t;
+  }
+};
 
 template <typename T, int NT, bool kEntropy, bool kList>
 __device__ __forceinline__ void far_row(const LogitsGradArgs& a, const T* x, T* dx, const int32_t* ids_s, const float* q_s,
@@ -177,11 +194,20 @@ __device__ __forceinline__ void far_row(const LogitsGradArgs& a, const T* x, T* 
   const auto exp_from = [&](float v, float top) {
     return v <= -kLogitBound || v > top ? 0.0f : exp2_approx((v - top) * c);
   };
+  LongSum all{0.0f, 0.0f}, rest{0.0f, 0.0f};
   float2 s = make_float2(0.0f, 0.0f);
-  for_row<T, NT>(x, V, [&](int, float v) {
-    s.x += exp_from(v, m);
-    if (tail) s.y += exp_from(v, m_rest);
-  });
+  for_row<T, NT>(
+      x, V,
+      [&](int, float v) {
+        s.x += exp_from(v, m);
+        if (tail) s.y += exp_from(v, m_rest);
+      },
+      [&] {
+        all.add(s.x);
+        if (tail) rest.add(s.y);
+        s = make_float2(0.0f, 0.0f);
+      });
+  s = make_float2(all.s, rest.s);
   // the listed columns' terms come out of the second sum: at most k of 1, beside at least one unlisted of 1
   if (tail && mine >= 0) s.y -= exp_from(mine_x, m_rest);
   s = cta_sum<NT / 32>(s, red.sum);

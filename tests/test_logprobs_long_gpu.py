@@ -1,0 +1,86 @@
+"""The logits operators on long rows, against 64-bit definitions."""
+import numpy as np
+import pytest
+import torch
+
+from tests import _logits as G
+from tests import _parity as P
+from tests.test_logprobs_gpu import dev, f64, nv, relative  # noqa: F401  (nv: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def far_and_long(V):
+    """fp32 rows whose lse is past 2^12, of terms that a plain chain of additions drifts with: all but one column (or
+    three) at one value, and an ordinary row moved."""
+    x = np.full((3, V), -6000.0, np.float32)
+    x[0, V // 3] = -5999.0
+    x[1, [5, V // 2, V - 1]] = -5999.75
+    x[2] = G.make(1, V, "f32", 131)[0] - np.float32(8000.0)
+    return x
+
+
+# The widths of a row's CTA: 256 threads without a list, 64, 128, 256 by the list's length.
+@pytest.mark.parametrize("V", [152064, (1 << 22) - 3])
+@pytest.mark.parametrize("form", ["logp", "entropy", "k20", "k20 tail", "k100", "k200 tail"])
+def test_gradient_of_long_far_rows(nv, form, V):
+    """A far row's sum is good to (4 E[D] + 30) u whatever its length: its terms to (4 D + 4) u (x - max, c, their product,
+    the exponential), groups of 8 in turn 8 u, the compensated sum of the groups 2 u, the tree over 32 lanes and up to 8
+    warps 13 u, 1 / s and its product with a term 3 u. p is good to that and its own term's (4 D + 4) u."""
+    x = far_and_long(V)
+    M = len(x)
+    lp, h, ln_s, ED = relative(x, 1.0, V)
+    p = np.exp(lp)
+    S = ((4 * ED + 30) * G.U)[:, None]
+    D = -(lp + ln_s[:, None])
+    e = S + (4 * D + 4) * G.U
+    lse = G.values(x).max(1) + ln_s
+    dl = np.array([1.0, -0.75, 2.0], np.float32)
+    w = np.abs(dl.astype(np.float64))[:, None]
+    xd, lsed = dev(x), P.dev(lse.astype(np.float32))
+    if not form.startswith("k"):
+        tok = np.array([V // 3, 1, V - 2], np.int32)
+        hit = np.zeros((M, V))
+        hit[np.arange(M), tok] = 1.0
+        dh = np.array([0.5, 1.0, -0.25], np.float32) if form == "entropy" else None
+        kw = {} if dh is None else dict(entropy=P.dev(h.astype(np.float32)), dentropy=P.dev(dh))
+        got = nv.token_logprobs_backward(xd, P.dev(tok), lsed, P.dev(dl), **kw)
+        ref = dl[:, None] * (hit - p)
+        tol = w * p * e
+        if dh is not None:
+            # ln p + H: ln s by S and 2 u of itself, the score by 2 u D, H and the sum by 2 u of their parts
+            part = S + 4 * G.U * (np.abs(lp) + ln_s[:, None] + h[:, None])
+            ref = ref - dh[:, None] * p * (lp + h[:, None])
+            tol = tol + np.abs(dh)[:, None] * p * (e * np.abs(lp + h[:, None]) + part)
+        tol = tol + 4 * G.U * w * hit
+    else:
+        k, tail = int(form.split()[0][1:]), form.endswith("tail")
+        ids, t = G.teacher(M, k, V, 132)
+        ids[:, 1] = V // 3
+        at = ids.astype(np.int64)
+        lq = t.astype(np.float64)
+        if not tail:
+            lq = lq - np.log(np.exp(lq).sum(1, keepdims=True))
+        q = np.zeros((M, V))
+        np.put_along_axis(q, at, np.exp(lq), 1)
+        rest, b, q0 = None, 0.0, np.zeros(M)
+        if tail:
+            un = lp.copy()
+            np.put_along_axis(un, at, -np.inf, 1)
+            top = un.max(1)
+            ln_p0 = top + np.log(np.exp(un - top[:, None]).sum(1))
+            q0 = 1 - q.sum(1)
+            b = np.exp(un - ln_p0[:, None])
+            rest = P.dev((lse + ln_p0).astype(np.float32))
+        got = nv.topk_distill_backward(xd, P.dev(ids), P.dev(t), lsed, P.dev(dl), tail=tail, lse_tail=rest)
+        ref = dl[:, None] * (p - q - q0[:, None] * b)
+        # q by its exponential and the list's sums (4 |ln q| + k + 24) u, q_0 by the k + 1 exponentials' (k + 16) u. The
+        # bucket's sum holds the listed terms until they are taken out: below twice its size here.
+        e_q = (4 * np.abs(lq).max() + k + 24) * G.U
+        tol = w * (p * (e + (k + 16) * G.U * tail) + q * e_q)
+        if tail:
+            tol = tol + w * b * (q0[:, None] * (2 * e + S) + (k + 16) * G.U)
+    torch.cuda.synchronize()
+    # the result's own additions and its rounding: 4 u of their parts
+    tol = tol + 4 * G.U * (np.abs(ref) + w * p)
+    G.close(f64(got), ref, tol * 1.02 + 2.0 ** -120, f"dlogits {form} {V}")
