@@ -328,18 +328,31 @@ def _logits_call(name, device, *args):
         raise Nvfp4rlError(st, name)
 
 
+def _mark_written(given):
+    """The caller's tensors that a call wrote into count as modified in place: a graph that saved one of them, or the
+    logits that a gradient replaced, raises in its backward pass instead of using the new contents."""
+    import torch
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy: bool = True, logp=None, h=None,
                    lse=None, top_ids=None, top_logp=None, stream=None):
     """Log-probs of tokens (int32 [M]) under softmax(scale * logits) (bf16 or fp32 [M, V], rows may be strided),
     each row's entropy and log-sum-exp, and its k largest logits -> (logp, entropy, lse fp32 [M], top_ids
     int32 [M, k], top_logp fp32 [M, k]); None where tokens is None, entropy is False or k is 0. Rows whose
-    token is outside [0, V) are ignored (0, and ids -1)."""
+    token is outside [0, V) are ignored (0, and ids -1).
+
+    As of all four logits operators, the results carry no autograd graph, whether or not the logits require a gradient:
+    the gradients are the _backward calls' own. Tensors given as outputs count as modified in place."""
     import torch
     if stream is not None:
         return _on_stream(stream, logits, token_logprobs, logits, tokens, scale, k, entropy, logp, h, lse,
                           top_ids, top_logp)
     dt, M, V, ld, dev = _logit_rows(logits)
     empty, f32, i32, rows = torch.empty, torch.float32, torch.int32, (M,)
+    given = [t for t in (logp, h if entropy else None, lse, top_ids if k > 0 else None, top_logp if k > 0 else None)
+             if t is not None]
     p_tok = p_logp = p_h = p_ids = p_top = None
     if tokens is not None:
         p_tok = _row_array(tokens, "tokens", i32, rows, dev)
@@ -370,6 +383,7 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy:
         top_ids = top_logp = None
     _logits_call("token_logprobs", dev, logits.data_ptr(), dt, M, V, ld, p_tok, float(scale), k, p_logp, p_h, p_lse,
                  p_ids, p_top)
+    _mark_written(given)
     return logp, h, lse, top_ids, top_logp
 
 
@@ -394,11 +408,13 @@ def token_logprobs_backward(logits, tokens, lse, dlogp, scale: float = 1.0, entr
                           dentropy, out)
     dt, M, V, ld, dev = _logit_rows(logits)
     f32, rows = torch.float32, (M,)
+    given = [] if out is None else [out]
     out, ldd = _dlogits(logits, out, M, V, dev)
     _logits_call("token_logprobs_backward", dev, logits.data_ptr(), dt, M, V, ld,
                  _row_array(tokens, "tokens", torch.int32, rows, dev), float(scale), _row_array(lse, "lse", f32, rows, dev),
                  _row_array(entropy, "entropy", f32, rows, dev), _row_array(dlogp, "dlogp", f32, rows, dev),
                  _row_array(dentropy, "dentropy", f32, rows, dev), out.data_ptr(), ldd)
+    _mark_written(given)
     return out
 
 
@@ -413,6 +429,7 @@ def topk_distill(logits, ids, teacher_logp, scale: float = 1.0, tail: bool = Fal
     dt, M, V, ld, dev = _logit_rows(logits)
     empty, f32, rows = torch.empty, torch.float32, (M,)
     k = ids.shape[1] if ids.dim() == 2 else 0
+    given = [t for t in (loss, lse, lse_tail if tail else None) if t is not None]
     loss = empty(M, dtype=f32, device=dev) if loss is None else loss
     lse = empty(M, dtype=f32, device=dev) if lse is None else lse
     lse_tail = None if not tail else empty(M, dtype=f32, device=dev) if lse_tail is None else lse_tail
@@ -421,6 +438,7 @@ def topk_distill(logits, ids, teacher_logp, scale: float = 1.0, tail: bool = Fal
                  _row_array(teacher_logp, "teacher_logp", f32, (M, k), dev), k,
                  DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(loss, "loss", f32, rows, dev),
                  _row_array(lse, "lse", f32, rows, dev), _row_array(lse_tail, "lse_tail", f32, rows, dev))
+    _mark_written(given)
     return loss, lse, lse_tail
 
 
@@ -435,6 +453,7 @@ def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 
     dt, M, V, ld, dev = _logit_rows(logits)
     f32, rows = torch.float32, (M,)
     k = ids.shape[1] if ids.dim() == 2 else 0
+    given = [] if out is None else [out]
     out, ldd = _dlogits(logits, out, M, V, dev)
     _logits_call("topk_distill_backward", dev, logits.data_ptr(), dt, M, V, ld, float(scale),
                  _row_array(ids, "ids", torch.int32, (M, k), dev),
@@ -442,6 +461,7 @@ def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 
                  DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(lse, "lse", f32, rows, dev),
                  _row_array(lse_tail, "lse_tail", f32, rows, dev), _row_array(dloss, "dloss", f32, rows, dev),
                  out.data_ptr(), ldd)
+    _mark_written(given)
     return out
 
 

@@ -84,3 +84,41 @@ def test_gradient_of_long_far_rows(nv, form, V):
     # the result's own additions and its rounding: 4 u of their parts
     tol = tol + 4 * G.U * (np.abs(ref) + w * p)
     G.close(f64(got), ref, tol * 1.02 + 2.0 ** -120, f"dlogits {form} {V}")
+
+
+def test_tensors_given_as_outputs_count_as_modified(nv):
+    """A graph that saved the logits must not go on with the gradient in their place."""
+    V, k = 1000, 4
+    leaf = torch.randn(6, 1024, device="cuda", requires_grad=True)
+    tok = torch.arange(6, dtype=torch.int32, device="cuda")
+    one = torch.ones(6, device="cuda")
+    for write in ("token", "distill"):
+        for view in (lambda t: t, lambda t: t[:, :V], lambda t: t.detach()[:, :V]):
+            logits = leaf * 2.0
+            penalty = logits.square().sum()  # saves the logits
+            x = view(logits)
+            _, _, lse, ids, top = nv.token_logprobs(x, tok, k=k)
+            torch.autograd.grad(penalty, leaf, retain_graph=True)  # the forward call changes nothing
+            if write == "token":
+                nv.token_logprobs_backward(x, tok, lse, one, out=x)
+            else:
+                nv.topk_distill_backward(x, ids, top, lse, one, out=x)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                torch.autograd.grad(penalty, leaf)
+    f32 = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    x = leaf.detach()
+    outs = dict(logp=f32(6), h=f32(6), lse=f32(6), top_ids=torch.empty(6, k, dtype=torch.int32, device="cuda"), top_logp=f32(6, k))
+    nv.token_logprobs(x, tok, k=k, **outs)
+    assert [t._version for t in outs.values()] == [1] * 5
+    nv.token_logprobs(x, tok, entropy=False, **outs)  # writes neither the entropies nor the lists
+    assert [t._version for t in outs.values()] == [2, 1, 2, 1, 1]
+    loss, rest = f32(6), f32(6)
+    nv.topk_distill(x, outs["top_ids"], outs["top_logp"], loss=loss, lse=outs["lse"], lse_tail=rest)
+    assert (loss._version, outs["lse"]._version, rest._version) == (1, 3, 0)
+    nv.topk_distill(x, outs["top_ids"], outs["top_logp"], tail=True, loss=loss, lse_tail=rest)
+    assert (loss._version, rest._version) == (2, 1)
+    with torch.inference_mode():  # tensors without versions
+        y = torch.randn(6, V, device="cuda")
+        lse = nv.token_logprobs(y, tok, lse=f32(6))[2]
+        nv.token_logprobs_backward(y, tok, lse, one, out=y)
+    nv.token_logprobs_backward(y, tok, lse, one, out=y)
