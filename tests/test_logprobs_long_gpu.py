@@ -5,7 +5,7 @@ import torch
 
 from tests import _logits as G
 from tests import _parity as P
-from tests.test_logprobs_gpu import dev, f64, nv, relative  # noqa: F401  (nv: the fixture)
+from tests.test_logprobs_gpu import _bits, dev, f64, nv, relative  # noqa: F401  (nv: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,73 @@ def test_tensors_given_as_outputs_count_as_modified(nv):
         lse = nv.token_logprobs(y, tok, lse=f32(6))[2]
         nv.token_logprobs_backward(y, tok, lse, one, out=y)
     nv.token_logprobs_backward(y, tok, lse, one, out=y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1000.0, 2.0 ** 15, 2.0 ** 20])
+def test_gradients_at_large_scales(nv, dtype, scale):
+    """Scores of thousands to millions: tied and neighbouring largest logits, equal rows, masked columns, and rows on
+    either side of |lse| = 2^12, against softmaxes formed from differences to the maximum in 64 bits."""
+    M, V = 7, 2500
+    x = G.make(M, V, "f32", 134)
+    x[1, [3, 70, 71]] = 13.0
+    x[2, 100:108] = 13.0 - 2.0 ** -20 * np.arange(8)  # neighbours in fp32: a score apart at 2^20; equal in bf16
+    x[3] = 0.25
+    x[4, ::2] = -np.inf
+    x[5] *= np.float32(2.0 ** -10)
+    x[6] -= np.float32(20.0)
+    if dtype == "bf16":
+        x = _bits(x)
+    lp, h, ln_s, ED = relative(x, scale, V)
+    p = np.exp(lp)
+    ln = np.where(p > 0, lp, 0.0)
+    best = np.argmax(G.values(x), axis=1)
+    tok = best.astype(np.int32)
+    tok[2] = 103
+    tok[::3] = 9
+    dl = np.linspace(-1.0, 1.5, M).astype(np.float32)
+    dh = np.linspace(0.5, -0.7, M).astype(np.float32)
+    hit = np.zeros((M, V))
+    hit[np.arange(M), tok] = 1.0
+    xd, td = dev(x), P.dev(tok)
+    _, hd, lse, _, _ = nv.token_logprobs(xd, td, scale)
+
+    def p_error(ref_lse, lp):
+        """Of p, relative: the sums' S, and 6 u |ln p| + 40 u of its own score and exponential; taken from a 32-bit lse
+        (up to 2^12) also 14 u |lse|: its rounding and those of lse log2 e and of z = lse + ln p."""
+        S = (3 * ED + 4 + V / 64 + 64) * G.U
+        near = np.where(np.abs(ref_lse) > 2.0 ** 12, 0.0, np.abs(ref_lse))
+        return S[:, None] + G.U * (6 * np.abs(lp) + 40 + 14 * near[:, None])
+
+    e = p_error(f64(lse), ln)
+    for g_h in (None, dh):
+        kw = {} if g_h is None else dict(entropy=hd, dentropy=P.dev(g_h))
+        got = f64(nv.token_logprobs_backward(xd, td, lse, P.dev(dl), scale, **kw).float())
+        ref = dl[:, None] * (hit - p) - (0.0 if g_h is None else g_h[:, None] * p * (ln + h[:, None]))
+        part = np.abs(dl)[:, None] + np.abs(dh)[:, None] * (np.abs(ln) + h[:, None] + 1)
+        tol = 4 * e * p * part + 16 * G.U * hit + 2.0 ** -120
+        G.close(got, ref * scale, tol * scale + G.half_ulp(ref * scale, dtype), f"dlogits entropy {g_h is not None}")
+    k = 12
+    ids, t = G.teacher(M, k, V, 135)
+    ids[1::2, 0] = best[1::2]
+    ids[1::2, 1:] = (best[1::2, None] + 1 + np.arange(k - 1)) % V
+    at = ids.astype(np.int64)
+    q = np.zeros((M, V))
+    np.put_along_axis(q, at, np.exp(t.astype(np.float64)), 1)
+    for tail in (False, True):
+        _, l2, lt = nv.topk_distill(xd, P.dev(ids), P.dev(t), scale, tail=tail)
+        got = nv.topk_distill_backward(xd, P.dev(ids), P.dev(t), l2, P.dev(dl), scale, tail=tail, lse_tail=lt)
+        got = f64(got.float())
+        b, Q, e2 = np.zeros_like(p), q.sum(1, keepdims=True), e
+        if tail:
+            un = G.values(x) * float(np.float32(scale))
+            np.put_along_axis(un, at, -np.inf, 1)
+            un -= un.max(1, keepdims=True)
+            b = np.exp(un)
+            b /= b.sum(1, keepdims=True)  # the bucket's own softmax
+            ref = dl[:, None] * (p - q - (1 - Q) * b)
+            e2 = np.maximum(e, p_error(f64(lt), np.where(b > 0, np.log(np.maximum(b, 1e-300)), 0.0)))
+        else:
+            ref = dl[:, None] * (p - q / Q)
+        tol = 4 * e2 * (p + b) + 60 * G.U * (p + q + b) + 2.0 ** -120
+        G.close(got, ref * scale, tol * scale * np.abs(dl)[:, None] + G.half_ulp(ref * scale, dtype), f"distill tail {tail}")
