@@ -192,3 +192,99 @@ def test_gradients_at_large_scales(nv, dtype, scale):
             ref = dl[:, None] * (p - q / Q)
         tol = 4 * e2 * (p + b) + 60 * G.U * (p + q + b) + 2.0 ** -120
         G.close(got, ref * scale, tol * scale * np.abs(dl)[:, None] + G.half_ulp(ref * scale, dtype), f"distill tail {tail}")
+
+
+def hard_rows(M, V, t, seed):
+    """Ordinary logits, and among the first rows: a constant, rising and falling ramps, two values, masks up to far into the
+    row and up to the last three columns, negative values, ties for the last places at the row's end."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = (torch.randn(M, V, generator=g, device="cuda") * 2).to(t)
+    ramp = torch.linspace(-9, 9, V, device="cuda").to(t)
+    x[1] = 1.5
+    x[2] = ramp
+    x[3] = (torch.rand(V, generator=g, device="cuda") < 0.5).to(t)
+    x[4, :V * 7 // 8] = -torch.inf
+    x[5, :-3] = torch.finfo(t).min
+    x[6] = ramp.flip(0)
+    x[7] = -5 - torch.rand(V, generator=g, device="cuda").to(t)
+    x[8, V - V // 40:] = 3.0
+    return x, torch.randint(0, V, (M,), generator=g, device="cuda").int()
+
+
+def exact_rows(x):
+    """ln p, lse and entropy in 64 bits."""
+    f = x.double()
+    z = torch.where(f <= G.MASKED, -torch.inf, f)
+    lse = torch.logsumexp(z, 1)
+    lp = z - lse[:, None]
+    return z, lp, lse, -(lp.exp() * torch.where(lp == -torch.inf, 0.0, lp)).sum(1)
+
+
+@pytest.mark.parametrize("dtype,M,V,ks", [
+    ("f32", 610, 100003, (1, 20, 96)),            # CTAs of 128 threads: a block of steps is 81920 columns
+    ("bf16", 610, 200003, (1, 20, 96)),           # 163840
+    ("f32", 9, (1 << 22) - 3, (5, 70, 256)),      # clusters of 8 CTAs: four blocks in each share
+    ("bf16", 9, (1 << 22) - 3, (5, 70, 256))])    # two
+def test_alternatives_over_several_blocks(nv, dtype, M, V, ks):
+    """Rows whose step maxima fill more than one block, in narrow CTAs and in clusters."""
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, tok = hard_rows(M, V, t, 141)
+    tok[5] = V - 1
+    n = min(M, 12)
+    z, lp, ref_lse, ref_h = exact_rows(x[:n])
+    order = torch.sort(x[:n].float(), dim=1, descending=True, stable=True).indices[:, :max(ks)]
+    # S of _logits.py with V / 256 additions in a chain at most, E[D] <= ln V < 16
+    tol = (3 * 16 + 4 + V / 256 + 64) * G.U + 8 * G.U * (ref_lse.abs() + 16)
+    for k in ks:
+        logp, h, lse, ids, top = nv.token_logprobs(x, tok, k=k)
+        at = order[:, :k]
+        there = z.gather(1, at) > -torch.inf
+        assert torch.equal(ids[:n].long(), torch.where(there, at, -1))
+        assert torch.all((lse[:n].double() - ref_lse).abs() <= tol)
+        assert torch.all((h[:n].double() - ref_h).abs() <= tol * (1 + 3 * 16))
+        want = torch.where(there, lp.gather(1, at), -torch.inf)
+        got = top[:n].double()
+        assert torch.equal(there, torch.isfinite(got))
+        assert torch.all(((got - want).abs() <= tol[:, None] + 8 * G.U * want.abs())[there])
+        got, want = logp[:n].double(), lp.gather(1, tok[:n].long()[:, None])[:, 0]
+        fin = torch.isfinite(want)
+        assert torch.equal(fin, torch.isfinite(got)) and torch.all(((got - want).abs() <= tol + 8 * G.U * want.abs())[fin])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_with_several_maps_to_a_share(nv, dtype):
+    """Clusters of 8 CTAs, each with more columns than its bit map of the listed ones holds: columns listed at the borders
+    of the shares and of the maps within them (256000 columns of bf16, 261120 of fp32)."""
+    M, V = 5, (1 << 22) - 3
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(151)
+    x = (torch.randn(M, V, generator=g, device="cuda") * 2).to(t)
+    share, per_map = 524288, 256000 if dtype == "bf16" else 261120
+    edges = {0, 1, V - 2, V - 1}
+    for r in (0, 1, 4, 7):
+        for m in range(3):
+            at = r * share + m * per_map
+            edges |= {c for c in (at - 9, at - 8, at - 4, at - 1, at, at + 1, at + 7, at + 8) if 0 <= c < V}
+    cols = torch.tensor(sorted(edges), device="cuda")
+    k = len(cols)
+    x[1, cols] = 12.0  # the listed columns hold most of p: the bucket's sum must not see them
+    ids = cols.expand(M, -1).int().contiguous()
+    tl = torch.log_softmax(torch.randn(M, k + 1, generator=g, device="cuda"), 1)[:, :k].contiguous()
+    z, lp, ref_lse, _ = exact_rows(x)
+    q = tl.double().exp()
+    q0 = 1 - q.sum(1)
+    ref_rest = torch.logsumexp(z.index_fill(1, cols, -torch.inf), 1)
+    # S of _logits.py with V / 256 additions in a chain at most, E[D] <= ln V < 16, of the row as of its unlisted columns
+    tol = (3 * 16 + 4 + V / 256 + 64) * G.U + 8 * G.U * (ref_lse.abs() + 16)
+    loss, lse, rest = nv.topk_distill(x, ids, tl, tail=True)
+    assert torch.all((lse.double() - ref_lse).abs() <= 2 * tol) and torch.all((rest.double() - ref_rest).abs() <= tol)
+    at = lp[:, cols]
+    ref = (q * (tl.double() - at)).sum(1) + q0 * (q0.log() - (ref_rest - ref_lse))
+    size = (q * (tl.double().abs() + at.abs())).sum(1) + (q0.log().abs() + (ref_rest - ref_lse).abs())
+    # ln p and ln p_0 by the sums' tol; every other part by (k + 60) u, as of its size
+    assert torch.all((loss.double() - ref).abs() <= 3 * tol + (k + 60) * G.U * (size + 1))
+    loss, lse, rest = nv.topk_distill(x, ids, tl)
+    total = torch.logsumexp(tl.double(), 1, keepdim=True)
+    ref = ((tl.double() - total).exp() * (tl.double() - total - at)).sum(1)
+    assert rest is None and torch.all((lse.double() - ref_lse).abs() <= 2 * tol)
+    assert torch.all((loss.double() - ref).abs() <= 2 * tol + (k + 60) * G.U * (size + 1))
