@@ -332,8 +332,7 @@ def _mark_written(given):
     """The caller's tensors that a call wrote into count as modified in place: a graph that saved one of them, or the
     logits that a gradient replaced, raises in its backward pass instead of using the new contents."""
     import torch
-    if given:
-        torch.autograd.graph.increment_version(given)
+    torch.autograd.graph.increment_version(given)
 
 
 def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy: bool = True, logp=None, h=None,
@@ -351,15 +350,16 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy:
                           top_ids, top_logp)
     dt, M, V, ld, dev = _logit_rows(logits)
     empty, f32, i32, rows = torch.empty, torch.float32, torch.int32, (M,)
-    given = [t for t in (logp, h if entropy else None, lse, top_ids if k > 0 else None, top_logp if k > 0 else None)
-             if t is not None]
+    given = []  # outputs of the caller's that this call writes
     p_tok = p_logp = p_h = p_ids = p_top = None
     if tokens is not None:
         p_tok = _row_array(tokens, "tokens", i32, rows, dev)
-        p_logp = _row_array(logp, "logp", f32, rows, dev)
-        if p_logp is None:
+        if logp is None:
             logp = empty(M, dtype=f32, device=dev)
             p_logp = logp.data_ptr()
+        else:
+            p_logp = _row_array(logp, "logp", f32, rows, dev)
+            given.append(logp)
     elif logp is not None:
         raise ValueError("logp needs tokens")
     if not entropy:
@@ -369,21 +369,30 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, k: int = 0, entropy:
         p_h = h.data_ptr()
     else:
         p_h = _row_array(h, "h", f32, rows, dev)
+        given.append(h)
     if lse is None:
         lse = empty(M, dtype=f32, device=dev)
         p_lse = lse.data_ptr()
     else:
         p_lse = _row_array(lse, "lse", f32, rows, dev)
+        given.append(lse)
     if k > 0:
-        top_ids = empty(M, k, dtype=i32, device=dev) if top_ids is None else top_ids
-        top_logp = empty(M, k, dtype=f32, device=dev) if top_logp is None else top_logp
+        if top_ids is None:
+            top_ids = empty(M, k, dtype=i32, device=dev)
+        else:
+            given.append(top_ids)
+        if top_logp is None:
+            top_logp = empty(M, k, dtype=f32, device=dev)
+        else:
+            given.append(top_logp)
         p_ids = _row_array(top_ids, "top_ids", i32, (M, k), dev)
         p_top = _row_array(top_logp, "top_logp", f32, (M, k), dev)
     else:
         top_ids = top_logp = None
     _logits_call("token_logprobs", dev, logits.data_ptr(), dt, M, V, ld, p_tok, float(scale), k, p_logp, p_h, p_lse,
                  p_ids, p_top)
-    _mark_written(given)
+    if given:
+        _mark_written(given)
     return logp, h, lse, top_ids, top_logp
 
 
@@ -414,7 +423,8 @@ def token_logprobs_backward(logits, tokens, lse, dlogp, scale: float = 1.0, entr
                  _row_array(tokens, "tokens", torch.int32, rows, dev), float(scale), _row_array(lse, "lse", f32, rows, dev),
                  _row_array(entropy, "entropy", f32, rows, dev), _row_array(dlogp, "dlogp", f32, rows, dev),
                  _row_array(dentropy, "dentropy", f32, rows, dev), out.data_ptr(), ldd)
-    _mark_written(given)
+    if given:
+        _mark_written(given)
     return out
 
 
@@ -438,7 +448,8 @@ def topk_distill(logits, ids, teacher_logp, scale: float = 1.0, tail: bool = Fal
                  _row_array(teacher_logp, "teacher_logp", f32, (M, k), dev), k,
                  DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(loss, "loss", f32, rows, dev),
                  _row_array(lse, "lse", f32, rows, dev), _row_array(lse_tail, "lse_tail", f32, rows, dev))
-    _mark_written(given)
+    if given:
+        _mark_written(given)
     return loss, lse, lse_tail
 
 
@@ -461,7 +472,8 @@ def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 
                  DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(lse, "lse", f32, rows, dev),
                  _row_array(lse_tail, "lse_tail", f32, rows, dev), _row_array(dloss, "dloss", f32, rows, dev),
                  out.data_ptr(), ldd)
-    _mark_written(given)
+    if given:
+        _mark_written(given)
     return out
 
 
