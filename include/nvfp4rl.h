@@ -252,10 +252,15 @@ NVFP4RL_API nvfp4rl_status ais_mixing(const float* logp_rollout, const float* lo
  *   A logit at or below -2^100 (-inf, the type's lowest value) is MASKED: its p is 0. A row that
  *   holds a NaN or a logit above 2^100 has NaN for every result. Other rows are not affected.
  *   Per-row arrays are fp32 or int32, aligned to 4 bytes.
- *   Sums run in fp32 (V / 512 terms per lane, then a tree), exponentials are ex2.approx of
- *   scores in log2 units, relative to the largest logit: an offset of a row's logits costs the forward calls
- *   nothing. The gradients take p from lse (and lse_tail), whose rounding is up to |lse| 2^-24 of p;
- *   rows where one is past 2^12 (nothing in them but, say, -1e9) get their sums anew, a few times slower. No workspace, no atomics on floating values: equal inputs give equal bits.
+ *   Sums run in fp32: chains of at most V / 256 terms (V / 128 in rows of up to 40960 columns), then a
+ *   tree. Exponentials are ex2.approx of scores in log2 units, relative to the largest logit: an offset
+ *   of a row's logits costs the forward calls nothing. The gradients take p from lse (and lse_tail), whose
+ *   rounding is up to |lse| 2^-24 of p. Rows where |lse| or |lse_tail| is past 2^12 (and finite) get their
+ *   sums anew, compensated, from one CTA: logits that lie far from 0 as a whole, and, with
+ *   NVFP4RL_DISTILL_TAIL, ordinary rows whose unlisted columns hold nothing but a finite mask (-1e4, -1e9;
+ *   not -inf, which leaves no unlisted p). That is slow: a batch of 4096 x 152064 bf16 takes 2.0 ms instead
+ *   of 0.35 (token form) or 2.9 instead of 0.38 (64 listed), a single row 0.16 ms or 0.58 ms instead of 3 us
+ *   or 4 us. No workspace, no atomics on floating values: equal inputs give equal bits.
  * Errors: NVFP4RL_ERR_INVALID_ARG (bad dtype or mode, negative sizes, ld < V, k out of range, scale
  *   out of range, NULL pointers), NVFP4RL_ERR_UNSUPPORTED_SHAPE (V, M, M * ld or k too large),
  *   NVFP4RL_ERR_MISALIGNED, NVFP4RL_ERR_ALIAS. M == 0 is a no-op.

@@ -11,7 +11,8 @@ constexpr float kLogitBound = 1.2676506002282294e30f;  // 2^100
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLog2ELow = 1.9259629911e-8f;  // log2 e - kLog2E
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int64_t kMaxVocab = int64_t(1) << 22;  // columns: a thread's fp32 sum then has at most 8192 terms per lane
+// Columns: a thread's fp32 sum then has at most 16384 terms per lane (in CTAs of 128 threads; of 256: 8192).
+constexpr int64_t kMaxVocab = int64_t(1) << 22;
 constexpr int kMaxListed = 256;  // alternatives or listed teacher columns per row
 
 // 2^x (ex2.approx: about 2 ulp; results below 2^-126 are 0).

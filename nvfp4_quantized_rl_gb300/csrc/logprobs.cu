@@ -23,12 +23,12 @@
 // the few thread-steps that reach it are read again, dealt out over the CTA, and the logits above the bound go to a
 // list in shared memory as 64-bit keys (value order, then the lower column). A list that is too long is cut by a
 // histogram; the rest is ranked by counting. The result does not depend on the order of the appends. 64 of each of
-// 2048 x 152064 bf16: 119 us, 0.77 of the copy rate (96 us without any), bound by the latency of the row's end; testing
-// every logit against a bound in the loop took 164 us. Rows of equal logits are dearer (2048 rows of zeros 147 us).
+// 2048 x 152064 bf16: 116 us, 0.79 of the copy rate (93 us without any), bound by the latency of the row's end; testing
+// every logit against a bound in the loop took 164 us. Rows of equal logits are dearer (2048 rows of zeros 139 us).
 //
 // Distillation with a tail bucket: listed columns are marked in a bit map in shared memory and masked as they are
 // read, so that the streamed sum is the tail's own, relative to its own maximum; the listed ones are gathered and
-// added at the end. 1 - sum p would lose a small tail. 4096 x 152064 bf16, 64 listed: 194 us, 0.95 of the copy rate.
+// added at the end. 1 - sum p would lose a small tail. 4096 x 152064 bf16, 64 listed: 192 us, 0.96 of the copy rate.
 #include <atomic>
 
 #include "logits.cuh"
@@ -309,7 +309,8 @@ __device__ void gather_lists(TopShared<NT>& sh, const unsigned long long* from, 
   }
   __syncthreads();
   if (sh.count <= TopShared<NT>::kCandidates) return;
-  // (a list is short, so that the bound is 0) list by list, cut to a list's length each time
+  // Too many reach the bound (it is 0 where a list is short; or most of the largest are in few of the lists, as in a rising
+  // row): list by list, cut to a list's length each time.
   int n = 0;
   __syncthreads();
   for (int l = 0; l < lists; ++l) {
@@ -591,7 +592,9 @@ __device__ uint32_t refine_bound(TopShared<NT>& sh, uint32_t mask, int k, float&
 
 // CTAs to an SM. Five of 256 threads where 48 registers do: 2048 x 152064 bf16 (floor 92 us), without alternatives, 4
 // vectors and 4 CTAs 106 us, 4 and 5 99 us, 5 and 5 96 us, 6 and 5 98 us, 8 and 4 99 us. With 64 alternatives: 4 CTAs of
-// 256 threads 124 us, 5 163 us (spills), 6, 7, 8 CTAs of 128 threads 134, 119, 121 us.
+// 256 threads 124 us, 5 163 us (spills), 6, 7, 8 CTAs of 128 threads 134, 119, 121 us. fp32 takes the same numbers: 4096 x
+// 152064 (floor 367 us) with entropy 355 us, with 20 and 64 alternatives 382 and 408 us; its entropy kernels, its
+// alternatives with 256 threads and the bf16 tail kernels spill 4 to 12 bytes at these bounds.
 template <bool kTop, int NT>
 constexpr int kPerSm = NT == 256 ? (kTop ? 4 : 5) : NT == 128 ? (kTop ? 7 : 10) : (kTop ? 13 : 18);
 
@@ -990,7 +993,8 @@ nvfp4rl_status launch_width(const LogitsArgs& a, unsigned cluster, const DeviceI
 // tail: 32 listed): 400 x 16000 ent 6.7, 5.3, 6.6, top 9.4, 7.9, 9.8, tail 9.1, 7.4, 9.4; 1064 x 8000 ent 7.4, 6.6, 6.6,
 // top 14.1, 9.3, 9.8, tail 10.9, 9.3, 8.1; 2128 x 16000 ent 19.1, 16.6, 16.0, top 30.4, 22.7, 17.9, tail 25.0, 19.7, 19.0;
 // 760 x 50257 ent 15.4, 16.9, 23.0, top 24.3, 21.0, 26.9, tail 19.0, 18.9, 26.3; 400 x 152064 ent 30.7, 34.7, 54.1, top 29.5,
-// 36.0, 59.7; 2128 x 152064 ent 99, 108, 108, top 115.8, 109.5, 109.6, tail 104, 117, 140.
+// 36.0, 59.7; 2128 x 152064 ent 99, 108, 108, top 115.8, 109.5, 109.6, tail 104, 117, 140. fp32 rows go by their vectors, as bf16 rows of
+// twice their length.
 int width_of(const LogitsArgs& a, int64_t vecs, int sms) {
   const bool list = a.ids != nullptr, top = !list && a.k > 0;
   int w = 256;
@@ -1010,7 +1014,7 @@ int width_of(const LogitsArgs& a, int64_t vecs, int sms) {
 
 template <typename T>
 nvfp4rl_status launch_type(const LogitsArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  // CTAs per row: two to an SM at most, and no share below one step. 152064 columns, 5 alternatives: 64 rows with 8 CTAs
+  // CTAs per row: two to an SM at most, and no share below a vector to a thread. 152064 columns, 5 alternatives: 64 rows with 8 CTAs
   // each 11.6 us, with 4 10.1, with 2 11.9; 152 rows with 2 15.9 us, with 1 20.0; 200 rows with 2 23.1 us, with 1 22.2.
   unsigned cluster = kMaxCluster;
   while (cluster > 1 && (a.M * cluster > 2 * dev.sm_count || a.V < static_cast<int64_t>(cluster) * kThreads * kVecOf<T>))

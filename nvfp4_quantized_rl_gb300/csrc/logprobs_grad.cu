@@ -7,15 +7,16 @@
 //   distillation, unlisted columns:  dx_j = alpha 2^t; NORMALIZED: alpha = scale dloss, R as above; TAIL: the factor
 //     Q - q_0 / p_0 would overflow for a small p_0, so alpha = scale dloss (Q p_0 - q_0) with R = lse_tail log2 e;
 //   listed columns:  dx_j = scale dloss (Q p_j - q_j), written over the above after a block barrier.
-// Bound by HBM: each logit is read once, each gradient written once (4096 x 152064 bf16 with entropy 335 us, 1.03 of the
-// copy rate counted in the bytes it cannot do without; distillation with 64 listed 375 us, 0.98). A CTA takes
+// Bound by HBM: each logit is read once, each gradient written once (4096 x 152064 bf16 with entropy, an eighth of
+// the rows padding, 333 us, 1.03 of the copy rate counted in the bytes it cannot do without, all rows live 346 us;
+// distillation with 64 listed 376 us, 0.98, with 200, whose CTAs of 256 threads spill 40 bytes, 436-444 us). A CTA takes
 // a chunk of one row, 16-byte vectors aligned for the stores; where the row of logits starts at another element of
 // a vector than the row of gradients, a vector is put together from two aligned loads by funnel shifts (the second one
 // hits L1/L2). Vectors at a row's ends, whose 16 bytes are not all inside it, go element by element. A list costs every
 // chunk the same (the teacher's row, the barriers): chunks of four steps where the CTAs suffice (eight: 378 us);
-// an fp32 batch of 100 rows stays at 0.69 (19.1 us).
+// an fp32 batch of 100 rows of 128257 with 128 listed stays at 0.69 (19.1 us): 1600 CTAs, of which 1368 run at once.
 // Rows of scores past 2^12, where lse itself is too coarse, get their sums anew from one CTA (far_row): 4096 x 152064 bf16 of
-// them 2.0 ms, with a list 2.8 ms, one alone 0.2 and 0.6 ms.
+// them 2.0 ms with entropy, 2.8-2.9 ms with 64 listed, 2.1-2.2 ms with 200 (more threads); one alone 0.16, 0.58, 0.17 ms.
 #include "logits.cuh"
 
 namespace nvfp4rl {
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(NT) logits_grad_kernel(const LogitsGradArgs a,
   griddep_wait();
   griddep_launch_dependents();
   const int64_t row = blockIdx.x / chunks;
-  // vectors and columns in 32 bits: V <= 2^30, and a chunk is longer than 2^17 vectors only where V < 2^20
+  // vectors and columns in 32 bits: V <= 2^22
   const int V = static_cast<int>(a.V);
   const int v_begin = static_cast<int>(blockIdx.x % chunks) * steps * (kU * NT);
   const T* x = static_cast<const T*>(a.x) + row * a.ld;
@@ -437,8 +438,8 @@ nvfp4rl_status launch_width(const LogitsGradArgs& a, cudaStream_t st) {
 }
 
 // As many threads as the list has entries, at least 64: with 64 listed, 256, 128 and 64 threads took 381, 370, 371 us at
-// 4096 x 152064 bf16, 39, 20, 14.5 us at 4096 x 1001. Without a list 256 for long rows (351.2 us, with 128 352.7), 128 for
-// short ones (6.6 us at 4096 x 1001, with 256 9.1).
+// 4096 x 152064 bf16, 39, 20, 14.5 us at 4096 x 1001. Without a list 256 for long rows (4096 x 152064, every row live, no
+// entropy: 351.2 us, with 128 352.7), 128 for short ones (6.6 us at 4096 x 1001, with 256 9.1).
 template <typename T>
 nvfp4rl_status launch_type(const LogitsGradArgs& a, cudaStream_t st) {
   if (a.ids && a.k <= 64) return launch_width<T, 64>(a, st);
