@@ -15,12 +15,14 @@
  *   - "TRACE: rollout-guided quantization-aware training" summary (sns.style),
  *     sections "TRACE の中心的なアイデア" and "仕組みの工学的な理解".
  * Around them stand the operators between a model's logits and that correction: token log-probs
- * with entropy and top alternatives, top-k distillation, and the gradients of both.
+ * with entropy and top alternatives, top-k distillation, and the gradients of both; and what a step over groups of
+ * responses to one prompt needs besides: prompts written to the KV cache and read back, decode attention of sequences
+ * that share a prefix, the clipped policy loss and the preference loss with their gradients.
  *
  * Conventions shared by every entry point:
  *   - Memory: every pointer argument is DEVICE memory, allocated and owned by
- *     the caller, and must be 16-byte aligned (the logits operators ask for their elements'
- *     alignment only). The library allocates nothing;
+ *     the caller, and must be 16-byte aligned (the logits operators and the losses ask for their
+ *     elements' alignment only). The library allocates nothing;
  *     it keeps only per-device cached attributes and kernel resources.
  *   - Streams: `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream). Calls are asynchronous on that stream; outputs are complete when
@@ -78,6 +80,9 @@ enum { NVFP4RL_BF16 = 0, NVFP4RL_F32 = 1 };
 /* How topk_distill reads a teacher's listed log-probs. */
 enum { NVFP4RL_DISTILL_NORMALIZED = 0, NVFP4RL_DISTILL_TAIL = 1 };
 
+/* How policy_loss joins its tokens. */
+enum { NVFP4RL_LOSS_TOKEN_MEAN = 0, NVFP4RL_LOSS_SEQ_MEAN = 1, NVFP4RL_LOSS_SUM = 2 };
+
 /* Operations for nvfp4rl_workspace_bytes(). */
 enum {
   NVFP4RL_OP_QUANTIZE = 0,
@@ -87,7 +92,10 @@ enum {
   NVFP4RL_OP_RMSNORM_QUANTIZE = 4,
   NVFP4RL_OP_AIS = 5,
   NVFP4RL_OP_KV_ATTENTION = 6, /* M = B, N = Hkv, K = Lmax */
-  NVFP4RL_OP_LINEAR_W4A4_QUANTIZED = 7
+  NVFP4RL_OP_LINEAR_W4A4_QUANTIZED = 7,
+  NVFP4RL_OP_KV_PREFIX_ATTENTION = 8, /* M = B, N = Hkv, K = Lmax, r = Hq / Hkv, num_groups = P */
+  NVFP4RL_OP_POLICY_LOSS = 9,         /* M = n, N = B */
+  NVFP4RL_OP_PREFERENCE_LOSS = 10     /* M = n, N = pairs */
 };
 
 /*
@@ -390,6 +398,151 @@ NVFP4RL_API nvfp4rl_status nvfp4_kv_decode_attention(const uint16_t* q, const ui
                                                      int64_t Hkv, int64_t D, int64_t Lmax, float scale,
                                                      uint16_t* out, void* workspace, size_t workspace_bytes,
                                                      void* stream);
+
+/*
+ * nvfp4_kv_append_ragged -- writes the keys and values of whole prompts (or chunks of them) into an NVFP4 KV cache: the
+ *   prefill's side of nvfp4_kv_append (TRACE summary, "実験結果と性能": FP4 KV cache), with the same encoding, cache
+ *   layout and given gk, gv. The T packed rows hold B sequences one after another: sequence b's rows are
+ *   [offsets[b], offsets[b+1]), and its i-th row goes to cache row (b, pos[b] + i).
+ * Arguments:
+ *   k, v     device bf16 or fp32 (dtype), T rows of [Hkv][D] elements; row t starts at k + t ldk (v + t ldv) elements:
+ *            a slice of a fused projection's rows is taken as it lies. 16-byte aligned, ldk and ldv at least Hkv D and a
+ *            multiple of 16 bytes. D a multiple of 16, Hkv D <= 2^20, T <= 2^31 - 1.
+ *   offsets  device int32 [B + 1], non-decreasing; pos device int32 [B], or NULL (all 0). 4-byte aligned.
+ *   B        sequences (caches), <= 2^20. gk, gv, the caches, Lmax as nvfp4_kv_append.
+ * Rows before offsets[0] or at offsets[B] and behind, and rows whose place lies outside [0, Lmax), are passed over. Only
+ * the cache rows named are written. Offsets that fall, or a pos that overflows, write unspecified rows of the
+ * cache, never outside it.
+ * Errors: NVFP4RL_ERR_INVALID_ARG (bad dtype, negative sizes, ld < Hkv D, NULL pointers), NVFP4RL_ERR_UNSUPPORTED_SHAPE
+ *   (D, ld, sizes), NVFP4RL_ERR_MISALIGNED, NVFP4RL_ERR_ALIAS. T == 0 or B == 0 is a no-op.
+ */
+NVFP4RL_API nvfp4rl_status nvfp4_kv_append_ragged(const void* k, const void* v, int32_t dtype, int64_t T, int64_t ldk,
+                                                  int64_t ldv, int64_t Hkv, int64_t D, const int32_t* offsets,
+                                                  const int32_t* pos, int64_t B, const float* gk, const float* gv,
+                                                  uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                                                  uint8_t* v_scales, int64_t Lmax, void* stream);
+
+/*
+ * nvfp4_kv_read -- the values that a cache holds: packed row t of k and v (out, laid out and addressed as
+ *   nvfp4_kv_append_ragged takes them) = E2M1 code x E4M3 block scale x g of its cache row, rounded to fp32 and, for bf16,
+ *   from there: what a prefill over a cached prefix attends to, so that it sees what decoding sees.
+ *   Rows of a sequence whose place lies outside [0, Lmax) are 0; rows of no sequence are left as they were.
+ *   Scale bytes as for nvfp4_kv_decode_attention. Arguments and errors as nvfp4_kv_append_ragged.
+ */
+NVFP4RL_API nvfp4rl_status nvfp4_kv_read(const uint8_t* k_codes, const uint8_t* k_scales, const float* gk,
+                                         const uint8_t* v_codes, const uint8_t* v_scales, const float* gv, int64_t Lmax,
+                                         int64_t Hkv, int64_t D, const int32_t* offsets, const int32_t* pos, int64_t B,
+                                         int64_t T, void* k, void* v, int32_t dtype, int64_t ldk, int64_t ldv,
+                                         void* stream);
+
+/*
+ * nvfp4_kv_prefix_attention -- one decode step of attention for a batch in groups that share a prefix each (the responses
+ *   sampled for one prompt): for sequence b of group p
+ *     out[b][h] = softmax(scale q[b][h] . K^) V^ over the first prefix_lens[p] rows of prefix cache p and the first lens[b]
+ *     rows of b's own cache together, of KV head h / (Hq / Hkv),
+ *   K^ and V^ the dequantized rows. A prefix is read once for its whole group.
+ * Arguments:
+ *   q        device bf16, row b at q + b ldq elements, [Hq][D]; 16-byte aligned, ldq >= Hq D, a multiple of 8. D must be
+ *            128, Hq a multiple of Hkv, Hq / Hkv <= 16, (B + P) Hkv <= 65535.
+ *   pk_codes, pk_scales, pv_codes, pv_scales  the prefixes, [P][Lp][Hkv][D/2] and [D/16], as nvfp4_kv_append_ragged
+ *            writes them; P in [1, 1024], P Lp < 2^31 - 128.
+ *   prefix_lens  device int32 [P], clamped to [0, Lp].
+ *   group_offsets  device int32 [P + 1], non-decreasing: sequences [group_offsets[p], group_offsets[p+1]) share
+ *            prefix p. Sequences of no group have no prefix. (Offsets that fall give unspecified results, no fault.)
+ *   k_codes .. v_scales, lens, Lmax  the sequences' own caches, as for nvfp4_kv_decode_attention; Lmax 0: there are none
+ *            (the pointers and lens are not used).
+ *   gk, gv   device fp32 scalars, of both caches.
+ *   scale    finite. out  device bf16 [B][Hq][D], 16-byte aligned; may overlap no input.
+ *   workspace >= nvfp4rl_workspace_bytes(NVFP4RL_OP_KV_PREFIX_ATTENTION, B, Hkv, Lmax, Hq / Hkv, P) bytes, device, 16-byte
+ *            aligned; scratch.
+ * A sequence that attends to nothing gets 0. Precision as nvfp4_kv_decode_attention; partial results are fp32, joined
+ * in a fixed order: equal inputs give equal bits.
+ * Errors as nvfp4_kv_decode_attention.
+ */
+NVFP4RL_API nvfp4rl_status nvfp4_kv_prefix_attention(
+    const uint16_t* q, int64_t ldq, const uint8_t* pk_codes, const uint8_t* pk_scales, const uint8_t* pv_codes,
+    const uint8_t* pv_scales, const int32_t* prefix_lens, const int32_t* group_offsets, int64_t P, int64_t Lp,
+    const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+    const int32_t* lens, int64_t Lmax, const float* gk, const float* gv, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+    float scale, uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * policy_loss -- the clipped policy loss over packed responses, with a KL term (the objective that ais_mixing's weights
+ *   enter: AIS summary, section 2.2 "GRPO への統合"; the pages have no recipe for it, so it is stated here).
+ *   Sequence b has tokens [offsets[b], offsets[b+1]) of n; a token counts (m_i = 1) when it is of a sequence and mask, if
+ *   given, is not 0 there. With d = logp - logp_old, r = e^d, A its advantage and w its weight (1 without weights):
+ *     l_i = -w min(r A, clip(r, 1 - eps_low, 1 + eps_high) A), for A < 0 and dual_clip > 0 at most -w dual_clip A,
+ *     k_i = e^x - x - 1 with x = logp_ref - logp (0 without logp_ref),
+ *     loss = sum_i c_i l_i + kl_coef sum_i c_i k_i,  c_i = m_i coef[b]:
+ *     NVFP4RL_LOSS_TOKEN_MEAN: coef[b] = 1 / (number of counted tokens);
+ *     NVFP4RL_LOSS_SEQ_MEAN: 1 / (b's counted tokens x number of sequences with one);
+ *     NVFP4RL_LOSS_SUM: 1 / norm.  Without a counted token: loss 0.
+ * Arguments:
+ *   logp, logp_old  fp32 [n]; logp_ref, weights fp32 [n] or NULL; mask bytes [n] or NULL.
+ *   adv      fp32 [B], or [n] with adv_per_token != 0.
+ *   offsets  int32 [B + 1], non-decreasing, within [0, n]. n <= 2^31 - 1, B <= 2^31 - 2. Tokens of no sequence do not count.
+ *   eps_low in [0, 1), eps_high >= 0, dual_clip 0 or >= 1, kl_coef >= 0, norm > 0 (SUM only), all finite.
+ *   loss     out, fp32 [1]. coef  out, fp32 [B], or NULL: what policy_loss_backward takes.
+ *   stats    out, fp32 [8], or NULL: the loss, sum c_i l_i, sum c_i k_i, and over the counted tokens the share that
+ *            clipping decided, the mean of e^d - d - 1 (divergence from the old policy), the mean of r, their number,
+ *            and the number of sequences with one.
+ *   workspace >= nvfp4rl_workspace_bytes(NVFP4RL_OP_POLICY_LOSS, n, B, 0, 0, 0) bytes, device, 16-byte aligned; scratch.
+ *   Other arrays are aligned to their elements (mask to 1 byte).
+ * What a token that does not count holds is not looked at (NaN, -inf). A NaN in a counted one gives a NaN loss. An advantage
+ * of 0 gives l = 0 whatever r is. Whether r lies beyond a bound is decided on the exact d against the logarithm of the
+ * bound (to 2^-48), so that it does not depend on a rounding. Sums run in fp32 over 256 tokens, then in pairs of
+ * fp32. No atomics on floating values: equal inputs give equal bits. Offsets that fall give unspecified values, no fault.
+ * Errors: NVFP4RL_ERR_INVALID_ARG, NVFP4RL_ERR_UNSUPPORTED_SHAPE, NVFP4RL_ERR_MISALIGNED, NVFP4RL_ERR_WORKSPACE,
+ *   NVFP4RL_ERR_ALIAS.
+ */
+NVFP4RL_API nvfp4rl_status policy_loss(const float* logp, const float* logp_old, const float* logp_ref, const float* adv,
+                                       int32_t adv_per_token, const float* weights, const uint8_t* mask,
+                                       const int32_t* offsets, int64_t n, int64_t B, float eps_low, float eps_high,
+                                       float dual_clip, float kl_coef, int32_t mode, float norm, float* loss,
+                                       float* stats, float* coef, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/*
+ * policy_loss_backward -- gradient of dloss x loss to logp:
+ *   dlogp[i] = dloss c_i (-w r A where clipping did not decide the token, else 0, + kl_coef (1 - e^x)),
+ *   0 for tokens that do not count: what token_logprobs_backward takes.
+ * Arguments as policy_loss, and coef as it wrote them; dloss fp32 [1] on the device, or NULL (1).
+ *   dlogp    out, fp32 [n]: every element is written. It may overlap no input.
+ */
+NVFP4RL_API nvfp4rl_status policy_loss_backward(const float* logp, const float* logp_old, const float* logp_ref,
+                                                const float* adv, int32_t adv_per_token, const float* weights,
+                                                const uint8_t* mask, const int32_t* offsets, int64_t n, int64_t B,
+                                                float eps_low, float eps_high, float dual_clip, float kl_coef,
+                                                const float* coef, const float* dloss, float* dlogp, void* stream);
+
+/*
+ * preference_loss -- the loss of paired log ratios over packed responses: sequence 2 p is the chosen and 2 p + 1 the
+ *   rejected response of pair p, with tokens and mask as policy_loss has them.
+ *     s_b = sum of (logp - logp_ref) over b's counted tokens (logp alone without logp_ref), with mean != 0 divided by
+ *           their number (0 for none),
+ *     h = beta (s_2p - s_2p+1) - margin,
+ *     loss[p] = -(1 - smoothing) ln sigma(h) - smoothing ln sigma(-h).
+ * Arguments: logp fp32 [n], logp_ref fp32 [n] or NULL, mask bytes [n] or NULL, offsets int32 [2 pairs + 1]; n <= 2^31 - 1,
+ *   pairs <= 2^30 - 1; beta > 0, margin and smoothing in [0, 1) finite.
+ *   loss     out, fp32 [pairs]. rewards out, fp32 [2 pairs], or NULL: beta s_b. coef out, fp32 [2 pairs], or NULL: the
+ *            gradient of loss[p] to a counted token of sequence b.
+ *   workspace >= nvfp4rl_workspace_bytes(NVFP4RL_OP_PREFERENCE_LOSS, n, pairs, 0, 0, 0) bytes, device, 16-byte
+ *            aligned; scratch. Other arrays are aligned to their elements.
+ * s_b is summed as pairs of fp32 (44 bits), and so is the difference. Tokens that do not count, NaN, determinism and errors
+ * as policy_loss.
+ */
+NVFP4RL_API nvfp4rl_status preference_loss(const float* logp, const float* logp_ref, const uint8_t* mask,
+                                           const int32_t* offsets, int64_t n, int64_t pairs, float beta, float margin,
+                                           float smoothing, int32_t mean, float* loss, float* rewards, float* coef,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * preference_loss_backward -- gradient of sum_p dloss[p] loss[p] to logp: dlogp[i] = dloss[p] coef[b] for counted tokens, 0
+ *   for the others; every element is written.
+ *   coef as preference_loss wrote it; dloss fp32 [pairs], or NULL (1); dlogp out, fp32 [n], may overlap no input.
+ */
+NVFP4RL_API nvfp4rl_status preference_loss_backward(const uint8_t* mask, const int32_t* offsets, int64_t n, int64_t pairs,
+                                                    const float* coef, const float* dloss, float* dlogp, void* stream);
 
 /*
  * aqn_sigma -- AQN exponential noise schedule (QeRL explainer, "AQNの仕組み":

@@ -9,8 +9,9 @@ library or a GPU is missing -- there is no CPU fallback.
 
 Functions carry the C names: nvfp4_amax, nvfp4_quantize, nvfp4_quantize_guided,
 nvfp4_quantize_record, nvfp4_quantize_cached, nvfp4_quantize_batch, nvfp4_kv_append,
-nvfp4_kv_decode_attention, ais_mixing, token_logprobs, token_logprobs_backward, topk_distill,
-topk_distill_backward, aqn_sigma, rmsnorm_aqn, rmsnorm_aqn_quantize, nvfp4_lora_linear,
+nvfp4_kv_append_ragged, nvfp4_kv_read, nvfp4_kv_decode_attention, nvfp4_kv_prefix_attention, ais_mixing,
+token_logprobs, token_logprobs_backward, topk_distill, topk_distill_backward, policy_loss, policy_loss_backward,
+preference_loss, preference_loss_backward, aqn_sigma, rmsnorm_aqn, rmsnorm_aqn_quantize, nvfp4_lora_linear,
 nvfp4_lora_linear_w4a4.
 """
 from __future__ import annotations
@@ -26,8 +27,9 @@ LIB_PATH = _build.LIB
 OK = 0
 BF16, F32 = 0, 1
 DISTILL_NORMALIZED, DISTILL_TAIL = 0, 1
+LOSS_TOKEN_MEAN, LOSS_SEQ_MEAN, LOSS_SUM = 0, 1, 2
 (OP_QUANTIZE, OP_LINEAR_W4A16, OP_LINEAR_W4A4, OP_QUANTIZE_BATCH, OP_RMSNORM_QUANTIZE, OP_AIS, OP_KV_ATTENTION,
- OP_LINEAR_W4A4_QUANTIZED) = (0, 1, 2, 3, 4, 5, 6, 7)
+ OP_LINEAR_W4A4_QUANTIZED, OP_KV_PREFIX_ATTENTION, OP_POLICY_LOSS, OP_PREFERENCE_LOSS) = range(11)
 
 _lock = threading.Lock()
 _lib = None
@@ -53,6 +55,14 @@ def _signatures():
         "token_logprobs_backward": (c.c_int, [p, i32, i64, i64, i64, p, f32, p, p, p, p, p, i64, p]),
         "topk_distill": (c.c_int, [p, i32, i64, i64, i64, f32, p, p, i32, i32, p, p, p, p]),
         "topk_distill_backward": (c.c_int, [p, i32, i64, i64, i64, f32, p, p, i32, i32, p, p, p, p, i64, p]),
+        "nvfp4_kv_append_ragged": (c.c_int, [p, p, i32, i64, i64, i64, i64, i64, p, p, i64, p, p, p, p, p, p, i64, p]),
+        "nvfp4_kv_read": (c.c_int, [p, p, p, p, p, p, i64, i64, i64, p, p, i64, i64, p, p, i32, i64, i64, p]),
+        "nvfp4_kv_prefix_attention": (c.c_int, [p, i64, p, p, p, p, p, p, i64, i64, p, p, p, p, p, i64, p, p, i64, i64,
+                                                i64, i64, f32, p, p, sz, p]),
+        "policy_loss": (c.c_int, [p, p, p, p, i32, p, p, p, i64, i64, f32, f32, f32, f32, i32, f32, p, p, p, p, sz, p]),
+        "policy_loss_backward": (c.c_int, [p, p, p, p, i32, p, p, p, i64, i64, f32, f32, f32, f32, p, p, p, p]),
+        "preference_loss": (c.c_int, [p, p, p, p, i64, i64, f32, f32, f32, i32, p, p, p, p, sz, p]),
+        "preference_loss_backward": (c.c_int, [p, p, i64, i64, p, p, p, p]),
         "nvfp4_quantize_batch": (c.c_int, [i32, p, p, p, i32, p, p, p, p, sz, p]),
         "aqn_sigma": (f64, [f64, f64, i64, i64]),
         "rmsnorm_aqn": (c.c_int, [p, i64, i64, p, p, f32, f32, p, p]),
@@ -472,6 +482,305 @@ def topk_distill_backward(logits, ids, teacher_logp, lse, dloss, scale: float = 
                  DISTILL_TAIL if tail else DISTILL_NORMALIZED, _row_array(lse, "lse", f32, rows, dev),
                  _row_array(lse_tail, "lse_tail", f32, rows, dev), _row_array(dloss, "dloss", f32, rows, dev),
                  out.data_ptr(), ldd)
+    if given:
+        _mark_written(given)
+    return out
+
+
+def _packed_rows(x, what):
+    """dtype code, T, Hkv, D, row stride and device index of packed rows [T, Hkv, D] (bf16 or fp32), a token's heads
+    contiguous: the rows may be parts of longer ones."""
+    import torch
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("nvfp4rl works on CUDA tensors only (no CPU path)")
+    dt = BF16 if x.dtype is torch.bfloat16 else F32 if x.dtype is torch.float32 else None
+    if dt is None:
+        raise TypeError(f"{what} must be bf16 or fp32")
+    if x.dim() != 3:
+        raise ValueError(f"{what} must be [tokens, heads, dim]")
+    T, H, D = x.shape
+    ld, head, step = x.stride()
+    if T <= 1:
+        ld = H * D
+    if (D > 1 and step != 1) or (H > 1 and head != D) or ld < H * D:
+        raise ValueError(f"{what}: the heads of a token must be contiguous, and rows must not overlap")
+    return dt, T, H, D, ld, device
+
+
+def _given_array(t, name, dtype, shape, device):
+    """The address of one argument (None: NULL): contiguous, of this dtype and shape, on the call's device."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device}")
+    return t.data_ptr()
+
+
+def _cache_arrays(arrays, D, device, what=""):
+    """Addresses and B, Lmax, Hkv of a cache's four uint8 arrays (codes and scales of K, then of V)."""
+    import torch
+    shape = arrays[0].shape
+    if len(shape) != 4 or shape[3] * 2 != D:
+        raise ValueError(f"{what}k_codes must be [sequences, rows, heads, {D} / 2]")
+    at = []
+    for name, t, w in zip(("k_codes", "k_scales", "v_codes", "v_scales"), arrays, (2, 16, 2, 16)):
+        at.append(_given_array(t, what + name, torch.uint8, (shape[0], shape[1], shape[2], D // w), device))
+    return at, shape[0], shape[1], shape[2]
+
+
+def _scale_arrays(gk, gv, device):
+    """Addresses of the two fp32 tensor scales (one element each)."""
+    import torch
+    at = []
+    for name, t in (("gk", gk), ("gv", gv)):
+        if t.dtype is not torch.float32 or t.numel() != 1 or t.get_device() != device:
+            raise ValueError(f"{name} must be one fp32 element on cuda:{device}")
+        at.append(t.data_ptr())
+    return at
+
+
+def nvfp4_kv_append_ragged(k, v, offsets, pos, gk, gv, k_codes, k_scales, v_codes, v_scales, stream=None):
+    """Writes the packed keys and values of B sequences (bf16 or fp32 [T, Hkv, D]; a token's heads contiguous, rows may
+    be parts of longer ones) into an NVFP4 KV cache: rows offsets[b] .. offsets[b+1] (int32 [B + 1]) go to the rows of
+    cache b from pos[b] on (int32 [B], or None: 0). Caches and scales as nvfp4_kv_append; the caches count as
+    modified in place."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, k, nvfp4_kv_append_ragged, k, v, offsets, pos, gk, gv, k_codes, k_scales, v_codes,
+                          v_scales)
+    dt, T, H, D, ldk, dev = _packed_rows(k, "k")
+    dtv, Tv, Hv, Dv, ldv, devv = _packed_rows(v, "v")
+    if (dtv, Tv, Hv, Dv, devv) != (dt, T, H, D, dev):
+        raise ValueError("k and v must have one dtype, shape and device")
+    caches = (k_codes, k_scales, v_codes, v_scales)
+    at, B, Lmax, Hkv = _cache_arrays(caches, D, dev)
+    if Hkv != H:
+        raise ValueError("k and the caches have different numbers of heads")
+    g = _scale_arrays(gk, gv, dev)
+    _logits_call("nvfp4_kv_append_ragged", dev, k.data_ptr(), v.data_ptr(), dt, T, ldk, ldv, H, D,
+                 _given_array(offsets, "offsets", torch.int32, (B + 1,), dev),
+                 _given_array(pos, "pos", torch.int32, (B,), dev), B, g[0], g[1], *at, Lmax)
+    _mark_written(caches)
+
+
+def nvfp4_kv_read(k_codes, k_scales, gk, v_codes, v_scales, gv, offsets, pos=None, tokens=None, dtype=None, k=None,
+                  v=None, stream=None):
+    """The values that an NVFP4 KV cache holds, as packed rows -> (k, v) [tokens, Hkv, D] of dtype (bf16 or fp32; bf16
+    when None): rows offsets[b] .. offsets[b+1] are the rows of cache b from pos[b] on. Rows outside the cache are 0; rows
+    of no sequence are not written. k and v may be given (both; their rows may be parts of longer ones)."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, k_codes, nvfp4_kv_read, k_codes, k_scales, gk, v_codes, v_scales, gv, offsets, pos,
+                          tokens, dtype, k, v)
+    dev = k_codes.get_device()
+    if dev < 0:
+        raise ValueError("nvfp4rl works on CUDA tensors only (no CPU path)")
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v, or neither")
+    D = k_codes.shape[-1] * 2
+    at, B, Lmax, H = _cache_arrays((k_codes, k_scales, v_codes, v_scales), D, dev)
+    g = _scale_arrays(gk, gv, dev)
+    given = k is not None
+    if given:
+        dt, T, Hk, Dk, ldk, devk = _packed_rows(k, "k")
+        if (dt, T, Hk, Dk, devk) != (_packed_rows(v, "v")[:4] + (v.get_device(),)) or (Hk, Dk, devk) != (H, D, dev):
+            raise ValueError("k and v must have one dtype and shape, and the caches' heads and device")
+        if (dtype is not None and dtype is not k.dtype) or (tokens is not None and tokens != T):
+            raise ValueError("k and v differ from dtype or tokens")
+        ldv = _packed_rows(v, "v")[4]
+    else:
+        if tokens is None:
+            raise ValueError("give the number of packed rows (tokens), or k and v")
+        dtype = torch.bfloat16 if dtype is None else dtype
+        dt, T, ldk, ldv = {torch.bfloat16: BF16, torch.float32: F32}.get(dtype), tokens, H * D, H * D
+        if dt is None:
+            raise TypeError("dtype must be bf16 or fp32")
+        k = torch.empty(T, H, D, dtype=dtype, device=dev)
+        v = torch.empty(T, H, D, dtype=dtype, device=dev)
+    _logits_call("nvfp4_kv_read", dev, at[0], at[1], g[0], at[2], at[3], g[1], Lmax, H, D,
+                 _given_array(offsets, "offsets", torch.int32, (B + 1,), dev),
+                 _given_array(pos, "pos", torch.int32, (B,), dev), B, T, k.data_ptr(), v.data_ptr(), dt, ldk, ldv)
+    if given:
+        _mark_written((k, v))
+    return k, v
+
+
+def nvfp4_kv_prefix_attention(q, pk_codes, pk_scales, pv_codes, pv_scales, prefix_lens, group_offsets, k_codes,
+                              k_scales, v_codes, v_scales, lens, gk, gv, scale, out=None, workspace=None, stream=None):
+    """One decode step of attention for sequences in groups that share a prefix each: q bf16 [B, Hq, 128] (rows may be
+    parts of longer ones) -> out bf16 [B, Hq, 128]. Sequences group_offsets[p] .. group_offsets[p+1] (int32 [P + 1])
+    attend to the first prefix_lens[p] rows of prefix cache p ([P, Lp, Hkv, ..]) and the first lens[b] rows of their own
+    (int32 [B]; caches [B, Lmax, Hkv, ..], or all five None: prefixes only)."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, q, nvfp4_kv_prefix_attention, q, pk_codes, pk_scales, pv_codes, pv_scales, prefix_lens,
+                          group_offsets, k_codes, k_scales, v_codes, v_scales, lens, gk, gv, scale, out, workspace)
+    dt, B, Hq, D, ldq, dev = _packed_rows(q, "q")
+    if dt != BF16:
+        raise TypeError("q must be bf16")
+    pre, P, Lp, Hkv = _cache_arrays((pk_codes, pk_scales, pv_codes, pv_scales), D, dev, "p")
+    own = (k_codes, k_scales, v_codes, v_scales)
+    if all(t is None for t in own) and lens is None:
+        at, Lmax, p_lens = (None,) * 4, 0, None
+    elif any(t is None for t in own) or lens is None:
+        raise ValueError("give the own caches and lens, or none of them")
+    else:
+        at, Bc, Lmax, Hc = _cache_arrays(own, D, dev)
+        if (Bc, Hc) != (B, Hkv):
+            raise ValueError("the own caches must be [B, rows, Hkv, ..]")
+        p_lens = _given_array(lens, "lens", torch.int32, (B,), dev)
+    g = _scale_arrays(gk, gv, dev)
+    given = out is not None
+    if not given:
+        out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=dev)
+    if workspace is None:
+        need = lib().nvfp4rl_workspace_bytes(OP_KV_PREFIX_ATTENTION, B, Hkv, Lmax, Hq // max(Hkv, 1), P)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev:
+        raise ValueError("the workspace is on another device")
+    _logits_call("nvfp4_kv_prefix_attention", dev, q.data_ptr(), ldq, *pre,
+                 _given_array(prefix_lens, "prefix_lens", torch.int32, (P,), dev),
+                 _given_array(group_offsets, "group_offsets", torch.int32, (P + 1,), dev), P, Lp, *at, p_lens, Lmax,
+                 g[0], g[1], B, Hq, Hkv, D, float(scale), _given_array(out, "out", torch.bfloat16, (B, Hq, D), dev),
+                 workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if given:
+        _mark_written((out,))
+    return out
+
+
+def _loss_arrays(logp, offsets, per_sequence, arrays, mask):
+    """Device index, n, sequences and addresses of the losses' arrays: fp32 [n] (None: NULL), the mask bytes
+    [n] and the offsets int32 [sequences + 1]."""
+    import torch
+    dev = logp.get_device()
+    if dev < 0:
+        raise ValueError("nvfp4rl works on CUDA tensors only (no CPU path)")
+    if logp.dim() != 1 or offsets.dim() != 1 or offsets.shape[0] < 1 or (offsets.shape[0] - 1) % per_sequence:
+        raise ValueError("logp must be [n], and offsets [sequences + 1]")
+    n, seqs = logp.shape[0], offsets.shape[0] - 1
+    at = [_given_array(t, name, torch.float32, (n,), dev) for name, t in arrays]
+    return dev, n, seqs, at, _mask_array(mask, n, dev), _given_array(offsets, "offsets", torch.int32, (seqs + 1,), dev)
+
+
+def _mask_array(mask, n, dev):
+    import torch
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("mask must be bool or uint8")
+    return None if mask is None else _given_array(mask, "mask", mask.dtype, (n,), dev)
+
+
+POLICY_STATS = ("loss", "policy", "kl", "clip_frac", "old_kl", "ratio", "tokens", "sequences")
+
+
+def policy_loss(logp, logp_old, adv, offsets, logp_ref=None, weights=None, mask=None, eps_low: float = 0.2,
+                eps_high: float = 0.2, dual_clip: float = 0.0, kl_coef: float = 0.0, mode: int = LOSS_TOKEN_MEAN,
+                norm: float = 1.0, adv_per_token: bool = False, loss=None, stats=None, coef=None, workspace=None,
+                stream=None):
+    """The clipped policy loss of packed responses (logp, logp_old fp32 [n]; sequence b has tokens offsets[b] ..
+    offsets[b+1], int32 [B + 1]; adv fp32 [B], or [n] with adv_per_token) with kl_coef times the estimated divergence
+    from logp_ref; weights fp32 [n] (e.g. ais_mixing's) scale each token's policy term, mask (bool or uint8 [n]) says
+    which tokens count -> (loss fp32 [1], stats fp32 [8] in the order of POLICY_STATS, coef fp32 [B] for
+    policy_loss_backward). The results carry no autograd graph."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, logp, policy_loss, logp, logp_old, adv, offsets, logp_ref, weights, mask, eps_low,
+                          eps_high, dual_clip, kl_coef, mode, norm, adv_per_token, loss, stats, coef, workspace)
+    dev, n, B, at, p_mask, p_off = _loss_arrays(logp, offsets, 1, (("logp", logp), ("logp_old", logp_old),
+                                                                   ("logp_ref", logp_ref), ("weights", weights)), mask)
+    f32 = torch.float32
+    given = [t for t in (loss, stats, coef) if t is not None]
+    loss = torch.empty(1, dtype=f32, device=dev) if loss is None else loss
+    stats = torch.empty(8, dtype=f32, device=dev) if stats is None else stats
+    coef = torch.empty(B, dtype=f32, device=dev) if coef is None else coef
+    if workspace is None:
+        workspace = torch.empty(lib().nvfp4rl_workspace_bytes(OP_POLICY_LOSS, n, B, 0, 0, 0), dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev:
+        raise ValueError("the workspace is on another device")
+    _logits_call("policy_loss", dev, at[0], at[1], at[2],
+                 _given_array(adv, "adv", f32, (n,) if adv_per_token else (B,), dev), 1 if adv_per_token else 0, at[3],
+                 p_mask, p_off, n, B, float(eps_low), float(eps_high), float(dual_clip), float(kl_coef), mode, float(norm),
+                 _given_array(loss, "loss", f32, (1,), dev), _given_array(stats, "stats", f32, (8,), dev),
+                 _given_array(coef, "coef", f32, (B,), dev), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size())
+    if given:
+        _mark_written(given)
+    return loss, stats, coef
+
+
+def policy_loss_backward(logp, logp_old, adv, offsets, coef, dloss=None, logp_ref=None, weights=None, mask=None,
+                         eps_low: float = 0.2, eps_high: float = 0.2, dual_clip: float = 0.0, kl_coef: float = 0.0,
+                         adv_per_token: bool = False, out=None, stream=None):
+    """Gradient of dloss (fp32 [1], or None: 1) times policy_loss's loss to logp -> out fp32 [n] (0 for tokens that do
+    not count), what token_logprobs_backward takes as dlogp. coef as policy_loss gave it for the same arguments."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, logp, policy_loss_backward, logp, logp_old, adv, offsets, coef, dloss, logp_ref, weights,
+                          mask, eps_low, eps_high, dual_clip, kl_coef, adv_per_token, out)
+    dev, n, B, at, p_mask, p_off = _loss_arrays(logp, offsets, 1, (("logp", logp), ("logp_old", logp_old),
+                                                                   ("logp_ref", logp_ref), ("weights", weights)), mask)
+    f32 = torch.float32
+    given = [] if out is None else [out]
+    out = torch.empty(n, dtype=f32, device=dev) if out is None else out
+    _logits_call("policy_loss_backward", dev, at[0], at[1], at[2],
+                 _given_array(adv, "adv", f32, (n,) if adv_per_token else (B,), dev), 1 if adv_per_token else 0, at[3],
+                 p_mask, p_off, n, B, float(eps_low), float(eps_high), float(dual_clip), float(kl_coef),
+                 _given_array(coef, "coef", f32, (B,), dev), _given_array(dloss, "dloss", f32, (1,), dev),
+                 _given_array(out, "out", f32, (n,), dev))
+    if given:
+        _mark_written(given)
+    return out
+
+
+def preference_loss(logp, offsets, logp_ref=None, mask=None, beta: float = 0.1, margin: float = 0.0,
+                    smoothing: float = 0.0, mean: bool = False, loss=None, rewards=None, coef=None, workspace=None,
+                    stream=None):
+    """The loss of paired log ratios over packed responses: sequences 2p (chosen) and 2p+1 (rejected) have tokens
+    offsets[b] .. offsets[b+1] (int32 [2P + 1]) of logp (fp32 [n]), less logp_ref where given, summed or (mean) averaged
+    over the counted ones -> (loss fp32 [P], rewards fp32 [2P], coef fp32 [2P] for preference_loss_backward). The
+    results carry no autograd graph."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, logp, preference_loss, logp, offsets, logp_ref, mask, beta, margin, smoothing, mean, loss,
+                          rewards, coef, workspace)
+    dev, n, seqs, at, p_mask, p_off = _loss_arrays(logp, offsets, 2, (("logp", logp), ("logp_ref", logp_ref)), mask)
+    f32, pairs = torch.float32, seqs // 2
+    given = [t for t in (loss, rewards, coef) if t is not None]
+    loss = torch.empty(pairs, dtype=f32, device=dev) if loss is None else loss
+    rewards = torch.empty(seqs, dtype=f32, device=dev) if rewards is None else rewards
+    coef = torch.empty(seqs, dtype=f32, device=dev) if coef is None else coef
+    if workspace is None:
+        workspace = torch.empty(lib().nvfp4rl_workspace_bytes(OP_PREFERENCE_LOSS, n, pairs, 0, 0, 0), dtype=torch.uint8,
+                                device=dev)
+    elif workspace.get_device() != dev:
+        raise ValueError("the workspace is on another device")
+    _logits_call("preference_loss", dev, at[0], at[1], p_mask, p_off, n, pairs, float(beta), float(margin),
+                 float(smoothing), 1 if mean else 0, _given_array(loss, "loss", f32, (pairs,), dev),
+                 _given_array(rewards, "rewards", f32, (seqs,), dev), _given_array(coef, "coef", f32, (seqs,), dev),
+                 workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if given:
+        _mark_written(given)
+    return loss, rewards, coef
+
+
+def preference_loss_backward(offsets, coef, dloss, n: int, mask=None, out=None, stream=None):
+    """Gradient of sum(dloss * loss) (dloss fp32 [P], or None: ones) to logp -> out fp32 [n]: dloss[p] coef[b] at the
+    counted tokens, 0 elsewhere. coef as preference_loss gave it."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, coef, preference_loss_backward, offsets, coef, dloss, n, mask, out)
+    dev = coef.get_device()
+    if dev < 0:
+        raise ValueError("nvfp4rl works on CUDA tensors only (no CPU path)")
+    f32, seqs = torch.float32, coef.shape[0] if coef.dim() == 1 else -1
+    if seqs < 0 or seqs % 2:
+        raise ValueError("coef must be [2 pairs]")
+    given = [] if out is None else [out]
+    out = torch.empty(n, dtype=f32, device=dev) if out is None else out
+    _logits_call("preference_loss_backward", dev, _mask_array(mask, n, dev),
+                 _given_array(offsets, "offsets", torch.int32, (seqs + 1,), dev), n, seqs // 2,
+                 _given_array(coef, "coef", f32, (seqs,), dev), _given_array(dloss, "dloss", f32, (seqs // 2,), dev),
+                 _given_array(out, "out", f32, (n,), dev))
     if given:
         _mark_written(given)
     return out

@@ -8,7 +8,9 @@
 #include <vector>
 
 #include "common.cuh"
+#include "kv_ragged.cuh"
 #include "logits.cuh"
+#include "losses.cuh"
 #include "sm100.cuh"
 
 namespace nvfp4rl {
@@ -247,6 +249,97 @@ nvfp4rl_status check_dlogits(const void* x, int64_t ld, size_t xbytes, const voi
   if (reinterpret_cast<uintptr_t>(dx) % esz) return NVFP4RL_ERR_MISALIGNED;
   *bytes = (static_cast<size_t>(M - 1) * ldd + V) * esz;
   if (!(dx == x && ldd == ld) && overlap(dx, *bytes, x, xbytes)) return NVFP4RL_ERR_ALIAS;
+  return NVFP4RL_OK;
+}
+
+// Packed rows against an NVFP4 KV cache: what nvfp4_kv_append_ragged and nvfp4_kv_read share. `write`: the caches are
+// the outputs, else k and v.
+nvfp4rl_status check_ragged(const void* k, const void* v, int32_t dtype, int64_t T, int64_t ldk, int64_t ldv, int64_t Hkv,
+                            int64_t D, const int32_t* offsets, const int32_t* pos, int64_t B, const float* gk,
+                            const float* gv, const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const uint8_t* vs,
+                            int64_t Lmax, bool write, bool* skip) {
+  *skip = false;
+  if (dtype != NVFP4RL_BF16 && dtype != NVFP4RL_F32) return NVFP4RL_ERR_INVALID_ARG;
+  if (T < 0 || B < 0 || Hkv <= 0 || D <= 0 || Lmax <= 0) return NVFP4RL_ERR_INVALID_ARG;
+  if (D % 16 != 0 || D > (1 << 20) || Hkv > (1 << 20) / D || T > 2147483647LL || B > (1 << 20))
+    return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  const int64_t row = Hkv * D;
+  if (ldk < row || ldv < row) return NVFP4RL_ERR_INVALID_ARG;
+  const int64_t esz = dtype == NVFP4RL_BF16 ? 2 : 4, most = int64_t(1) << 48;
+  if (ldk > most || ldv > most || ldk * esz % 16 || ldv * esz % 16) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0 || B == 0) {
+    *skip = true;
+    return NVFP4RL_OK;
+  }
+  if (ldk > most / T || ldv > most / T || Lmax > most / (B * row)) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (!k || !v || !offsets || !gk || !gv || !kc || !ks || !vc || !vs) return NVFP4RL_ERR_INVALID_ARG;
+  for (const void* p : {k, v, static_cast<const void*>(kc), static_cast<const void*>(ks), static_cast<const void*>(vc),
+                        static_cast<const void*>(vs)})
+    if (!aligned16(p)) return NVFP4RL_ERR_MISALIGNED;
+  if (!aligned4({offsets, pos, gk, gv})) return NVFP4RL_ERR_MISALIGNED;
+  const size_t elements = static_cast<size_t>(B * row) * static_cast<size_t>(Lmax);
+  const Span caches[4] = {{kc, elements / 2}, {ks, elements / 16}, {vc, elements / 2}, {vs, elements / 16}};
+  const Span rows[2] = {{k, static_cast<size_t>((T - 1) * ldk + row) * esz}, {v, static_cast<size_t>((T - 1) * ldv + row) * esz}};
+  const Span small[4] = {{offsets, static_cast<size_t>(B + 1) * 4}, {pos, static_cast<size_t>(B) * 4}, {gk, 4}, {gv, 4}};
+  nvfp4rl_status st;
+  if (write) {
+    const Span ins[6] = {rows[0], rows[1], small[0], small[1], small[2], small[3]};
+    st = check_spans(caches, ins);
+  } else {
+    // two slices of one fused row may interleave: that is checked row by row
+    const Span ins[8] = {caches[0], caches[1], caches[2], caches[3], small[0], small[1], small[2], small[3]};
+    const Span out_k[1] = {rows[0]}, out_v[1] = {rows[1]};
+    st = check_spans(out_k, ins);
+    if (st == NVFP4RL_OK) st = check_spans(out_v, ins);
+    if (st == NVFP4RL_OK && overlap(rows[0].p, rows[0].n, rows[1].p, rows[1].n)) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(k), b = reinterpret_cast<uintptr_t>(v);
+      const uintptr_t step = static_cast<uintptr_t>(ldk * esz), width = static_cast<uintptr_t>(row * esz);
+      const uintptr_t apart = (a < b ? b - a : a - b) % step;
+      if (ldk != ldv || apart < width || step - apart < width) st = NVFP4RL_ERR_ALIAS;
+    }
+  }
+  return st;
+}
+
+// A positive number as ln x = hi + lo, for comparisons with exact differences of log-probs.
+SplitFloat split_log1p(double x) {
+  const double l = std::log1p(x);
+  const float hi = static_cast<float>(l);
+  return {hi, static_cast<float>(l - static_cast<double>(hi))};
+}
+
+// What policy_loss and its gradient share.
+nvfp4rl_status check_policy(const float* logp, const float* logp_old, const float* logp_ref, const float* adv,
+                            int32_t adv_per_token, const float* weights, const uint8_t* mask, const int32_t* offsets,
+                            int64_t n, int64_t B, float eps_low, float eps_high, float dual_clip, float kl_coef,
+                            PolicyArgs* a) {
+  if (n < 0 || B < 0) return NVFP4RL_ERR_INVALID_ARG;
+  if (!(eps_low >= 0.0f && eps_low < 1.0f) || !(eps_high >= 0.0f) || !std::isfinite(eps_high) ||
+      !(dual_clip == 0.0f || dual_clip >= 1.0f) || !std::isfinite(dual_clip) || !(kl_coef >= 0.0f) ||
+      !std::isfinite(kl_coef))
+    return NVFP4RL_ERR_INVALID_ARG;
+  if (n > 2147483647LL || B > 2147483646LL) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (n > 0 && (!logp || !logp_old)) return NVFP4RL_ERR_INVALID_ARG;
+  if (!offsets || (!adv && (adv_per_token ? n : B) > 0)) return NVFP4RL_ERR_INVALID_ARG;
+  if (!aligned4({logp, logp_old, logp_ref, adv, weights, offsets})) return NVFP4RL_ERR_MISALIGNED;
+  *a = PolicyArgs{};
+  a->logp = logp;
+  a->logp_old = logp_old;
+  a->logp_ref = logp_ref;
+  a->adv = adv;
+  a->adv_per_token = adv_per_token != 0;
+  a->weights = weights;
+  a->mask = mask;
+  a->offsets = offsets;
+  a->n = n;
+  a->B = B;
+  a->ln_low = split_log1p(-static_cast<double>(eps_low));
+  a->ln_high = split_log1p(static_cast<double>(eps_high));
+  a->ln_dual = dual_clip > 0.0f ? split_log1p(static_cast<double>(dual_clip) - 1.0) : SplitFloat{INFINITY, 0.0f};
+  a->low = 1.0f - eps_low;
+  a->high = 1.0f + eps_high;
+  a->dual = dual_clip;
+  a->kl = kl_coef;
   return NVFP4RL_OK;
 }
 
@@ -546,6 +639,200 @@ nvfp4rl_status nvfp4_kv_decode_attention(const uint16_t* q, const uint8_t* kc, c
                              static_cast<cudaStream_t>(stream));
 }
 
+nvfp4rl_status nvfp4_kv_append_ragged(const void* k, const void* v, int32_t dtype, int64_t T, int64_t ldk, int64_t ldv,
+                                      int64_t Hkv, int64_t D, const int32_t* offsets, const int32_t* pos, int64_t B,
+                                      const float* gk, const float* gv, uint8_t* kc, uint8_t* ks, uint8_t* vc,
+                                      uint8_t* vs, int64_t Lmax, void* stream) {
+  bool skip;
+  nvfp4rl_status st = check_ragged(k, v, dtype, T, ldk, ldv, Hkv, D, offsets, pos, B, gk, gv, kc, ks, vc, vs, Lmax, true, &skip);
+  if (st != NVFP4RL_OK || skip) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  return launch_kv_append_ragged(k, v, dtype, ldk, ldv, Hkv, D, RaggedArgs{offsets, pos, B, T, Lmax}, gk, gv, kc, ks, vc,
+                                 vs, dev, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status nvfp4_kv_read(const uint8_t* kc, const uint8_t* ks, const float* gk, const uint8_t* vc, const uint8_t* vs,
+                             const float* gv, int64_t Lmax, int64_t Hkv, int64_t D, const int32_t* offsets,
+                             const int32_t* pos, int64_t B, int64_t T, void* k, void* v, int32_t dtype, int64_t ldk,
+                             int64_t ldv, void* stream) {
+  bool skip;
+  nvfp4rl_status st = check_ragged(k, v, dtype, T, ldk, ldv, Hkv, D, offsets, pos, B, gk, gv, kc, ks, vc, vs, Lmax, false, &skip);
+  if (st != NVFP4RL_OK || skip) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  return launch_kv_read(kc, ks, gk, vc, vs, gv, Hkv, D, RaggedArgs{offsets, pos, B, T, Lmax}, k, v, dtype, ldk, ldv, dev,
+                        static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status nvfp4_kv_prefix_attention(const uint16_t* q, int64_t ldq, const uint8_t* pkc, const uint8_t* pks,
+                                         const uint8_t* pvc, const uint8_t* pvs, const int32_t* prefix_lens,
+                                         const int32_t* groups, int64_t P, int64_t Lp, const uint8_t* kc,
+                                         const uint8_t* ks, const uint8_t* vc, const uint8_t* vs, const int32_t* lens,
+                                         int64_t Lmax, const float* gk, const float* gv, int64_t B, int64_t Hq,
+                                         int64_t Hkv, int64_t D, float scale, uint16_t* out, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Lp <= 0 || Lmax < 0 || P < 1 || P > 1024 || !std::isfinite(scale))
+    return NVFP4RL_ERR_INVALID_ARG;
+  if (D != 128 || Hq % Hkv != 0 || Hq / Hkv > 16 || B > 65535 || Hkv > 65535 || (B + P) * Hkv > 65535)
+    return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  const int64_t rows = 2147483647LL - 128;
+  if (Lp > rows || Lmax > rows || P * Lp > rows || B * Lmax > rows) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (ldq < Hq * D) return NVFP4RL_ERR_INVALID_ARG;
+  if (ldq % 8 || ldq > (int64_t(1) << 40)) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (B == 0) return NVFP4RL_OK;
+  if (!q || !pkc || !pks || !pvc || !pvs || !prefix_lens || !groups || !gk || !gv || !out) return NVFP4RL_ERR_INVALID_ARG;
+  if (Lmax == 0) {
+    kc = ks = vc = vs = nullptr;
+    lens = nullptr;
+  } else if (!kc || !ks || !vc || !vs || !lens) {
+    return NVFP4RL_ERR_INVALID_ARG;
+  }
+  for (const void* p : {static_cast<const void*>(q), static_cast<const void*>(pkc), static_cast<const void*>(pks),
+                        static_cast<const void*>(pvc), static_cast<const void*>(pvs), static_cast<const void*>(kc),
+                        static_cast<const void*>(ks), static_cast<const void*>(vc), static_cast<const void*>(vs),
+                        static_cast<const void*>(out)})
+    if (!aligned16(p)) return NVFP4RL_ERR_MISALIGNED;
+  if (!aligned4({prefix_lens, groups, lens, gk, gv})) return NVFP4RL_ERR_MISALIGNED;
+  const size_t need = prefix_attention_workspace_bytes(B, Hkv, Lmax, Hq / Hkv, P);
+  if (!workspace || workspace_bytes < need) return NVFP4RL_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return NVFP4RL_ERR_MISALIGNED;
+  const size_t pre = static_cast<size_t>(P * Lp * Hkv), own = static_cast<size_t>(B * Lmax * Hkv);
+  const Span outs[2] = {{out, static_cast<size_t>(B * Hq * D) * 2}, {workspace, need}};
+  const Span ins[14] = {{q, static_cast<size_t>((B - 1) * ldq + Hq * D) * 2},
+                        {pkc, pre * 64}, {pks, pre * 8}, {pvc, pre * 64}, {pvs, pre * 8},
+                        {kc, own * 64}, {ks, own * 8}, {vc, own * 64}, {vs, own * 8},
+                        {prefix_lens, static_cast<size_t>(P) * 4}, {groups, static_cast<size_t>(P + 1) * 4},
+                        {lens, static_cast<size_t>(B) * 4}, {gk, 4}, {gv, 4}};
+  nvfp4rl_status st = check_spans(outs, ins);
+  if (st != NVFP4RL_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  const PrefixAttnArgs a{q, ldq, pkc, pks, pvc, pvs, prefix_lens, groups, P, Lp, kc, ks, vc, vs, lens, Lmax, gk, gv,
+                         B, Hq, Hkv, scale, out, workspace};
+  return launch_prefix_attention(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status policy_loss(const float* logp, const float* logp_old, const float* logp_ref, const float* adv,
+                           int32_t adv_per_token, const float* weights, const uint8_t* mask, const int32_t* offsets,
+                           int64_t n, int64_t B, float eps_low, float eps_high, float dual_clip, float kl_coef,
+                           int32_t mode, float norm, float* loss, float* stats, float* coef, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  PolicyArgs a;
+  nvfp4rl_status st = check_policy(logp, logp_old, logp_ref, adv, adv_per_token, weights, mask, offsets, n, B, eps_low,
+                                   eps_high, dual_clip, kl_coef, &a);
+  if (st != NVFP4RL_OK) return st;
+  if (mode != NVFP4RL_LOSS_TOKEN_MEAN && mode != NVFP4RL_LOSS_SEQ_MEAN && mode != NVFP4RL_LOSS_SUM)
+    return NVFP4RL_ERR_INVALID_ARG;
+  if (mode == NVFP4RL_LOSS_SUM && (!(norm > 0.0f) || !std::isfinite(norm))) return NVFP4RL_ERR_INVALID_ARG;
+  if (!loss) return NVFP4RL_ERR_INVALID_ARG;
+  if (!aligned4({loss, stats, coef})) return NVFP4RL_ERR_MISALIGNED;
+  const size_t need = policy_workspace_bytes(n, B), nb = static_cast<size_t>(n) * 4, bb = static_cast<size_t>(B) * 4;
+  if (!workspace || workspace_bytes < need) return NVFP4RL_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return NVFP4RL_ERR_MISALIGNED;
+  const Span outs[4] = {{loss, 4}, {stats, 32}, {coef, bb}, {workspace, need}};
+  const Span ins[7] = {{logp, nb}, {logp_old, nb}, {logp_ref, nb}, {adv, adv_per_token ? nb : bb}, {weights, nb},
+                       {mask, static_cast<size_t>(n)}, {offsets, bb + 4}};
+  if ((st = check_spans(outs, ins)) != NVFP4RL_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  a.mode = mode;
+  a.norm = norm;
+  a.loss = loss;
+  a.stats = stats;
+  a.coef = coef;
+  a.ws = workspace;
+  return launch_policy_loss(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status policy_loss_backward(const float* logp, const float* logp_old, const float* logp_ref, const float* adv,
+                                    int32_t adv_per_token, const float* weights, const uint8_t* mask,
+                                    const int32_t* offsets, int64_t n, int64_t B, float eps_low, float eps_high,
+                                    float dual_clip, float kl_coef, const float* coef, const float* dloss, float* dlogp,
+                                    void* stream) {
+  PolicyArgs a;
+  nvfp4rl_status st = check_policy(logp, logp_old, logp_ref, adv, adv_per_token, weights, mask, offsets, n, B, eps_low,
+                                   eps_high, dual_clip, kl_coef, &a);
+  if (st != NVFP4RL_OK || n == 0) return st;
+  if ((!coef && B > 0) || !dlogp) return NVFP4RL_ERR_INVALID_ARG;
+  if (!aligned4({coef, dloss, dlogp})) return NVFP4RL_ERR_MISALIGNED;
+  const size_t nb = static_cast<size_t>(n) * 4, bb = static_cast<size_t>(B) * 4;
+  const Span outs[1] = {{dlogp, nb}};
+  const Span ins[9] = {{logp, nb}, {logp_old, nb}, {logp_ref, nb}, {adv, adv_per_token ? nb : bb}, {weights, nb},
+                       {mask, static_cast<size_t>(n)}, {offsets, bb + 4}, {coef, bb}, {dloss, 4}};
+  if ((st = check_spans(outs, ins)) != NVFP4RL_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  a.coef_in = coef;
+  a.dloss = dloss;
+  a.dlogp = dlogp;
+  return launch_policy_loss_grad(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status preference_loss(const float* logp, const float* logp_ref, const uint8_t* mask, const int32_t* offsets,
+                               int64_t n, int64_t pairs, float beta, float margin, float smoothing, int32_t mean,
+                               float* loss, float* rewards, float* coef, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (n < 0 || pairs < 0) return NVFP4RL_ERR_INVALID_ARG;
+  if (!(beta > 0.0f) || !std::isfinite(beta) || !std::isfinite(margin) || !(smoothing >= 0.0f && smoothing < 1.0f))
+    return NVFP4RL_ERR_INVALID_ARG;
+  if (n > 2147483647LL || pairs > (1LL << 30) - 1) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (pairs == 0) return NVFP4RL_OK;
+  if ((n > 0 && !logp) || !offsets || !loss) return NVFP4RL_ERR_INVALID_ARG;
+  if (!aligned4({logp, logp_ref, offsets, loss, rewards, coef})) return NVFP4RL_ERR_MISALIGNED;
+  const size_t need = preference_workspace_bytes(n, pairs), nb = static_cast<size_t>(n) * 4;
+  const size_t pb = static_cast<size_t>(pairs) * 4;
+  if (!workspace || workspace_bytes < need) return NVFP4RL_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return NVFP4RL_ERR_MISALIGNED;
+  const Span outs[4] = {{loss, pb}, {rewards, 2 * pb}, {coef, 2 * pb}, {workspace, need}};
+  const Span ins[4] = {{logp, nb}, {logp_ref, nb}, {mask, static_cast<size_t>(n)}, {offsets, 2 * pb + 4}};
+  nvfp4rl_status st = check_spans(outs, ins);
+  if (st != NVFP4RL_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  PreferenceArgs a{};
+  a.logp = logp;
+  a.logp_ref = logp_ref;
+  a.mask = mask;
+  a.offsets = offsets;
+  a.n = n;
+  a.pairs = pairs;
+  a.beta = beta;
+  a.margin = margin;
+  a.smoothing = smoothing;
+  a.mean = mean != 0;
+  a.loss = loss;
+  a.rewards = rewards;
+  a.coef = coef;
+  a.ws = workspace;
+  return launch_preference_loss(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4rl_status preference_loss_backward(const uint8_t* mask, const int32_t* offsets, int64_t n, int64_t pairs,
+                                        const float* coef, const float* dloss, float* dlogp, void* stream) {
+  if (n < 0 || pairs < 0) return NVFP4RL_ERR_INVALID_ARG;
+  if (n > 2147483647LL || pairs > (1LL << 30) - 1) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (n == 0) return NVFP4RL_OK;
+  if (!offsets || (!coef && pairs > 0) || !dlogp) return NVFP4RL_ERR_INVALID_ARG;
+  if (!aligned4({offsets, coef, dloss, dlogp})) return NVFP4RL_ERR_MISALIGNED;
+  const size_t pb = static_cast<size_t>(pairs) * 4;
+  const Span outs[1] = {{dlogp, static_cast<size_t>(n) * 4}};
+  const Span ins[4] = {{mask, static_cast<size_t>(n)}, {offsets, 2 * pb + 4}, {coef, 2 * pb}, {dloss, pb}};
+  nvfp4rl_status st = check_spans(outs, ins);
+  if (st != NVFP4RL_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4RL_OK) return st;
+  PreferenceArgs a{};
+  a.mask = mask;
+  a.offsets = offsets;
+  a.n = n;
+  a.pairs = pairs;
+  a.coef_in = coef;
+  a.dloss = dloss;
+  a.dlogp = dlogp;
+  return launch_preference_loss_grad(a, dev, static_cast<cudaStream_t>(stream));
+}
+
 nvfp4rl_status nvfp4_quantize_batch(int32_t count, const void* const* x, const int64_t* rows, const int64_t* cols,
                                     int32_t dtype, uint8_t* const* codes, uint8_t* const* scales, float* const* g,
                                     void* workspace, size_t workspace_bytes, void* stream) {
@@ -677,6 +964,14 @@ size_t nvfp4rl_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int3
     case NVFP4RL_OP_RMSNORM_QUANTIZE: return kQuantizeWorkspace;
     case NVFP4RL_OP_AIS: return ais_workspace_bytes();
     case NVFP4RL_OP_KV_ATTENTION: return N > 0 && K > 0 ? attention_workspace_bytes(M, N, K) : 0;
+    case NVFP4RL_OP_KV_PREFIX_ATTENTION:
+      return N > 0 && N <= 65535 && M <= 65535 && K <= 2147483647LL && r >= 1 && r <= 16 && num_groups >= 1
+                 ? prefix_attention_workspace_bytes(M, N, K, r, num_groups)
+                 : 0;
+    case NVFP4RL_OP_POLICY_LOSS:
+      return M <= 2147483647LL && N <= 2147483646LL ? policy_workspace_bytes(M, N) : 0;
+    case NVFP4RL_OP_PREFERENCE_LOSS:
+      return M <= 2147483647LL && N <= (1LL << 30) - 1 ? preference_workspace_bytes(M, N) : 0;
     case NVFP4RL_OP_LINEAR_W4A16: return linear_workspace_bytes(false, M, N, K, r, 1);
     case NVFP4RL_OP_LINEAR_W4A4: return linear_workspace_bytes(true, M, N, K, r, num_groups > 0 ? num_groups : 1);
     case NVFP4RL_OP_LINEAR_W4A4_QUANTIZED:

@@ -158,6 +158,25 @@ nvfp4rl_status launch_kv_attention(const uint16_t* q, const uint8_t* kc, const u
                                    int64_t B, int64_t Hq, int64_t Hkv, int64_t Lmax, float scale, uint16_t* out,
                                    void* workspace, const DeviceInfo& dev, cudaStream_t st);
 
+// Decode attention of sequences in groups that share a prefix cache each, beside their own caches (attention.cu).
+struct PrefixAttnArgs {
+  const uint16_t* q;
+  int64_t ldq;
+  const uint8_t *pkc, *pks, *pvc, *pvs;
+  const int32_t *prefix_lens, *groups;
+  int64_t P, Lp;
+  const uint8_t *kc, *ks, *vc, *vs;
+  const int32_t* lens;
+  int64_t Lmax;
+  const float *gk, *gv;
+  int64_t B, Hq, Hkv;
+  float scale;
+  uint16_t* out;
+  void* workspace;
+};
+size_t prefix_attention_workspace_bytes(int64_t B, int64_t Hkv, int64_t Lmax, int64_t heads, int64_t P);
+nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& a, const DeviceInfo& dev, cudaStream_t st);
+
 // AIS mixing coefficient and rectified weights of n tokens (ais.cu); workspace: a barrier counter
 // and one slot of partial sums per CTA (at most kAisMaxCtas CTAs).
 constexpr int kAisMaxCtas = 1024;

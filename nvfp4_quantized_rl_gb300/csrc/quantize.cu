@@ -25,6 +25,7 @@
 //   rmsnorm_quant_kernel  RMSNorm-AQN and the quantization of its output in one cooperative
 //                    kernel, the normalized rows kept in shared memory across a grid barrier.
 //   kv_append_kernel one decode step's K/V rows encoded at a given g into an NVFP4 KV cache.
+//   kv_append_ragged_kernel  the same for the packed rows of several sequences (prompts).
 //
 // Exactness without division per element: for an fp32 value a and a real P,
 //   a > P  <=>  a > RD(P)      a >= P  <=>  a >= RU(P)
@@ -38,6 +39,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "kv_ragged.cuh"
 #include "sm100.cuh"
 
 namespace nvfp4rl {
@@ -1259,6 +1261,41 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const uint16_t* __restri
   }
 }
 
+// Writes packed rows of several sequences (prompts, or chunks of them) to an NVFP4 KV cache: each 16-element block of
+// k and v ([T] rows of Hkv D elements, ldk and ldv apart) is encoded with the given g. A CTA takes eight packed
+// rows and looks up their cache rows once; a token's heads and blocks lie one after another in the row and in the cache
+// alike, so that a block's place needs no head index. Rows of no sequence or outside the cache are passed over.
+constexpr int kRaggedTile = 8;
+
+template <int kDtype>
+__global__ void __launch_bounds__(256) kv_append_ragged_kernel(const void* __restrict__ k, const void* __restrict__ v,
+                                                               int64_t ldk, int64_t ldv, uint32_t nb, RaggedArgs r,
+                                                               const float* __restrict__ gk, const float* __restrict__ gv,
+                                                               uint8_t* __restrict__ kc, uint8_t* __restrict__ ks,
+                                                               uint8_t* __restrict__ vc, uint8_t* __restrict__ vs) {
+  __shared__ int64_t rows[kRaggedTile];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRaggedTile;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(kRaggedTile), r.T - t0));
+  if (threadIdx.x < tokens) rows[threadIdx.x] = ragged_cache_row(r, t0 + threadIdx.x);
+  __syncthreads();
+  constexpr int kSize = kDtype == NVFP4RL_BF16 ? 2 : 4;
+  const uint32_t per = 2 * nb, total = tokens * per;
+  for (uint32_t i = threadIdx.x; i < total; i += 256) {
+    const uint32_t tok = i / per, u = i - tok * per;
+    const bool is_v = u >= nb;
+    const int64_t row = rows[tok], blk = is_v ? u - nb : u;
+    if (row < 0) continue;
+    const float g = is_v ? __ldg(gv) : __ldg(gk);
+    const float est_scale = g < 0x1p-60f ? 0x1p64f : 1.0f;  // as in quantize_kernel
+    BlockWords<kDtype> w;
+    load_block<kDtype>(static_cast<const uint8_t*>(is_v ? v : k) + (t0 + tok) * (is_v ? ldv : ldk) * kSize, blk, w);
+    encode_block<kDtype, kModePlain>(w, blk, g, est_scale, 6.0f * (g * est_scale), nullptr,
+                                     (is_v ? vc : kc) + row * nb * 8, (is_v ? vs : ks) + row * nb, nullptr, nullptr);
+  }
+}
+
 // Clears the amax accumulator word (a kernel rather than a memset, so that it chains with the
 // neighbouring kernels by programmatic dependent launch).
 __global__ void zero_word_kernel(uint32_t* __restrict__ p) {
@@ -1440,6 +1477,19 @@ nvfp4rl_status launch_kv_append(const uint16_t* k, const uint16_t* v, int64_t B,
   if (launch_pdl(kv_append_kernel, dim3(grid), dim3(256), 0, st, k, v, B, Hkv, D, pos, gk, gv, kc, ks, vc, vs, Lmax) !=
       cudaSuccess)
     return NVFP4RL_ERR_CUDA;
+  return launch_status();
+}
+
+nvfp4rl_status launch_kv_append_ragged(const void* k, const void* v, int dtype, int64_t ldk, int64_t ldv, int64_t Hkv,
+                                       int64_t D, const RaggedArgs& r, const float* gk, const float* gv, uint8_t* kc,
+                                       uint8_t* ks, uint8_t* vc, uint8_t* vs, const DeviceInfo&, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>((r.T + kRaggedTile - 1) / kRaggedTile));
+  const uint32_t nb = static_cast<uint32_t>(Hkv * D / 16);
+  const cudaError_t e =
+      dtype == NVFP4RL_BF16
+          ? launch_pdl(kv_append_ragged_kernel<NVFP4RL_BF16>, grid, dim3(256), 0, st, k, v, ldk, ldv, nb, r, gk, gv, kc, ks, vc, vs)
+          : launch_pdl(kv_append_ragged_kernel<NVFP4RL_F32>, grid, dim3(256), 0, st, k, v, ldk, ldv, nb, r, gk, gv, kc, ks, vc, vs);
+  if (e != cudaSuccess) return NVFP4RL_ERR_CUDA;
   return launch_status();
 }
 
