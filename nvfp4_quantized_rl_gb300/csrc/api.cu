@@ -677,7 +677,8 @@ nvfp4rl_status nvfp4_kv_prefix_attention(const uint16_t* q, int64_t ldq, const u
   if (D != 128 || Hq % Hkv != 0 || Hq / Hkv > 16 || B > 65535 || Hkv > 65535 || (B + P) * Hkv > 65535)
     return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
   const int64_t rows = 2147483647LL - 128;
-  if (Lp > rows || Lmax > rows || P * Lp > rows || B * Lmax > rows) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
+  if (Lp > rows || Lmax > rows || P * Lp > rows || B * Lmax > rows || !prefix_attention_fits(B, Hkv, Hq / Hkv, P, Lp))
+    return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
   if (ldq < Hq * D) return NVFP4RL_ERR_INVALID_ARG;
   if (ldq % 8 || ldq > (int64_t(1) << 40)) return NVFP4RL_ERR_UNSUPPORTED_SHAPE;
   if (B == 0) return NVFP4RL_OK;

@@ -47,7 +47,7 @@ constexpr int kScaleBytes = kTok * kHeadDim / 16;               // one head's sc
 constexpr int kSlotBytes = 2 * kCodeBytes + 2 * kScaleBytes;    // K codes | V codes | K scales | V scales
 constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
 constexpr int kAttnSmem = kRingBytes + 1024;                    // + room to align the ring to 1024 B
-constexpr int kPartFloats = 132;                                // per (span, head): max, sum, O[128], padding
+constexpr int kPartFloats = kOwnFloats;                         // per (span, head): max, sum, O[128], padding
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kSlotBytes % 1024 == 0 && kCodeBytes % 1024 == 0, "boxes start on 1024-byte boundaries");
 static_assert(kRingBytes >= kWarps * 16 * kHeadDim * 4, "the ring doubles as the merge area");
@@ -163,8 +163,7 @@ __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.
 // What a CTA of kv_attention_kernel attends for.
 enum : int {
   kDecode = 0,  // the heads of one sequence over its own cache, the whole of the attention
-  kOwn = 1,     // the same beside a shared prefix: always a partial result
-  kPrefix = 2,  // 16 (sequence, head) rows of a group of sequences over the prefix that they share: partial
+  kOwn = 1,     // the same beside a shared prefix (prefix_attention.cu): always a partial result
 };
 
 struct AttnArgs {
@@ -178,56 +177,8 @@ struct AttnArgs {
   uint16_t* out;     // used when nsplit == 1
   float* part;       // [B*Hkv][nsplit][16][kPartFloats] when nsplit > 1
   uint32_t* status;  // the library's error word: a wait that gave up sets a timeout bit
-  // kOwn and kPrefix (whose caches, lens and Lmax are the prefixes'):
-  int64_t ldq;            // elements between two sequences' queries
-  const int32_t* groups;  // [P + 1]: sequences [groups[p], groups[p + 1]) share prefix p
-  int64_t P, B;
+  int64_t ldq = 0;  // kOwn: elements between two sequences' queries
 };
-
-constexpr int kTileRows = 16;  // rows of a prefix tile
-
-// A prefix group: its sequences [first, first + members) and the number of row tiles before its own.
-struct PrefixGroup {
-  int64_t p, first, members, tile0;
-};
-
-// The group that holds `want`, a sequence (kByTile false) or a row tile; p = -1 without one. Whole warp. Groups
-// are clamped to the B sequences, so that any offsets give rows within the batch.
-template <bool kByTile>
-__device__ __forceinline__ PrefixGroup find_group(const int32_t* __restrict__ groups, int64_t P, int64_t B, int64_t heads,
-                                                  int rows, int64_t want) {
-  const int lane = threadIdx.x & 31;
-  int64_t before = 0;
-  for (int64_t p0 = 0; p0 < P; p0 += 32) {
-    int64_t lo = 0, n = 0;
-    if (p0 + lane < P) {
-      lo = min(max(static_cast<int64_t>(__ldg(groups + p0 + lane)), int64_t(0)), B);
-      n = max(min(static_cast<int64_t>(__ldg(groups + p0 + lane + 1)), B) - lo, int64_t(0));
-    }
-    const int64_t tiles = (n * heads + rows - 1) / rows;
-    int64_t upto = tiles;  // tiles up to and with this lane's
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const int64_t tile0 = before + upto - tiles;
-    const bool here = kByTile ? want >= tile0 && want < tile0 + tiles : want >= lo && want < lo + n;
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, here);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      return {p0 + l, __shfl_sync(0xFFFFFFFFu, lo, l), __shfl_sync(0xFFFFFFFFu, n, l), __shfl_sync(0xFFFFFFFFu, tile0, l)};
-    }
-    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
-  }
-  return {-1, 0, 0, 0};
-}
-
-// Partial results are taken over equal spans of the actual length, not of the cache: tokens per span (a multiple of
-// kTok) of `len` tokens in `nsplit` spans.
-__device__ __forceinline__ int64_t even_span(int64_t len, int nsplit) {
-  return ((len + kTok - 1) / kTok + nsplit - 1) / nsplit * kTok;
-}
 
 // kNH: 8-column tiles of query heads (1: up to 8 heads per KV head, 2: up to 16).
 template <int kNH, int kKind>
@@ -248,26 +199,16 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
     fence_barrier_init();
   }
   __syncwarp();
-  const int64_t bh = blockIdx.y, kvh = bh % a.Hkv;
+  const int64_t bh = blockIdx.y, b = bh / a.Hkv, kvh = bh % a.Hkv;
   const int group = static_cast<int>(a.Hq / a.Hkv);
   griddep_wait();
   griddep_launch_dependents();
-  int64_t b = bh / a.Hkv;                // the cache
-  int nrows = group;                     // query rows
-  int64_t first_row = 0, first_seq = b;  // kPrefix: the first row's place in its group, the group's first sequence
-  if constexpr (kKind == kPrefix) {
-    const PrefixGroup pg = find_group<true>(a.groups, a.P, a.B, group, kTileRows, b);
-    if (pg.p < 0) return;  // fewer tiles than the largest number
-    first_row = (b - pg.tile0) * kTileRows;
-    nrows = static_cast<int>(min(pg.members * group - first_row, static_cast<int64_t>(kTileRows)));
-    first_seq = pg.first;
-    b = pg.p;
-  }
   const int64_t len = min(max(static_cast<int64_t>(a.lens[b]), int64_t(0)), a.Lmax);
-  const int64_t span = kKind == kDecode ? a.span : even_span(len, a.nsplit);
+  // a partial result is of an equal span of the actual length, not of the cache
+  const int64_t span = kKind == kDecode ? a.span : own_span(len, a.nsplit);
   const int64_t t_begin = static_cast<int64_t>(blockIdx.x) * span;
   const int64_t t_end = min(t_begin + span, len);
-  if (kKind != kDecode && t_begin >= len) return;  // the merge leaves empty spans out
+  if (kKind == kOwn && t_begin >= len) return;  // empty spans are left out of the join
   const int ngroups = t_end > t_begin ? static_cast<int>((t_end - t_begin + kTok - 1) / kTok) : 0;
   const int mine = ngroups > warp ? (ngroups - warp + kWarps - 1) / kWarps : 0;  // groups warp, warp + 4, ...
   const int64_t row0 = b * a.Lmax;  // cache row of the sequence's token 0
@@ -310,12 +251,8 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
 #pragma unroll
   for (int h = 0; h < kNH; ++h) {
     const int hh = 8 * h + g;
-    if (hh < nrows) {
-      int64_t at = (b * a.Hq + kvh * group + hh) * kHeadDim;
-      if constexpr (kKind != kDecode) {
-        const int64_t r = first_row + hh;
-        at = (first_seq + r / group) * a.ldq + (kvh * group + r % group) * kHeadDim;
-      }
+    if (hh < group) {
+      const int64_t at = kKind == kDecode ? (b * a.Hq + kvh * group + hh) * kHeadDim : b * a.ldq + (kvh * group + hh) * kHeadDim;
       const uint4* src = reinterpret_cast<const uint4*>(a.q + at + 32 * q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -552,7 +489,7 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
             make_float2(oacc[m][h][e], oacc[m][h][2 + e]);
   __syncthreads();
   const float gv = __ldg(a.gv);
-  for (int i = threadIdx.x; i < nrows * kHeadDim; i += kAttnThreads) {
+  for (int i = threadIdx.x; i < group * kHeadDim; i += kAttnThreads) {
     const int r = i / kHeadDim, d = i % kHeadDim;
     float M = -INFINITY;
 #pragma unroll
@@ -612,129 +549,7 @@ __global__ void __launch_bounds__(128) kv_attention_merge_kernel(const float* __
   *reinterpret_cast<uint2*>(out + row * kHeadDim + 4 * lane) = packed;
 }
 
-// Joins the partial results of every (sequence, query head) over its group's prefix and over its own cache, as
-// kv_attention_merge_kernel does; one warp per row, four dims per lane. A row whose caches are both empty is 0.
-struct JoinArgs {
-  const float *pre, *own;  // partials
-  const int32_t *groups, *prefix_lens, *lens;
-  int64_t P, Lp, Lmax, B, Hq, Hkv, tiles;
-  int npre, nown;
-  const float* gv;
-  uint16_t* out;
-};
-
-__global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= a.B * a.Hq) return;
-  const int64_t b = row / a.Hq, h = row % a.Hq, group = a.Hq / a.Hkv, kvh = h / group, r = h % group;
-  float M = -INFINITY, L = 0.0f, O[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const auto add = [&](const float* base, int64_t len, int nsplit) {
-    const int64_t span = even_span(len, nsplit), used = len > 0 ? (len + span - 1) / span : 0;
-    for (int64_t s = 0; s < used; ++s) {
-      const float* pr = base + s * kTileRows * kPartFloats;
-      const float m = fmaxf(M, pr[0]);
-      if (m == -INFINITY) continue;
-      const float keep = exp2f(M - m), f = exp2f(pr[0] - m);
-      const float4 v = *reinterpret_cast<const float4*>(pr + 4 + 4 * lane);
-      L = L * keep + f * pr[1];
-      O[0] = O[0] * keep + f * v.x;
-      O[1] = O[1] * keep + f * v.y;
-      O[2] = O[2] * keep + f * v.z;
-      O[3] = O[3] * keep + f * v.w;
-      M = m;
-    }
-  };
-  const PrefixGroup pg = find_group<false>(a.groups, a.P, a.B, group, kTileRows, b);
-  if (pg.p >= 0) {
-    const int64_t at = (b - pg.first) * group + r, tile = pg.tile0 + at / kTileRows;
-    if (tile < a.tiles)
-      add(a.pre + ((tile * a.Hkv + kvh) * a.npre * kTileRows + at % kTileRows) * kPartFloats,
-          min(max(static_cast<int64_t>(a.prefix_lens[pg.p]), int64_t(0)), a.Lp), a.npre);
-  }
-  if (a.own)
-    add(a.own + ((b * a.Hkv + kvh) * a.nown * kTileRows + r) * kPartFloats,
-        min(max(static_cast<int64_t>(a.lens[b]), int64_t(0)), a.Lmax), a.nown);
-  const float inv = L > 0.0f ? __ldg(a.gv) / L : 0.0f;
-  uint2 packed;
-  packed.x = f32_to_bf16_bits(O[0] * inv) | (f32_to_bf16_bits(O[1] * inv) << 16);
-  packed.y = f32_to_bf16_bits(O[2] * inv) | (f32_to_bf16_bits(O[3] * inv) << 16);
-  *reinterpret_cast<uint2*>(a.out + row * kHeadDim + 4 * lane) = packed;
-}
-
-// Row tiles of P groups of B sequences, at most.
-int64_t prefix_tiles(int64_t B, int64_t heads, int64_t P) { return P + B * heads / kTileRows; }
-int prefix_splits(int64_t tiles, int64_t Hkv) {
-  return static_cast<int>(std::max<int64_t>(1, (2 * kNumSMsHint + tiles * Hkv - 1) / (tiles * Hkv)));
-}
-
 }  // namespace
-
-size_t prefix_attention_workspace_bytes(int64_t B, int64_t Hkv, int64_t Lmax, int64_t heads, int64_t P) {
-  const int64_t tiles = prefix_tiles(B, heads, P);
-  const int64_t own = B > 0 && Lmax > 0 ? B * Hkv * attention_splits(B, Hkv, Lmax) : 0;
-  return static_cast<size_t>(tiles * Hkv * prefix_splits(tiles, Hkv) + own) * kTileRows * kPartFloats * sizeof(float);
-}
-
-namespace {
-
-// Code rows as a [rows][Hkv 64] byte array; a box is one head's 64-byte rows of 64 tokens.
-bool code_map(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t Hkv) {
-  return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, static_cast<uint64_t>(Hkv) * 64,
-                            static_cast<uint64_t>(rows), 1, 64, kTok, CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
-// The kernel's dynamic shared memory limit, raised once per device.
-template <class K>
-bool allow_smem(K kernel, int device) {
-  static std::mutex mu;
-  static std::map<std::pair<const void*, int>, bool> set;
-  std::lock_guard<std::mutex> lock(mu);
-  bool& done = set[{reinterpret_cast<const void*>(kernel), device}];
-  if (!done) done = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) == cudaSuccess;
-  return done;
-}
-
-template <int kKind>
-nvfp4rl_status launch_partials(bool wide, dim3 grid, const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a,
-                               int device, cudaStream_t st) {
-  const auto kernel = wide ? kv_attention_kernel<2, kKind> : kv_attention_kernel<1, kKind>;
-  if (!allow_smem(kernel, device)) return NVFP4RL_ERR_CUDA;
-  if (launch_pdl(kernel, grid, dim3(kAttnThreads), kAttnSmem, st, mk, mv, a) != cudaSuccess) return NVFP4RL_ERR_CUDA;
-  return launch_status();
-}
-
-}  // namespace
-
-nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo& dev, cudaStream_t st) {
-  const int64_t heads = p.Hq / p.Hkv, tiles = prefix_tiles(p.B, heads, p.P);
-  const int npre = prefix_splits(tiles, p.Hkv), nown = p.Lmax > 0 ? attention_splits(p.B, p.Hkv, p.Lmax) : 0;
-  float* pre = static_cast<float*>(p.workspace);
-  float* own = p.Lmax > 0 ? pre + tiles * p.Hkv * npre * kTileRows * kPartFloats : nullptr;
-  CUtensorMap mk, mv;
-  if (!code_map(&mk, p.pkc, p.P * p.Lp, p.Hkv) || !code_map(&mv, p.pvc, p.P * p.Lp, p.Hkv)) return NVFP4RL_ERR_CUDA;
-  AttnArgs a{p.q, p.pks, p.pvs, p.gk, p.gv, p.prefix_lens, p.Hq, p.Hkv, p.Lp, npre, 0, p.scale, nullptr, pre, dev.status,
-             p.ldq, p.groups, p.P, p.B};
-  nvfp4rl_status s = launch_partials<kPrefix>(true, dim3(static_cast<unsigned>(npre), static_cast<unsigned>(tiles * p.Hkv)),
-                                              mk, mv, a, dev.device, st);
-  if (s != NVFP4RL_OK) return s;
-  if (own) {
-    if (!code_map(&mk, p.kc, p.B * p.Lmax, p.Hkv) || !code_map(&mv, p.vc, p.B * p.Lmax, p.Hkv)) return NVFP4RL_ERR_CUDA;
-    AttnArgs o{p.q, p.ks, p.vs, p.gk, p.gv, p.lens, p.Hq, p.Hkv, p.Lmax, nown, 0, p.scale, nullptr, own, dev.status,
-               p.ldq, nullptr, 0, p.B};
-    s = launch_partials<kOwn>(heads > 8, dim3(static_cast<unsigned>(nown), static_cast<unsigned>(p.B * p.Hkv)), mk, mv, o,
-                              dev.device, st);
-    if (s != NVFP4RL_OK) return s;
-  }
-  const JoinArgs j{pre, own, p.groups, p.prefix_lens, p.lens, p.P, p.Lp, p.Lmax, p.B, p.Hq, p.Hkv, tiles, npre, nown,
-                   p.gv, p.out};
-  if (launch_pdl(kv_prefix_join_kernel, dim3(static_cast<unsigned>((p.B * p.Hq + 3) / 4)), dim3(128), 0, st, j) !=
-      cudaSuccess)
-    return NVFP4RL_ERR_CUDA;
-  return launch_status();
-}
 
 int attention_splits(int64_t B, int64_t Hkv, int64_t Lmax) {
   const int64_t chunks = std::max<int64_t>(1, (Lmax + kTok - 1) / kTok);
@@ -747,6 +562,52 @@ size_t attention_workspace_bytes(int64_t B, int64_t Hkv, int64_t Lmax) {
   return ns == 1 ? 0 : static_cast<size_t>(B * Hkv) * ns * 16 * kPartFloats * sizeof(float);
 }
 
+namespace {
+
+// Code rows as a [rows][Hkv 64] byte array; a box is one head's 64-byte rows of 64 tokens.
+bool code_map(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t Hkv) {
+  return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, static_cast<uint64_t>(Hkv) * 64,
+                            static_cast<uint64_t>(rows), 1, 64, kTok, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// The kernels' dynamic shared memory limit, raised once per device.
+bool allow_smem(int device) {
+  static std::mutex mu;
+  static std::map<int, bool> set;
+  std::lock_guard<std::mutex> lock(mu);
+  bool& done = set[device];
+  const auto raise = [](auto* k) {
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) == cudaSuccess;
+  };
+  if (!done)
+    done = raise(kv_attention_kernel<1, kDecode>) && raise(kv_attention_kernel<2, kDecode>) &&
+           raise(kv_attention_kernel<1, kOwn>) && raise(kv_attention_kernel<2, kOwn>);
+  return done;
+}
+
+}  // namespace
+
+size_t own_partials_bytes(int64_t B, int64_t Hkv, int64_t Lmax) {
+  if (B == 0 || Lmax == 0) return 0;
+  return static_cast<size_t>(B * Hkv) * attention_splits(B, Hkv, Lmax) * kOwnRows * kOwnFloats * sizeof(float);
+}
+
+// The decode kernel over the sequences' own caches beside shared prefixes, for launch_prefix_attention.
+nvfp4rl_status launch_own_partials(const PrefixAttnArgs& p, float* part, OwnPartials* out, const DeviceInfo& dev,
+                                   cudaStream_t st) {
+  const int ns = attention_splits(p.B, p.Hkv, p.Lmax);
+  *out = {part, ns};
+  CUtensorMap mk, mv;
+  if (!code_map(&mk, p.kc, p.B * p.Lmax, p.Hkv) || !code_map(&mv, p.vc, p.B * p.Lmax, p.Hkv)) return NVFP4RL_ERR_CUDA;
+  const AttnArgs a{p.q, p.ks, p.vs, p.gk, p.gv, p.lens, p.Hq, p.Hkv, p.Lmax, ns, 0, p.scale, nullptr, part, dev.status, p.ldq};
+  const auto kernel = p.Hq / p.Hkv > 8 ? kv_attention_kernel<2, kOwn> : kv_attention_kernel<1, kOwn>;
+  if (!allow_smem(dev.device)) return NVFP4RL_ERR_CUDA;
+  if (launch_pdl(kernel, dim3(static_cast<unsigned>(ns), static_cast<unsigned>(p.B * p.Hkv)), dim3(kAttnThreads), kAttnSmem,
+                 st, mk, mv, a) != cudaSuccess)
+    return NVFP4RL_ERR_CUDA;
+  return launch_status();
+}
+
 nvfp4rl_status launch_kv_attention(const uint16_t* q, const uint8_t* kc, const uint8_t* ks, const float* gk,
                                    const uint8_t* vc, const uint8_t* vs, const float* gv, const int32_t* lens,
                                    int64_t B, int64_t Hq, int64_t Hkv, int64_t Lmax, float scale, uint16_t* out,
@@ -757,29 +618,12 @@ nvfp4rl_status launch_kv_attention(const uint16_t* q, const uint8_t* kc, const u
   const int ns = attention_splits(B, Hkv, Lmax);
   const int64_t chunks = (Lmax + kTok - 1) / kTok;
   const int span = static_cast<int>((chunks + ns - 1) / ns) * kTok;
-  // code rows as a [B Lmax][Hkv 64] byte array; a box is one head's 64-byte rows of 64 tokens
   CUtensorMap mk, mv;
-  if (!make_tensor_map_2d(&mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, kc, static_cast<uint64_t>(Hkv) * 64,
-                          static_cast<uint64_t>(B * Lmax), 1, 64, kTok, CU_TENSOR_MAP_SWIZZLE_64B) ||
-      !make_tensor_map_2d(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, vc, static_cast<uint64_t>(Hkv) * 64,
-                          static_cast<uint64_t>(B * Lmax), 1, 64, kTok, CU_TENSOR_MAP_SWIZZLE_64B))
-    return NVFP4RL_ERR_CUDA;
+  if (!code_map(&mk, kc, B * Lmax, Hkv) || !code_map(&mv, vc, B * Lmax, Hkv)) return NVFP4RL_ERR_CUDA;
   AttnArgs a{q, ks, vs, gk, gv, lens, Hq, Hkv, Lmax, ns, span, scale, out, static_cast<float*>(workspace),
              dev.status};
   const bool wide = Hq / Hkv > 8;
-  {
-    static std::mutex mu;
-    static std::map<int, bool> set;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!set[dev.device]) {
-      if (cudaFuncSetAttribute(kv_attention_kernel<1, kDecode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) !=
-              cudaSuccess ||
-          cudaFuncSetAttribute(kv_attention_kernel<2, kDecode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) !=
-              cudaSuccess)
-        return NVFP4RL_ERR_CUDA;
-      set[dev.device] = true;
-    }
-  }
+  if (!allow_smem(dev.device)) return NVFP4RL_ERR_CUDA;
   const dim3 grid(static_cast<unsigned>(ns), static_cast<unsigned>(B * Hkv));
   const cudaError_t e = wide ? launch_pdl(kv_attention_kernel<2, kDecode>, grid, dim3(kAttnThreads), kAttnSmem, st, mk, mv, a)
                              : launch_pdl(kv_attention_kernel<1, kDecode>, grid, dim3(kAttnThreads), kAttnSmem, st, mk, mv, a);

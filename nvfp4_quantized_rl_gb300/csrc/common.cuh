@@ -158,7 +158,8 @@ nvfp4rl_status launch_kv_attention(const uint16_t* q, const uint8_t* kc, const u
                                    int64_t B, int64_t Hq, int64_t Hkv, int64_t Lmax, float scale, uint16_t* out,
                                    void* workspace, const DeviceInfo& dev, cudaStream_t st);
 
-// Decode attention of sequences in groups that share a prefix cache each, beside their own caches (attention.cu).
+// Decode attention of sequences in groups that share a prefix cache each, beside their own caches
+// (prefix_attention.cu; the own caches by the decode kernel of attention.cu).
 struct PrefixAttnArgs {
   const uint16_t* q;
   int64_t ldq;
@@ -174,6 +175,22 @@ struct PrefixAttnArgs {
   uint16_t* out;
   void* workspace;
 };
+// Partial results of the decode kernel over own caches: [sequence, KV head][nsplit][kOwnRows][kOwnFloats] fp32, a row's
+// maximum (log2 units), sum, and O from float 4 on. The spans are equal parts of a sequence's length, multiples of 64
+// tokens; empty ones are not written.
+constexpr int kOwnRows = 16, kOwnFloats = 132;
+__host__ __device__ inline int64_t own_span(int64_t len, int nsplit) { return ((len + 63) / 64 + nsplit - 1) / nsplit * 64; }
+struct OwnPartials {
+  const float* part;
+  int nsplit;
+  __host__ __device__ int64_t spans(int64_t len) const {
+    return len > 0 ? (len + own_span(len, nsplit) - 1) / own_span(len, nsplit) : 0;
+  }
+};
+size_t own_partials_bytes(int64_t B, int64_t Hkv, int64_t Lmax);
+nvfp4rl_status launch_own_partials(const PrefixAttnArgs& p, float* part, OwnPartials* out, const DeviceInfo& dev,
+                                   cudaStream_t st);
+bool prefix_attention_fits(int64_t B, int64_t Hkv, int64_t heads, int64_t P, int64_t Lp);
 size_t prefix_attention_workspace_bytes(int64_t B, int64_t Hkv, int64_t Lmax, int64_t heads, int64_t P);
 nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& a, const DeviceInfo& dev, cudaStream_t st);
 
