@@ -11,15 +11,19 @@
 // so that one long prefix keeps every SM busy. A stretch is one segment per tile; CTA c's segment in tile t leaves its
 // partial in slot c + t (both only grow along the stretch).
 // Per block, in a pipeline of warps:
-//   - a copy warp brings the K and V code rows (TMA, 64-byte swizzle) and scale rows (8-byte cp.async, zeros behind the
-//     prefix's end, which makes those tokens' values zero) into a ring;
 //   - four warps decode K and four V: one thread to a token row, 128 codes to f16 (exact: code x scale has at most
-//     six significant bits), stored in the 128-byte swizzle of the MMA operands;
-//   - one warp issues S = Q K^T (tcgen05, f16, 128 x 128 x 128) and O += P V, V as it lies ([token][dim]: MN-major);
-//   - two groups of four warps take every second block each, with a maximum, a sum and an accumulator of their own, so that one
-//     group's exponentials run under the other's products. A thread owns a row: the maximum of its 128 scores, then
-//     p = 2^(s - ref), P in f16 over S's own TMEM columns. ref only moves when the maximum has grown by more than
-//     2^8; p is scaled by 2^6, so that f16 keeps 2^-30 of the largest, and stays below 2^14.
+//     six significant bits), stored in the 128-byte swizzle of the MMA operands. Each warp copies its own 32 rows into a ring
+//     of its own (cp.async, three blocks ahead; zeros behind the prefix's end, which makes those tokens' values zero),
+//     four lanes to a row of 64 bytes. Tensor copies of 64-byte rows were the pipeline's limit: 2200 clocks a block;
+//   - one warp issues S = Q K^T (tcgen05, f16, 128 x 128 x 128) and one O += P V, V as it lies ([token][dim]: MN-major): one
+//     warp for both spent as long on its waits as the tensor cores on the products;
+//   - two groups of four warps take every second block each, so that one group's exponentials run under the other's and under
+//     the products. A thread owns a row: the maximum of its 128 scores, then p = 2^(s - ref), P in f16 over S's own TMEM
+//     columns. ref only moves when the maximum has grown by more than 2^8 (then O is scaled, once the products so far
+//     are complete); a row's two threads hand it on from block to block. p is scaled by 2^6, so that f16 keeps 2^-30 of the
+//     largest, and stays below 2^14.
+//   TMEM: three S / P buffers and O, so that the scores of block n + 2 can follow the values of block n - 1 and are there
+//   when the softmax of block n ends.
 // Q enters as f16 scaled per row by a power of two that puts its largest element in [2^14, 2^15): exact down to 2^-31 of it.
 #include <climits>
 #include <map>
@@ -37,31 +41,34 @@ using namespace sm100;
 constexpr int kDim = 128;
 constexpr int kBlock = 128;  // tokens
 constexpr int kRows = 128;   // rows of a tile
-constexpr int kStages = 3;   // blocks of codes in flight
-constexpr int kCodeBytes = kBlock * kDim / 2, kScaleBytes = kBlock * kDim / 16;
-constexpr int kStageBytes = 2 * kCodeBytes + 2 * kScaleBytes;
+constexpr int kStages = 3;   // blocks of codes in a decoding warp's ring
+constexpr int kWarpRows = 32, kCodeRow = kDim / 2, kScaleRow = kDim / 16;        // what a decoding warp copies
+constexpr int kSlotBytes = kWarpRows * (kCodeRow + kScaleRow);                   // its code rows, then its scale rows
 constexpr int kTileBytes = kBlock * kDim * 2;  // an f16 operand: two panels of 64 columns, 128 bytes to a row
 constexpr int kPanel = kTileBytes / 2;
-constexpr int kSmemBytes = kTileBytes /*Q*/ + 4 * kTileBytes /*K, V twice*/ + kStages * kStageBytes + 1024 /*alignment*/;
-// warps: 0-3 and 4-7 softmax (every second block each), 8-11 decode K, 12-15 decode V, 16 MMA, 17 copies, 18 segments,
-// one idle that fills the warpgroup
-constexpr int kMmaWarp = 16, kCopyWarp = 17, kWalkWarp = 18, kThreads = 20 * 32;
-constexpr int kSegments = 4, kSegmentReaders = 18;  // a ring of segments, read by warps 0-17
+constexpr int kSmemBytes = kTileBytes /*Q*/ + 4 * kTileBytes /*K, V twice*/ + 8 * kStages * kSlotBytes + 1024 /*alignment*/;
+// warps: 0-3 and 4-7 softmax (every second block each), 8-11 decode K, 12-15 decode V, 16 scores, 17 values, 18 segments, one
+// idle that fills the warpgroup
+constexpr int kScoreWarp = 16, kValueWarp = 17, kWalkWarp = 18, kThreads = 20 * 32;
+constexpr int kSegments = 8, kSegmentReaders = 18;  // a ring of segments, read by warps 0-17
 // Registers by warpgroup, out of the 96 that each of the 640 threads starts with.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kDecodeRegs = 72, kOtherRegs = 64;
 static_assert(2 * kSoftmaxRegs + 2 * kDecodeRegs + kOtherRegs <= 5 * kLaunchRegs, "within the launch's registers");
-constexpr uint32_t kScol = 0, kOcol = 256, kTmemCols = 512;  // S of even and odd blocks, then O
+constexpr uint32_t kOcol = 384, kTmemCols = 512;  // S / P of blocks n % 3 from column 128 (n % 3) on, then O
 constexpr float kSlack = 8.0f, kLift = 6.0f;                 // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kSmemBytes <= 227 * 1024 - 2048, "fits one CTA's shared memory beside the static part");
 
 struct Bars {
-  uint64_t code_full[kStages], code_empty[kStages];
-  uint64_t k_full[2], v_full[2], p_full[2];
-  uint64_t s_done[2];   // S of a block is there, and its K operand free
-  uint64_t pv_done[2];  // a block is in O, and its V operand and S columns free
+  uint64_t k_full[2], v_full[2];  // by n & 1, as the operands
+  // by n % 3, as the S / P buffers. A barrier that two blocks' phases could pass before a waiter looks would be misread; here
+  // block n + 3 needs the values of block n in O, and those the scores and P of block n.
+  uint64_t s_done[3];   // the scores are there, and the K operand free
+  uint64_t p_full[3];
+  uint64_t pv_done[3];  // the block is in O, and its V operand and P free
+  uint64_t ref_done[4][2];        // by quarter of the rows and n & 1: the rows' references of block n stand
   uint64_t seg_full[kSegments], seg_empty[kSegments];
-  uint64_t q_full, stat_full, o_free, drain;
+  uint64_t q_full, stat_full, o_full, o_free, drain[2];
 };
 
 // A group of sequences as the tiles see it.
@@ -230,7 +237,7 @@ __device__ __forceinline__ int64_t part_at(int64_t slot, int four, int row) { re
 struct PrefixArgs {
   const uint16_t* q;
   int64_t ldq;
-  const uint8_t *ks, *vs;
+  const uint8_t *kc, *ks, *vc, *vs;
   const float* gk;
   Groups groups;
   int heads;
@@ -293,12 +300,17 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+// 8 or 16 bytes, or as many zeros.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8u : 0u) : "memory");
 }
-// One arrival on the mbarrier once every cp.async that this thread issued before has landed (counted in its expected number).
-__device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 template <int kRegs>
@@ -359,14 +371,18 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
   return d;
 }
 
-// One token row: 128 codes at `codes` (row r of a box stored with the 64-byte swizzle) and 8 scale bytes to f16 in the
-// 128-byte swizzle of an MMA operand.
-__device__ __forceinline__ void decode_row(uint32_t codes, uint32_t scales, uint32_t out, int r) {
-  const uint2 s = lds64(scales + 8 * r);
+// The 16-byte unit u of a ring's code row i lies at code_unit: eight rows' units of one number are in eight different
+// banks groups then, for the thread that reads a row and for the four that copy it.
+__device__ __forceinline__ uint32_t code_unit(int i, int u) { return kCodeRow * i + ((u ^ ((i >> 1) & 3)) << 4); }
+
+// One token row, row i of the warp's slot and row r of the block: 128 codes and 8 scale bytes to f16 in the 128-byte swizzle of
+// an MMA operand.
+__device__ __forceinline__ void decode_row(uint32_t slot, uint32_t out, int i, int r) {
+  const uint2 s = lds64(slot + kWarpRows * kCodeRow + kScaleRow * i);
   const uint32_t row = out + 128 * r, sw = r & 7;
   uint4 c[4];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) c[u] = lds128(codes + 64 * r + ((u ^ ((r >> 1) & 3)) << 4));
+  for (int u = 0; u < 4; ++u) c[u] = lds128(slot + code_unit(i, u));
 #pragma unroll
   for (int u = 0; u < 4; ++u) {  // 32 codes: two scale blocks
     const uint32_t two = e4m3x2_f16((u < 2 ? s.x : s.y) >> (16 * (u & 1)));
@@ -381,27 +397,25 @@ __device__ __forceinline__ void decode_row(uint32_t codes, uint32_t scales, uint
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                            const PrefixArgs a) {
+    prefix_attention_kernel(const PrefixArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars bars;
   __shared__ uint32_t tmem_slot;
-  __shared__ float row_scale[kRows];
+  __shared__ float row_scale[kRows], row_ref[kRows];
   __shared__ Segment segs[kSegments];
   __shared__ float2 stat[2][2][kRows];  // by the parity of the segment
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t qs = base, kvs = base + kTileBytes, ring = kvs + 4 * kTileBytes;  // K 0, K 1, V 0, V 1
   const auto bar = [&](uint64_t& b) { return smem_addr(&b); };
-  if (warp == kMmaWarp) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
+  if (warp == kScoreWarp) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(bars.code_full[i]), 33);  // the copy warp's expect_tx and 32 cp.async arrivals
-      mbar_init(bar(bars.code_empty[i]), 8);
-    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(bars.k_full[i]), 4);
       mbar_init(bar(bars.v_full[i]), 4);
+      for (int q = 0; q < 4; ++q) mbar_init(bar(bars.ref_done[q][i]), 1);
+    }
+    for (int i = 0; i < 3; ++i) {
       mbar_init(bar(bars.s_done[i]), 1);
       mbar_init(bar(bars.p_full[i]), 4);
       mbar_init(bar(bars.pv_done[i]), 1);
@@ -412,8 +426,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(bars.q_full), 4);
     mbar_init(bar(bars.stat_full), 8);
+    mbar_init(bar(bars.o_full), 1);
     mbar_init(bar(bars.o_free), 8);
-    mbar_init(bar(bars.drain), 1);
+    mbar_init(bar(bars.drain[0]), 1);
+    mbar_init(bar(bars.drain[1]), 1);
     fence_barrier_init();
   }
   griddep_wait();
@@ -442,11 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     more_registers<kSoftmaxRegs>();
     const int x = warp >> 2, r = threadIdx.x & (kRows - 1);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t scol = tmem + lanes + kScol + 128 * x, ocol = tmem + lanes + kOcol + 128 * x;
+    const uint32_t ocol = tmem + lanes + kOcol;
     const float gk = __ldg(a.gk);
     const int member = r / a.heads, head = r - member * a.heads;
     uint32_t n0 = 0, n_q = 0;  // blocks before this segment; segments
-    uint32_t n_x = 0;          // blocks of this group
     uint4 qv[16];              // the next segment's row of Q, loaded ahead of the last one's end
     const auto load_q = [&](const Segment& t) {
       const bool there = member < t.members;
@@ -495,10 +510,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tokens = s.len - s.block0 * kBlock;  // to the prefix's end
       const bool work = (warp & 3) * 32 < rows;  // a warp of rows that do not exist only keeps the pace
       const int j0 = (n0 & 1) == static_cast<uint32_t>(x) ? 0 : 1;
-      float ref = -INFINITY;
+      float ref = -INFINITY;  // the reference of this thread's sum
       F2 sum = pack2(0.0f, 0.0f);
       for (int j = j0; j < s.blocks; j += 2) {
-        ok = wait(bars.s_done[x], n_x & 1, kStatusTimeoutEpilogue);
+        const uint32_t n = n0 + j, third = n / 3, buf = n - 3 * third;
+        const uint32_t scol = tmem + lanes + 128 * buf;
+        ok = wait(bars.s_done[buf], third & 1, kStatusTimeoutEpilogue);
         if (!ok) break;
         tc_fence_after();
         if (work) {
@@ -530,14 +547,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) m[i & 3] = max3(m[i & 3], __uint_as_float(v[i]), __uint_as_float(w[i]));
           }
           const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * sl2;
-          const bool grew = top > ref + kSlack;  // also the first block: ref is -inf
-          if (__any_sync(0xFFFFFFFFu, grew)) {
-            const float now = grew ? top : ref;
-            if (j >= 2) {
-              // what is summed up so far moves to the new reference; the product of this group's last block is complete
-              // (issued before this block's S)
-              const float f = ex2(ref - now);
-              sum = mul2(sum, pack2(f, f));
+          // the reference: the last block's, or this one's maximum where that has grown past it
+          float now = top;
+          if (j > 0) {
+            ok = wait(bars.ref_done[warp & 3][x ^ 1], ((n - 1) >> 1) & 1, kStatusTimeoutEpilogue);
+            if (!ok) break;
+            const float last = row_ref[r];
+            const bool grew = top > last + kSlack;
+            if (!grew) now = last;
+            if (__any_sync(0xFFFFFFFFu, grew)) {
+              // what is summed up so far moves to the new reference, with every product up to block n - 1 complete
+              const uint32_t before = (n - 1) / 3;
+              ok = wait(bars.pv_done[n - 1 - 3 * before], before & 1, kStatusTimeoutEpilogue);
+              if (!ok) break;
+              tc_fence_after();
+              const float f = ex2(last - now);
 #pragma unroll 1
               for (int c = 0; c < 8; ++c) {
                 uint32_t o[16];
@@ -548,6 +572,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st16(ocol + 16 * c, o);
               }
             }
+          }
+          row_ref[r] = now;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bars.ref_done[warp & 3][x]));
+          if (now != ref) {
+            const float f = ex2(ref - now);
+            sum = mul2(sum, pack2(f, f));
             ref = now;
           }
           const F2 scale2 = pack2(sl2, sl2), shift2 = pack2(kLift - ref, kLift - ref);
@@ -578,11 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             powers(w, col + 32);
           }
           tmem_st_wait();
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bars.ref_done[warp & 3][x]));
         }
-        ++n_x;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars.p_full[x]));
+        if (lane == 0) mbar_arrive(bar(bars.p_full[buf]));
       }
       if (!ok) break;
       if (x == 0) {
@@ -590,44 +623,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (t.blocks > 0) load_q(t);
       }
-      if (s.blocks > j0) {
-        ok = wait(bars.pv_done[x], (n_x - 1) & 1, kStatusTimeoutEpilogue);
-        if (!ok) break;
-      }
+      ok = wait(bars.o_full, n_q & 1, kStatusTimeoutEpilogue);
+      if (!ok) break;
       tc_fence_after();
       float s0, s1;
       unpack2(sum, s0, s1);
-      stat[n_q & 1][x][r] = make_float2(ref - kLift, s0 + s1);
+      stat[n_q & 1][x][r] = make_float2(ref, s0 + s1);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars.stat_full));
       ok = wait(bars.stat_full, n_q & 1, kStatusTimeoutEpilogue);
       if (!ok) break;
-      // the row's two halves of the blocks: this thread joins 64 dims of the two accumulators
+      // the row's sums of both groups, the later reference being O's; this thread writes 64 of its dims
       if (work) {
-        const int first = n0 & 1;  // the group of the segment's first block; the other has some only behind it
-        const bool two = s.blocks > 1;
-        const float2 t0 = stat[n_q & 1][first][r], t1 = stat[n_q & 1][first ^ 1][r];
-        const float M = two ? fmaxf(t0.x, t1.x) : t0.x;
-        const float f0 = ex2(t0.x - M), f1 = two ? ex2(t1.x - M) : 0.0f;
-#pragma unroll
+        const float2 t0 = stat[n_q & 1][0][r], t1 = stat[n_q & 1][1][r];
+        const float M = fmaxf(t0.x, t1.x);  // -inf for a group without a block
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t o0[16], o1[16];
-          tmem_ld16(tmem + lanes + kOcol + 128 * first + 64 * x + 16 * c, o0);
-          if (two) tmem_ld16(tmem + lanes + kOcol + 128 * (first ^ 1) + 64 * x + 16 * c, o1);
+          uint32_t o[16];
+          tmem_ld16(ocol + 64 * x + 16 * c, o);
           tmem_ld_wait();
-          float o[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            o[i] = f0 * __uint_as_float(o0[i]);
-            if (two) o[i] = fmaf(f1, __uint_as_float(o1[i]), o[i]);
-          }
           if (r < rows) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              a.part[part_at(s.slot, 16 * x + 4 * c + i, r)] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              a.part[part_at(s.slot, 16 * x + 4 * c + i, r)] =
+                  make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                              __uint_as_float(o[4 * i + 3]));
           }
         }
-        if (x == 0 && r < rows) a.stats[static_cast<int64_t>(s.slot) * kRows + r] = make_float2(M, f0 * t0.y + (two ? f1 * t1.y : 0.0f));
+        if (x == 0 && r < rows)
+          a.stats[static_cast<int64_t>(s.slot) * kRows + r] = make_float2(M - kLift, ex2(t0.x - M) * t0.y + ex2(t1.x - M) * t1.y);
       }
       n0 += s.blocks;
       ++n_q;
@@ -635,123 +659,129 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars.o_free));
     }
-  } else if (warp < kMmaWarp) {
+  } else if (warp < kScoreWarp) {
     // ---- decoding: warps 8-11 K, 12-15 V; one thread to a token
     fewer_registers<kDecodeRegs>();
     const bool is_v = warp >= 12;
     const int r = threadIdx.x & (kBlock - 1);
     uint64_t* full = is_v ? bars.v_full : bars.k_full;
-    uint64_t* used = is_v ? bars.pv_done : bars.s_done;  // the operand's last product
-    const uint32_t codes = ring + (is_v ? kCodeBytes : 0), scales = ring + 2 * kCodeBytes + (is_v ? kScaleBytes : 0);
-    const uint32_t out = kvs + (is_v ? 2 * kTileBytes : 0);
-    uint32_t n = 0, st = 0, turn = 0;  // block, its ring slot, the ring's turn
-    for (uint32_t i = 0; ok; ++i) {
-      const int blocks = segment(i, kStatusTimeoutDequant).blocks;
-      if (!ok || blocks == 0) break;
-      release(i);
-      for (int j = 0; j < blocks; ++j, ++n) {
-        const uint32_t buf = n & 1;
-        ok = wait(bars.code_full[st], turn & 1, kStatusTimeoutDequant) && wait(used[buf], ((n >> 1) & 1) ^ 1, kStatusTimeoutDequant);
-        if (!ok) break;
-        decode_row(codes + st * kStageBytes, scales + st * kStageBytes, out + buf * kTileBytes, r);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(full[buf]));
-          mbar_arrive(bar(bars.code_empty[st]));
-        }
-        if (++st == kStages) {
-          st = 0;
-          ++turn;
-        }
+    const uint8_t* codes = is_v ? a.vc : a.kc;
+    const uint8_t* scales = is_v ? a.vs : a.ks;
+    const uint32_t slots = ring + (warp - 8) * (kStages * kSlotBytes), out = kvs + (is_v ? 2 * kTileBytes : 0);
+    const int row0 = r & ~31;  // of the warp's rows in a block
+    // The copies run three blocks ahead of the decoding: block j of segment seg is the next one. A group of copies is closed per
+    // block whether there is one or not.
+    Segment s{0, 0, 0, 0, 0, 0, 0, 0};
+    uint32_t seg = 0, copied = 0;
+    int j = 0;
+    bool more = true;
+    const auto copy_next = [&]() {
+      if (more && j == s.blocks) {
+        s = segment(seg, kStatusTimeoutDequant);
+        more = ok && s.blocks > 0;
+        if (more) release(seg);
+        ++seg;
+        j = 0;
       }
+      if (more) {
+        const uint32_t slot = slots + (copied % kStages) * kSlotBytes;
+        const int t0 = (s.block0 + j) * kBlock + row0;  // token of the warp's first row
+        const int64_t heads = a.groups.Hkv, at = (static_cast<int64_t>(s.p) * a.groups.Lp + t0) * heads + s.kvh;
+        const uint8_t* from = codes + (at + (lane >> 2) * heads) * kCodeRow + 16 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 8 * i + (lane >> 2);
+          const bool there = t0 + row < s.len;
+          cp_async16(slot + code_unit(row, lane & 3), there ? from + 8 * i * heads * kCodeRow : codes, there);
+        }
+        const bool there = t0 + lane < s.len;
+        cp_async8(slot + kWarpRows * kCodeRow + kScaleRow * lane, there ? scales + (at + lane * heads) * kScaleRow : scales, there);
+        ++j;
+        ++copied;
+      }
+      cp_async_commit();
+    };
+    for (int i = 0; i < kStages; ++i) copy_next();
+    for (uint32_t n = 0; ok && n < copied; ++n) {
+      const uint32_t buf = n & 1;
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      if (n >= 2) {  // the operand's last product, of block n - 2, is complete
+        const uint32_t third = (n - 2) / 3;
+        ok = wait((is_v ? bars.pv_done : bars.s_done)[n - 2 - 3 * third], third & 1, kStatusTimeoutDequant);
+        if (!ok) break;
+      }
+      decode_row(slots + (n % kStages) * kSlotBytes, out + buf * kTileBytes, lane, r);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(full[buf]));
+      copy_next();
     }
+    cp_async_wait<0>();  // every copy has landed before the CTA leaves
   } else {
     fewer_registers<kOtherRegs>();
-    if (warp == kMmaWarp) {
-      // ---- products, issued by one elected lane of the converged warp. Block n of the CTA uses the operands, S, P and O of
-      // parity n & 1.
-      constexpr uint32_t idesc_s = idesc_f16_f32(kRows, kBlock, false), idesc_o = idesc_f16_f32(kRows, kDim, true);
+    // what the issuing warps make of a value that is the same in every lane: the shuffle tells the compiler, which then
+    // keeps the products' operands in uniform registers
+    const auto uniform = [](uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+    // the products in flight of an issuing warp end before shared memory and TMEM go
+    const auto drain = [&](uint64_t& b) {
+      if (elect_one()) mma_commit(bar(b));
+      __syncwarp();
+      mbar_wait(bar(b), 0, a.status, kStatusTimeoutDrain);
+    };
+    if (warp == kScoreWarp) {
+      // ---- S = Q K^T, issued by one elected lane of the converged warp
+      constexpr uint32_t idesc = idesc_f16_f32(kRows, kBlock, false);
       const uint64_t qdesc = smem_desc(qs, 16, 1024, 2);
-      // the same in every lane, by a shuffle: so the compiler keeps what is made of it in uniform registers
-      const auto uniform = [](uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
       const uint32_t tmem_u = uniform(tmem);
-      uint32_t n = 0, n_q = 0;
-      const auto scores = [&](uint32_t i) {  // S of the CTA's block i
-        const uint32_t x = uniform(i & 1);
-        if (!wait(bars.k_full[x], (i >> 1) & 1, kStatusTimeoutMma)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t kdesc = smem_desc(kvs + x * kTileBytes, 16, 1024, 2);
-          mma8_scores(tmem_u + kScol + 128 * x, qdesc, kdesc, idesc_s);
-          mma_commit(bar(bars.s_done[x]));
-        }
-        __syncwarp();
-        return true;
-      };
-      while (true) {
-        const int blocks = segment(n_q, kStatusTimeoutMma).blocks;
+      uint32_t n = 0;
+      for (uint32_t i = 0; ok; ++i) {
+        const int blocks = segment(i, kStatusTimeoutMma).blocks;
         if (!ok || blocks == 0) break;
-        release(n_q);
-        ok = wait(bars.q_full, n_q & 1, kStatusTimeoutMma) && scores(n);
+        release(i);
+        ok = wait(bars.q_full, i & 1, kStatusTimeoutMma);
         for (int j = 0; j < blocks && ok; ++j, ++n) {
-          if (j + 1 < blocks) ok = scores(n + 1);
-          const uint32_t x = uniform(n & 1), parity = (n >> 1) & 1;
-          ok = ok && wait(bars.v_full[x], parity, kStatusTimeoutMma) && wait(bars.p_full[x], parity, kStatusTimeoutMma);
-          // the first products into the accumulators: the last segment's have been read
-          if (ok && j == 0 && n_q > 0) ok = wait(bars.o_free, (n_q - 1) & 1, kStatusTimeoutMma);
+          const uint32_t x = uniform(n & 1), third = n / 3, buf = uniform(n - 3 * third);
+          ok = wait(bars.k_full[x], (n >> 1) & 1, kStatusTimeoutMma);
+          // the buffer is free: the values of block n - 3 are in O
+          if (ok && n >= 3) ok = wait(bars.pv_done[buf], (third & 1) ^ 1, kStatusTimeoutMma);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma8_scores(tmem_u + 128 * buf, qdesc, smem_desc(kvs + x * kTileBytes, 16, 1024, 2), idesc);
+            mma_commit(bar(bars.s_done[buf]));
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) drain(bars.drain[0]);
+    } else if (warp == kValueWarp) {
+      // ---- O += P V
+      constexpr uint32_t idesc = idesc_f16_f32(kRows, kDim, true);
+      const uint32_t tmem_u = uniform(tmem);
+      uint32_t n = 0;
+      for (uint32_t i = 0; ok; ++i) {
+        const int blocks = segment(i, kStatusTimeoutMma).blocks;
+        if (!ok || blocks == 0) break;
+        release(i);
+        for (int j = 0; j < blocks && ok; ++j, ++n) {
+          const uint32_t x = uniform(n & 1), third = n / 3, buf = uniform(n - 3 * third);
+          ok = wait(bars.v_full[x], (n >> 1) & 1, kStatusTimeoutMma) && wait(bars.p_full[buf], third & 1, kStatusTimeoutMma);
+          // the first products into O: the last segment's has been read
+          if (ok && j == 0 && i > 0) ok = wait(bars.o_free, (i - 1) & 1, kStatusTimeoutMma);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             // V is [token][dim]: the contiguous dims are N (two panels), eight tokens to 1024 bytes
-            const uint64_t vdesc = smem_desc(kvs + (2 + x) * kTileBytes, kPanel, 1024, 2);
-            mma8_values(tmem_u + kOcol + 128 * x, tmem_u + kScol + 128 * x, vdesc, idesc_o, j >= 2 ? 1u : 0u);
-            mma_commit(bar(bars.pv_done[x]));
+            mma8_values(tmem_u + kOcol, tmem_u + 128 * buf, smem_desc(kvs + (2 + x) * kTileBytes, kPanel, 1024, 2), idesc,
+                        j > 0 ? 1u : 0u);
+            mma_commit(bar(bars.pv_done[buf]));
+            if (j == blocks - 1) mma_commit(bar(bars.o_full));
           }
           __syncwarp();
         }
-        if (!ok) break;
-        ++n_q;
       }
-      if (!ok) {  // what is in flight ends before shared memory and TMEM go
-        if (elect_one()) mma_commit(bar(bars.drain));
-        __syncwarp();
-        mbar_wait(bar(bars.drain), 0, a.status, kStatusTimeoutDrain);
-      }
-    } else if (warp == kCopyWarp) {
-      // ---- copies
-      uint32_t n = 0;
-      for (uint32_t i = 0; ok; ++i) {
-        const Segment s = segment(i, kStatusTimeoutProducer);
-        if (!ok || s.blocks == 0) break;
-        release(i);
-        const int64_t row0 = static_cast<int64_t>(s.p) * a.groups.Lp;
-        for (int j = 0; j < s.blocks; ++j, ++n) {
-          const uint32_t st = n % kStages;
-          ok = wait(bars.code_empty[st], ((n / kStages) & 1) ^ 1, kStatusTimeoutProducer);
-          if (!ok) break;
-          const uint32_t dst = ring + st * kStageBytes, full = bar(bars.code_full[st]);
-          const int64_t t0 = static_cast<int64_t>(s.block0 + j) * kBlock;
-          if (lane == 0) {
-            fence_proxy_async();  // the readers of the slot's last contents come before the copies
-            mbar_arrive_expect_tx(full, 2 * kCodeBytes);
-            tma_load_2d(dst, &map_k, s.kvh * (kDim / 2), static_cast<int32_t>(row0 + t0), full);
-            tma_load_2d(dst + kCodeBytes, &map_v, s.kvh * (kDim / 2), static_cast<int32_t>(row0 + t0), full);
-          }
-#pragma unroll
-          for (int i = 0; i < kBlock / 32; ++i) {
-            const int t = lane + 32 * i;
-            const bool in = t0 + t < s.len;
-            const int64_t at = in ? ((row0 + t0 + t) * a.groups.Hkv + s.kvh) * (kDim / 16) : 0;
-            cp_async8(dst + 2 * kCodeBytes + 8 * t, a.ks + at, in ? 8u : 0u);
-            cp_async8(dst + 2 * kCodeBytes + kScaleBytes + 8 * t, a.vs + at, in ? 8u : 0u);
-          }
-          cp_async_arrive_noinc(full);
-        }
-      }
-      if (!ok)  // every copy has landed before the CTA leaves
-        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
-          mbar_wait(bar(bars.code_full[i % kStages]), (i / kStages) & 1, a.status, kStatusTimeoutDrain);
+      if (!ok) drain(bars.drain[1]);
     } else if (warp == kWalkWarp) {
       // ---- segments
       Walk walk = begin_walk(a.groups, gridDim.x, blockIdx.x);
@@ -771,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Joins the partial results of every (sequence, query head); one warp per row, four dims per lane. A row that attends to
@@ -874,13 +904,6 @@ nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo
   auto* own = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + prefix_bytes(slots));
   const Groups groups{p.groups, p.prefix_lens, static_cast<int>(p.P), static_cast<int>(p.Lp), static_cast<int>(p.B),
                       static_cast<int>(p.Hkv), kRows / heads, static_cast<int>(tiles)};
-  // code rows as a [P Lp][Hkv 64] byte array; a box is one head's 64-byte rows of a block
-  CUtensorMap mk, mv;
-  const auto map = [&](CUtensorMap* m, const uint8_t* codes) {
-    return make_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, static_cast<uint64_t>(p.Hkv) * (kDim / 2),
-                              static_cast<uint64_t>(p.P * p.Lp), 1, kDim / 2, kBlock, CU_TENSOR_MAP_SWIZZLE_64B);
-  };
-  if (!map(&mk, p.pkc) || !map(&mv, p.pvc)) return NVFP4RL_ERR_CUDA;
   {
     static std::mutex mu;
     static std::map<int, bool> set;
@@ -893,8 +916,8 @@ nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo
     }
   }
   const int grid = std::min(dev.sm_count, kPlanSMs);
-  const PrefixArgs a{p.q, p.ldq, p.pks, p.pvs, p.gk, groups, heads, p.scale, part, stats, dev.status};
-  if (launch_pdl(prefix_attention_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, st, mk, mv, a) !=
+  const PrefixArgs a{p.q, p.ldq, p.pkc, p.pks, p.pvc, p.pvs, p.gk, groups, heads, p.scale, part, stats, dev.status};
+  if (launch_pdl(prefix_attention_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, st, a) !=
       cudaSuccess)
     return NVFP4RL_ERR_CUDA;
   nvfp4rl_status s = launch_status();
