@@ -375,24 +375,26 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
 // banks groups then, for the thread that reads a row and for the four that copy it.
 __device__ __forceinline__ uint32_t code_unit(int i, int u) { return kCodeRow * i + ((u ^ ((i >> 1) & 3)) << 4); }
 
-// One token row, row i of the warp's slot and row r of the block: 128 codes and 8 scale bytes to f16 in the 128-byte swizzle of
-// an MMA operand.
-__device__ __forceinline__ void decode_row(uint32_t slot, uint32_t out, int i, int r) {
+// One token row, row i of the warp's slot: 128 codes and 8 scale bytes to f16 in the operand row at `row`, in the 128-byte
+// swizzle: 16-byte chunk c of a panel lies at chunk c ^ (row & 7), chunk[k] being the place of chunk k < 4 in bytes.
+__device__ __forceinline__ void decode_row(uint32_t slot, uint32_t row, const uint32_t (&chunk)[4], int i) {
   const uint2 s = lds64(slot + kWarpRows * kCodeRow + kScaleRow * i);
-  const uint32_t row = out + 128 * r, sw = r & 7;
   uint4 c[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) c[u] = lds128(slot + code_unit(i, u));
+  uint32_t at[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) at[k] = row + (chunk[k & 3] ^ (16 * (k & 4)));
 #pragma unroll
   for (int u = 0; u < 4; ++u) {  // 32 codes: two scale blocks
     const uint32_t two = e4m3x2_f16((u < 2 ? s.x : s.y) >> (16 * (u & 1)));
     const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
-    const uint32_t panel = row + (u >> 1) * kPanel;
-    const uint32_t c0 = 4 * (u & 1);
-    decode8_store(panel + (((c0 + 0) ^ sw) << 4), c[u].x, s0);
-    decode8_store(panel + (((c0 + 1) ^ sw) << 4), c[u].y, s0);
-    decode8_store(panel + (((c0 + 2) ^ sw) << 4), c[u].z, s1);
-    decode8_store(panel + (((c0 + 3) ^ sw) << 4), c[u].w, s1);
+    const uint32_t* p = at + 4 * (u & 1);
+    const uint32_t panel = (u >> 1) * kPanel;
+    decode8_store(p[0] + panel, c[u].x, s0);
+    decode8_store(p[1] + panel, c[u].y, s0);
+    decode8_store(p[2] + panel, c[u].z, s1);
+    decode8_store(p[3] + panel, c[u].w, s1);
   }
 }
 
@@ -667,36 +669,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* full = is_v ? bars.v_full : bars.k_full;
     const uint8_t* codes = is_v ? a.vc : a.kc;
     const uint8_t* scales = is_v ? a.vs : a.ks;
-    const uint32_t slots = ring + (warp - 8) * (kStages * kSlotBytes), out = kvs + (is_v ? 2 * kTileBytes : 0);
+    const uint32_t slots = ring + (warp - 8) * (kStages * kSlotBytes), out = kvs + (is_v ? 2 * kTileBytes : 0) + 128 * r;
+    uint32_t chunk[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) chunk[k] = (k ^ (r & 7)) << 4;
     const int row0 = r & ~31;  // of the warp's rows in a block
-    // The copies run three blocks ahead of the decoding: block j of segment seg is the next one. A group of copies is closed per
-    // block whether there is one or not.
-    Segment s{0, 0, 0, 0, 0, 0, 0, 0};
+    // The copies run three blocks ahead of the decoding: `left` blocks of segment seg - 1 are still to come, `tokens` tokens from
+    // the warp's first row of the next one on, which the lane's pointers are at. A group of copies is closed per block
+    // whether there is one or not.
+    const int64_t code_step = static_cast<int64_t>(a.groups.Hkv) * kCodeRow, scale_step = static_cast<int64_t>(a.groups.Hkv) * kScaleRow;
+    const uint8_t *from = codes, *scale_from = scales;
     uint32_t seg = 0, copied = 0;
-    int j = 0;
+    int left = 0, tokens = 0;
     bool more = true;
     const auto copy_next = [&]() {
-      if (more && j == s.blocks) {
-        s = segment(seg, kStatusTimeoutDequant);
-        more = ok && s.blocks > 0;
-        if (more) release(seg);
+      if (more && left == 0) {
+        const Segment& s = segment(seg, kStatusTimeoutDequant);
+        left = s.blocks;
+        more = ok && left > 0;
+        if (more) {
+          const int t0 = s.block0 * kBlock + row0;
+          const int64_t at = (static_cast<int64_t>(s.p) * a.groups.Lp + t0) * a.groups.Hkv + s.kvh;
+          tokens = s.len - t0;
+          from = codes + at * kCodeRow + (lane >> 2) * code_step + 16 * (lane & 3);
+          scale_from = scales + at * kScaleRow + lane * scale_step;
+          release(seg);
+        }
         ++seg;
-        j = 0;
       }
       if (more) {
         const uint32_t slot = slots + (copied % kStages) * kSlotBytes;
-        const int t0 = (s.block0 + j) * kBlock + row0;  // token of the warp's first row
-        const int64_t heads = a.groups.Hkv, at = (static_cast<int64_t>(s.p) * a.groups.Lp + t0) * heads + s.kvh;
-        const uint8_t* from = codes + (at + (lane >> 2) * heads) * kCodeRow + 16 * (lane & 3);
+        const uint32_t to = slot + code_unit(lane >> 2, lane & 3), scale_to = slot + kWarpRows * kCodeRow + kScaleRow * lane;
+        if (tokens >= kWarpRows) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 8 * i + (lane >> 2);
-          const bool there = t0 + row < s.len;
-          cp_async16(slot + code_unit(row, lane & 3), there ? from + 8 * i * heads * kCodeRow : codes, there);
+          for (int i = 0; i < 4; ++i) cp_async16(to + 8 * kCodeRow * i, from + 8 * i * code_step, true);
+          cp_async8(scale_to, scale_from, true);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool there = 8 * i + (lane >> 2) < tokens;
+            cp_async16(to + 8 * kCodeRow * i, there ? from + 8 * i * code_step : codes, there);
+          }
+          cp_async8(scale_to, lane < tokens ? scale_from : scales, lane < tokens);
         }
-        const bool there = t0 + lane < s.len;
-        cp_async8(slot + kWarpRows * kCodeRow + kScaleRow * lane, there ? scales + (at + lane * heads) * kScaleRow : scales, there);
-        ++j;
+        from += kBlock * code_step;
+        scale_from += kBlock * scale_step;
+        tokens -= kBlock;
+        --left;
         ++copied;
       }
       cp_async_commit();
@@ -711,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait((is_v ? bars.pv_done : bars.s_done)[n - 2 - 3 * third], third & 1, kStatusTimeoutDequant);
         if (!ok) break;
       }
-      decode_row(slots + (n % kStages) * kSlotBytes, out + buf * kTileBytes, lane, r);
+      decode_row(slots + (n % kStages) * kSlotBytes, out + buf * kTileBytes, chunk, lane);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(full[buf]));
