@@ -2,14 +2,18 @@
 // preference loss of paired log ratios, forward and backward. include/nvfp4rl.h states the formulas.
 //
 // All four stream a few fp32 arrays once, so HBM (or L2) bounds them. A warp takes a step of 256
-// consecutive tokens (coalesced 4-byte loads at any alignment, eight per array in flight per lane) and
-// walks the sequences that meet the step; it sums each one's tokens over its lanes and leaves the sums in the
-// slot (step + sequence). A second kernel adds a sequence's slots in order, one warp to a sequence, and the
-// CTA that finishes last joins the sequences. No floating-point atomics: equal inputs give equal bits.
+// consecutive tokens (coalesced 4-byte loads at any alignment, eight per array in flight per lane), computes its eight
+// tokens per lane without branches (with one in the token, and the tokens one after another, the policy sums of 4 Mi
+// tokens took 87 us), walks the sequences that meet the step, sums each one's tokens over its lanes and leaves the sums in
+// the slot (step + sequence). A second kernel adds a sequence's slots in order, one warp to a sequence, and the
+// CTA that finishes last joins the sequences; small batches do both in one CTA. No floating-point atomics: equal inputs give
+// equal bits.
 //
 // Ratios next to a bound: whether r = e^d lies above 1 + eps is decided as d > ln(1 + eps), with d the exact
 // difference of the two log-probs (two floats, from one TwoSum) and the logarithm split into two floats, so
 // that clipping does not depend on the rounding of d or of the exponential.
+#include <climits>
+
 #include "losses.cuh"
 
 namespace nvfp4rl {
@@ -43,10 +47,9 @@ __device__ __forceinline__ SplitFloat warp_sum_split(SplitFloat v) {
 __device__ __forceinline__ bool above(SplitFloat d, SplitFloat t) { return d.hi > t.hi || (d.hi == t.hi && d.lo > t.lo); }
 __device__ __forceinline__ bool below(SplitFloat d, SplitFloat t) { return d.hi < t.hi || (d.hi == t.hi && d.lo < t.lo); }
 
-// e^x - x - 1 >= 0: its power series up to x^9 below 1/2 (truncated at 2e-9 of the sum), where the
+// e^x - x - 1 >= 0, with ex = e^x: its power series up to x^9 below 1/2 (truncated at 2e-9 of the sum), where the
 // difference would lose x's digits.
-__device__ __forceinline__ float expm1_less(float x) {
-  if (fabsf(x) >= 0.5f) return expm1f(x) - x;
+__device__ __forceinline__ float expm1_less(float x, float ex) {
   float p = fmaf(x, 1.0f / 362880.0f, 1.0f / 40320.0f);
   p = fmaf(x, p, 1.0f / 5040.0f);
   p = fmaf(x, p, 1.0f / 720.0f);
@@ -54,7 +57,7 @@ __device__ __forceinline__ float expm1_less(float x) {
   p = fmaf(x, p, 1.0f / 24.0f);
   p = fmaf(x, p, 1.0f / 6.0f);
   p = fmaf(x, p, 0.5f);
-  return x * x * p;
+  return fabsf(x) < 0.5f ? x * x * p : (ex - 1.0f) - x;
 }
 
 // How many of offsets[0 .. count) are at most t: whole warp, 32 probes a round.
@@ -73,19 +76,40 @@ __device__ __forceinline__ int64_t count_up_to(const int32_t* __restrict__ offse
   return lo;
 }
 
+// 32 sequences from the one that holds token t0 on: lane l has the end of sequence first + l (first -1: tokens ahead of all
+// sequences). Made once per step; a walk over the step's sequences then takes a shuffle each.
+struct Window {
+  int64_t first;
+  int end;
+};
+__device__ __forceinline__ Window window_at(const int32_t* __restrict__ offsets, int64_t B, int64_t t0) {
+  const int64_t c = count_up_to(offsets, B + 1, t0), at = c + (threadIdx.x & 31);
+  return {c - 1, at <= B ? __ldg(offsets + at) : INT_MAX};
+}
+
 // The sequences of tokens [t0, t1), in order: f(b, s, e) for the part [s, e) that sequence b has of them;
 // b = -1 for tokens of no sequence. Whole warp. Offsets that fall are answered with some split of the
 // tokens, each in one part.
 template <class F>
-__device__ __forceinline__ void for_sequences(const int32_t* __restrict__ offsets, int64_t B, int64_t t0, int64_t t1,
-                                              F&& f) {
-  int64_t t = t0;
+__device__ __forceinline__ void for_sequences(const int32_t* __restrict__ offsets, int64_t B, Window w, int64_t t0,
+                                              int64_t t1, F&& f) {
+  int64_t t = t0, seen = -1;
+  int k = 0;
   while (t < t1) {
-    const int64_t c = count_up_to(offsets, B + 1, t);
-    const int64_t b = c > B ? -1 : c - 1;
-    int64_t e = c > B ? t1 : min(t1, static_cast<int64_t>(__ldg(offsets + c)));
-    e = max(e, t + 1);
-    f(b, t, e);
+    if (k == 32) {  // more sequences (or empty ones) than the window has
+      if (t == seen) {  // offsets that fall: the rest is of no sequence
+        f(int64_t(-1), t, t1);
+        return;
+      }
+      w = window_at(offsets, B, t);
+      seen = t;
+      k = 0;
+    }
+    const int64_t e = min(t1, static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, w.end, k)));
+    const int64_t b = w.first + k;
+    ++k;
+    if (e <= t) continue;
+    f(b < B ? b : int64_t(-1), t, e);
     t = e;
   }
 }
@@ -99,134 +123,211 @@ struct Token {
   bool clipped;
 };
 
-template <bool kGrad>
-__device__ __forceinline__ Token policy_token(const PolicyArgs& a, float lp, float lo, float ref, float adv, float w) {
+// Where clipping acts for one sign of the advantage: above `over` the ratio is `cap`, below `under` it is 1 - eps_low. Made
+// once per sequence.
+struct Clip {
+  SplitFloat over, under;
+  float cap;
+};
+__device__ __forceinline__ Clip clip_for(const PolicyArgs& a, float adv) {
+  Clip c;
+  const bool gain = adv > 0.0f;
+  c.over = gain ? a.ln_high : a.ln_dual;
+  c.under = gain ? SplitFloat{-INFINITY, 0.0f} : a.ln_low;
+  c.cap = gain ? a.high : a.dual;
+  if (adv == 0.0f) c.over = {INFINITY, 0.0f}, c.under = {-INFINITY, 0.0f};
+  return c;
+}
+
+template <bool kGrad, bool kRef>
+__device__ __forceinline__ Token policy_token(const PolicyArgs& a, const Clip& c, float lp, float lo, float ref, float adv,
+                                              float w) {
   Token t;
   const SplitFloat d = two_sum(lp, -lo);
   const float e = expf(d.hi);
-  t.ratio = isfinite(d.hi) && isfinite(e) ? fmaf(e, d.lo, e) : e;
-  const bool over = adv > 0.0f && above(d, a.ln_high);
-  const bool under = adv < 0.0f && below(d, a.ln_low);
-  const bool far = adv < 0.0f && above(d, a.ln_dual);
-  t.clipped = over || under || far;
-  const float used = far ? a.dual : over ? a.high : under ? a.low : t.ratio;
+  t.ratio = fabsf(d.hi) < 80.0f ? fmaf(e, d.lo, e) : e;
+  const bool over = above(d, c.over), under = below(d, c.under);
+  t.clipped = over || under;
+  const float used = over ? c.cap : under ? a.low : t.ratio;
   t.term = adv == 0.0f ? 0.0f : -(w * (used * adv));
-  t.grad = t.clipped ? 0.0f : t.term;
-  t.div = 0.0f;
-  if (a.logp_ref) {
-    const float x = ref - lp;
-    if constexpr (kGrad) t.grad = fmaf(-a.kl, expm1f(x), t.grad);
-    else t.div = expm1_less(x);
+  t.div = t.grad = t.drift = 0.0f;
+  const float x = ref - lp;
+  if constexpr (kGrad) {
+    t.grad = t.clipped ? 0.0f : t.term;
+    if constexpr (kRef) {  // 1 - e^x = -(x + (e^x - x - 1)), or as it stands where |x| is large
+      const float ex = expf(x);
+      t.grad = fmaf(-a.kl, fabsf(x) < 0.5f ? x + expm1_less(x, ex) : ex - 1.0f, t.grad);
+    }
+  } else {
+    if constexpr (kRef) t.div = expm1_less(x, expf(x));
+    t.drift = expm1_less(d.hi, e);
   }
-  if constexpr (!kGrad) t.drift = expm1_less(d.hi);
   return t;
 }
 
-// Slots and sequences hold the same eight floats. A slot: sums of term, div, drift and ratio, then the numbers of
-// tokens and of clipped ones. A sequence: term and div as split floats, then drift, ratio and the two numbers.
-struct SlotSums {
-  float4 a, b;
+// A step's tokens of this lane: token 32 j + lane of the step, live where it counts, with its advantage.
+struct Step {
+  float lp[kPerLane], lo[kPerLane], ref[kPerLane], w[kPerLane], adv[kPerLane];
+  uint32_t live;  // bit j
 };
 
-__global__ void __launch_bounds__(kThreads) policy_sums_kernel(const PolicyArgs a, unsigned int* __restrict__ ticket,
-                                                               SlotSums* __restrict__ slots) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0u;  // for the kernel behind this one
-  const int64_t s = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
-  const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
-  if (t0 >= a.n) return;
-  float lp[kPerLane], lo[kPerLane], ref[kPerLane], w[kPerLane], adv[kPerLane];
-  bool live[kPerLane];
+// One array of a step, `count` tokens long, from its first token of this lane on: constant offsets, no bounds in whole steps.
+template <class T>
+__device__ __forceinline__ void load_array(const T* __restrict__ p, int count, T (&v)[kPerLane]) {
+  if (count == kLossStep) {
 #pragma unroll
-  for (int j = 0; j < kPerLane; ++j) {
-    const int64_t t = t0 + 32 * j + lane;
-    const bool in = t < t1;
-    live[j] = in && (!a.mask || __ldg(a.mask + t) != 0);
-    lp[j] = in ? __ldg(a.logp + t) : 0.0f;
-    lo[j] = in ? __ldg(a.logp_old + t) : 0.0f;
-    ref[j] = a.logp_ref && in ? __ldg(a.logp_ref + t) : 0.0f;
-    w[j] = a.weights && in ? __ldg(a.weights + t) : 1.0f;
-    adv[j] = a.adv_per_token && in ? __ldg(a.adv + t) : 0.0f;
+    for (int j = 0; j < kPerLane; ++j) v[j] = __ldg(p + 32 * j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) v[j] = 32 * j + static_cast<int>(threadIdx.x & 31) < count ? __ldg(p + 32 * j) : T(0);
   }
-  for_sequences(a.offsets, a.B, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
-    if (b < 0) return;
-    const float seq_adv = a.adv_per_token ? 0.0f : __ldg(a.adv + b);
-    float term = 0.0f, div = 0.0f, drift = 0.0f, ratio = 0.0f;
-    uint32_t counts = 0;  // tokens, and clipped ones from bit 16 on: at most 256 of each
+}
+// Which of the lane's tokens are there and not masked.
+__device__ __forceinline__ uint32_t load_mask(const uint8_t* __restrict__ mask, int64_t at, int count) {
+  uint32_t live = 0;
+  if (mask) {
+    uint8_t m[kPerLane];
+    load_array(mask + at, count, m);
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      const int64_t t = t0 + 32 * j + lane;
-      if (live[j] && t >= from && t < to) {
-        const Token k = policy_token<false>(a, lp[j], lo[j], ref[j], a.adv_per_token ? adv[j] : seq_adv, w[j]);
-        term += k.term;
-        div += k.div;
-        drift += k.drift;
-        ratio += k.ratio;
-        counts += k.clipped ? 0x10001u : 1u;
+    for (int j = 0; j < kPerLane; ++j) live |= m[j] ? 1u << j : 0u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) live |= 32 * j + static_cast<int>(threadIdx.x & 31) < count ? 1u << j : 0u;
+  }
+  return live;
+}
+
+__device__ __forceinline__ void load_step(const PolicyArgs& a, int64_t t0, int count, Step& s) {
+  const int64_t at = t0 + (threadIdx.x & 31);
+  load_array(a.logp + at, count, s.lp);
+  load_array(a.logp_old + at, count, s.lo);
+  if (a.logp_ref) load_array(a.logp_ref + at, count, s.ref);
+  if (a.adv_per_token) load_array(a.adv + at, count, s.adv);
+  if (a.weights) {
+    load_array(a.weights + at, count, s.w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) s.w[j] = 1.0f;
+  }
+  s.live = load_mask(a.mask, at, count);
+}
+
+// A slot: sums of term, div, drift and ratio, then the numbers of tokens and of clipped ones. A sequence: term and div as
+// split floats, drift and ratio (heads), the two numbers.
+struct SlotSums {
+  float v[4];
+  uint32_t tokens, clipped, unused[2];
+};
+struct SeqSums {
+  SplitFloat term, div;
+  float drift, ratio;
+  uint32_t tokens, clipped;
+};
+static_assert(sizeof(SlotSums) == 32 && sizeof(SeqSums) == 32, "as policy_workspace_bytes has them");
+
+template <bool kRef>
+__device__ __forceinline__ void policy_step(const PolicyArgs& a, int64_t s, SlotSums* __restrict__ slots) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
+  Step st;
+  load_step(a, t0, static_cast<int>(t1 - t0), st);
+  const Window win = window_at(a.offsets, a.B, t0);
+  const auto put = [&](int64_t b, float (&u)[4], uint32_t c) {
+    c = __reduce_add_sync(0xFFFFFFFFu, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = warp_sum(u[i]);
+    if (lane == 0) slots[s + b] = {{u[0], u[1], u[2], u[3]}, c & 0xFFFFu, c >> 16, {0u, 0u}};
+  };
+  // token j's four sums, and its count: one, and from bit 16 on the clipped ones (at most 256 of each in a step)
+  const auto token = [&](int j, const Clip& clip, float adv, bool live, float (&u)[4], uint32_t& c) {
+    const Token k = policy_token<false, kRef>(a, clip, st.lp[j], st.lo[j], kRef ? st.ref[j] : 0.0f, adv, st.w[j]);
+    u[0] += live ? k.term : 0.0f;
+    if (kRef) u[1] += live ? k.div : 0.0f;
+    u[2] += live ? k.drift : 0.0f;
+    u[3] += live ? k.ratio : 0.0f;
+    c += !live ? 0u : k.clipped ? 0x10001u : 1u;
+  };
+  for_sequences(a.offsets, a.B, win, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
+    if (b < 0) return;
+    float u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t c = 0;
+    const int lo = static_cast<int>(from - t0), hi = static_cast<int>(to - t0);
+    if (a.adv_per_token) {
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) {
+        const int i = 32 * j + lane;
+        token(j, clip_for(a, st.adv[j]), st.adv[j], (st.live >> j & 1) && i >= lo && i < hi, u, c);
+      }
+    } else {
+      const float adv = __ldg(a.adv + b);
+      const Clip clip = clip_for(a, adv);
+      if (hi - lo >= kLossStep / 4) {  // most tokens of the step: all eight side by side
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+          const int i = 32 * j + lane;
+          token(j, clip, adv, (st.live >> j & 1) && i >= lo && i < hi, u, c);
+        }
+      } else {  // a short sequence: only the rows of 32 tokens that it meets
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+          if (32 * j + 32 <= lo || 32 * j >= hi) continue;
+          const int i = 32 * j + lane;
+          token(j, clip, adv, (st.live >> j & 1) && i >= lo && i < hi, u, c);
+        }
       }
     }
-    counts = __reduce_add_sync(0xFFFFFFFFu, counts);
-    term = warp_sum(term);
-    div = warp_sum(div);
-    drift = warp_sum(drift);
-    ratio = warp_sum(ratio);
-    if (lane == 0)
-      slots[s + b] = {make_float4(term, div, drift, ratio),
-                      make_float4(static_cast<float>(counts & 0xFFFFu), static_cast<float>(counts >> 16), 0.0f, 0.0f)};
+    put(b, u, c);
   });
 }
 
-// Sums of sequence b's slots, in lanes' strides and then a tree: get(slot, i) is the i-th of kN numbers of a slot.
-template <int kN, class Get>
-__device__ __forceinline__ void sum_slots(const int32_t* __restrict__ offsets, int64_t n, int64_t b, SplitFloat (&v)[kN],
-                                          Get&& get) {
-#pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = {0.0f, 0.0f};
+// The slots of sequence b, [first, end): of the steps that hold its tokens.
+__device__ __forceinline__ void slot_range(const int32_t* __restrict__ offsets, int64_t n, int64_t b, int64_t& first,
+                                           int64_t& end) {
   const int64_t s = min(max(static_cast<int64_t>(__ldg(offsets + b)), int64_t(0)), n);
   const int64_t e = min(max(static_cast<int64_t>(__ldg(offsets + b + 1)), int64_t(0)), n);
-  if (e <= s) return;
-  for (int64_t k = s / kLossStep + (threadIdx.x & 31); k <= (e - 1) / kLossStep; k += 32) get(k + b, v);
-#pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = warp_sum_split(v[i]);
+  first = s / kLossStep + b;
+  end = e > s ? (e - 1) / kLossStep + b + 1 : first;
 }
 
-__global__ void __launch_bounds__(kThreads) policy_join_kernel(const PolicyArgs a, unsigned int* __restrict__ ticket,
-                                                               const SlotSums* __restrict__ slots,
-                                                               SlotSums* __restrict__ seqs) {
-  __shared__ SplitFloat part[7][kWarpsPerCta];
-  __shared__ int last;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarpsPerCta;
-  for (int64_t b = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + warp; b < a.B; b += warps) {
-    SplitFloat v[6];
-    sum_slots<6>(a.offsets, a.n, b, v, [&](int64_t i, SplitFloat (&u)[6]) {
-      const float4 x = __ldcg(&slots[i].a), y = __ldcg(&slots[i].b);
-      const float z[6] = {x.x, x.y, x.z, x.w, y.x, y.y};
+// Sequence b of the policy loss: its slots in lanes' strides, then a tree. Whole warp.
+__device__ __forceinline__ void policy_sequence(const PolicyArgs& a, int64_t b, const SlotSums* __restrict__ slots,
+                                                SeqSums* __restrict__ seqs) {
+  const int lane = threadIdx.x & 31;
+  int64_t first, end;
+  slot_range(a.offsets, a.n, b, first, end);
+  SplitFloat v[4] = {{0.0f, 0.0f}, {0.0f, 0.0f}, {0.0f, 0.0f}, {0.0f, 0.0f}};
+  uint32_t tokens = 0, clipped = 0;
+#pragma unroll 2
+  for (int64_t k = first + lane; k < end; k += 32) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(slots + k));
+    const uint2 c = __ldcg(reinterpret_cast<const uint2*>(&slots[k].tokens));
+    const float u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int k = 0; k < 6; ++k) u[k] = split_add(u[k], {z[k], 0.0f});
-    });
-    if (lane == 0)
-      seqs[b] = {make_float4(v[0].hi, v[0].lo, v[1].hi, v[1].lo), make_float4(v[2].hi, v[3].hi, v[4].hi, v[5].hi)};
+    for (int i = 0; i < 4; ++i) v[i] = split_add(v[i], {u[i], 0.0f});
+    tokens += c.x;
+    clipped += c.y;
   }
-  __threadfence();  // this thread's sequences are visible before the CTA's ticket
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(ticket, 1u) == gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();  // and every other CTA's from here on
-  // term, div, drift, ratio, tokens, clipped, sequences with a token
-  SplitFloat v[7];
 #pragma unroll
-  for (int i = 0; i < 7; ++i) v[i] = {0.0f, 0.0f};
-  for (int64_t b = threadIdx.x; b < a.B; b += kThreads) {
-    const float4 x = __ldcg(&seqs[b].a), y = __ldcg(&seqs[b].b);
+  for (int i = 0; i < 4; ++i) v[i] = warp_sum_split(v[i]);
+  tokens = __reduce_add_sync(0xFFFFFFFFu, tokens);
+  clipped = __reduce_add_sync(0xFFFFFFFFu, clipped);
+  if (lane == 0) seqs[b] = {v[0], v[1], v[2].hi, v[3].hi, tokens, clipped};
+}
+
+// The sequences' sums to the loss, the statistics and the coefficients. Whole CTA.
+__device__ __forceinline__ void policy_finish(const PolicyArgs& a, const SeqSums* __restrict__ seqs) {
+  __shared__ SplitFloat part[4][32];
+  __shared__ uint32_t parts[3][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  SplitFloat v[4] = {{0.0f, 0.0f}, {0.0f, 0.0f}, {0.0f, 0.0f}, {0.0f, 0.0f}};
+  uint32_t c[3] = {0, 0, 0};  // tokens, clipped, sequences with a token: at most 2^31
+  for (int64_t b = threadIdx.x; b < a.B; b += blockDim.x) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(seqs + b));
+    const float2 y = __ldcg(reinterpret_cast<const float2*>(&seqs[b].drift));
+    const uint2 z = __ldcg(reinterpret_cast<const uint2*>(&seqs[b].tokens));
     SplitFloat term{x.x, x.y}, div{x.z, x.w};
     if (a.mode == NVFP4RL_LOSS_SEQ_MEAN) {
-      const float len = fmaxf(y.z, 1.0f);
+      const float len = fmaxf(static_cast<float>(z.x), 1.0f);
       term = {term.hi / len, term.lo / len};
       div = {div.hi / len, div.lo / len};
     }
@@ -234,24 +335,28 @@ __global__ void __launch_bounds__(kThreads) policy_join_kernel(const PolicyArgs 
     v[1] = split_add(v[1], div);
     v[2] = split_add(v[2], {y.x, 0.0f});
     v[3] = split_add(v[3], {y.y, 0.0f});
-    v[4] = split_add(v[4], {y.z, 0.0f});
-    v[5] = split_add(v[5], {y.w, 0.0f});
-    v[6] = split_add(v[6], {y.z > 0.0f ? 1.0f : 0.0f, 0.0f});
+    c[0] += z.x;
+    c[1] += z.y;
+    c[2] += z.x > 0 ? 1u : 0u;
   }
 #pragma unroll
-  for (int i = 0; i < 7; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const SplitFloat t = warp_sum_split(v[i]);
     if (lane == 0) part[i][warp] = t;
   }
-  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 7; ++i) {
-    v[i] = part[i][0];
-    for (int w = 1; w < kWarpsPerCta; ++w) v[i] = split_add(v[i], part[i][w]);
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t t = __reduce_add_sync(0xFFFFFFFFu, c[i]);
+    if (lane == 0) parts[i][warp] = t;
   }
-  const float tokens = v[4].hi, there = v[6].hi, per_token = 1.0f / fmaxf(tokens, 1.0f);
-  const float share = a.mode == NVFP4RL_LOSS_TOKEN_MEAN ? fmaxf(tokens, 1.0f)
-                      : a.mode == NVFP4RL_LOSS_SEQ_MEAN ? fmaxf(there, 1.0f) : a.norm;
+  __syncthreads();
+  // every warp joins the warps alike: the coefficients need the numbers
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = warp_sum_split(lane < warps ? part[i][lane] : SplitFloat{0.0f, 0.0f});
+#pragma unroll
+  for (int i = 0; i < 3; ++i) c[i] = __reduce_add_sync(0xFFFFFFFFu, lane < warps ? parts[i][lane] : 0u);
+  const float tokens = static_cast<float>(c[0]), there = static_cast<float>(c[2]), many = fmaxf(tokens, 1.0f);
+  const float share = a.mode == NVFP4RL_LOSS_TOKEN_MEAN ? many : a.mode == NVFP4RL_LOSS_SEQ_MEAN ? fmaxf(there, 1.0f) : a.norm;
   if (threadIdx.x == 0) {
     const float policy = v[0].hi / share, div = v[1].hi / share;
     const float loss = a.logp_ref && a.kl != 0.0f ? fmaf(a.kl, div, policy) : policy;
@@ -260,55 +365,102 @@ __global__ void __launch_bounds__(kThreads) policy_join_kernel(const PolicyArgs 
       a.stats[0] = loss;
       a.stats[1] = policy;
       a.stats[2] = div;
-      a.stats[3] = v[5].hi * per_token;
-      a.stats[4] = v[2].hi * per_token;
-      a.stats[5] = v[3].hi * per_token;
+      a.stats[3] = static_cast<float>(c[1]) / many;
+      a.stats[4] = v[2].hi / many;
+      a.stats[5] = v[3].hi / many;
       a.stats[6] = tokens;
       a.stats[7] = there;
     }
   }
   if (!a.coef) return;
-  for (int64_t b = threadIdx.x; b < a.B; b += kThreads) {
-    float c = 1.0f / share;
-    if (a.mode == NVFP4RL_LOSS_SEQ_MEAN) c = 1.0f / (fmaxf(__ldcg(&seqs[b].b).z, 1.0f) * share);
-    a.coef[b] = c;
+  const float same = 1.0f / share;
+  for (int64_t b = threadIdx.x; b < a.B; b += blockDim.x)
+    a.coef[b] = a.mode == NVFP4RL_LOSS_SEQ_MEAN
+                    ? 1.0f / (fmaxf(static_cast<float>(__ldcg(&seqs[b].tokens)), 1.0f) * share)
+                    : same;
+}
+
+__global__ void __launch_bounds__(kThreads) policy_sums_kernel(const PolicyArgs a, unsigned int* __restrict__ ticket,
+                                                               SlotSums* __restrict__ slots) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0u;  // for the kernel behind this one
+  const int64_t s = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
+  if (s * kLossStep >= a.n) return;
+  if (a.logp_ref) policy_step<true>(a, s, slots);
+  else policy_step<false>(a, s, slots);
+}
+
+__global__ void __launch_bounds__(kThreads) policy_join_kernel(const PolicyArgs a, unsigned int* __restrict__ ticket,
+                                                               const SlotSums* __restrict__ slots,
+                                                               SeqSums* __restrict__ seqs) {
+  __shared__ int last;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarpsPerCta;
+  for (int64_t b = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5); b < a.B; b += warps)
+    policy_sequence(a, b, slots, seqs);
+  __threadfence();  // this thread's sequences are visible before the CTA's ticket
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();  // and every other CTA's from here on
+  policy_finish(a, seqs);
+}
+
+// The whole of the loss in one CTA of 32 warps, for batches of few steps and sequences: one launch instead of two, and no
+// ticket (1843 tokens in 8 sequences: the two launches take 12 us one after the other, this one 7).
+constexpr int kOneWarps = 32, kOneRounds = 2;
+
+__global__ void __launch_bounds__(32 * kOneWarps) policy_one_kernel(const PolicyArgs a, SlotSums* __restrict__ slots,
+                                                                    SeqSums* __restrict__ seqs) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5;
+  for (int64_t s = warp; s * kLossStep < a.n; s += kOneWarps) {
+    if (a.logp_ref) policy_step<true>(a, s, slots);
+    else policy_step<false>(a, s, slots);
   }
+  __syncthreads();
+  for (int64_t b = warp; b < a.B; b += kOneWarps) policy_sequence(a, b, slots, seqs);
+  __syncthreads();
+  policy_finish(a, seqs);
+}
+
+template <bool kRef>
+__device__ __forceinline__ void policy_grad_step(const PolicyArgs& a, int64_t s) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
+  const float dloss = a.dloss ? __ldg(a.dloss) : 1.0f;
+  Step st;
+  load_step(a, t0, static_cast<int>(t1 - t0), st);
+  const Window win = window_at(a.offsets, a.B, t0);
+  float* out = a.dlogp + t0 + lane;
+  for_sequences(a.offsets, a.B, win, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
+    const int lo = static_cast<int>(from - t0), hi = static_cast<int>(to - t0);
+    const float coef = b < 0 ? 0.0f : dloss * __ldg(a.coef_in + b);
+    const float seq_adv = b < 0 || a.adv_per_token ? 0.0f : __ldg(a.adv + b);
+    const Clip seq_clip = clip_for(a, seq_adv);
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      if (32 * j + 32 <= lo || 32 * j >= hi) continue;
+      const int i = 32 * j + lane;
+      const float adv = a.adv_per_token ? st.adv[j] : seq_adv;
+      const Clip clip = a.adv_per_token ? clip_for(a, adv) : seq_clip;
+      const float g = coef * policy_token<true, kRef>(a, clip, st.lp[j], st.lo[j], kRef ? st.ref[j] : 0.0f, adv, st.w[j]).grad;
+      if (i >= lo && i < hi) out[32 * j] = (st.live >> j & 1) && b >= 0 ? g : 0.0f;
+    }
+  });
 }
 
 __global__ void __launch_bounds__(kThreads) policy_grad_kernel(const PolicyArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
   const int64_t s = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
-  const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
-  if (t0 >= a.n) return;
-  const float dloss = a.dloss ? __ldg(a.dloss) : 1.0f;
-  float lp[kPerLane], lo[kPerLane], ref[kPerLane], w[kPerLane], adv[kPerLane];
-  bool live[kPerLane];
-#pragma unroll
-  for (int j = 0; j < kPerLane; ++j) {
-    const int64_t t = t0 + 32 * j + lane;
-    const bool in = t < t1;
-    live[j] = in && (!a.mask || __ldg(a.mask + t) != 0);
-    lp[j] = in ? __ldg(a.logp + t) : 0.0f;
-    lo[j] = in ? __ldg(a.logp_old + t) : 0.0f;
-    ref[j] = a.logp_ref && in ? __ldg(a.logp_ref + t) : 0.0f;
-    w[j] = a.weights && in ? __ldg(a.weights + t) : 1.0f;
-    adv[j] = a.adv_per_token && in ? __ldg(a.adv + t) : 0.0f;
-  }
-  for_sequences(a.offsets, a.B, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
-    const float seq_adv = b < 0 || a.adv_per_token ? 0.0f : __ldg(a.adv + b);
-    const float c = b < 0 ? 0.0f : dloss * __ldg(a.coef_in + b);
-#pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      const int64_t t = t0 + 32 * j + lane;
-      if (t < from || t >= to) continue;
-      float g = 0.0f;
-      if (b >= 0 && live[j])
-        g = c * policy_token<true>(a, lp[j], lo[j], ref[j], a.adv_per_token ? adv[j] : seq_adv, w[j]).grad;
-      a.dlogp[t] = g;
-    }
-  });
+  if (s * kLossStep >= a.n) return;
+  if (a.logp_ref && a.kl != 0.0f) policy_grad_step<true>(a, s);
+  else policy_grad_step<false>(a, s);
 }
 
 // ---- the preference loss ----------------------------------------------------------------------------------
@@ -321,33 +473,38 @@ __global__ void __launch_bounds__(kThreads) preference_sums_kernel(const Prefere
   const int64_t s = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
   const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
   if (t0 >= a.n) return;
+  const int count = static_cast<int>(t1 - t0);
   float lp[kPerLane], ref[kPerLane];
-  bool live[kPerLane];
+  load_array(a.logp + t0 + lane, count, lp);
+  if (a.logp_ref) {
+    load_array(a.logp_ref + t0 + lane, count, ref);
+  } else {
 #pragma unroll
-  for (int j = 0; j < kPerLane; ++j) {
-    const int64_t t = t0 + 32 * j + lane;
-    const bool in = t < t1;
-    live[j] = in && (!a.mask || __ldg(a.mask + t) != 0);
-    lp[j] = in ? __ldg(a.logp + t) : 0.0f;
-    ref[j] = a.logp_ref && in ? __ldg(a.logp_ref + t) : 0.0f;
+    for (int j = 0; j < kPerLane; ++j) ref[j] = 0.0f;
   }
-  for_sequences(a.offsets, 2 * a.pairs, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
+  const uint32_t live = load_mask(a.mask, t0 + lane, count);
+  const Window win = window_at(a.offsets, 2 * a.pairs, t0);
+  for_sequences(a.offsets, 2 * a.pairs, win, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
     if (b < 0) return;
-    SplitFloat v{0.0f, 0.0f};
+    const int lo = static_cast<int>(from - t0), hi = static_cast<int>(to - t0);
+    // heads and rounding errors, in two sums side by side; an infinite head keeps no tail
+    SplitFloat v[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
     uint32_t tokens = 0;
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-      const int64_t t = t0 + 32 * j + lane;
-      if (live[j] && t >= from && t < to) {
-        SplitFloat d = two_sum(lp[j], -ref[j]);
-        if (!isfinite(d.hi)) d.lo = 0.0f;
-        v = split_add(v, d);
-        ++tokens;
-      }
+      const int i = 32 * j + lane;
+      const bool in = (live >> j & 1) && i >= lo && i < hi;
+      const SplitFloat d = two_sum(in ? lp[j] : 0.0f, in ? -ref[j] : 0.0f);  // logp - logp_ref, exactly
+      const SplitFloat h = two_sum(v[j & 1].hi, d.hi);
+      v[j & 1] = {h.hi, v[j & 1].lo + (h.lo + d.lo)};
+      tokens += in ? 1u : 0u;
     }
-    v = warp_sum_split(v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (!isfinite(v[i].hi)) v[i].lo = 0.0f;
+    const SplitFloat sum = warp_sum_split(split_add(v[0], v[1]));
     tokens = __reduce_add_sync(0xFFFFFFFFu, tokens);
-    if (lane == 0) slots[s + b] = make_float4(v.hi, v.lo, static_cast<float>(tokens), 0.0f);
+    if (lane == 0) slots[s + b] = make_float4(sum.hi, sum.lo, static_cast<float>(tokens), 0.0f);
   });
 }
 
@@ -362,12 +519,16 @@ __global__ void __launch_bounds__(kThreads) preference_join_kernel(const Prefere
   float share[2];
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
-    SplitFloat v[2];
-    sum_slots<2>(a.offsets, a.n, 2 * p + side, v, [&](int64_t i, SplitFloat (&u)[2]) {
-      const float4 x = __ldcg(slots + i);
-      u[0] = split_add(u[0], {x.x, x.y});
-      u[1] = split_add(u[1], {x.z, 0.0f});
-    });
+    SplitFloat v[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // the sum and the number of tokens
+    int64_t first, end;
+    slot_range(a.offsets, a.n, 2 * p + side, first, end);
+    for (int64_t k = first + (threadIdx.x & 31); k < end; k += 32) {
+      const float4 x = __ldcg(slots + k);
+      v[0] = split_add(v[0], {x.x, x.y});
+      v[1] = split_add(v[1], {x.z, 0.0f});
+    }
+    v[0] = warp_sum_split(v[0]);
+    v[1] = warp_sum_split(v[1]);
     total[side] = v[0];
     share[side] = 1.0f;
     if (a.mean) {
@@ -408,19 +569,20 @@ __global__ void __launch_bounds__(kThreads) preference_grad_kernel(const Prefere
   const int64_t s = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
   const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
   if (t0 >= a.n) return;
-  bool live[kPerLane];
-#pragma unroll
-  for (int j = 0; j < kPerLane; ++j) {
-    const int64_t t = t0 + 32 * j + lane;
-    live[j] = t < t1 && (!a.mask || __ldg(a.mask + t) != 0);
-  }
-  for_sequences(a.offsets, 2 * a.pairs, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
+  const uint32_t live = load_mask(a.mask, t0 + lane, static_cast<int>(t1 - t0));
+  const Window win = window_at(a.offsets, 2 * a.pairs, t0);
+  float* out = a.dlogp + t0 + lane;
+  for_sequences(a.offsets, 2 * a.pairs, win, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
+    const int lo = static_cast<int>(from - t0), hi = static_cast<int>(to - t0);
     const float c = b < 0 ? 0.0f : __ldg(a.coef_in + b) * (a.dloss ? __ldg(a.dloss + (b >> 1)) : 1.0f);
+    if (lo == 0 && hi == kLossStep) {
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      const int64_t t = t0 + 32 * j + lane;
-      if (t >= from && t < to) a.dlogp[t] = live[j] ? c : 0.0f;
+      for (int j = 0; j < kPerLane; ++j) out[32 * j] = live >> j & 1 ? c : 0.0f;
+      return;
     }
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j)
+      if (32 * j + lane >= lo && 32 * j + lane < hi) out[32 * j] = live >> j & 1 ? c : 0.0f;
   });
 }
 
@@ -433,7 +595,12 @@ dim3 warps_grid(int64_t warps) {
 nvfp4rl_status launch_policy_loss(const PolicyArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   auto* ticket = static_cast<unsigned int*>(a.ws);
   auto* slots = reinterpret_cast<SlotSums*>(static_cast<uint8_t*>(a.ws) + 256);
-  SlotSums* seqs = slots + loss_steps(a.n) + a.B;
+  auto* seqs = reinterpret_cast<SeqSums*>(slots + loss_steps(a.n) + a.B);
+  if (loss_steps(a.n) <= kOneRounds * kOneWarps && a.B <= kOneRounds * kOneWarps) {
+    if (launch_pdl(policy_one_kernel, dim3(1), dim3(32 * kOneWarps), 0, st, a, slots, seqs) != cudaSuccess)
+      return NVFP4RL_ERR_CUDA;
+    return launch_status();
+  }
   if (launch_pdl(policy_sums_kernel, warps_grid(loss_steps(a.n)), dim3(kThreads), 0, st, a, ticket, slots) != cudaSuccess)
     return NVFP4RL_ERR_CUDA;
   if (launch_status() != NVFP4RL_OK) return NVFP4RL_ERR_CUDA;

@@ -54,6 +54,7 @@ constexpr int kSegments = 8, kSegmentReaders = 18;  // a ring of segments, read 
 // Registers by warpgroup, out of the 96 that each of the 640 threads starts with.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kDecodeRegs = 72, kOtherRegs = 64;
 static_assert(2 * kSoftmaxRegs + 2 * kDecodeRegs + kOtherRegs <= 5 * kLaunchRegs, "within the launch's registers");
+static_assert(kSoftmaxRegs >= kLaunchRegs && kDecodeRegs <= kLaunchRegs && kOtherRegs <= kLaunchRegs, "inc raises, dec lowers");
 constexpr uint32_t kOcol = 384, kTmemCols = 512;  // S / P of blocks n % 3 from column 128 (n % 3) on, then O
 constexpr float kSlack = 8.0f, kLift = 6.0f;                 // log2 units
 constexpr float kLog2e = 1.4426950408889634f;

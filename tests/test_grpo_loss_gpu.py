@@ -268,3 +268,12 @@ def test_given_outputs_count_as_modified(nv):
                          workspace=ws)
     g = nv.policy_loss_backward(dev(logp), dev(old), dev(np.ones(2, np.float32)), off, outs[2], out=outs[3])
     assert got[0] is outs[0] and g is outs[3] and all(t._version > w for t, w in zip(outs, v))
+
+
+def test_no_weight_on_the_divergence_leaves_it_out(nv):
+    """kl_coef 0 with a reference far off (e^x overflows): the gradient and the loss do not see it."""
+    old = np.array([-1, -2, -300], np.float32)
+    ref = np.array([-1.5, -1, 0], np.float32)
+    adv, off = np.array([0.5], np.float32), np.array([0, 3], np.int32)
+    a, b = (run_policy(nv, old, old, adv, off, ref=r) for r in (ref, None))
+    assert a["stats"][2] == np.inf and np.array_equal(a["loss"], b["loss"]) and np.array_equal(a["dlogp"], b["dlogp"])
