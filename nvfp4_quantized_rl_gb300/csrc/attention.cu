@@ -163,7 +163,11 @@ __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.
 // What a CTA of kv_attention_kernel attends for.
 enum : int {
   kDecode = 0,  // the heads of one sequence over its own cache, the whole of the attention
-  kOwn = 1,     // the same beside a shared prefix (prefix_attention.cu): always a partial result
+  // The same beside a shared prefix (prefix_attention.cu), always a partial result: each warp has a span of its own, since
+  // the own caches are short, and a CTA's start and the joining of its warps took longer than a warp's few groups (256
+  // sequences of 8 KV heads with up to 500 tokens behind long prefixes: 176 us by CTAs, 165 by warps, 64 of 4 with up to 700: 51
+  // and 48)
+  kOwn = 1,
 };
 
 struct AttnArgs {
@@ -177,7 +181,7 @@ struct AttnArgs {
   uint16_t* out;     // used when nsplit == 1
   float* part;       // [B*Hkv][nsplit][16][kPartFloats] when nsplit > 1
   uint32_t* status;  // the library's error word: a wait that gave up sets a timeout bit
-  int64_t ldq = 0;  // kOwn: elements between two sequences' queries
+  int64_t ldq = 0, B = 0;  // kOwn: elements between two sequences' queries, sequences
 };
 
 // kNH: 8-column tiles of query heads (1: up to 8 heads per KV head, 2: up to 16).
@@ -199,29 +203,41 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
     fence_barrier_init();
   }
   __syncwarp();
-  const int64_t bh = blockIdx.y, b = bh / a.Hkv, kvh = bh % a.Hkv;
+  constexpr int kShare = kKind == kOwn ? 1 : kWarps;  // warps to a span
+  const int part = kKind == kOwn ? 0 : warp;          // which of them
+  const int64_t bh = kKind == kOwn ? static_cast<int64_t>(blockIdx.y) * kWarps + warp : blockIdx.y, b = bh / a.Hkv, kvh = bh % a.Hkv;
   const int group = static_cast<int>(a.Hq / a.Hkv);
-  griddep_wait();
+  // kOwn: the kernel ahead is the prefix kernel, of whose results this one takes nothing; its CTAs start this
+  // one's only behind their own wait for what came before them, the queries and caches among it. So the two run side
+  // by side where there is room (8 sequences behind one short prefix 22 -> 18 us, 64 behind four 56 -> 51), and one CTA's
+  // wait at its end keeps the order for the kernel behind.
+  const auto in_order = [&]() {
+    if (kKind == kOwn && blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();
+  };
+  if (kKind == kDecode) griddep_wait();
   griddep_launch_dependents();
-  const int64_t len = min(max(static_cast<int64_t>(a.lens[b]), int64_t(0)), a.Lmax);
+  const int64_t len = kKind == kOwn && b >= a.B ? 0 : min(max(static_cast<int64_t>(a.lens[b]), int64_t(0)), a.Lmax);
   // a partial result is of an equal span of the actual length, not of the cache
-  const int64_t span = kKind == kDecode ? a.span : own_span(len, a.nsplit);
+  const int64_t span = kKind == kOwn ? own_span(len, a.nsplit) : a.span;
   const int64_t t_begin = static_cast<int64_t>(blockIdx.x) * span;
   const int64_t t_end = min(t_begin + span, len);
-  if (kKind == kOwn && t_begin >= len) return;  // empty spans are left out of the join
+  if (kKind == kOwn && t_begin >= len) {  // empty spans are left out of the join
+    in_order();
+    return;
+  }
   const int ngroups = t_end > t_begin ? static_cast<int>((t_end - t_begin + kTok - 1) / kTok) : 0;
-  const int mine = ngroups > warp ? (ngroups - warp + kWarps - 1) / kWarps : 0;  // groups warp, warp + 4, ...
+  const int mine = ngroups > part ? (ngroups - part + kShare - 1) / kShare : 0;  // groups part, part + kShare, ..
   const int64_t row0 = b * a.Lmax;  // cache row of the sequence's token 0
   // scale rows: lane l copies rows l and l + 32 of each group; sr = the row offset of its first
   // row of group 0, advanced by one stride per group
-  const int64_t srow_step = static_cast<int64_t>(kWarps) * kTok * a.Hkv * (kHeadDim / 16);
-  const int64_t sr0 = ((row0 + t_begin + static_cast<int64_t>(warp) * kTok + lane) * a.Hkv + kvh) * (kHeadDim / 16);
-  const int64_t t_lane = t_begin + static_cast<int64_t>(warp) * kTok + lane;  // token of that row
+  const int64_t srow_step = static_cast<int64_t>(kShare) * kTok * a.Hkv * (kHeadDim / 16);
+  const int64_t sr0 = ((row0 + t_begin + static_cast<int64_t>(part) * kTok + lane) * a.Hkv + kvh) * (kHeadDim / 16);
+  const int64_t t_lane = t_begin + static_cast<int64_t>(part) * kTok + lane;  // token of that row
 
-  // group n of this warp (tokens t_begin + 64 (warp + 4 n) ..) into slot n % kStages
+  // group n of this warp (tokens t_begin + 64 (part + kShare n) ..) into slot n % kStages
   const auto issue = [&](int n) {
     const int slot = n % kStages;
-    const int64_t t0 = t_begin + static_cast<int64_t>(warp + n * kWarps) * kTok;
+    const int64_t t0 = t_begin + static_cast<int64_t>(part + n * kShare) * kTok;
     const uint32_t sb = ring + slot * kSlotBytes, bar = bar0 + 8 * slot;
     if (lane == 0) {
       fence_proxy_async();  // this warp's reads of the slot's previous bytes come before the copies
@@ -231,7 +247,7 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
     }
     // rows at or past t_end read nothing and land as zeros, which zeroes those tokens' K and V
     // whatever their code bytes
-    const int64_t t = t_lane + static_cast<int64_t>(n) * kWarps * kTok;
+    const int64_t t = t_lane + static_cast<int64_t>(n) * kShare * kTok;
     const int64_t off = sr0 + n * srow_step;
     const int64_t off32 = off + 32 * a.Hkv * (kHeadDim / 16);
     const bool live0 = t < t_end, live1 = t + 32 < t_end;
@@ -314,7 +330,7 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
     }
     const uint32_t kb = ring + slot * kSlotBytes, vb = kb + kCodeBytes, ksb = kb + 2 * kCodeBytes,
                    vsb = ksb + kScaleBytes;
-    const int64_t t0 = t_begin + static_cast<int64_t>(warp + done * kWarps) * kTok;
+    const int64_t t0 = t_begin + static_cast<int64_t>(part + done * kShare) * kTok;
 
     // S^T = K Q^T, one 16-token step (rows step_token(g), step_token(g + 8)) at a time
     float sacc[4][kNH][4];
@@ -468,6 +484,28 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
       l_run[h][e] += __shfl_xor_sync(0xFFFFFFFFu, l_run[h][e], 8);
       l_run[h][e] += __shfl_xor_sync(0xFFFFFFFFu, l_run[h][e], 16);
     }
+  if constexpr (kKind == kOwn) {
+    // this warp's result is the span's: through its ring, a row at a time to its place
+    __syncwarp();
+    float* rows = reinterpret_cast<float*>(smem_raw + (ring - raw));  // [16 heads][128 dims]
+    float* pr = a.part + (bh * a.nsplit + blockIdx.x) * (kOwnRows * kPartFloats);
+    static_assert(kStages * kSlotBytes >= kOwnRows * kHeadDim * sizeof(float), "the ring holds the rows");
+#pragma unroll
+    for (int h = 0; h < kNH; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * h + 2 * q + e;
+        if (g == 0 && r < group) *reinterpret_cast<float2*>(pr + r * kPartFloats) = make_float2(m_run[h][e], l_run[h][e]);
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          *reinterpret_cast<float2*>(rows + r * kHeadDim + 16 * g + 2 * m) = make_float2(oacc[m][h][e], oacc[m][h][2 + e]);
+      }
+    __syncwarp();
+    for (int r = 0; r < group; ++r)
+      *reinterpret_cast<float4*>(pr + r * kPartFloats + 4 + 4 * lane) = *reinterpret_cast<const float4*>(rows + r * kHeadDim + 4 * lane);
+    in_order();
+    return;
+  }
   __syncthreads();  // every warp is done with its ring: it becomes the merge area
   float* Osm = reinterpret_cast<float*>(smem_raw + (ring0 - raw));  // [warp][16 heads][128 dims]
   if (g == 0) {
@@ -513,6 +551,7 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
       pr[4 + d] = O;
     }
   }
+  in_order();
 }
 
 // Merges the spans of every (sequence, query head): out = sum_s f_s O_s / sum_s f_s L_s * gv,
@@ -587,23 +626,32 @@ bool allow_smem(int device) {
 
 }  // namespace
 
+namespace {
+// Spans of an own cache beside a prefix: about two rounds of the warps that the GPU holds (one round left 256 sequences of 8
+// KV heads at 171 us, two 165).
+int own_splits(int64_t B, int64_t Hkv, int64_t Lmax) {
+  const int64_t chunks = std::max<int64_t>(1, (Lmax + kTok - 1) / kTok), warps = 2 * 3 * kWarps * kNumSMsHint;
+  return static_cast<int>(std::min<int64_t>({chunks, (warps + B * Hkv - 1) / (B * Hkv), 256}));
+}
+}  // namespace
+
 size_t own_partials_bytes(int64_t B, int64_t Hkv, int64_t Lmax) {
   if (B == 0 || Lmax == 0) return 0;
-  return static_cast<size_t>(B * Hkv) * attention_splits(B, Hkv, Lmax) * kOwnRows * kOwnFloats * sizeof(float);
+  return static_cast<size_t>(B * Hkv) * own_splits(B, Hkv, Lmax) * kOwnRows * kOwnFloats * sizeof(float);
 }
 
 // The decode kernel over the sequences' own caches beside shared prefixes, for launch_prefix_attention.
 nvfp4rl_status launch_own_partials(const PrefixAttnArgs& p, float* part, OwnPartials* out, const DeviceInfo& dev,
                                    cudaStream_t st) {
-  const int ns = attention_splits(p.B, p.Hkv, p.Lmax);
+  const int ns = own_splits(p.B, p.Hkv, p.Lmax);
   *out = {part, ns};
   CUtensorMap mk, mv;
   if (!code_map(&mk, p.kc, p.B * p.Lmax, p.Hkv) || !code_map(&mv, p.vc, p.B * p.Lmax, p.Hkv)) return NVFP4RL_ERR_CUDA;
-  const AttnArgs a{p.q, p.ks, p.vs, p.gk, p.gv, p.lens, p.Hq, p.Hkv, p.Lmax, ns, 0, p.scale, nullptr, part, dev.status, p.ldq};
+  const AttnArgs a{p.q, p.ks, p.vs, p.gk, p.gv, p.lens, p.Hq, p.Hkv, p.Lmax, ns, 0, p.scale, nullptr, part, dev.status, p.ldq, p.B};
   const auto kernel = p.Hq / p.Hkv > 8 ? kv_attention_kernel<2, kOwn> : kv_attention_kernel<1, kOwn>;
   if (!allow_smem(dev.device)) return NVFP4RL_ERR_CUDA;
-  if (launch_pdl(kernel, dim3(static_cast<unsigned>(ns), static_cast<unsigned>(p.B * p.Hkv)), dim3(kAttnThreads), kAttnSmem,
-                 st, mk, mv, a) != cudaSuccess)
+  const dim3 grid(static_cast<unsigned>(ns), static_cast<unsigned>((p.B * p.Hkv + kWarps - 1) / kWarps));
+  if (launch_pdl(kernel, grid, dim3(kAttnThreads), kAttnSmem, st, mk, mv, a) != cudaSuccess)
     return NVFP4RL_ERR_CUDA;
   return launch_status();
 }

@@ -839,6 +839,11 @@ struct JoinArgs {
   uint16_t* out;
 };
 
+// A warp per row; kAhead partials in flight. Sixteen where the rows are no more than the warps that then fit the GPU (1792 rows of
+// up to 17 partials: the whole call 42 us, by fours 47), four where more rows at a time do better (10240 of about 5:
+// 165 us, by sixteens 173).
+constexpr int kJoinFew = 16;  // warps per SM
+template <int kAhead>
 __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
   griddep_wait();
   griddep_launch_dependents();
@@ -883,16 +888,24 @@ __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) O[q] *= keep;
     M = m;
-#pragma unroll 4
-    for (int k = 0; k < count; ++k) {
-      const float w = __shfl_sync(0xFFFFFFFFu, f, k);
-      // the four rows of a CTA's warps share their sectors in L1
-      const float4 v = i0 + k < npre ? a.part[part_at(s0 + i0 + k, lane, tile_row)]
-                                     : reinterpret_cast<const float4*>(own_at(i0 + k) + 4)[lane];
-      O[0] = fmaf(w, v.x, O[0]);
-      O[1] = fmaf(w, v.y, O[1]);
-      O[2] = fmaf(w, v.z, O[2]);
-      O[3] = fmaf(w, v.w, O[3]);
+#pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += kAhead) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int at = i0 + k0 + k;
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // the four rows of a CTA's warps share their sectors in L1
+        if (k0 + k < count) v[k] = at < npre ? a.part[part_at(s0 + at, lane, tile_row)] : reinterpret_cast<const float4*>(own_at(at) + 4)[lane];
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float w = __shfl_sync(0xFFFFFFFFu, f, (k0 + k) & 31);  // past the end: times zeros
+        O[0] = fmaf(w, v[k].x, O[0]);
+        O[1] = fmaf(w, v[k].y, O[1]);
+        O[2] = fmaf(w, v[k].z, O[2]);
+        O[3] = fmaf(w, v[k].w, O[3]);
+      }
     }
   }
   const float inv = L > 0.0f ? __ldg(a.gv) / L : 0.0f;
@@ -935,7 +948,9 @@ nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo
       done = true;
     }
   }
-  const int grid = std::min(dev.sm_count, kPlanSMs);
+  // no more CTAs than blocks there can be, so that few leave SMs to the kernel behind
+  const int64_t units = tiles * p.Hkv * ((p.Lp + kBlock - 1) / kBlock);
+  const int grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(units, 1), std::min(dev.sm_count, kPlanSMs)));
   const PrefixArgs a{p.q, p.ldq, p.pkc, p.pks, p.pvc, p.pvs, p.gk, groups, heads, p.scale, part, stats, dev.status};
   if (launch_pdl(prefix_attention_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, st, a) !=
       cudaSuccess)
@@ -948,8 +963,8 @@ nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo
     if (s != NVFP4RL_OK) return s;
   }
   const JoinArgs j{part, stats, grid, groups, partials, p.lens, p.Lmax, static_cast<int>(p.Hq), heads, p.gv, p.out};
-  if (launch_pdl(kv_prefix_join_kernel, dim3(static_cast<unsigned>(p.B * ((p.Hq + 3) / 4))), dim3(128), 0, st, j) !=
-      cudaSuccess)
+  const auto join = p.B * p.Hq <= static_cast<int64_t>(kJoinFew) * dev.sm_count ? kv_prefix_join_kernel<16> : kv_prefix_join_kernel<4>;
+  if (launch_pdl(join, dim3(static_cast<unsigned>(p.B * ((p.Hq + 3) / 4))), dim3(128), 0, st, j) != cudaSuccess)
     return NVFP4RL_ERR_CUDA;
   return launch_status();
 }
