@@ -1,16 +1,17 @@
 // Losses over packed token log-probs (sm_103a): the clipped policy loss with a KL term and the
 // preference loss of paired log ratios, forward and backward. include/nvfp4rl.h states the formulas.
 //
-// All four stream a few fp32 arrays once, so HBM (or L2) would bound them; the policy loss's arithmetic, some 100 instructions
-// a token, and its loads' latency do. A warp takes a step of 256 consecutive tokens (coalesced 4-byte loads at any
-// alignment, eight per array in flight per lane), computes its eight tokens per lane in pairs (packed fp32) and without
-// branches, walks the sequences that meet the step, sums each one's tokens over its lanes and leaves the sums in the slot
-// (step + sequence). A second kernel adds a sequence's slots in order, one warp to a sequence, and the CTA that finishes
-// last joins the sequences; small batches do both in one CTA. No floating-point atomics: equal inputs give equal bits.
+// All four stream a few fp32 arrays once, so HBM (or L2) would bound them; the policy loss's arithmetic, some 110 instructions
+// a token, half of them compares and selects, and its loads' latency do. A warp takes steps of 256 consecutive tokens
+// (coalesced 4-byte loads at any alignment, eight per array in flight per lane), computes its eight tokens per lane in pairs
+// (packed fp32) and without branches, walks the sequences that meet the step, sums each one's tokens over its lanes and
+// leaves the sums in the slot (step + sequence). A second kernel adds a sequence's slots in order, one warp to a sequence,
+// and the CTA that finishes last joins the sequences; small batches do both in one CTA. No floating-point atomics: equal
+// inputs give equal bits.
 //
-// 4 Mi tokens in 512 sequences with every term: forward and backward 58 us, 0.22 of the measured copy bandwidth (tokens one
-// at a time and expf 65 us, branches in the token 137). Three CTAs of 80 registers an SM: two of 106 take 62 us, four of
-// 64 63 us. 2 Mi tokens in 2048 sequences of the preference loss: 20 us, 0.2.
+// 4 Mi tokens in 512 sequences with every term: forward and backward 54 us, 0.24 of the measured copy bandwidth, in one
+// wave of warps that each take a stretch of the steps and load the next step ahead (a warp for each step 58 us; tokens one
+// at a time and expf 65; branches in the token 137). 2 Mi tokens in 2048 sequences of the preference loss: 20 us, 0.2.
 //
 // Ratios next to a bound: whether r = e^d lies above 1 + eps is decided as d > ln(1 + eps), with d the exact
 // difference of the two log-probs (two floats, from one TwoSum) and the logarithm split into two floats, so
@@ -136,13 +137,14 @@ __device__ __forceinline__ Window window_at(const int32_t* __restrict__ offsets,
 }
 
 // The sequences of tokens [t0, t1), in order: f(b, s, e) for the part [s, e) that sequence b has of them;
-// b = -1 for tokens of no sequence. Whole warp. Offsets that fall are answered with some split of the
+// b = -1 for tokens of no sequence. Whole warp. The window is of t0 or earlier tokens, and moves on where it ends. Offsets that fall are answered with some split of the
 // tokens, each in one part.
 template <class F>
-__device__ __forceinline__ void for_sequences(const int32_t* __restrict__ offsets, int64_t B, Window w, int64_t t0,
+__device__ __forceinline__ void for_sequences(const int32_t* __restrict__ offsets, int64_t B, Window& w, int64_t t0,
                                               int64_t t1, F&& f) {
   int64_t t = t0, seen = -1;
-  int k = 0;
+  const uint32_t behind = __ballot_sync(0xFFFFFFFFu, w.end > t0);
+  int k = behind ? __ffs(behind) - 1 : 32;
   while (t < t1) {
     if (k == 32) {  // more sequences (or empty ones) than the window has
       if (t == seen) {  // offsets that fall: the rest is of no sequence
@@ -220,10 +222,11 @@ __device__ __forceinline__ Pair policy_pair(const PolicyArgs& a, const Clip& c0,
   return t;
 }
 
-// A step's tokens of this lane: token 32 j + lane of the step, live where it counts, with its advantage.
+// A step's tokens of this lane: token 32 j + lane of the step, with its advantage and whether it counts (nonzero).
+template <bool kRef, bool kTok>
 struct Step {
-  float lp[kPerLane], lo[kPerLane], ref[kPerLane], w[kPerLane], adv[kPerLane];
-  uint32_t live;  // bit j
+  float lp[kPerLane], lo[kPerLane], ref[kRef ? kPerLane : 1], w[kPerLane], adv[kTok ? kPerLane : 1];
+  uint8_t mask[kPerLane];
 };
 
 // One array of a step, `count` tokens long, from its first token of this lane on: constant offsets, no bounds in whole steps.
@@ -237,34 +240,55 @@ __device__ __forceinline__ void load_array(const T* __restrict__ p, int count, T
     for (int j = 0; j < kPerLane; ++j) v[j] = 32 * j + static_cast<int>(threadIdx.x & 31) < count ? __ldg(p + 32 * j) : T(0);
   }
 }
-// Which of the lane's tokens are there and not masked.
-__device__ __forceinline__ uint32_t load_mask(const uint8_t* __restrict__ mask, int64_t at, int count) {
-  uint32_t live = 0;
+// Whether the lane's tokens are there and not masked.
+__device__ __forceinline__ void load_mask(const uint8_t* __restrict__ mask, int64_t at, int count, uint8_t (&m)[kPerLane]) {
   if (mask) {
-    uint8_t m[kPerLane];
     load_array(mask + at, count, m);
-#pragma unroll
-    for (int j = 0; j < kPerLane; ++j) live |= m[j] ? 1u << j : 0u;
   } else {
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) live |= 32 * j + static_cast<int>(threadIdx.x & 31) < count ? 1u << j : 0u;
+    for (int j = 0; j < kPerLane; ++j) m[j] = 32 * j + static_cast<int>(threadIdx.x & 31) < count;
   }
+}
+__device__ __forceinline__ uint32_t mask_bits(const uint8_t (&m)[kPerLane]) {
+  uint32_t live = 0;
+#pragma unroll
+  for (int j = 0; j < kPerLane; ++j) live |= m[j] ? 1u << j : 0u;
   return live;
 }
 
-__device__ __forceinline__ void load_step(const PolicyArgs& a, int64_t t0, int count, Step& s) {
+template <bool kRef, bool kTok>
+__device__ __forceinline__ void load_step(const PolicyArgs& a, int64_t t0, Step<kRef, kTok>& s) {
   const int64_t at = t0 + (threadIdx.x & 31);
+  const int count = static_cast<int>(min(a.n - t0, static_cast<int64_t>(kLossStep)));
   load_array(a.logp + at, count, s.lp);
   load_array(a.logp_old + at, count, s.lo);
-  if (a.logp_ref) load_array(a.logp_ref + at, count, s.ref);
-  if (a.adv_per_token) load_array(a.adv + at, count, s.adv);
+  if constexpr (kRef) load_array(a.logp_ref + at, count, s.ref);
+  if constexpr (kTok) load_array(a.adv + at, count, s.adv);
   if (a.weights) {
     load_array(a.weights + at, count, s.w);
   } else {
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) s.w[j] = 1.0f;
   }
-  s.live = load_mask(a.mask, at, count);
+  load_mask(a.mask, at, count, s.mask);
+}
+
+// A warp's equal stretch of the steps: f(s, step, window) for each, the next one's loads under way meanwhile.
+template <bool kRef, bool kTok, class F>
+__device__ __forceinline__ void for_steps(const PolicyArgs& a, F&& f) {
+  const int64_t steps = (a.n + kLossStep - 1) / kLossStep, warps = static_cast<int64_t>(gridDim.x) * kWarpsPerCta;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5), end = steps * (w + 1) / warps;
+  int64_t s = steps * w / warps;
+  if (s >= end) return;
+  Step<kRef, kTok> next;
+  load_step(a, s * kLossStep, next);
+  Window win = window_at(a.offsets, a.B, s * kLossStep);
+#pragma unroll 1
+  for (; s < end; ++s) {
+    const Step<kRef, kTok> st = next;
+    if (s + 1 < end) load_step(a, (s + 1) * kLossStep, next);
+    f(s, st, win);
+  }
 }
 
 // Bit j: token 32 j + lane of the step is in [lo, hi), parts of 0 .. 256.
@@ -287,22 +311,21 @@ struct SeqSums {
 };
 static_assert(sizeof(SlotSums) == 32 && sizeof(SeqSums) == 32, "as policy_workspace_bytes has them");
 
-template <bool kRef>
-__device__ __forceinline__ void policy_step(const PolicyArgs& a, int64_t s, SlotSums* __restrict__ slots) {
+template <bool kRef, bool kTok>
+__device__ __forceinline__ void policy_step(const PolicyArgs& a, int64_t s, const Step<kRef, kTok>& st, Window& win,
+                                            SlotSums* __restrict__ slots) {
   const int lane = threadIdx.x & 31;
   const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
-  Step st;
-  load_step(a, t0, static_cast<int>(t1 - t0), st);
-  const Window win = window_at(a.offsets, a.B, t0);
+  const uint32_t there = mask_bits(st.mask);
   for_sequences(a.offsets, a.B, win, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
     if (b < 0) return;
     const int lo = static_cast<int>(from - t0), hi = static_cast<int>(to - t0);
-    const uint32_t live = st.live & part_mask(lo, hi);
+    const uint32_t live = there & part_mask(lo, hi);
     F2 u[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
     uint32_t clipped = 0;
     // tokens j and j + 1 of the lane
     const auto pair = [&](int j, const Clip& c0, const Clip& c1, float adv0, float adv1) {
-      const F2 ref = kRef ? pack2(st.ref[j], st.ref[j + 1]) : both(0.0f);
+      const F2 ref = kRef ? pack2(st.ref[kRef ? j : 0], st.ref[kRef ? j + 1 : 0]) : both(0.0f);
       const Pair k = policy_pair<false, kRef>(a, c0, c1, pack2(st.lp[j], st.lp[j + 1]), pack2(st.lo[j], st.lo[j + 1]), ref,
                                               adv0, adv1, pack2(st.w[j], st.w[j + 1]));
       const bool in0 = live >> j & 1, in1 = live >> (j + 1) & 1;
@@ -313,7 +336,7 @@ __device__ __forceinline__ void policy_step(const PolicyArgs& a, int64_t s, Slot
       u[3] = add2(u[3], pick2(in0, in1, k.ratio, none));
       clipped |= (k.clipped[0] ? 1u << j : 0u) | (k.clipped[1] ? 2u << j : 0u);
     };
-    if (a.adv_per_token) {
+    if constexpr (kTok) {
 #pragma unroll
       for (int j = 0; j < kPerLane; j += 2) pair(j, clip_for(a, st.adv[j]), clip_for(a, st.adv[j + 1]), st.adv[j], st.adv[j + 1]);
     } else {
@@ -441,17 +464,16 @@ __device__ __forceinline__ void policy_finish(const PolicyArgs& a, const SeqSums
                     : same;
 }
 
-constexpr int kPolicyCtas = 3;  // per SM
+// Per SM: two of 128 registers, which hold two steps (three of 80 spill them: 74 us instead of 54).
+constexpr int kPolicyCtas = 2;
 
+template <bool kRef, bool kTok>
 __global__ void __launch_bounds__(kThreads, kPolicyCtas) policy_sums_kernel(const PolicyArgs a, unsigned int* __restrict__ ticket,
-                                                               SlotSums* __restrict__ slots) {
+                                                                            SlotSums* __restrict__ slots) {
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0u;  // for the kernel behind this one
-  const int64_t s = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
-  if (s * kLossStep >= a.n) return;
-  if (a.logp_ref) policy_step<true>(a, s, slots);
-  else policy_step<false>(a, s, slots);
+  for_steps<kRef, kTok>(a, [&](int64_t s, const Step<kRef, kTok>& st, Window& win) { policy_step(a, s, st, win, slots); });
 }
 
 __global__ void __launch_bounds__(kThreads) policy_join_kernel(const PolicyArgs a, unsigned int* __restrict__ ticket,
@@ -477,14 +499,18 @@ __global__ void __launch_bounds__(kThreads) policy_join_kernel(const PolicyArgs 
 // 8000 took 12.4 instead of 8.3, and 32 warps, with half the registers, 10.6 for the 1843).
 constexpr int kOneWarps = 16;
 
+template <bool kRef, bool kTok>
 __global__ void __launch_bounds__(32 * kOneWarps) policy_one_kernel(const PolicyArgs a, SlotSums* __restrict__ slots,
                                                                     SeqSums* __restrict__ seqs) {
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5;
-  if (static_cast<int64_t>(warp) * kLossStep < a.n) {
-    if (a.logp_ref) policy_step<true>(a, warp, slots);
-    else policy_step<false>(a, warp, slots);
+  const int64_t t0 = static_cast<int64_t>(warp) * kLossStep;
+  if (t0 < a.n) {
+    Step<kRef, kTok> st;
+    load_step(a, t0, st);
+    Window win = window_at(a.offsets, a.B, t0);
+    policy_step(a, warp, st, win, slots);
   }
   __syncthreads();
   if (warp < a.B) policy_sequence(a, warp, slots, seqs);
@@ -492,27 +518,24 @@ __global__ void __launch_bounds__(32 * kOneWarps) policy_one_kernel(const Policy
   policy_finish(a, seqs);
 }
 
-template <bool kRef>
-__device__ __forceinline__ void policy_grad_step(const PolicyArgs& a, int64_t s) {
+template <bool kRef, bool kTok>
+__device__ __forceinline__ void policy_grad_step(const PolicyArgs& a, float dloss, int64_t s, const Step<kRef, kTok>& st, Window& win) {
   const int lane = threadIdx.x & 31;
   const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
-  const float dloss = a.dloss ? __ldg(a.dloss) : 1.0f;
-  Step st;
-  load_step(a, t0, static_cast<int>(t1 - t0), st);
-  const Window win = window_at(a.offsets, a.B, t0);
+  const uint32_t there = mask_bits(st.mask);
   float* out = a.dlogp + t0 + lane;
   for_sequences(a.offsets, a.B, win, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
     const int lo = static_cast<int>(from - t0), hi = static_cast<int>(to - t0);
     const float coef = b < 0 ? 0.0f : dloss * __ldg(a.coef_in + b);
-    const float seq_adv = b < 0 || a.adv_per_token ? 0.0f : __ldg(a.adv + b);
+    const float seq_adv = b < 0 || kTok ? 0.0f : __ldg(a.adv + b);
     const Clip seq_clip = clip_for(a, seq_adv);
-    const uint32_t part = part_mask(lo, hi), live = b >= 0 ? st.live & part : 0u;
+    const uint32_t part = part_mask(lo, hi), live = b >= 0 ? there & part : 0u;
 #pragma unroll
     for (int j = 0; j < kPerLane; j += 2) {
       if (32 * j + 64 <= lo || 32 * j >= hi) continue;
-      const float adv0 = a.adv_per_token ? st.adv[j] : seq_adv, adv1 = a.adv_per_token ? st.adv[j + 1] : seq_adv;
-      const Clip c0 = a.adv_per_token ? clip_for(a, adv0) : seq_clip, c1 = a.adv_per_token ? clip_for(a, adv1) : seq_clip;
-      const F2 ref = kRef ? pack2(st.ref[j], st.ref[j + 1]) : both(0.0f);
+      const float adv0 = kTok ? st.adv[kTok ? j : 0] : seq_adv, adv1 = kTok ? st.adv[kTok ? j + 1 : 0] : seq_adv;
+      const Clip c0 = kTok ? clip_for(a, adv0) : seq_clip, c1 = kTok ? clip_for(a, adv1) : seq_clip;
+      const F2 ref = kRef ? pack2(st.ref[kRef ? j : 0], st.ref[kRef ? j + 1 : 0]) : both(0.0f);
       const Pair k = policy_pair<true, kRef>(a, c0, c1, pack2(st.lp[j], st.lp[j + 1]), pack2(st.lo[j], st.lo[j + 1]), ref, adv0,
                                              adv1, pack2(st.w[j], st.w[j + 1]));
       float g0, g1;
@@ -523,13 +546,12 @@ __device__ __forceinline__ void policy_grad_step(const PolicyArgs& a, int64_t s)
   });
 }
 
+template <bool kRef, bool kTok>
 __global__ void __launch_bounds__(kThreads, kPolicyCtas) policy_grad_kernel(const PolicyArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t s = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
-  if (s * kLossStep >= a.n) return;
-  if (a.logp_ref && a.kl != 0.0f) policy_grad_step<true>(a, s);
-  else policy_grad_step<false>(a, s);
+  const float dloss = a.dloss ? __ldg(a.dloss) : 1.0f;
+  for_steps<kRef, kTok>(a, [&](int64_t s, const Step<kRef, kTok>& st, Window& win) { policy_grad_step(a, dloss, s, st, win); });
 }
 
 // ---- the preference loss ----------------------------------------------------------------------------------
@@ -551,8 +573,10 @@ __global__ void __launch_bounds__(kThreads) preference_sums_kernel(const Prefere
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) ref[j] = 0.0f;
   }
-  const uint32_t live = load_mask(a.mask, t0 + lane, count);
-  const Window win = window_at(a.offsets, 2 * a.pairs, t0);
+  uint8_t m[kPerLane];
+  load_mask(a.mask, t0 + lane, count, m);
+  Window win = window_at(a.offsets, 2 * a.pairs, t0);
+  const uint32_t live = mask_bits(m);
   for_sequences(a.offsets, 2 * a.pairs, win, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
     if (b < 0) return;
     const int lo = static_cast<int>(from - t0), hi = static_cast<int>(to - t0);
@@ -638,8 +662,10 @@ __global__ void __launch_bounds__(kThreads) preference_grad_kernel(const Prefere
   const int64_t s = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
   const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
   if (t0 >= a.n) return;
-  const uint32_t live = load_mask(a.mask, t0 + lane, static_cast<int>(t1 - t0));
-  const Window win = window_at(a.offsets, 2 * a.pairs, t0);
+  uint8_t m[kPerLane];
+  load_mask(a.mask, t0 + lane, static_cast<int>(t1 - t0), m);
+  Window win = window_at(a.offsets, 2 * a.pairs, t0);
+  const uint32_t live = mask_bits(m);
   float* out = a.dlogp + t0 + lane;
   for_sequences(a.offsets, 2 * a.pairs, win, t0, t1, [&](int64_t b, int64_t from, int64_t to) {
     const int lo = static_cast<int>(from - t0), hi = static_cast<int>(to - t0);
@@ -661,16 +687,26 @@ dim3 warps_grid(int64_t warps) {
 
 }  // namespace
 
-nvfp4rl_status launch_policy_loss(const PolicyArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+namespace {
+
+// One wave of CTAs at most: each warp takes a stretch of the steps.
+dim3 policy_grid(int64_t n, const DeviceInfo& dev) {
+  dim3 grid = warps_grid(loss_steps(n));
+  grid.x = std::min(grid.x, static_cast<unsigned>(dev.sm_count * kPolicyCtas));
+  return grid;
+}
+
+template <bool kRef, bool kTok>
+nvfp4rl_status policy_forward(const PolicyArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   auto* ticket = static_cast<unsigned int*>(a.ws);
   auto* slots = reinterpret_cast<SlotSums*>(static_cast<uint8_t*>(a.ws) + 256);
   auto* seqs = reinterpret_cast<SeqSums*>(slots + loss_steps(a.n) + a.B);
   if (loss_steps(a.n) <= kOneWarps && a.B <= kOneWarps) {
-    if (launch_pdl(policy_one_kernel, dim3(1), dim3(32 * kOneWarps), 0, st, a, slots, seqs) != cudaSuccess)
+    if (launch_pdl(policy_one_kernel<kRef, kTok>, dim3(1), dim3(32 * kOneWarps), 0, st, a, slots, seqs) != cudaSuccess)
       return NVFP4RL_ERR_CUDA;
     return launch_status();
   }
-  if (launch_pdl(policy_sums_kernel, warps_grid(loss_steps(a.n)), dim3(kThreads), 0, st, a, ticket, slots) != cudaSuccess)
+  if (launch_pdl(policy_sums_kernel<kRef, kTok>, policy_grid(a.n, dev), dim3(kThreads), 0, st, a, ticket, slots) != cudaSuccess)
     return NVFP4RL_ERR_CUDA;
   if (launch_status() != NVFP4RL_OK) return NVFP4RL_ERR_CUDA;
   dim3 grid = warps_grid(a.B);
@@ -681,10 +717,23 @@ nvfp4rl_status launch_policy_loss(const PolicyArgs& a, const DeviceInfo& dev, cu
   return launch_status();
 }
 
-nvfp4rl_status launch_policy_loss_grad(const PolicyArgs& a, const DeviceInfo&, cudaStream_t st) {
-  if (launch_pdl(policy_grad_kernel, warps_grid(loss_steps(a.n)), dim3(kThreads), 0, st, a) != cudaSuccess)
+template <bool kRef, bool kTok>
+nvfp4rl_status policy_backward(const PolicyArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  if (launch_pdl(policy_grad_kernel<kRef, kTok>, policy_grid(a.n, dev), dim3(kThreads), 0, st, a) != cudaSuccess)
     return NVFP4RL_ERR_CUDA;
   return launch_status();
+}
+
+}  // namespace
+
+nvfp4rl_status launch_policy_loss(const PolicyArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  if (a.logp_ref) return a.adv_per_token ? policy_forward<true, true>(a, dev, st) : policy_forward<true, false>(a, dev, st);
+  return a.adv_per_token ? policy_forward<false, true>(a, dev, st) : policy_forward<false, false>(a, dev, st);
+}
+
+nvfp4rl_status launch_policy_loss_grad(const PolicyArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  if (a.logp_ref && a.kl != 0.0f) return a.adv_per_token ? policy_backward<true, true>(a, dev, st) : policy_backward<true, false>(a, dev, st);
+  return a.adv_per_token ? policy_backward<false, true>(a, dev, st) : policy_backward<false, false>(a, dev, st);
 }
 
 nvfp4rl_status launch_preference_loss(const PreferenceArgs& a, const DeviceInfo&, cudaStream_t st) {
