@@ -457,7 +457,8 @@ NVFP4RL_API nvfp4rl_status nvfp4_kv_read(const uint8_t* k_codes, const uint8_t* 
  *            aligned; scratch.
  * A sequence that attends to nothing gets 0. Precision as nvfp4_kv_decode_attention; partial results are fp32, joined
  * in a fixed order: equal inputs give equal bits.
- * Errors as nvfp4_kv_decode_attention.
+ * Errors as nvfp4_kv_decode_attention; also NVFP4RL_ERR_UNSUPPORTED_SHAPE where (P + B / (128 / (Hq / Hkv))) Hkv
+ * ceil(Lp / 128) is above 2^31 - 1.
  */
 NVFP4RL_API nvfp4rl_status nvfp4_kv_prefix_attention(
     const uint16_t* q, int64_t ldq, const uint8_t* pk_codes, const uint8_t* pk_scales, const uint8_t* pv_codes,
