@@ -109,6 +109,22 @@ def test_append_matches_the_one_token_append(nv):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("g", [0.002, 1e-36, 50.0])
+def test_append_of_infinities_and_nans_matches_the_one_token_append(nv, g):
+    B, H, D = 6, 2, 64
+    x = synth.rng(10).standard_normal((B, H, D)).astype(np.float32)
+    for b, bad in enumerate((np.inf, -np.inf, np.nan, -np.nan, 3.3e38)):
+        x[b, 1, 16 * (b % 4) + 3 * b] = bad
+    x[2, 0, :20] = np.nan
+    k = P.dev_bf16(synth.bf16_bits(x))
+    want, pos = caches(B, 1, H, D), ints([0] * B)
+    nv.nvfp4_kv_append(k, k, pos, one(g), one(g), *want)
+    for rows_ in (k, k.float()):
+        got = caches(B, 1, H, D)
+        nv.nvfp4_kv_append_ragged(rows_, rows_, ints(range(B + 1)), None, one(g), one(g), *got)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_append_with_many_empty_sequences_and_odd_offsets(nv):
     """Offsets that fall or leave the range, and places outside the cache: no fault, and nothing outside the rows."""
     B, T, H, D = 2000, 64, 1, 32
@@ -252,6 +268,32 @@ def test_offsets_that_fall_do_not_fault(nv):
         attend(nv, q, pre, own, [90, 33], groups, [12, 0, 3, 4, 5, 6], 0.1)
         attend(nv, q, pre, None, [90, 33], groups, None, 0.1)
     torch.cuda.synchronize()
+
+
+def test_rows_past_32_bits_of_bytes(nv):
+    """The third of three caches of 4.5 million rows of 8 heads lies 4.6 GB behind the first."""
+    P_, L, H, Hq, T = 3, 4_500_000, 8, 16, 300
+    c = tuple(torch.empty(P_, L, H, 128 // w, dtype=torch.uint8, device="cuda") for w in (2, 16, 2, 16))
+    k, kh = rows(T, H, 128, "bf16", 91)
+    v, vh = rows(T, H, 128, "bf16", 92)
+    gk, gv = np.float32(0.002), np.float32(0.003)
+    off = ints([0, 0, 0, T])
+    enc = G.encode(kh, gk) + G.encode(vh, gv)
+    vals = [G.values(enc[0], enc[1], gk), G.values(enc[2], enc[3], gv)]
+    for place, there in ((0, T), (L - 50, 50)):  # the second ends behind the cache
+        pos = ints([0, 0, place])
+        nv.nvfp4_kv_append_ragged(k, v, off, pos, one(gk), one(gv), *c)
+        for got, e in zip(c, enc):
+            assert np.array_equal(got[2, place:place + there].cpu().numpy(), e[:there])
+        for got, want in zip(nv.nvfp4_kv_read(c[0], c[1], one(gk), c[2], c[3], one(gv), off, pos, T, torch.float32), vals):
+            assert np.array_equal(got[:there].cpu().numpy(), want[:there]) and not got[there:].any()
+    q = synth.bf16_bits(synth.rng(93).standard_normal((P_, Hq, 128)).astype(np.float32))
+    n = [0, 0, T]
+    got = nv.nvfp4_kv_prefix_attention(P.dev_bf16(q), *c, ints(n), ints([0, 1, 2, 3]), *c, ints(n), one(gk), one(gv), 0.09)
+    x = [np.concatenate([np.zeros((2,) + t.shape), t[None]]).astype(np.float64) for t in vals]
+    want, tol = G.attention(P.dev_bf16(q).double().cpu().numpy(), x, x, n, [0, 1, 2, 3], n,
+                            G.f32(0.09))
+    G.close(got.double().cpu().numpy(), want, tol, "out")
 
 
 def test_equal_bits_on_streams_and_in_graphs(nv):
