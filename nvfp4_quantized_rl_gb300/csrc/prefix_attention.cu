@@ -8,13 +8,16 @@
 //
 // prefix_attention_kernel: one persistent CTA per SM. A tile is up to 128 rows (whole sequences) of one group and KV head;
 // the 128-token blocks of all tiles lie in one row, and each CTA takes an equal stretch of it, whatever the lengths,
-// so that one long prefix keeps every SM busy. A stretch is one segment per tile; CTA c's segment in tile t leaves its
-// partial in slot c + t (both only grow along the stretch).
+// so that one long prefix keeps every SM busy. Up to eight KV heads are walked side by side, a CTA each over the same blocks:
+// their rows of a token share the lines that DRAM gives (a head alone has 64 bytes of codes and 8 of scales there: it read
+// 570 MB where 276 do). A
+// stretch is one segment per tile; stretch c's segment in tile t leaves its partial in slot c + t of its head (both only grow
+// along the stretch).
 // Per block, in a pipeline of warps:
 //   - four warps decode K and four V: one thread to a token row, 128 codes to f16 (exact: code x scale has at most
 //     six significant bits), stored in the 128-byte swizzle of the MMA operands. Each warp copies its own 32 rows into a ring
 //     of its own (cp.async, three blocks ahead; zeros behind the prefix's end, which makes those tokens' values zero),
-//     four lanes to a row of 64 bytes. Tensor copies of 64-byte rows were the pipeline's limit: 2200 clocks a block;
+//     four lanes to a row of 64 bytes. (With one warp's tensor copies of 64-byte rows a block took 2200 clocks.);
 //   - one warp issues S = Q K^T (tcgen05, f16, 128 x 128 x 128) and one O += P V, V as it lies ([token][dim]: MN-major): one
 //     warp for both spent as long on its waits as the tensor cores on the products;
 //   - two groups of four warps take every second block each, so that one group's exponentials run under the other's and under
@@ -24,6 +27,10 @@
 //     largest, and stays below 2^14.
 //   TMEM: three S / P buffers and O, so that the scores of block n + 2 can follow the values of block n - 1 and are there
 //   when the softmax of block n ends.
+// A block takes 0.94 us (1800 clocks) in long stretches, 0.44 of the measured copy bandwidth, and a call 18 to 25 us beside its
+// blocks (256 sequences behind sixteen prefixes). No unit is full: copies of the kernel that left out work took, of 125 us,
+// without the decoding 113, without exponentials and half of the maximum 116, with an eighth of the products 111 to 121, without
+// the copies 118, without any of these 78: what remains is the chain scores - softmax - values around the three score buffers.
 // Q enters as f16 scaled per row by a power of two that puts its largest element in [2^14, 2^15): exact down to 2^-31 of it.
 #include <climits>
 #include <map>
@@ -50,6 +57,7 @@ constexpr int kSmemBytes = kTileBytes /*Q*/ + 4 * kTileBytes /*K, V twice*/ + 8 
 // warps: 0-3 and 4-7 softmax (every second block each), 8-11 decode K, 12-15 decode V, 16 scores, 17 values, 18 segments, one
 // idle that fills the warpgroup
 constexpr int kScoreWarp = 16, kValueWarp = 17, kWalkWarp = 18, kThreads = 20 * 32;
+constexpr int kBeside = 8;  // KV heads side by side, or the largest half of it that divides their number (256 sequences: 161 us, one 165)
 constexpr int kSegments = 8, kSegmentReaders = 18;  // a ring of segments, read by warps 0-17
 // Registers by warpgroup, out of the 96 that each of the 640 threads starts with.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kDecodeRegs = 72, kOtherRegs = 64;
@@ -76,7 +84,7 @@ struct Bars {
 struct Group {
   int first, members;  // its sequences
   int tile0, tiles;    // the tiles before it, its own
-  int unit0, units;    // the blocks of all tiles and heads before it, its own
+  int unit0, units;    // the blocks of all tiles and head sets before it, its own
   int p, blocks;       // the prefix (-1: none) and its blocks
 };
 
@@ -86,6 +94,8 @@ struct Groups {
   int P, Lp, B, Hkv;
   int per_tile;   // sequences of a tile
   int max_tiles;  // P + B / per_tile
+  int beside;     // KV heads that as many CTAs walk side by side, and the sets of that many
+  int sets;
 };
 
 // The 32 groups from p0 on, one per lane, behind `tiles0` tiles and `units0` blocks, which move on. Whole warp. Offsets are
@@ -113,7 +123,7 @@ __device__ __forceinline__ Group scan_groups(const Groups& a, int p0, int& tiles
   g.tile0 = min(upto - g.tiles, a.max_tiles);
   g.tiles = min(upto, a.max_tiles) - g.tile0;
   tiles0 = __shfl_sync(0xFFFFFFFFu, upto, 31);
-  g.units = g.tiles * g.blocks * a.Hkv;
+  g.units = g.tiles * g.blocks * a.sets;
   upto = units0 + sum_up_to(g.units);
   g.unit0 = upto - g.units;
   units0 = __shfl_sync(0xFFFFFFFFu, upto, 31);
@@ -177,7 +187,7 @@ struct Segment {
 struct Walk {
   Group g;        // the group of block u
   int u, end;     // blocks to come
-  int tile, kvh;  // of u, within the group
+  int tile, set;  // of u, within the group
   int block0;     // and its place in the tile: 0 but for the CTA's first
   __device__ __forceinline__ Segment next(const Groups& a) {
     Segment s{0, 0, 0, 0, 0, 0, 0, 0};
@@ -186,27 +196,28 @@ struct Walk {
       const int want = u;
       g = find_group(a, nullptr, [want](const Group& x) { return want >= x.unit0 && want - x.unit0 < x.units; });
       if (g.p < 0) return s;
-      tile = kvh = 0;
+      tile = set = 0;
     }
     s.p = g.p;
-    s.kvh = kvh;
+    const int which = static_cast<int>(blockIdx.x) % a.beside, cta = static_cast<int>(blockIdx.x) / a.beside;
+    s.kvh = set * a.beside + which;
     s.first_seq = g.first + tile * a.per_tile;
     s.members = min(a.per_tile, g.members - tile * a.per_tile);
-    s.slot = static_cast<int>(blockIdx.x) + (g.tile0 + tile) * a.Hkv + kvh;
+    s.slot = (cta + (g.tile0 + tile) * a.sets + set) * a.beside + which;
     s.block0 = block0;
     s.blocks = min(g.blocks - block0, end - u);
     s.len = min(max(__ldg(a.lens + g.p), 0), a.Lp);
     block0 = 0;
     u += s.blocks;
-    if (++kvh == a.Hkv) {
-      kvh = 0;
+    if (++set == a.sets) {
+      set = 0;
       ++tile;
     }
     return s;
   }
 };
 
-// The walk of CTA c of `grid`. Whole warp.
+// The walk of the CTAs c (`beside` of them, a head of each set each) of `grid`. Whole warp.
 __device__ __forceinline__ Walk begin_walk(const Groups& a, int grid, int c) {
   Walk w;
   int total = 0, tiles0 = 0;
@@ -215,7 +226,7 @@ __device__ __forceinline__ Walk begin_walk(const Groups& a, int grid, int c) {
   for (int p0 = 32; p0 < a.P; p0 += 32) scan_groups(a, p0, tiles0, total);
   const Shares shares(total, grid);
   w.u = w.end = 0;
-  w.tile = w.kvh = w.block0 = 0;
+  w.tile = w.set = w.block0 = 0;
   w.g = g;
   if (total == 0 || c >= shares.ctas) return w;
   const int begin = shares.begin(c);
@@ -224,10 +235,10 @@ __device__ __forceinline__ Walk begin_walk(const Groups& a, int grid, int c) {
   const auto here = [begin](const Group& x) { return begin >= x.unit0 && begin - x.unit0 < x.units; };
   w.g = pick_group(g, __ballot_sync(0xFFFFFFFFu, g.p < a.P && here(g)));
   if (w.g.p < 0) w.g = find_group(a, nullptr, here);  // behind the first 32 groups
-  const int in = begin - w.g.unit0, head = in / w.g.blocks;
-  w.block0 = in - head * w.g.blocks;
-  w.tile = head / a.Hkv;
-  w.kvh = head - w.tile * a.Hkv;
+  const int in = begin - w.g.unit0, row = in / w.g.blocks;
+  w.block0 = in - row * w.g.blocks;
+  w.tile = row / a.sets;
+  w.set = row - w.tile * a.sets;
   return w;
 }
 
@@ -804,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) drain(bars.drain[1]);
     } else if (warp == kWalkWarp) {
       // ---- segments
-      Walk walk = begin_walk(a.groups, gridDim.x, blockIdx.x);
+      Walk walk = begin_walk(a.groups, gridDim.x / a.groups.beside, blockIdx.x / a.groups.beside);
       for (uint32_t i = 0; ok; ++i) {
         const Segment s = walk.next(a.groups);
         ok = wait(bars.seg_empty[i % kSegments], ((i / kSegments) & 1) ^ 1, kStatusTimeoutProducer);
@@ -829,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct JoinArgs {
   const float4* part;
   const float2* stats;
-  int grid;  // CTAs of the prefix kernel
+  int grid;  // stretches of the prefix kernel
   Groups groups;
   OwnPartials own;
   const int32_t* lens;
@@ -858,13 +869,13 @@ __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
   int64_t s0 = 0;
   int tile_row = 0, npre = 0, nown = 0;
   if (g.p >= 0) {
-    const int tile = (b - g.first) / a.groups.per_tile, tile_head = (g.tile0 + tile) * a.groups.Hkv + kvh;
+    const int tile = (b - g.first) / a.groups.per_tile, set = kvh / a.groups.beside;
     if (g.blocks > 0 && tile < g.tiles) {
-      const int u0 = g.unit0 + (tile * a.groups.Hkv + kvh) * g.blocks;
+      const int u0 = g.unit0 + (tile * a.groups.sets + set) * g.blocks;
       const Shares shares(total, a.grid);
       const int c0 = shares.owner(u0);
       tile_row = (b - g.first - tile * a.groups.per_tile) * a.heads + r;
-      s0 = c0 + tile_head;
+      s0 = (c0 + (g.tile0 + tile) * a.groups.sets + set) * a.groups.beside + kvh % a.groups.beside;
       npre = shares.owner(u0 + g.blocks - 1) - c0 + 1;
     }
   }
@@ -879,7 +890,7 @@ __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
   for (int i0 = 0; i0 < n; i0 += 32) {  // a lane to a partial's statistics
     const int i = i0 + lane, count = min(32, n - i0);
     float2 t = make_float2(-INFINITY, 0.0f);
-    if (i < npre) t = a.stats[(s0 + i) * kRows + tile_row];
+    if (i < npre) t = a.stats[(s0 + i * a.groups.beside) * kRows + tile_row];
     else if (i < n) t = make_float2(own_at(i)[0], own_at(i)[1]);
     const float m = fmaxf(M, warp_max(t.x));
     if (m == -INFINITY) continue;
@@ -896,7 +907,7 @@ __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
         const int at = i0 + k0 + k;
         v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         // the four rows of a CTA's warps share their sectors in L1
-        if (k0 + k < count) v[k] = at < npre ? a.part[part_at(s0 + at, lane, tile_row)] : reinterpret_cast<const float4*>(own_at(at) + 4)[lane];
+        if (k0 + k < count) v[k] = at < npre ? a.part[part_at(s0 + at * a.groups.beside, lane, tile_row)] : reinterpret_cast<const float4*>(own_at(at) + 4)[lane];
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -935,8 +946,10 @@ nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo
   auto* part = static_cast<float4*>(p.workspace);
   auto* stats = reinterpret_cast<float2*>(part + slots * kRows * (kDim / 4));
   auto* own = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + prefix_bytes(slots));
+  int beside = kBeside;
+  while (p.Hkv % beside != 0) beside /= 2;
   const Groups groups{p.groups, p.prefix_lens, static_cast<int>(p.P), static_cast<int>(p.Lp), static_cast<int>(p.B),
-                      static_cast<int>(p.Hkv), kRows / heads, static_cast<int>(tiles)};
+                      static_cast<int>(p.Hkv), kRows / heads, static_cast<int>(tiles), beside, static_cast<int>(p.Hkv) / beside};
   {
     static std::mutex mu;
     static std::map<int, bool> set;
@@ -949,10 +962,10 @@ nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo
     }
   }
   // no more CTAs than blocks there can be, so that few leave SMs to the kernel behind
-  const int64_t units = tiles * p.Hkv * ((p.Lp + kBlock - 1) / kBlock);
-  const int grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(units, 1), std::min(dev.sm_count, kPlanSMs)));
+  const int64_t units = tiles * groups.sets * ((p.Lp + kBlock - 1) / kBlock);
+  const int stretches = static_cast<int>(std::min<int64_t>(std::max<int64_t>(units, 1), std::min(dev.sm_count, kPlanSMs) / beside));
   const PrefixArgs a{p.q, p.ldq, p.pkc, p.pks, p.pvc, p.pvs, p.gk, groups, heads, p.scale, part, stats, dev.status};
-  if (launch_pdl(prefix_attention_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, st, a) !=
+  if (launch_pdl(prefix_attention_kernel, dim3(static_cast<unsigned>(stretches * beside)), dim3(kThreads), kSmemBytes, st, a) !=
       cudaSuccess)
     return NVFP4RL_ERR_CUDA;
   nvfp4rl_status s = launch_status();
@@ -962,7 +975,7 @@ nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo
     s = launch_own_partials(p, own, &partials, dev, st);
     if (s != NVFP4RL_OK) return s;
   }
-  const JoinArgs j{part, stats, grid, groups, partials, p.lens, p.Lmax, static_cast<int>(p.Hq), heads, p.gv, p.out};
+  const JoinArgs j{part, stats, stretches, groups, partials, p.lens, p.Lmax, static_cast<int>(p.Hq), heads, p.gv, p.out};
   const auto join = p.B * p.Hq <= static_cast<int64_t>(kJoinFew) * dev.sm_count ? kv_prefix_join_kernel<16> : kv_prefix_join_kernel<4>;
   if (launch_pdl(join, dim3(static_cast<unsigned>(p.B * ((p.Hq + 3) / 4))), dim3(128), 0, st, j) != cudaSuccess)
     return NVFP4RL_ERR_CUDA;
