@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
   __syncwarp();
   constexpr int kShare = kKind == kOwn ? 1 : kWarps;  // warps to a span
   const int part = kKind == kOwn ? 0 : warp;          // which of them
-  const int64_t bh = kKind == kOwn ? static_cast<int64_t>(blockIdx.y) * kWarps + warp : blockIdx.y, b = bh / a.Hkv, kvh = bh % a.Hkv;
+  const int64_t bh = kKind == kOwn ? static_cast<int64_t>(blockIdx.y) * kWarps + warp : blockIdx.y;
+  const int64_t b = bh / a.Hkv, kvh = bh % a.Hkv;
   const int group = static_cast<int>(a.Hq / a.Hkv);
   // kOwn: the kernel ahead is the prefix kernel, of whose results this one takes nothing; its CTAs start this
   // one's only behind their own wait for what came before them, the queries and caches among it. So the two run side
@@ -501,8 +502,10 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
           *reinterpret_cast<float2*>(rows + r * kHeadDim + 16 * g + 2 * m) = make_float2(oacc[m][h][e], oacc[m][h][2 + e]);
       }
     __syncwarp();
-    for (int r = 0; r < group; ++r)
-      *reinterpret_cast<float4*>(pr + r * kPartFloats + 4 + 4 * lane) = *reinterpret_cast<const float4*>(rows + r * kHeadDim + 4 * lane);
+    for (int r = 0; r < group; ++r) {
+      const float4 o = *reinterpret_cast<const float4*>(rows + r * kHeadDim + 4 * lane);
+      *reinterpret_cast<float4*>(pr + r * kPartFloats + 4 + 4 * lane) = o;
+    }
     in_order();
     return;
   }
@@ -647,7 +650,8 @@ nvfp4rl_status launch_own_partials(const PrefixAttnArgs& p, float* part, OwnPart
   *out = {part, ns};
   CUtensorMap mk, mv;
   if (!code_map(&mk, p.kc, p.B * p.Lmax, p.Hkv) || !code_map(&mv, p.vc, p.B * p.Lmax, p.Hkv)) return NVFP4RL_ERR_CUDA;
-  const AttnArgs a{p.q, p.ks, p.vs, p.gk, p.gv, p.lens, p.Hq, p.Hkv, p.Lmax, ns, 0, p.scale, nullptr, part, dev.status, p.ldq, p.B};
+  const AttnArgs a{p.q, p.ks, p.vs, p.gk, p.gv, p.lens, p.Hq, p.Hkv, p.Lmax, ns, 0, p.scale, nullptr, part, dev.status,
+                   p.ldq, p.B};
   const auto kernel = p.Hq / p.Hkv > 8 ? kv_attention_kernel<2, kOwn> : kv_attention_kernel<1, kOwn>;
   if (!allow_smem(dev.device)) return NVFP4RL_ERR_CUDA;
   const dim3 grid(static_cast<unsigned>(ns), static_cast<unsigned>((p.B * p.Hkv + kWarps - 1) / kWarps));

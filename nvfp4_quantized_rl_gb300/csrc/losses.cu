@@ -137,7 +137,8 @@ __device__ __forceinline__ Window window_at(const int32_t* __restrict__ offsets,
 }
 
 // The sequences of tokens [t0, t1), in order: f(b, s, e) for the part [s, e) that sequence b has of them;
-// b = -1 for tokens of no sequence. Whole warp. The window is of t0 or earlier tokens, and moves on where it ends. Offsets that fall are answered with some split of the
+// b = -1 for tokens of no sequence. Whole warp. The window is of t0 or earlier tokens, and moves on where it ends. Offsets
+// that fall are answered with some split of the
 // tokens, each in one part.
 template <class F>
 __device__ __forceinline__ void for_sequences(const int32_t* __restrict__ offsets, int64_t B, Window& w, int64_t t0,
@@ -519,7 +520,8 @@ __global__ void __launch_bounds__(32 * kOneWarps) policy_one_kernel(const Policy
 }
 
 template <bool kRef, bool kTok>
-__device__ __forceinline__ void policy_grad_step(const PolicyArgs& a, float dloss, int64_t s, const Step<kRef, kTok>& st, Window& win) {
+__device__ __forceinline__ void policy_grad_step(const PolicyArgs& a, float dloss, int64_t s, const Step<kRef, kTok>& st,
+                                                 Window& win) {
   const int lane = threadIdx.x & 31;
   const int64_t t0 = s * kLossStep, t1 = min(a.n, t0 + kLossStep);
   const uint32_t there = mask_bits(st.mask);
@@ -732,7 +734,8 @@ nvfp4rl_status launch_policy_loss(const PolicyArgs& a, const DeviceInfo& dev, cu
 }
 
 nvfp4rl_status launch_policy_loss_grad(const PolicyArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  if (a.logp_ref && a.kl != 0.0f) return a.adv_per_token ? policy_backward<true, true>(a, dev, st) : policy_backward<true, false>(a, dev, st);
+  if (a.logp_ref && a.kl != 0.0f)
+    return a.adv_per_token ? policy_backward<true, true>(a, dev, st) : policy_backward<true, false>(a, dev, st);
   return a.adv_per_token ? policy_backward<false, true>(a, dev, st) : policy_backward<false, false>(a, dev, st);
 }
 

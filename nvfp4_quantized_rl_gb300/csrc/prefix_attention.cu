@@ -17,7 +17,7 @@
 //   - four warps decode K and four V: one thread to a token row, 128 codes to f16 (exact: code x scale has at most
 //     six significant bits), stored in the 128-byte swizzle of the MMA operands. Each warp copies its own 32 rows into a ring
 //     of its own (cp.async, three blocks ahead; zeros behind the prefix's end, which makes those tokens' values zero),
-//     four lanes to a row of 64 bytes. (With one warp's tensor copies of 64-byte rows a block took 2200 clocks.);
+//     four lanes to a row of 64 bytes. (With one warp's tensor copies of 64-byte rows a block took 2200 clocks.)
 //   - one warp issues S = Q K^T (tcgen05, f16, 128 x 128 x 128) and one O += P V, V as it lies ([token][dim]: MN-major): one
 //     warp for both spent as long on its waits as the tensor cores on the products;
 //   - two groups of four warps take every second block each, so that one group's exponentials run under the other's and under
@@ -57,7 +57,9 @@ constexpr int kSmemBytes = kTileBytes /*Q*/ + 4 * kTileBytes /*K, V twice*/ + 8 
 // warps: 0-3 and 4-7 softmax (every second block each), 8-11 decode K, 12-15 decode V, 16 scores, 17 values, 18 segments, one
 // idle that fills the warpgroup
 constexpr int kScoreWarp = 16, kValueWarp = 17, kWalkWarp = 18, kThreads = 20 * 32;
-constexpr int kBeside = 8;  // KV heads side by side, or the largest half of it that divides their number (256 sequences: 161 us, one 165)
+// KV heads side by side: this many, or the largest power of two below that divides their number (256 sequences: 161 us,
+// one head after the other 165).
+constexpr int kBeside = 8;
 constexpr int kSegments = 8, kSegmentReaders = 18;  // a ring of segments, read by warps 0-17
 // Registers by warpgroup, out of the 96 that each of the 640 threads starts with.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kDecodeRegs = 72, kOtherRegs = 64;
@@ -689,7 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The copies run three blocks ahead of the decoding: `left` blocks of segment seg - 1 are still to come, `tokens` tokens from
     // the warp's first row of the next one on, which the lane's pointers are at. A group of copies is closed per block
     // whether there is one or not.
-    const int64_t code_step = static_cast<int64_t>(a.groups.Hkv) * kCodeRow, scale_step = static_cast<int64_t>(a.groups.Hkv) * kScaleRow;
+    const int64_t code_step = static_cast<int64_t>(a.groups.Hkv) * kCodeRow;
+    const int64_t scale_step = static_cast<int64_t>(a.groups.Hkv) * kScaleRow;
     const uint8_t *from = codes, *scale_from = scales;
     uint32_t seg = 0, copied = 0;
     int left = 0, tokens = 0;
@@ -907,7 +910,9 @@ __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
         const int at = i0 + k0 + k;
         v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         // the four rows of a CTA's warps share their sectors in L1
-        if (k0 + k < count) v[k] = at < npre ? a.part[part_at(s0 + at * a.groups.beside, lane, tile_row)] : reinterpret_cast<const float4*>(own_at(at) + 4)[lane];
+        if (k0 + k < count)
+          v[k] = at < npre ? a.part[part_at(s0 + at * a.groups.beside, lane, tile_row)]
+                           : reinterpret_cast<const float4*>(own_at(at) + 4)[lane];
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -963,7 +968,8 @@ nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo
   }
   // no more CTAs than blocks there can be, so that few leave SMs to the kernel behind
   const int64_t units = tiles * groups.sets * ((p.Lp + kBlock - 1) / kBlock);
-  const int stretches = static_cast<int>(std::min<int64_t>(std::max<int64_t>(units, 1), std::min(dev.sm_count, kPlanSMs) / beside));
+  const int most = std::min(dev.sm_count, kPlanSMs) / beside;
+  const int stretches = static_cast<int>(std::min<int64_t>(std::max<int64_t>(units, 1), most));
   const PrefixArgs a{p.q, p.ldq, p.pkc, p.pks, p.pvc, p.pvs, p.gk, groups, heads, p.scale, part, stats, dev.status};
   if (launch_pdl(prefix_attention_kernel, dim3(static_cast<unsigned>(stretches * beside)), dim3(kThreads), kSmemBytes, st, a) !=
       cudaSuccess)
@@ -976,7 +982,8 @@ nvfp4rl_status launch_prefix_attention(const PrefixAttnArgs& p, const DeviceInfo
     if (s != NVFP4RL_OK) return s;
   }
   const JoinArgs j{part, stats, stretches, groups, partials, p.lens, p.Lmax, static_cast<int>(p.Hq), heads, p.gv, p.out};
-  const auto join = p.B * p.Hq <= static_cast<int64_t>(kJoinFew) * dev.sm_count ? kv_prefix_join_kernel<16> : kv_prefix_join_kernel<4>;
+  const bool few = p.B * p.Hq <= static_cast<int64_t>(kJoinFew) * dev.sm_count;
+  const auto join = few ? kv_prefix_join_kernel<16> : kv_prefix_join_kernel<4>;
   if (launch_pdl(join, dim3(static_cast<unsigned>(p.B * ((p.Hq + 3) / 4))), dim3(128), 0, st, j) != cudaSuccess)
     return NVFP4RL_ERR_CUDA;
   return launch_status();

@@ -1366,7 +1366,8 @@ kv_append_ragged_kernel(const void* __restrict__ k, const void* __restrict__ v, 
     BlockWords<kDtype> next;
     const auto load = [&]() {
       const bool is_v = u >= nb;
-      load_block<kDtype>(static_cast<const uint8_t*>(is_v ? v : k) + (t0 + tok) * (is_v ? ldv : ldk) * kSize, is_v ? u - nb : u, next);
+      const uint8_t* row = static_cast<const uint8_t*>(is_v ? v : k) + (t0 + tok) * (is_v ? ldv : ldk) * kSize;
+      load_block<kDtype>(row, is_v ? u - nb : u, next);
     };
     if (tok < n) load();
     while (tok < n) {
@@ -1584,11 +1585,9 @@ nvfp4rl_status launch_kv_append_ragged(const void* k, const void* v, int dtype, 
   const int64_t wave = static_cast<int64_t>(dev.sm_count) * (dtype == NVFP4RL_BF16 ? 4 : 3);
   const dim3 grid(static_cast<unsigned>(std::min((r.T + kMinRows - 1) / kMinRows, wave)));
   const uint32_t nb = static_cast<uint32_t>(Hkv * D / 16);
-  const cudaError_t e =
-      dtype == NVFP4RL_BF16
-          ? launch_pdl(kv_append_ragged_kernel<NVFP4RL_BF16>, grid, dim3(256), 0, st, k, v, ldk, ldv, nb, r, gk, gv, kc, ks, vc, vs)
-          : launch_pdl(kv_append_ragged_kernel<NVFP4RL_F32>, grid, dim3(256), 0, st, k, v, ldk, ldv, nb, r, gk, gv, kc, ks, vc, vs);
-  if (e != cudaSuccess) return NVFP4RL_ERR_CUDA;
+  const auto kernel = dtype == NVFP4RL_BF16 ? kv_append_ragged_kernel<NVFP4RL_BF16> : kv_append_ragged_kernel<NVFP4RL_F32>;
+  if (launch_pdl(kernel, grid, dim3(kRaggedThreads), 0, st, k, v, ldk, ldv, nb, r, gk, gv, kc, ks, vc, vs) != cudaSuccess)
+    return NVFP4RL_ERR_CUDA;
   return launch_status();
 }
 

@@ -10,7 +10,7 @@ Tolerances, from the kernels' arithmetic, with u = 2^-24 (half an ulp of fp32, r
     P enters the second product rounded to f16 (2^-11 relative; below 2^-14 of the step's reference by at most
     2^-25 absolute, times the number of tokens). Sums over up to N tokens in fp32: 2 N u at most. Numerator and
     denominator have these errors each; the result is off by that times A = sum p |v|, then half a bf16 step (2^-8).
-  * Policy loss: e^d (expf 2 ulp, one fma) and two products: 8u of a term, e^x - x - 1: 16u and 4u |x| e^|x| / k of it
+  * Policy loss: e^d (2^t within 2^-22 = 4u, one fma) and two products: 8u of a term, e^x - x - 1: 16u and 4u |x| e^|x| / k of it
     (x is rounded once); a step's sums: 13 additions; the rest (pairs, a division, the last fma): 5u. A gradient the
     same without sums; 1 - e^x is off by 4u of itself and u |x| e^x.
   * Preference loss: s_b in pairs (2^-40 of the magnitudes), h by dh = 3u (|beta s| + |margin|); a loss by dh + 10u (loss + 1),
