@@ -134,6 +134,23 @@ def test_policy_extremes(nv):
     assert np.isnan(got["loss"][0]) and np.isnan(got["dlogp"][4]) and np.all(np.isfinite(got["dlogp"][:3]))
 
 
+def test_policy_ratios_over_the_whole_range(nv):
+    """e^d and 1 - e^x wherever fp32 holds them, through the gradients of tokens that are not clipped."""
+    d = np.concatenate([np.linspace(-95, 88.7, 30011), np.linspace(-1, 1, 20011), [-0.5, 0.5, np.nextafter(0.5, 0), 0.0]]).astype(np.float32)
+    n = len(d)
+    zero, off = np.zeros(n, np.float32), np.array([0, n], np.int32)
+    adv = np.where(d < 0, 1, -1).astype(np.float32)
+    for kw in (dict(), dict(ref=zero, kl=1.0)):
+        for logp in (d, -d):
+            a = adv if not kw else zero
+            got = run_policy(nv, logp, zero, a if logp is d else -a, off, mode=2, norm=1.0, per_token=True, low=0.999, high=3e38, **kw)
+            want = G.policy(logp, zero, a if logp is d else -a, off, mode=2, norm=1.0, per_token=True, low=0.999, high=3e38, **kw)
+            # what lies beyond the largest fp32 (from d = 88.7229 on; no d here is within its tolerance of that) is infinite in fp32
+            top = float(np.finfo(np.float32).max)
+            exact = np.where(np.abs(want["dlogp"]) > top, np.copysign(np.inf, want["dlogp"]), want["dlogp"])
+            G.close(got["dlogp"], exact, want["tol"]["dlogp"], "dlogp")
+
+
 def test_policy_gradient_against_differences(nv):
     """Central differences of the 64-bit loss."""
     offsets = np.array([0, 7, 7, 20], np.int32)

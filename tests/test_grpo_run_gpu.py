@@ -190,3 +190,19 @@ def test_graphs_that_share_a_workspace(nv):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(graphs[turn][1], want[turn])), turn
         ws.fill_(0xFF)
+
+
+def test_two_steps_at_once(nv):
+    """Two steps on two streams, each with caches of its own, side by side: the bits of one after the other."""
+    steps = [(Step(nv), inputs(5)), (Step(nv), inputs(6))]
+    want = [bits(step(x)) for step, x in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(10):
+        got = []
+        for s, (step, x) in zip(streams, steps):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(step(x))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(g[k], w[k]) for k in w)
