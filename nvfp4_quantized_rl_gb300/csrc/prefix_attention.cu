@@ -859,8 +859,8 @@ struct JoinArgs {
 constexpr int kJoinFew = 16;  // warps per SM
 template <int kAhead>
 __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
+  // Ahead of the wait for the partials: the offsets and lengths, which were complete before the prefix kernel's CTAs let any
+  // kernel behind it start.
   const int fours = (a.Hq + 3) / 4;  // CTAs of a sequence: one per four heads
   const int b = blockIdx.x / fours, h = (blockIdx.x - b * fours) * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (h >= a.Hq) return;
@@ -887,6 +887,8 @@ __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
     nown = static_cast<int>(a.own.spans(min(max(static_cast<int64_t>(own_len), int64_t(0)), a.Lmax)));
     own = a.own.part + ((static_cast<int64_t>(b) * a.groups.Hkv + kvh) * a.own.nsplit * kOwnRows + r) * kOwnFloats;
   }
+  griddep_wait();
+  griddep_launch_dependents();
   const int n = npre + nown;
   const auto own_at = [&](int i) { return own + static_cast<int64_t>(i - npre) * kOwnRows * kOwnFloats; };
   float M = -INFINITY, L = 0.0f, O[4] = {0.0f, 0.0f, 0.0f, 0.0f};

@@ -206,3 +206,33 @@ def test_two_steps_at_once(nv):
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert all(torch.equal(g[k], w[k]) for k in w)
+
+
+def test_many_decode_steps_without_waiting(nv):
+    """Each step appends a row next to rows that the last one read and lengthens the caches in place: kernel behind kernel equals
+    a wait after each."""
+    steps, seqs, rows = 300, 40, 320
+    r = synth.rng(8)
+    bf = lambda *s: P.dev_bf16(synth.bf16_bits(r.standard_normal(s).astype(np.float32)))
+    q, k, v = bf(steps, seqs, 4, D), bf(steps, seqs, 1, D), bf(steps, seqs, 1, D)
+    pre = tuple(P.dev(a) for a in G.cache(2, 200, 1, 81)[:2] + G.cache(2, 200, 1, 82)[:2])
+    g = torch.tensor([4.5 / 2688], device="cuda")
+    groups, plens = ints([0, 11, seqs]), ints([200, 77])
+
+    def run(between):
+        own = tuple(torch.zeros(seqs, rows, 1, D // w, dtype=torch.uint8, device="cuda") for w in (2, 16, 2, 16))
+        pos, lens, outs = ints([0] * seqs), ints([0] * seqs), []
+        for t in range(steps):
+            nv.nvfp4_kv_append(k[t], v[t], pos, g, g, *own)
+            between()
+            lens.add_(1)
+            between()
+            outs.append(nv.nvfp4_kv_prefix_attention(q[t], *pre, plens, groups, *own, lens, g, g, 0.1))
+            between()
+            pos.add_(1)
+            between()
+        return torch.stack(outs)
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(5):
+        assert torch.equal(run(lambda: None), want)
