@@ -469,10 +469,16 @@ __device__ __noinline__ void encode_block_bf16_compare(uint4 v0, uint4 v1, int64
   scales[blk] = static_cast<uint8_t>(b);
 }
 
+// encode_block in its plain mode as a function of its own: the way out of the faster forms (defined behind encode_block).
+template <int kDtype>
+__device__ __noinline__ void encode_block_exact(BlockWords<kDtype> w, int64_t blk, float g, float est_scale,
+                                                uint8_t* __restrict__ codes, uint8_t* __restrict__ scales);
+
 // Plain encoding of one block of bf16 values: the exact scale byte from the block amax, then the
 // codes by the hardware conversion of fl32(x) / (E4M3(s) g) where cvt_reciprocal shows that
 // exact, else by the compare form. The scale byte's midpoint products come from the per-tensor
-// tables in shared memory.
+// tables in shared memory. kNanScale: a block with a NaN gets encode_block's scale byte (NaN), which the tables do not have.
+template <bool kNanScale = false>
 __device__ __forceinline__ void encode_block_bf16(const uint4 (&v)[2], int64_t blk, float g, float inv_g6,
                                                   float est_scale, const EncodeTables& tab,
                                                   uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
@@ -486,6 +492,10 @@ __device__ __forceinline__ void encode_block_bf16(const uint4 (&v)[2], int64_t b
   if (g > 0.0f) b = scale_byte_tab(bamax, (bamax * est_scale) * inv_g6, tab);
   const float rcp = tab.rcp[b];
   if (!(rcp >= 0.0f && bamax_bits < 0x7F80u)) {
+    if (kNanScale && bamax_bits > 0x7F80u) {
+      encode_block_exact<NVFP4RL_BF16>(BlockWords<NVFP4RL_BF16>{{v[0], v[1]}}, blk, g, est_scale, codes, scales);
+      return;
+    }
     encode_block_bf16_compare(v[0], v[1], blk, b, tab, codes, scales);
     return;
   }
@@ -1261,20 +1271,10 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const uint16_t* __restri
   }
 }
 
-// encode_block as a function of its own: the way out of the faster forms.
 template <int kDtype>
 __device__ __noinline__ void encode_block_exact(BlockWords<kDtype> w, int64_t blk, float g, float est_scale,
                                                 uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   encode_block<kDtype, kModePlain>(w, blk, g, est_scale, 6.0f * (g * est_scale), nullptr, codes, scales, nullptr, nullptr);
-}
-
-__device__ __forceinline__ bool block_has_nan(const BlockWords<NVFP4RL_BF16>& w) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    m = __vmaxu2(__vmaxu2(__vmaxu2(m, w.v[q].x & 0x7FFF7FFFu), w.v[q].y & 0x7FFF7FFFu),
-                 __vmaxu2(w.v[q].z & 0x7FFF7FFFu, w.v[q].w & 0x7FFF7FFFu));
-  return max(m & 0xFFFFu, m >> 16) > 0x7F80u;
 }
 
 // Plain encoding of one fp32 block without tables: with r = fl(1 / fl(E4M3(s) g)), x r is within 2^-21 of the
@@ -1332,7 +1332,7 @@ __device__ __forceinline__ void encode_block_bracket(const BlockWords<NVFP4RL_F3
 // are passed over. A thread loads its next block ahead of encoding this one. bf16 blocks are encoded by tables for the two
 // g's, which each CTA makes at its start: against compares without tables 5.0 to 6.1 us for 37 rows of 8 heads of 128, 73
 // to 158 us for 65536. For fp32, whose bits no table holds, the bracketing conversions. In this form 65536 bf16 rows take
-// 66 us and 30000 fp32 rows 47 us, 0.77 and 0.87 of the measured copy bandwidth.
+// 63 us and 30000 fp32 rows 47 us, 0.80 and 0.87 of the measured copy bandwidth.
 constexpr int kMinRows = 2;  // of a CTA, where there are as many
 
 template <int kDtype>
@@ -1385,9 +1385,8 @@ kv_append_ragged_kernel(const void* __restrict__ k, const void* __restrict__ v, 
       const float gq = is_v ? g[1] : g[0], inv = is_v ? inv_g6[1] : inv_g6[0], est = is_v ? est_scale[1] : est_scale[0];
       uint8_t *codes = (is_v ? vc : kc) + row * nb * 8, *scales = (is_v ? vs : ks) + row * nb;
       if constexpr (kTables) {
-        // a block with a NaN gets the scale byte that nvfp4_kv_append gives it (NaN), which the tables do not have
-        if (block_has_nan(w)) encode_block_exact<NVFP4RL_BF16>(w, blk, gq, est, codes, scales);
-        else encode_block_bf16(w.v, blk, gq, inv, est, tables[is_v ? 1 : 0], codes, scales);
+        // NaN as in nvfp4_kv_append
+        encode_block_bf16<true>(w.v, blk, gq, inv, est, tables[is_v ? 1 : 0], codes, scales);
       } else {
         encode_block_bracket(w, blk, gq, inv, est, codes, scales);
       }
