@@ -236,3 +236,38 @@ def test_many_decode_steps_without_waiting(nv):
     want = run(torch.cuda.synchronize)
     for _ in range(5):
         assert torch.equal(run(lambda: None), want)
+
+
+def test_offsets_rewritten_in_place_between_calls(nv):
+    """Offsets, lengths and group bounds that a kernel rewrites right ahead of each call: the bits of calls with waits between."""
+    n, seqs, pairs = 20000, 40, 20
+    r = synth.rng(9)
+    logp = P.dev((-3 * r.random(n)).astype(np.float32))
+    old, adv = logp + 0.1, P.dev(r.standard_normal(seqs).astype(np.float32))
+    offs = [P.dev(np.sort(r.integers(0, n + 1, seqs + 1)).astype(np.int32)) for _ in range(7)]
+    pre = tuple(P.dev(a) for a in G.cache(3, 500, 2, 91)[:2] + G.cache(3, 500, 2, 92)[:2])
+    own = tuple(P.dev(a) for a in G.cache(30, 90, 2, 93)[:2] + G.cache(30, 90, 2, 94)[:2])
+    q = P.dev_bf16(synth.bf16_bits(r.standard_normal((30, 6, D)).astype(np.float32)))
+    g = torch.tensor([0.002], device="cuda")
+    groups = [ints(np.sort(r.integers(0, 31, 4))) for _ in range(7)]
+    plens, lens = [ints(r.integers(0, 501, 3)) for _ in range(7)], [ints(r.integers(0, 91, 30)) for _ in range(7)]
+
+    def run(between):
+        off, gr, pl, ln, outs = offs[0].clone(), groups[0].clone(), plens[0].clone(), lens[0].clone(), []
+        for i in range(200):
+            for into, of in ((off, offs), (gr, groups), (pl, plens), (ln, lens)):
+                into.copy_(of[i % 7])
+            between()
+            outs.append(nv.policy_loss(logp, old, adv, off)[1])
+            between()
+            off.copy_(offs[(i + 3) % 7])
+            between()
+            outs.append(nv.preference_loss(logp, off)[0])
+            between()
+            outs.append(nv.nvfp4_kv_prefix_attention(q, *pre, pl, gr, *own, ln, g, g, 0.1).float().sum((1, 2)))
+            between()
+        return torch.cat(outs)
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(5):
+        assert torch.equal(run(lambda: None), want)
