@@ -14,8 +14,8 @@
 //   - computes S^T = K Q^T with mma.sync m16n8k16 in f16: K is the A operand, its fragments built
 //     in registers straight from the code bytes (one cvt e2m1x2 -> f16x2 per byte, one f16x2
 //     multiply by the E4M3 block scale: both exact), the group's query heads the N columns (one
-//     8-column tile, two for more than 8 heads). Q enters as f16 scaled by a power of two that puts
-//     max |q| of the group in [2^14, 2^15): exact for every bf16 element down to 2^-31 of the max;
+//     8-column tile, two for more than 8 heads). Each head's q enters as f16 scaled by a power of two
+//     that puts its max |q| in [2^14, 2^15): exact for every bf16 element down to 2^-31 of the max;
 //   - keeps an online softmax in exp2 (ex2.approx) per query head (column), rescaling O only when
 //     a maximum grows;
 //   - transposes P (f16) with movmatrix and adds O^T += V^T P^T, V^T the A operand: a nibble
@@ -261,10 +261,10 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
   const int pre = min(mine, kStages);
   for (int n = 0; n < pre; ++n) issue(n);
 
-  // Q^T fragments: head 8 h + g (zero past the group), dims 32 q .. 32 q + 31 as f16 times 2^e,
-  // 2^e putting max |q| over the group's heads in [2^14, 2^15); k-step s takes words 2 s, 2 s + 1
-  uint32_t qb[kNH][16];
-  uint32_t amax16 = 0;
+  // Q^T fragments: head 8 h + g (zero past the group), dims 32 q .. 32 q + 31 as f16 times 2^e, 2^e putting the head's
+  // max |q| in [2^14, 2^15); k-step s takes words 2 s, 2 s + 1. A power of two for all heads would round a head's
+  // elements away beside one 2^31 times as large, or beside an infinity.
+  uint32_t qb[kNH][16], up[kNH];  // up: e + 127
 #pragma unroll
   for (int h = 0; h < kNH; ++h) {
     const int hh = 8 * h + g;
@@ -283,18 +283,19 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
 #pragma unroll
       for (int i = 0; i < 16; ++i) qb[h][i] = 0u;
     }
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax16 = __vmaxu2(amax16, qb[h][i] & 0x7FFF7FFFu);
-  }
-  amax16 = __reduce_max_sync(0xFFFFFFFFu, max(amax16 & 0xFFFFu, amax16 >> 16));
-  const int qexp = static_cast<int>((amax16 >> 7) & 0xFFu);  // biased exponent of max |q|
-  const float qscale = __uint_as_float(static_cast<uint32_t>(min(max(268 - qexp, 1), 254)) << 23);
-#pragma unroll
-  for (int h = 0; h < kNH; ++h)
+    for (int i = 0; i < 16; ++i) top = __vmaxu2(top, qb[h][i] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const int qexp = static_cast<int>(top >> 7);  // biased exponent of max |q|
+    up[h] = static_cast<uint32_t>(min(max(268 - qexp, 1), 253));  // 2^-e is normal, too
+    const float qscale = __uint_as_float(up[h] << 23);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       qb[h][i] = pack_f16(__uint_as_float(qb[h][i] << 16) * qscale, __uint_as_float(qb[h][i] & 0xFFFF0000u) * qscale);
-  const float sl2 = a.scale * __ldg(a.gk) * kLog2e / qscale;  // scores in log2 units
+  }
 
   // per-thread constant offsets: K rows step_token(g), step_token(g + 8) (16-byte unit q); V rows
   // step_token(2 q + {0, 1, 8, 9}) (bytes 8 g .. 8 g + 7); their scale bytes
@@ -319,6 +320,15 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
 #pragma unroll
     for (int h = 0; h < kNH; ++h) oacc[m][h][0] = oacc[m][h][1] = oacc[m][h][2] = oacc[m][h][3] = 0.0f;
 
+  // scores of heads 8 h + 2 q + e to log2 units (here, where the queries' conversion does not wait for the shuffles: 256
+  // sequences of 8 KV heads 37.2 us, made with the queries 37.6)
+  float sl2[kNH][2];
+  const float gscale = a.scale * __ldg(a.gk) * kLog2e;
+#pragma unroll
+  for (int h = 0; h < kNH; ++h)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      sl2[h][e] = gscale * __uint_as_float((254u - __shfl_sync(0xFFFFFFFFu, up[h], 4 * (2 * q + e))) << 23);
   int done = 0;
   bool ok = true;
   for (; done < mine; ++done) {
@@ -374,7 +384,7 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
 #pragma unroll
       for (int h = 0; h < kNH; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sacc[kk][h][i] *= sl2;
+        for (int i = 0; i < 4; ++i) sacc[kk][h][i] *= sl2[h][i & 1];
     if (t0 + kTok > t_end) {  // the span's last group: tokens at or past t_end do not count
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {

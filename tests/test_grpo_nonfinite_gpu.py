@@ -1,0 +1,98 @@
+"""GPU: decode attention with queries that hold a NaN or an infinity, and with heads far apart in size: a bad head's row is
+NaN and stays alone (an infinite element makes every score an infinity or a NaN, of which there is no softmax)."""
+import numpy as np
+import pytest
+import torch
+
+from tests import _grpo as G
+from tests import _parity as P
+from tests.test_grpo_kv_gpu import attend, ints, one, setup
+
+pytestmark = pytest.mark.gpu
+
+BF16 = {"nan": 0x7FC1, "-nan": 0xFFC1, "inf": 0x7F80, "-inf": 0xFF80}
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import nvfp4_quantized_rl_gb300 as m
+    m.lib()
+    return m
+
+
+def values(c):
+    return c and tuple(G.values(*x).astype(np.float64) for x in c)
+
+
+def definition(q, pre, own, plens, groups, lens, scale):
+    with np.errstate(invalid="ignore", over="ignore"):
+        return G.attention(P.bf16_f64(q), values(pre), values(own), plens, groups, lens, scale)
+
+
+def decode(nv, q, own, lens, scale):
+    k, v = own
+    out = nv.nvfp4_kv_decode_attention(P.dev_bf16(q), P.dev(k[0]), P.dev(k[1]), one(k[2]), P.dev(v[0]), P.dev(v[1]), one(v[2]),
+                                       ints(lens), scale)
+    torch.cuda.synchronize()
+    return P.bf16_f64(P.host_bits(out))
+
+
+def spoil(q, where, bad):
+    for b, h, d in where:
+        q[b, h, d] = BF16[bad]
+    return q
+
+
+# (sequence, head, element): in the middle of a KV head's heads, and in the last one's last element
+WHERE = [(1, 1, 5), (3, 6, 127), (4, 0, 64)]
+
+
+def others(shape, where):
+    m = np.ones(shape, bool)
+    for b, h, _ in where:
+        m[b, h] = False
+    return m
+
+
+@pytest.mark.parametrize("bad", sorted(BF16))
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (14, 1), (7, 7)])
+@pytest.mark.parametrize("parts", ["both", "prefix", "own"])
+def test_heads_beside_a_bad_one_keep_their_values(nv, bad, Hq, Hkv, parts):
+    q, pre, own = setup(2, 6, Hq, Hkv, 200, 150 if parts != "prefix" else 0, 111, 2.0)
+    plens = [0, 0] if parts == "own" else [200, 131]
+    lens = [150, 149, 1, 70, 64, 0]
+    spoil(q, WHERE, bad)
+    args = (q, pre, own, plens, [0, 4, 6], lens if own else None, 0.09)
+    want, tol = definition(*args)
+    got = P.bf16_f64(P.host_bits(attend(nv, *args)))
+    m = others((6, Hq), WHERE)
+    G.close(got[m], want[m], tol[m], "the other heads")
+
+
+@pytest.mark.parametrize("bad", sorted(BF16))
+@pytest.mark.parametrize("Hq,Hkv,B", [(8, 2, 6), (14, 1, 6), (8, 2, 160)])
+def test_decode_heads_beside_a_bad_one_keep_their_values(nv, bad, Hq, Hkv, B):
+    """With several spans to a sequence and (160 sequences) with one."""
+    q, _, own = setup(1, B, Hq, Hkv, 1, 150, 121, 2.0)
+    lens = [150, 149, 1, 70, 64, 0] + [33] * (B - 6)
+    spoil(q, WHERE, bad)
+    want, tol = definition(q, None, own, [], [0], lens, 0.09)
+    m = others((B, Hq), WHERE)
+    G.close(decode(nv, q, own, lens, 0.09)[m], want[m], tol[m], "the other heads")
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (14, 1)])
+def test_heads_far_apart_in_size(nv, Hq, Hkv):
+    """A head 2^40 times as large as the others of its KV head: theirs keep every digit."""
+    q, pre, own = setup(2, 6, Hq, Hkv, 200, 150, 131, 2.0)
+    big = P.bf16_f64(q[:, 2]) * 2.0 ** 40  # a power of two: exact in bf16
+    q[:, 2] = (big.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    lens = [150, 149, 1, 70, 64, 0]
+    m = others((6, Hq), [(b, 2, 0) for b in range(6)])
+    for plens in ([200, 131], [0, 0]):
+        args = (q, pre, own, plens, [0, 4, 6], lens, 0.09)
+        want, tol = definition(*args)
+        got = P.bf16_f64(P.host_bits(attend(nv, *args)))
+        G.close(got[m], want[m], tol[m], "the other heads")
+    want, tol = definition(q, None, own, [], [0], lens, 0.09)
+    G.close(decode(nv, q, own, lens, 0.09)[m], want[m], tol[m], "the other heads of a decode step")
