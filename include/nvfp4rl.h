@@ -380,6 +380,7 @@ NVFP4RL_API nvfp4rl_status nvfp4_kv_append(const uint16_t* k, const uint16_t* v,
  *            Scale bytes are 0x00 .. 0x7E as the encoder writes them; other bytes give unspecified
  *            (finite or not) results but no fault.
  *   lens     device int32 [B]: tokens attended per sequence, clamped to [0, Lmax]; 0 gives zeros.
+ *            A head of q with a NaN or an infinity gives NaN (its own row alone) where its length is not 0.
  *   scale    softmax scale (typically 1/sqrt(D)), finite.
  *   out      device bf16 [B][Hq][D], 16-byte aligned; may overlap no input.
  *   workspace >= nvfp4rl_workspace_bytes(NVFP4RL_OP_KV_ATTENTION, B, Hkv, Lmax, 0, 0) bytes (may be 0
@@ -455,8 +456,8 @@ NVFP4RL_API nvfp4rl_status nvfp4_kv_read(const uint8_t* k_codes, const uint8_t* 
  *   scale    finite. out  device bf16 [B][Hq][D], 16-byte aligned; may overlap no input.
  *   workspace >= nvfp4rl_workspace_bytes(NVFP4RL_OP_KV_PREFIX_ATTENTION, B, Hkv, Lmax, Hq / Hkv, P) bytes, device, 16-byte
  *            aligned; scratch.
- * A sequence that attends to nothing gets 0. Precision as nvfp4_kv_decode_attention; partial results are fp32, joined
- * in a fixed order: equal inputs give equal bits.
+ * A sequence that attends to nothing gets 0, a head of q with a NaN or an infinity that attends to something NaN. Precision
+ * as nvfp4_kv_decode_attention; partial results are fp32, joined in a fixed order: equal inputs give equal bits.
  * Errors as nvfp4_kv_decode_attention; also NVFP4RL_ERR_UNSUPPORTED_SHAPE where (P + B / (128 / (Hq / Hkv))) Hkv
  * ceil(Lp / 128) is above 2^31 - 1.
  */

@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     const int qexp = static_cast<int>(top >> 7);  // biased exponent of max |q|
     up[h] = static_cast<uint32_t>(min(max(268 - qexp, 1), 253));  // 2^-e is normal, too
-    const float qscale = __uint_as_float(up[h] << 23);
+    // a head with a NaN or an infinity has no softmax: it is all NaN, and so are its scores, its sum and its result
+    const float qscale = qexp == 255 ? NAN : __uint_as_float(up[h] << 23);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       qb[h][i] = pack_f16(__uint_as_float(qb[h][i] << 16) * qscale, __uint_as_float(qb[h][i] & 0xFFFF0000u) * qscale);
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
       O += f * Osm[(w * 16 + r) * kHeadDim + d];
     }
     if (kKind == kDecode && a.nsplit == 1) {
-      const float y = L > 0.0f ? O / L * gv : 0.0f;
+      const float y = L == 0.0f ? 0.0f : O / L * gv;  // a NaN stays
       a.out[(b * a.Hq + kvh * group + r) * kHeadDim + d] = static_cast<uint16_t>(f32_to_bf16_bits(y));
     } else {
       float* pr = a.part + ((bh * a.nsplit + blockIdx.x) * 16 + r) * kPartFloats;
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(128) kv_attention_merge_kernel(const float* __
     O[3] += f * v.w;
   }
   const float gv = __ldg(gvp);
-  const float inv = L > 0.0f ? gv / L : 0.0f;
+  const float inv = L == 0.0f ? 0.0f : gv / L;  // a NaN stays
   uint2 packed;
   packed.x = f32_to_bf16_bits(O[0] * inv) | (f32_to_bf16_bits(O[1] * inv) << 16);
   packed.y = f32_to_bf16_bits(O[2] * inv) | (f32_to_bf16_bits(O[3] * inv) << 16);

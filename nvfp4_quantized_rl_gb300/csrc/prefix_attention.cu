@@ -503,8 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                          __vmaxu2(qv[i].z & 0x7FFF7FFFu, qv[i].w & 0x7FFF7FFFu));
         const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);  // biased exponent of the largest
         const float up = __uint_as_float(static_cast<uint32_t>(min(max(268 - e, 1), 254)) << 23);
-        // S is taken times |scale| below: the scale's sign goes into Q. Rows that do not exist are 0.
-        const float f = member >= s.members ? 0.0f : a.scale < 0.0f ? -up : up;
+        // S is taken times |scale| below: the scale's sign goes into Q. A row with a NaN or an infinity has no softmax: it
+        // is all NaN, and so are its scores, its sum and its result. Rows that do not exist are 0.
+        const float f = member >= s.members ? 0.0f : e == 255 ? NAN : a.scale < 0.0f ? -up : up;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
@@ -898,7 +899,8 @@ __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
     if (i < npre) t = a.stats[(s0 + i * a.groups.beside) * kRows + tile_row];
     else if (i < n) t = make_float2(own_at(i)[0], own_at(i)[1]);
     const float m = fmaxf(M, warp_max(t.x));
-    if (m == -INFINITY) continue;
+    // an empty partial is (-inf, 0); a maximum passes over NaN, so that one of a row of NaN is (-inf, NaN)
+    if (m == -INFINITY && !__any_sync(0xFFFFFFFFu, t.y != 0.0f)) continue;
     const float keep = ex2(M - m), f = ex2(t.x - m);
     L = L * keep + warp_sum(f * t.y);
 #pragma unroll
@@ -926,7 +928,7 @@ __global__ void __launch_bounds__(128) kv_prefix_join_kernel(const JoinArgs a) {
       }
     }
   }
-  const float inv = L > 0.0f ? __ldg(a.gv) / L : 0.0f;
+  const float inv = L == 0.0f ? 0.0f : __ldg(a.gv) / L;  // a NaN stays
   reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(b) * a.Hq + h) * kDim)[lane] =
       make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv), pack_bf16x2(O[2] * inv, O[3] * inv));
 }

@@ -96,3 +96,33 @@ def test_heads_far_apart_in_size(nv, Hq, Hkv):
         G.close(got[m], want[m], tol[m], "the other heads")
     want, tol = definition(q, None, own, [], [0], lens, 0.09)
     G.close(decode(nv, q, own, lens, 0.09)[m], want[m], tol[m], "the other heads of a decode step")
+
+
+@pytest.mark.parametrize("bad", sorted(BF16))
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (14, 1), (7, 7)])
+@pytest.mark.parametrize("parts", ["both", "prefix", "own"])
+def test_a_bad_head_is_nan_where_it_attends(nv, bad, Hq, Hkv, parts):
+    """And 0 where there is nothing to attend to (the last sequence of the group without a prefix)."""
+    q, pre, own = setup(2, 6, Hq, Hkv, 200, 150 if parts != "prefix" else 0, 141, 2.0)
+    plens = [0, 0] if parts == "own" else [200, 0]
+    lens = [150, 149, 1, 70, 64, 0]
+    where = WHERE[:2] + [(5, 0, 0)]
+    spoil(q, where, bad)
+    args = (q, pre, own, plens, [0, 4, 6], lens if own else None, 0.09)
+    want, tol = definition(*args)
+    got = P.bf16_f64(P.host_bits(attend(nv, *args)))
+    assert np.isnan(got[1, 1]).all() and np.isnan(got[3, 6]).all() and not got[5].any()
+    G.close(got, want, tol, "attention")
+
+
+@pytest.mark.parametrize("bad", sorted(BF16))
+@pytest.mark.parametrize("Hq,Hkv,B", [(8, 2, 6), (14, 1, 6), (8, 2, 160)])
+def test_a_bad_head_of_a_decode_step_is_nan_where_it_attends(nv, bad, Hq, Hkv, B):
+    q, _, own = setup(1, B, Hq, Hkv, 1, 150, 151, 2.0)
+    lens = [150, 149, 1, 70, 64, 0] + [33] * (B - 6)
+    where = WHERE[:2] + [(5, 0, 0)]
+    spoil(q, where, bad)
+    want, tol = definition(q, None, own, [], [0], lens, 0.09)
+    got = decode(nv, q, own, lens, 0.09)
+    assert np.isnan(got[1, 1]).all() and np.isnan(got[3, 6]).all() and not got[5].any()
+    G.close(got, want, tol, "decode")
