@@ -452,7 +452,7 @@ NVFP4RL_API nvfp4rl_status nvfp4_kv_read(const uint8_t* k_codes, const uint8_t* 
  *            prefix p. Sequences of no group have no prefix. (Offsets that fall give unspecified results, no fault.)
  *   k_codes .. v_scales, lens, Lmax  the sequences' own caches, as for nvfp4_kv_decode_attention; Lmax 0: there are none
  *            (the pointers and lens are not used).
- *   gk, gv   device fp32 scalars, of both caches.
+ *   gk, gv   device fp32 scalars of any sign, of both caches.
  *   scale    finite. out  device bf16 [B][Hq][D], 16-byte aligned; may overlap no input.
  *   workspace >= nvfp4rl_workspace_bytes(NVFP4RL_OP_KV_PREFIX_ATTENTION, B, Hkv, Lmax, Hq / Hkv, P) bytes, device, 16-byte
  *            aligned; scratch.

@@ -503,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                          __vmaxu2(qv[i].z & 0x7FFF7FFFu, qv[i].w & 0x7FFF7FFFu));
         const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);  // biased exponent of the largest
         const float up = __uint_as_float(static_cast<uint32_t>(min(max(268 - e, 1), 254)) << 23);
-        // S is taken times |scale| below: the scale's sign goes into Q. A row with a NaN or an infinity has no softmax: it
+        // S is taken times |scale gk| below: the sign goes into Q. A row with a NaN or an infinity has no softmax: it
         // is all NaN, and so are its scores, its sum and its result. Rows that do not exist are 0.
-        const float f = member >= s.members ? 0.0f : e == 255 ? NAN : a.scale < 0.0f ? -up : up;
+        const float f = member >= s.members ? 0.0f : e == 255 ? NAN : (a.scale < 0.0f) != (gk < 0.0f) ? -up : up;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
@@ -515,8 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             h[j] = pack_f16(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xFFFF0000u) * f);
           sts128(qs + (i >> 3) * kPanel + 128 * r + (((i & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
         }
-        // at least 2^-100: a masked score, -inf, stays that where the scale is 0
-        row_scale[r] = fmaxf(fabsf(a.scale) * gk * kLog2e / up, 0x1p-100f);
+        // at least 2^-100: a masked score, -inf, stays that where the scale or gk is 0 (a NaN stays)
+        const float to_log2 = fabsf(a.scale) * fabsf(gk) * kLog2e / up;
+        row_scale[r] = to_log2 < 0x1p-100f ? 0x1p-100f : to_log2;
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bars.q_full));

@@ -126,3 +126,19 @@ def test_a_bad_head_of_a_decode_step_is_nan_where_it_attends(nv, bad, Hq, Hkv, B
     got = decode(nv, q, own, lens, 0.09)
     assert np.isnan(got[1, 1]).all() and np.isnan(got[3, 6]).all() and not got[5].any()
     G.close(got, want, tol, "decode")
+
+
+@pytest.mark.parametrize("gk", [-0.0021, 0.0, -0.0, float("nan")])
+@pytest.mark.parametrize("scale", [0.09, -0.09])
+def test_key_scales_of_any_sign(nv, gk, scale):
+    """A negative gk turns the scores' signs, 0 makes all weights equal, and a NaN leaves nothing but NaN."""
+    q, pre, own = setup(2, 6, 8, 2, 200, 150, 161, 2.0)
+    pre = ((*pre[0][:2], np.float32(gk)), pre[1])
+    own = ((*own[0][:2], np.float32(gk)), own[1])
+    for plens, lens in (([200, 131], [150, 149, 1, 70, 0, 0]), ([0, 0], [150, 149, 1, 70, 64, 0]), ([200, 0], [0] * 6)):
+        args = (q, pre, own, plens, [0, 4, 6], lens, scale)
+        want, tol = definition(*args)
+        got = P.bf16_f64(P.host_bits(attend(nv, *args)))
+        G.close(got, want, tol, "attention")
+    want, tol = definition(q, None, own, [], [0], lens, scale)
+    G.close(decode(nv, q, own, lens, scale), want, tol, "decode")
