@@ -518,54 +518,53 @@ __global__ void __launch_bounds__(kAttnThreads, kNH == 1 ? 3 : 2)
       *reinterpret_cast<float4*>(pr + r * kPartFloats + 4 + 4 * lane) = o;
     }
     in_order();
-    return;
-  }
-  __syncthreads();  // every warp is done with its ring: it becomes the merge area
-  float* Osm = reinterpret_cast<float*>(smem_raw + (ring0 - raw));  // [warp][16 heads][128 dims]
-  if (g == 0) {
+  } else {
+    __syncthreads();  // every warp is done with its ring: it becomes the merge area
+    float* Osm = reinterpret_cast<float*>(smem_raw + (ring0 - raw));  // [warp][16 heads][128 dims]
+    if (g == 0) {
 #pragma unroll
-    for (int h = 0; h < kNH; ++h)
+      for (int h = 0; h < kNH; ++h)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        msm[warp][8 * h + 2 * q + e] = m_run[h][e];
-        lsm[warp][8 * h + 2 * q + e] = l_run[h][e];
-      }
-  }
-#pragma unroll
-  for (int m = 0; m < 8; ++m)
-#pragma unroll
-    for (int h = 0; h < kNH; ++h)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *reinterpret_cast<float2*>(Osm + (warp * 16 + 8 * h + 2 * q + e) * kHeadDim + 16 * g + 2 * m) =
-            make_float2(oacc[m][h][e], oacc[m][h][2 + e]);
-  __syncthreads();
-  const float gv = __ldg(a.gv);
-  for (int i = threadIdx.x; i < group * kHeadDim; i += kAttnThreads) {
-    const int r = i / kHeadDim, d = i % kHeadDim;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, msm[w][r]);
-    float L = 0.0f, O = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = msm[w][r] == -INFINITY ? 0.0f : exp2f(msm[w][r] - M);
-      L += f * lsm[w][r];
-      O += f * Osm[(w * 16 + r) * kHeadDim + d];
+        for (int e = 0; e < 2; ++e) {
+          msm[warp][8 * h + 2 * q + e] = m_run[h][e];
+          lsm[warp][8 * h + 2 * q + e] = l_run[h][e];
+        }
     }
-    if (kKind == kDecode && a.nsplit == 1) {
-      const float y = L == 0.0f ? 0.0f : O / L * gv;  // a NaN stays
-      a.out[(b * a.Hq + kvh * group + r) * kHeadDim + d] = static_cast<uint16_t>(f32_to_bf16_bits(y));
-    } else {
-      float* pr = a.part + ((bh * a.nsplit + blockIdx.x) * 16 + r) * kPartFloats;
-      if (d == 0) {
-        pr[0] = M;
-        pr[1] = L;
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+      for (int h = 0; h < kNH; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2*>(Osm + (warp * 16 + 8 * h + 2 * q + e) * kHeadDim + 16 * g + 2 * m) =
+              make_float2(oacc[m][h][e], oacc[m][h][2 + e]);
+    __syncthreads();
+    const float gv = __ldg(a.gv);
+    for (int i = threadIdx.x; i < group * kHeadDim; i += kAttnThreads) {
+      const int r = i / kHeadDim, d = i % kHeadDim;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, msm[w][r]);
+      float L = 0.0f, O = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = msm[w][r] == -INFINITY ? 0.0f : exp2f(msm[w][r] - M);
+        L += f * lsm[w][r];
+        O += f * Osm[(w * 16 + r) * kHeadDim + d];
       }
-      pr[4 + d] = O;
+      if (a.nsplit == 1) {
+        const float y = L == 0.0f ? 0.0f : O / L * gv;  // a NaN stays
+        a.out[(b * a.Hq + kvh * group + r) * kHeadDim + d] = static_cast<uint16_t>(f32_to_bf16_bits(y));
+      } else {
+        float* pr = a.part + ((bh * a.nsplit + blockIdx.x) * 16 + r) * kPartFloats;
+        if (d == 0) {
+          pr[0] = M;
+          pr[1] = L;
+        }
+        pr[4 + d] = O;
+      }
     }
   }
-  in_order();
 }
 
 // Merges the spans of every (sequence, query head): out = sum_s f_s O_s / sum_s f_s L_s * gv,

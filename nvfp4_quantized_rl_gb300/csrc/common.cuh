@@ -90,7 +90,16 @@ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // no-op for a kernel launched without the attribute). The library's kernels on the decode path
 // call griddep_wait before touching global memory and only then griddep_launch_dependents, so
 // every kernel still observes all earlier kernels complete, while the next launch overlaps the
-// current kernel's tail.
+// current kernel's tail. Two kinds of kernel touch memory ahead of that wait, and only behind a kernel of the
+// same call that follows the rule above (its CTAs let this one start behind their own wait, so that whatever came
+// before the call is complete):
+//   - the joins of the shared-prefix attention and of the losses read the call's offsets and lengths, which
+//     no kernel of the call writes;
+//   - the own caches' kernel of the shared-prefix attention (kOwn in attention.cu) takes nothing from the prefix kernel
+//     ahead of it: it reads the call's inputs and writes its part of the workspace without a wait. Its first CTA
+//     waits at its end, so that the kernel's completion implies the prefix kernel's, for the join behind it.
+// A kernel placed between those of such a call has to keep both: wait before it lets the next one start, and write
+// nothing that the next one reads ahead.
 #ifdef __CUDACC__
 __device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
