@@ -485,12 +485,14 @@ NVFP4RL_API nvfp4rl_status nvfp4_kv_prefix_attention(
  *   offsets  int32 [B + 1], non-decreasing, within [0, n]. n <= 2^31 - 1, B <= 2^31 - 2. Tokens of no sequence do not count.
  *   eps_low in [0, 1), eps_high >= 0, dual_clip 0 or >= 1, kl_coef >= 0, norm > 0 (SUM only), all finite.
  *   loss     out, fp32 [1]. coef  out, fp32 [B], or NULL: what policy_loss_backward takes.
+ *   A norm that only the device knows (a count over several calls): norm 1, and its inverse as policy_loss_backward's dloss.
  *   stats    out, fp32 [8], or NULL: the loss, sum c_i l_i, sum c_i k_i, and over the counted tokens the share that
  *            clipping decided, the mean of e^d - d - 1 (divergence from the old policy), the mean of r, their number,
  *            and the number of sequences with one.
  *   workspace >= nvfp4rl_workspace_bytes(NVFP4RL_OP_POLICY_LOSS, n, B, 0, 0, 0) bytes, device, 16-byte aligned; scratch.
  *   Other arrays are aligned to their elements (mask to 1 byte).
- * What a token that does not count holds is not looked at (NaN, -inf). A NaN in a counted one gives a NaN loss. An advantage
+ * What a token that does not count holds is not looked at (NaN, -inf). A NaN in a counted one gives a NaN loss, but where it has
+ * no part: with kl_coef 0 logp_ref only enters stats[2], and an advantage of 0 leaves r and w out of l. An advantage
  * of 0 gives l = 0 whatever r is. Whether r lies beyond a bound is decided on the exact d against the logarithm of the
  * bound (to 2^-48), so that it does not depend on a rounding. Sums run in fp32 over 256 tokens, then in pairs of
  * fp32. No atomics on floating values: equal inputs give equal bits. Offsets that fall give unspecified values, no fault.

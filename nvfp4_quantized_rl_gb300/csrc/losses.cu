@@ -9,9 +9,12 @@
 // and the CTA that finishes last joins the sequences; small batches do both in one CTA. No floating-point atomics: equal
 // inputs give equal bits.
 //
-// 4 Mi tokens in 512 sequences with every term: forward and backward 54 us, 0.24 of the measured copy bandwidth, in one
-// wave of warps that each take a stretch of the steps and load the next step ahead (a warp for each step 58 us; tokens one
-// at a time and expf 65; branches in the token 137). 2 Mi tokens in 2048 sequences of the preference loss: 19 us, 0.2.
+// 4 Mi tokens in 512 sequences with every term, 88 MB, forward and backward: 57 us from a cold L2 (0.23 of the measured copy
+// bandwidth), 46 us again and again on arrays that the L2 holds; 2 Mi tokens in 2048 sequences of the preference loss, 27 MB: 24
+// and 16 us. (Cold: a graph of one pass behind a write of 256 MB, of which a graph's start takes up to 7 us.) Steps that led here,
+// on arrays in L2, one pass to a graph: branches in the token 137 us; tokens one at a time and expf 65; a warp for each step
+// 58; one wave of warps that each take a stretch of the steps and load the next step ahead 54. The backward pass evaluates the
+// forward's exponentials again: what a token gives is not kept.
 //
 // Ratios next to a bound: whether r = e^d lies above 1 + eps is decided as d > ln(1 + eps), with d the exact
 // difference of the two log-probs (two floats, from one TwoSum) and the logarithm split into two floats, so

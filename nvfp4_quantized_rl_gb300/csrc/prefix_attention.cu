@@ -28,10 +28,14 @@
 //   TMEM: three S / P buffers and O, so that the scores of block n + 2 can follow the values of block n - 1 and are there
 //   when the softmax of block n ends.
 // A block takes 0.94 us (1800 clocks) in long stretches, 0.44 of the measured copy bandwidth, and a call 18 to 25 us beside its
-// blocks (256 sequences behind sixteen prefixes). No unit is full: copies of the kernel that left out work took, of 125 us,
-// without the decoding 113, without exponentials and half of the maximum 116, with an eighth of the products 111 to 121, without
-// the copies 118, without any of these 78: what remains is the chain scores - softmax - values around the three score buffers.
-// Q enters as f16 scaled per row by a power of two that puts its largest element in [2^14, 2^15): exact down to 2^-31 of it.
+// blocks (256 sequences behind sixteen prefixes, 154 us). What bounds it is the dependent chain scores - softmax - values with three
+// blocks in flight: no unit is full. (Copies that left out work, of a build that read the heads one after another and took 125 us
+// where this one takes 112: without the decoding 113, without exponentials and half of the maximum 116, with an eighth of the
+// products 111 to 121, without the copies 118, without any of these 78.) Rows as M take 128 columns of TMEM to a score buffer and
+// a whole tile's time whatever their number; rows as N would not, and is not built.
+// Q enters as f16 scaled per row by a power of two that puts its largest element in [2^14, 2^15): exact down to 2^-31 of it. P is
+// f16: results differ from those of an fp32 P by up to 8e-4 (relative), their distance from 64 bits stays that of
+// the rounding to bf16, 1.7e-3.
 #include <climits>
 #include <map>
 #include <mutex>

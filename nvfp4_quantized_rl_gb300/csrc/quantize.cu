@@ -1280,8 +1280,8 @@ __device__ __noinline__ void encode_block_exact(BlockWords<kDtype> w, int64_t bl
 // Plain encoding of one fp32 block without tables: with r = fl(1 / fl(E4M3(s) g)), x r is within 2^-21 of the
 // real quotient (relative), so that x r (1 - 2^-20) and x r (1 + 2^-20) lie on either side of it, and where
 // both round to one E2M1 code by the hardware conversion (nearest, rising), that is the quotient's code. Blocks with an
-// element next to a midpoint (one in 5000), not finite, or with a scale near the fp32 range's ends take the exact compares.
-// (bf16 values are next to a midpoint far more often: one block in 40 where g is a short fraction.)
+// element next to a midpoint (of normal fp32 rows one block in 16000), not finite, or with a scale near the fp32 range's ends
+// take the exact compares. (bf16 values lie on midpoints where g is a short fraction: one block in six at g = 2^-9.)
 __device__ __forceinline__ void encode_block_bracket(const BlockWords<NVFP4RL_F32>& w, int64_t blk, float g, float inv_g6,
                                                      float est_scale, uint8_t* __restrict__ codes,
                                                      uint8_t* __restrict__ scales) {

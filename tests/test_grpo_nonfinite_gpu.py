@@ -1,5 +1,6 @@
-"""GPU: decode attention with queries that hold a NaN or an infinity, and with heads far apart in size: a bad head's row is
-NaN and stays alone (an infinite element makes every score an infinity or a NaN, of which there is no softmax)."""
+"""GPU: decode attention with queries that hold a NaN or an infinity, with heads far apart in size and with scales of any sign:
+a bad head's row is NaN and stays alone (an infinite element makes every score an infinity or a NaN, of which there is no
+softmax). The policy loss with NaN where it has no part."""
 import numpy as np
 import pytest
 import torch
@@ -7,6 +8,7 @@ import torch
 from tests import _grpo as G
 from tests import _parity as P
 from tests.test_grpo_kv_gpu import attend, ints, one, setup
+from tests.test_grpo_loss_gpu import check_policy, run_policy, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +144,31 @@ def test_key_scales_of_any_sign(nv, gk, scale):
         G.close(got, want, tol, "attention")
     want, tol = definition(q, None, own, [], [0], lens, scale)
     G.close(decode(nv, q, own, lens, scale), want, tol, "decode")
+
+
+def test_policy_nan_without_a_part_in_the_loss(nv):
+    """An advantage of 0 leaves r and w out of the loss, a kl_coef of 0 the reference: they show in the statistics alone."""
+    old, logp, ref = tokens(60, 171)
+    adv, off = np.array([0.5, 0.0, -1.0], np.float32), np.array([0, 20, 40, 60], np.int32)
+    w = np.ones(60, np.float32)
+    w[22], logp[25], old[31] = np.nan, np.nan, np.nan
+    got = check_policy(nv, logp, old, adv, off, weights=w)
+    assert np.isfinite(got["loss"][0]) and np.isnan(got["stats"][4:6]).all() and not got["dlogp"][20:40].any()
+    old, logp, ref = tokens(60, 172)
+    ref[7] = np.nan
+    with_ref, without = (run_policy(nv, logp, old, adv, off, ref=r) for r in (ref, None))
+    assert np.isnan(with_ref["stats"][2]) and np.array_equal(with_ref["loss"], without["loss"])
+    assert np.array_equal(with_ref["dlogp"], without["dlogp"])
+
+
+def test_policy_norm_on_the_device(nv):
+    """A sum of norm 1 whose gradient is scaled by a count that only the device knows: the token mean's gradient."""
+    old, logp, ref = tokens(700, 173)
+    off, adv = np.array([0, 300, 700], np.int32), np.array([0.7, -1.3], np.float32)
+    want = G.policy(logp, old, adv, off, ref=ref, kl=0.1)
+    args = [P.dev(x) for x in (logp, old, adv, off)]
+    terms = dict(logp_ref=P.dev(ref), kl_coef=0.1)
+    coef = nv.policy_loss(*args, mode=nv.LOSS_SUM, norm=1.0, **terms)[2]
+    count = torch.full((1,), 700.0, device="cuda")
+    grad = nv.policy_loss_backward(*args, coef, 1 / count, **terms)
+    G.close(grad.cpu().numpy(), want["dlogp"], want["tol"]["dlogp"], "dlogp")
