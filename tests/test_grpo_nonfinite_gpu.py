@@ -146,6 +146,18 @@ def test_key_scales_of_any_sign(nv, gk, scale):
     G.close(decode(nv, q, own, lens, scale), want, tol, "decode")
 
 
+@pytest.mark.parametrize("bad", sorted(BF16))
+def test_a_bad_first_row_stays_out_of_the_rows_that_fill_a_tile(nv, bad):
+    """The batch's first head is bad, and every tile has rows without a sequence."""
+    q, pre, own = setup(3, 9, 14, 2, 300, 40, 175, 2.0)
+    spoil(q, [(0, 0, 0)], bad)
+    args = (q, pre, own, [300, 200, 77], [0, 1, 4, 9], [40, 0, 3, 5, 40, 1, 0, 2, 9], 0.09)
+    want, tol = definition(*args)
+    got = P.bf16_f64(P.host_bits(attend(nv, *args)))
+    assert np.isnan(got[0, 0]).all()
+    G.close(got, want, tol, "attention")
+
+
 def test_policy_nan_without_a_part_in_the_loss(nv):
     """An advantage of 0 leaves r and w out of the loss, a kl_coef of 0 the reference: they show in the statistics alone."""
     old, logp, ref = tokens(60, 171)
